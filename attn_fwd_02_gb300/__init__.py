@@ -26,6 +26,8 @@ from .binding import (  # noqa: F401
     paged_attn_prefill_fp8,
     paged_kv_append,
     paged_kv_append_fp8,
+    paged_kv_append_rope,
+    paged_kv_append_rope_fp8,
     paged_attn_decode_gqa_workspace_size,
     paged_attn_decode_workspace_size,
     paged_attn_decode_workspace_size_ctx,

@@ -426,6 +426,77 @@ ATTN_API int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_p
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+namespace {
+// Strides {batch, head, token} of a [B, H, N, d] input, in elements: the caller's (dims of size one
+// count as 0), or those of a contiguous tensor.  Rows are read as 16-byte vectors.
+int input_strides(const int64_t *given, int B, int H, int N, int d, int64_t (&out)[3]) {
+    const int64_t dense[3] = {(int64_t)H * N * d, (int64_t)N * d, d};
+    const int size[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i) {
+        out[i] = size[i] == 1 ? 0 : (given ? given[i] : dense[i]);
+        if (out[i] < 0 || out[i] > (1ll << 40)) return ATTN_ERR_INVALID_ARG;
+        if (out[i] % 8 != 0) return ATTN_ERR_MISALIGNED;
+    }
+    return ATTN_OK;
+}
+
+int append_rope(attn::RopeAppendArgs a, const int64_t *q_strides, const int64_t *k_strides, const int64_t *v_strides,
+                int page_size, attn_stream_t stream) {
+    if (!a.k_new || !a.v_new || !a.k_pages || !a.v_pages || !a.cos_sin || !a.page_table || !a.start_pos)
+        return ATTN_ERR_INVALID_ARG;
+    if ((a.q == nullptr) != (a.q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (a.B <= 0 || a.Hkv <= 0 || a.Nnew <= 0 || a.d <= 0 || page_size <= 0 || a.max_pages <= 0 || a.num_pages <= 0 ||
+        a.max_pos <= 0 || (a.q && a.H <= 0))
+        return ATTN_ERR_INVALID_ARG;
+    if (a.interleaved != 0 && a.interleaved != 1) return ATTN_ERR_INVALID_ARG;
+    if (a.kv_fp8 && (!finite_positive(a.k_scale) || !finite_positive(a.v_scale))) return ATTN_ERR_INVALID_ARG;
+    if (!prefill_head_dim(a.d) || page_size != 16) return ATTN_ERR_UNSUPPORTED;
+    if (a.rope_dim <= 0 || a.rope_dim > a.d || a.rope_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((uint64_t)a.max_pages * 16 > (1ull << 30)) return ATTN_ERR_INVALID_ARG;
+    if ((uint64_t)a.B * (uint64_t)a.Nnew > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
+    if ((uint64_t)(a.q ? a.H : 0) + 2 * (uint64_t)a.Hkv > (1u << 24)) return ATTN_ERR_INVALID_ARG;
+    if (!a.q) a.H = 0;
+    int st = input_strides(a.q ? q_strides : nullptr, a.B, a.q ? a.H : 1, a.Nnew, a.d, a.q_strides);
+    if (st == ATTN_OK) st = input_strides(k_strides, a.B, a.Hkv, a.Nnew, a.d, a.k_strides);
+    if (st == ATTN_OK) st = input_strides(v_strides, a.B, a.Hkv, a.Nnew, a.d, a.v_strides);
+    if (st != ATTN_OK) return st;
+    if (!aligned16(a.q) || !aligned16(a.q_out) || !aligned16(a.k_new) || !aligned16(a.v_new) || !aligned16(a.k_pages) ||
+        !aligned16(a.v_pages) || !aligned16(a.cos_sin))
+        return ATTN_ERR_MISALIGNED;
+    if (!aligned4(a.page_table) || !aligned4(a.start_pos) || !aligned4(a.new_lens)) return ATTN_ERR_MISALIGNED;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+}  // namespace
+
+ATTN_API int paged_kv_append_rope(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                                  const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages,
+                                  void *v_pages, const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                                  const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                                  int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                                  int num_pages, attn_stream_t stream) {
+    attn::RopeAppendArgs a{q, k_new, v_new, {}, {}, {}, q_out, k_pages, v_pages, cos_sin, rope_dim, max_pos,
+                           interleaved, page_table, start_pos, new_lens, B, H, Hkv, Nnew, d, max_pages_per_seq,
+                           num_pages};
+    return append_rope(a, q_strides, k_strides, v_strides, page_size, stream);
+}
+
+ATTN_API int paged_kv_append_rope_fp8(const void *q, const int64_t *q_strides, const void *k_new,
+                                      const int64_t *k_strides, const void *v_new, const int64_t *v_strides,
+                                      void *q_out, void *k_pages, void *v_pages, float k_scale, float v_scale,
+                                      const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                                      const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                                      int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                                      int num_pages, attn_stream_t stream) {
+    attn::RopeAppendArgs a{q, k_new, v_new, {}, {}, {}, q_out, k_pages, v_pages, cos_sin, rope_dim, max_pos,
+                           interleaved, page_table, start_pos, new_lens, B, H, Hkv, Nnew, d, max_pages_per_seq,
+                           num_pages, 1, k_scale, v_scale};
+    return append_rope(a, q_strides, k_strides, v_strides, page_size, stream);
+}
+
 ATTN_API int paged_attn_decode_gqa(const void *q, const void *k_pages, const void *v_pages,
                                    const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o,
                                    float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages,

@@ -89,6 +89,20 @@ cudaError_t launch_kv_append_fp8(const void *k_new, const void *v_new, void *k_p
                                  const int32_t *start_pos, int B, int Hkv, int Nnew, int d, int max_pages,
                                  int num_pages, cudaStream_t stream);
 
+// As the append, with the queries and keys rotated to their positions on the way.
+struct RopeAppendArgs {
+    const void *q, *k_new, *v_new;                   // q may be null (keys and values only)
+    int64_t q_strides[3], k_strides[3], v_strides[3];  // batch, head, token, in elements
+    void *q_out, *k_pages, *v_pages;
+    const float *cos_sin;  // [max_pos, rope_dim]
+    int rope_dim, max_pos, interleaved;
+    const int32_t *page_table, *start_pos, *new_lens;  // new_lens may be null
+    int B, H, Hkv, Nnew, d, max_pages, num_pages;
+    int kv_fp8 = 0;
+    float k_scale = 1.f, v_scale = 1.f;
+};
+cudaError_t launch_kv_append_rope(const RopeAppendArgs &a, cudaStream_t stream);
+
 // Launches the split kernel and the combine kernel.
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 

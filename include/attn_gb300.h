@@ -223,6 +223,44 @@ int paged_kv_append(const void *k_new, const void *v_new, void *k_pages, void *v
                     attn_stream_t stream);
 
 /*
+ * paged_kv_append with rotary position embedding on the way: the new tokens' queries and keys are
+ * rotated to their positions, keys and values go to the pages, the rotated queries to q_out.  Token t
+ * of sequence b sits at position p = max(start_pos[b], 0) + t.  The first rope_dim dims of a query or
+ * key row are rope_dim / 2 pairs (x, y) -- dims (i, i + rope_dim / 2), or (2i, 2i + 1) when
+ * interleaved is 1 -- and
+ *     x' = x cos[p][i] - y sin[p][i],   y' = y cos[p][i] + x sin[p][i];
+ * the other dims and the values are copied.  Computed in fp32 and rounded once.
+ *   q [B, H, Nnew, d], k_new, v_new [B, Hkv, Nnew, d] bf16; *_strides: HOST arrays of three strides
+ *     {batch, head, token} in elements (the last dim is contiguous), non-negative multiples of 8, so
+ *     views of a fused [B, Nnew, (H + 2 Hkv) d] projection need no copy; NULL means contiguous
+ *   q and q_out may both be NULL (keys and values only; H is then ignored)
+ *   q_out [B, H, Nnew, d] bf16, contiguous; may be q itself if q is contiguous, else must not
+ *     overlap an input
+ *   cos_sin [max_pos, rope_dim] fp32: row p holds cos of its rope_dim / 2 pairs, then their sin
+ *   rope_dim: a multiple of 16, at most d
+ *   start_pos [B] int32; new_lens [B] int32 (may be NULL: Nnew each): tokens t >= new_lens[b] are
+ *     padding.  Of padding, and of tokens at positions >= max_pos, nothing is written at all.
+ * Keys and values of positions past the page table's capacity and of page ids outside [0, num_pages)
+ * are skipped as in paged_kv_append; their queries are still rotated.  Two tokens of one call must
+ * not map to the same page slot.  d in {32, 64, 80, 96, 128}, page_size 16.
+ * paged_kv_append_rope_fp8: into an e4m3 cache (see below), the rotated fp32 key times 1 / k_scale
+ * rounded once to e4m3.
+ */
+int paged_kv_append_rope(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                         const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                         const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                         const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                         int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                         int num_pages, attn_stream_t stream);
+
+int paged_kv_append_rope_fp8(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                             const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                             float k_scale, float v_scale, const float *cos_sin, int rope_dim, int max_pos,
+                             int interleaved, const int32_t *page_table, const int32_t *start_pos,
+                             const int32_t *new_lens, int page_size, int B, int H, int Hkv, int Nnew, int d,
+                             int max_pages_per_seq, int num_pages, attn_stream_t stream);
+
+/*
  * FP8 KV cache.  The NanoInfer README's roadmap names FP8 e4m3 storage (cuda_fp8.h
  * __nv_fp8_e4m3) as the successor of INT8 with the quantisation math unchanged;
  * here it is the storage of the paged KV cache, which halves the bytes a decode
