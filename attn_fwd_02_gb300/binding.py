@@ -512,103 +512,123 @@ def paged_kv_append(k_new, v_new, k_pages, v_pages, page_table, start_pos, strea
     _check("paged_kv_append", st)
 
 
-def _same_device(device, **tensors):
-    """Every given tensor (None: not given) is on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-class _launch_on:
-    """Makes ``device`` the current one for a call and yields the pointer of ``stream`` (None: the
-    device's current stream).  Tensors allocated inside belong to that stream, so the allocator
-    does not hand their memory to another stream's work while the call still uses it."""
-
-    def __init__(self, device, stream):
+def _torch():
+    """torch, imported at the first call (the module itself loads without it)."""
+    global _t
+    if _t is None:
         import torch
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream must be on {device}, got {stream.device}")
-        self._ctx = None
-        if stream is not None:
-            self._ctx = torch.cuda.stream(stream)  # also makes the stream's device current
-        elif torch.cuda.current_device() != device.index:
-            self._ctx = torch.cuda.device(device)
-        self._device, self._stream = device, stream
-
-    def __enter__(self):
-        import torch
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        stream = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            return self._ctx.__exit__(*exc)
+        _t = torch
+    return _t
 
 
-def _strided_rows(t, name, shape):
-    """A [B, H, N, d] bf16 CUDA view with contiguous rows; returns its strides as a C array (the
-    strides of dims of size one, which torch leaves arbitrary, count as 0)."""
-    import torch
+_t = None
+
+
+def _in(t, name, dtype, ndim, device=None):
+    """Address of a contiguous CUDA tensor of this dtype and number of dims on ``device`` (None: any).
+    The checks of _require with one pass over the attributes: a call's host time counts where the
+    kernel takes a few microseconds."""
+    try:
+        if t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+            if t.is_cuda and (device is None or t.device == device):
+                return t.data_ptr()
+    except AttributeError:
+        pass
+    _require(t, name, dtype, ndim)
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _elsewhere(device, stream):
+    """Context that makes ``stream`` (None: the device's current stream) and its device current, or
+    None if they already are.  Tensors allocated inside belong to that stream, so the allocator does
+    not hand their memory to another stream's work while the call still uses it."""
+    torch = _t
+    if stream is None:
+        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _current_stream(device):
+    return _t._C._cuda_getCurrentRawStream(device.index)
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def _rows_in(t, name, shape, device=None):
+    """A [B, H, N, d] bf16 CUDA view with contiguous rows: its address and its strides as a C array
+    (None if contiguous; the strides of dims of size one, which torch leaves arbitrary, count as 0)."""
+    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    s = t.shape
+    if len(s) != 4 or (shape is not None and s != shape):
         raise ValueError(f"{name} must be [B, heads, Nnew, d]" +
-                         (f" = {tuple(shape)}" if shape is not None else "") + f", got {tuple(t.shape)}")
-    if t.stride(3) != 1:
+                         (f" = {tuple(shape)}" if shape is not None else "") + f", got {tuple(s)}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    b, h, n, e = t.stride()
+    if e != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
-    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-    if any(x % 8 for x in st):
-        raise ValueError(f"the strides of {name} must be multiples of 8 elements, got {tuple(t.stride())}")
-    return (ctypes.c_int64 * 3)(*st)
+    b, h, n = (0 if s[0] == 1 else b), (0 if s[1] == 1 else h), (0 if s[2] == 1 else n)
+    if (b | h | n) & 7:
+        raise ValueError(f"the strides of {name} must be multiples of 8 elements, got {t.stride()}")
+    return t.data_ptr(), _Strides(b, h, n)
 
 
 def _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_sin, page_table, start_pos,
                  interleaved, new_lens, q_out, stream):
-    import torch
-    ks = _strided_rows(k_new, "k_new", None)
+    torch = _torch()
+    kp, ks = _rows_in(k_new, "k_new", None)
+    device = k_new.device
     B, Hkv, N, d = k_new.shape
-    vs = _strided_rows(v_new, "v_new", k_new.shape)
-    _require(k_pages, "k_pages", page_dtype, 4)
-    _require(v_pages, "v_pages", page_dtype, 4)
-    _require(cos_sin, "cos_sin", torch.float32, 2)
-    _require(page_table, "page_table", torch.int32, 2)
-    _require(start_pos, "start_pos", torch.int32, 1)
+    vp, vs = _rows_in(v_new, "v_new", k_new.shape, device)
+    kpool, vpool = _in(k_pages, "k_pages", page_dtype, 4, device), _in(v_pages, "v_pages", page_dtype, 4, device)
+    cs = _in(cos_sin, "cos_sin", torch.float32, 2, device)
+    table = _in(page_table, "page_table", torch.int32, 2, device)
+    start = _in(start_pos, "start_pos", torch.int32, 1, device)
     num_pages, Hk, page_size, dk = k_pages.shape
     if (Hk, dk) != (Hkv, d) or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d] matching k_new")
-    if page_table.shape[0] != B or start_pos.shape[0] != B:
+    Bt, max_pages = page_table.shape
+    if Bt != B or start_pos.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages] and start_pos [B]")
+    new = None
     if new_lens is not None:
-        _require(new_lens, "new_lens", torch.int32, 1)
+        new = _in(new_lens, "new_lens", torch.int32, 1, device)
         if new_lens.shape[0] != B:
             raise ValueError("new_lens must be [B]")
-    device = k_new.device
-    H, qs = 0, None
+    H, qp, qs, qo = 0, None, None, None
     if q is not None:
         H = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
-        qs = _strided_rows(q, "q", (B, H, N, d))
+        qp, qs = _rows_in(q, "q", torch.Size((B, H, N, d)), device)
         if q_out is not None:
-            _require(q_out, "q_out", torch.bfloat16, 4)
+            qo = _in(q_out, "q_out", torch.bfloat16, 4, device)
             if q_out.shape != q.shape:
                 raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    _same_device(device, q=q, v_new=v_new, k_pages=k_pages, v_pages=v_pages, cos_sin=cos_sin, page_table=page_table,
-                 start_pos=start_pos, new_lens=new_lens, q_out=q_out)
-    with _launch_on(device, stream) as sp:
-        if q is not None and q_out is None:
-            q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
-        st = getattr(load_library(), fn)(
-            _dptr(q), qs, _dptr(k_new), ks, _dptr(v_new), vs, _dptr(q_out), _dptr(k_pages), _dptr(v_pages), *scales,
-            _dptr(cos_sin), cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)), _dptr(page_table),
-            _dptr(start_pos), _dptr(new_lens), page_size, B, H, Hkv, N, d, page_table.shape[1], num_pages, sp)
-    _check(fn, st)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_sin, page_table,
+                                start_pos, interleaved, new_lens, q_out, None)
+    if q is not None and q_out is None:
+        q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
+        qo = q_out.data_ptr()
+    st = getattr(load_library(), fn)(
+        qp, qs, kp, ks, vp, vs, qo, kpool, vpool, *scales, cs, cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)),
+        table, start, new, page_size, B, H, Hkv, N, d, max_pages, num_pages, _current_stream(device))
+    if st:
+        _check(fn, st)
     return q_out
 
 
@@ -621,16 +641,14 @@ def paged_kv_append_rope(q, k_new, v_new, k_pages, v_pages, cos_sin, page_table,
     optional [B] int32, the tokens past it being padding, of which nothing is written (allocated
     q_out rows of padding are uninitialised).  Returns q_out [B,H,Nnew,d] bf16, contiguous (q itself
     may be given if contiguous)."""
-    import torch
-    return _append_rope("paged_kv_append_rope", q, k_new, v_new, k_pages, v_pages, torch.bfloat16, (), cos_sin,
+    return _append_rope("paged_kv_append_rope", q, k_new, v_new, k_pages, v_pages, _torch().bfloat16, (), cos_sin,
                         page_table, start_pos, interleaved, new_lens, q_out, stream)
 
 
 def paged_kv_append_rope_fp8(q, k_new, v_new, k_pages, v_pages, k_scale: float, v_scale: float, cos_sin, page_table,
                              start_pos, interleaved: bool = False, new_lens=None, q_out=None, stream=None):
     """paged_kv_append_rope into an e4m3 cache (k_pages, v_pages uint8 [P,Hkv,16,d])."""
-    import torch
-    return _append_rope("paged_kv_append_rope_fp8", q, k_new, v_new, k_pages, v_pages, torch.uint8,
+    return _append_rope("paged_kv_append_rope_fp8", q, k_new, v_new, k_pages, v_pages, _torch().uint8,
                         (float(k_scale), float(v_scale)), cos_sin, page_table, start_pos, interleaved, new_lens,
                         q_out, stream)
 
