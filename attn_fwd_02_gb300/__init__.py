@@ -14,6 +14,7 @@ from .binding import (  # noqa: F401
     attn_fwd,
     attn_fwd_gqa,
     attn_fwd_kvlen,
+    attn_fwd_scoremod,
     attn_status_string,
     kv_quantize_fp8,
     library_path,

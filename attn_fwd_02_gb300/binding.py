@@ -46,6 +46,7 @@ SIGNATURES = {
     "attn_bwd": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, P, Z, P]),
     "paged_kv_append_rope": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
     "paged_kv_append_rope_fp8": (I, [P, P, P, P, P, P, P, P, P, F, F, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
+    "attn_fwd_scoremod": (I, [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P]),
     "attn_check_device_status": (I, [P]),
     "attn_last_device_status": (I, []),
     "attn_selftest_bounded_wait": (I, [P]),
@@ -651,6 +652,73 @@ def paged_kv_append_rope_fp8(q, k_new, v_new, k_pages, v_pages, k_scale: float, 
     return _append_rope("paged_kv_append_rope_fp8", q, k_new, v_new, k_pages, v_pages, _torch().uint8,
                         (float(k_scale), float(v_scale)), cos_sin, page_table, start_pos, interleaved, new_lens,
                         q_out, stream)
+
+
+def _optional(t, name, dtype, shape, device):
+    """Address of an optional tensor of this shape (None if not given)."""
+    if t is None:
+        return None
+    p = _in(t, name, dtype, len(shape), device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return p
+
+
+def _output(t, name, dtype, shape, device):
+    """The output given by the caller (checked) or a new one: tensor and address."""
+    if t is None:
+        t = _t.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    p = _in(t, name, dtype, len(shape), device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t, p
+
+
+def _dense_inputs(q, k, v):
+    """Addresses and sizes of q [B,Hq,Nq,d] and k, v [B,Hkv,Nkv,d], bf16 on one device."""
+    bf = _torch().bfloat16
+    qp = _in(q, "q", bf, 4)
+    device = q.device
+    kp, vp = _in(k, "k", bf, 4, device), _in(v, "v", bf, 4, device)
+    B, Hq, Nq, d = q.shape
+    Bk, Hkv, Nkv, dk = k.shape
+    if Bk != B or dk != d or v.shape != k.shape:
+        raise ValueError("k and v must be [B, Hkv, Nkv, d] matching q")
+    return device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d
+
+
+def _scoremod_inputs(device, B, Hq, Nq, alibi_slopes, key_begin, key_end, kv_lens):
+    i32 = _t.int32
+    return (_optional(alibi_slopes, "alibi_slopes", _t.float32, (Hq,), device),
+            _optional(key_begin, "key_begin", i32, (B, Nq), device),
+            _optional(key_end, "key_end", i32, (B, Nq), device), _optional(kv_lens, "kv_lens", i32, (B,), device))
+
+
+def attn_fwd_scoremod(q, k, v, causal: bool, scale: float | None = None, softcap: float = 0.0, alibi_slopes=None,
+                      key_begin=None, key_end=None, kv_lens=None, out=None, lse=None, return_lse: bool = True,
+                      stream=None):
+    """Prefill with modified scores: softcap * tanh(scale q.k / softcap) - alibi_slopes[h] * |distance|
+    over the keys key_begin[b,i] <= j < key_end[b,i] (and kv_lens, causal).  q [B,Hq,Nq,d], k/v
+    [B,Hkv,Nkv,d] bf16; alibi_slopes [Hq] fp32; key_begin, key_end [B,Nq] int32; kv_lens [B] int32, all
+    optional CUDA tensors; softcap 0 is none.  Returns (o, lse)."""
+    device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d = _dense_inputs(q, k, v)
+    mod = _scoremod_inputs(device, B, Hq, Nq, alibi_slopes, key_begin, key_end, kv_lens)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_fwd_scoremod(q, k, v, causal, scale, softcap, alibi_slopes, key_begin, key_end, kv_lens, out,
+                                     lse, return_lse)
+    out, op = _output(out, "out", _t.bfloat16, (B, Hq, Nq, d), device)
+    lp = None
+    if lse is not None or return_lse:
+        lse, lp = _output(lse, "lse", _t.float32, (B, Hq, Nq), device)
+    st = load_library().attn_fwd_scoremod(qp, kp, vp, op, lp, B, Hq, Hkv, Nq, Nkv, d, int(bool(causal)),
+                                          d ** -0.5 if scale is None else scale, softcap, *mod,
+                                          _current_stream(device))
+    if st:
+        _check("attn_fwd_scoremod", st)
+    return out, lse
 
 
 def attn_selftest_bounded_wait(stream=None) -> None:

@@ -218,6 +218,34 @@ ATTN_API int attn_fwd(const void *q, const void *k, const void *v, void *o, floa
     return attn_fwd_kvlen(q, k, v, o, lse, B, H, Nq, Nkv, d, causal, scale, nullptr, stream);
 }
 
+namespace {
+// The score modification's arguments: softcap 0 (none) or finite and positive, 4-byte aligned arrays.
+int scoremod_checks(float softcap, const float *alibi_slopes, const int32_t *key_begin, const int32_t *key_end) {
+    if (!(softcap >= 0.f) || !(softcap < 3.0e38f)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned4(alibi_slopes) || !aligned4(key_begin) || !aligned4(key_end)) return ATTN_ERR_MISALIGNED;
+    return ATTN_OK;
+}
+}  // namespace
+
+ATTN_API int attn_fwd_scoremod(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
+                               int Hkv, int Nq, int Nkv, int d, int causal, float scale, float softcap,
+                               const float *alibi_slopes, const int32_t *key_begin, const int32_t *key_end,
+                               const int32_t *kv_lens, attn_stream_t stream) {
+    int st = prefill_checks(q, k, v, o, lse, B, Hq, Hkv, Nq, Nkv, d, causal, scale, kv_lens);
+    if (st == ATTN_OK) st = scoremod_checks(softcap, alibi_slopes, key_begin, key_end);
+    if (st != ATTN_OK) return st;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    attn::PrefillArgs a{q, k, v, o, lse, kv_lens, status, B, Hq, Nq, Nkv, d, causal, scale, Hkv};
+    a.softcap = softcap;
+    a.slopes = alibi_slopes;
+    a.key_begin = key_begin;
+    a.key_end = key_end;
+    cudaError_t e = attn::launch_prefill_scoremod(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 ATTN_API size_t attn_bwd_workspace_size(int B, int Hq, int Nq) { return attn::bwd_workspace_bytes(B, Hq, Nq); }
 
 ATTN_API int attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dout,

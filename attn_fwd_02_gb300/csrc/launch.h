@@ -26,6 +26,10 @@ struct PrefillArgs {
     // paged mode over an e4m3 cache: k, v hold codes; value = e4m3(code) * k_scale / v_scale
     int kv_fp8 = 0;
     float k_scale = 1.f, v_scale = 1.f;
+    // modified scores (launch_prefill_scoremod): cap (0: none), slopes [H] and intervals [B, Nq] (null: none)
+    float softcap = 0.f;
+    const float *slopes = nullptr;
+    const int32_t *key_begin = nullptr, *key_end = nullptr;
 };
 
 struct DecodeArgs {
@@ -69,6 +73,8 @@ bool encode_page_map_u8(CUtensorMap *m, const void *ptr, int rows, int page_rows
 
 // Encodes the TMA descriptors and launches the prefill kernel.
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
+// The same with modified scores and per-query key intervals (contiguous K/V only).
+cudaError_t launch_prefill_scoremod(const PrefillArgs &a, cudaStream_t stream);
 
 // Backward: the row term D, then the dK/dV kernel and the dQ kernel.
 cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t stream);

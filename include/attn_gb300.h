@@ -123,6 +123,26 @@ int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *ls
                  const int32_t *kv_lens, attn_stream_t stream);
 
 /*
+ * Prefill forward with modified scores and an interval of visible keys per query.  With p_i = i + Nkv -
+ * Nq the position of query i among the keys (bottom-right alignment, as the causal mask's):
+ *     s_ij = cap tanh(scale <q_i, k_j> / cap) - slope[h] |p_i - j|       (softcap cap > 0)
+ *     s_ij = scale <q_i, k_j> - slope[h] |p_i - j|                       (softcap 0: no cap)
+ *     J    = { j : key_begin[b, i] <= j < key_end[b, i], 0 <= j < kv_lens[b], j <= p_i if causal }
+ * and O, LSE as in attn_fwd_gqa over these scores and keys (no visible key: O = 0, LSE = -inf).
+ *   softcap       0, or finite and positive
+ *   alibi_slopes  [Hq] fp32 (device), finite; NULL: no distance bias
+ *   key_begin, key_end [B, Nq] int32 (device): any values, clamped; NULL: 0 and Nkv
+ * The intervals say documents packed into a row (begin and end of the query's document), a prefix that
+ * every query sees (key_end = max(p_i + 1, prefix), causal 0), a window (key_begin = p_i - window + 1)
+ * and their combinations; key tiles that no row of a query tile sees are not visited.  Rows of k and v
+ * past kv_lens[b] may hold anything; those below it must be finite.  Other arguments as attn_fwd_gqa.
+ */
+int attn_fwd_scoremod(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq, int Hkv,
+                      int Nq, int Nkv, int d, int causal, float scale, float softcap, const float *alibi_slopes,
+                      const int32_t *key_begin, const int32_t *key_end, const int32_t *kv_lens,
+                      attn_stream_t stream);
+
+/*
  * Bytes of device workspace paged_attn_decode needs for these sizes (0 on
  * invalid sizes).  The caller allocates it (16-byte aligned) and may reuse it
  * across calls on the same stream; calls that overlap on the GPU need
