@@ -7,6 +7,8 @@ fallback: if the library is missing, every call raises.
 from .binding import (  # noqa: F401
     AttnError,
     attn_bwd,
+    attn_bwd_scoremod,
+    attn_bwd_scoremod_workspace_size,
     attn_bwd_workspace_size,
     attn_check_device_status,
     attn_last_device_status,

@@ -47,6 +47,8 @@ SIGNATURES = {
     "paged_kv_append_rope": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
     "paged_kv_append_rope_fp8": (I, [P, P, P, P, P, P, P, P, P, F, F, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
     "attn_fwd_scoremod": (I, [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P]),
+    "attn_bwd_scoremod_workspace_size": (Z, [I, I, I]),
+    "attn_bwd_scoremod": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P, Z, P]),
     "attn_check_device_status": (I, [P]),
     "attn_last_device_status": (I, []),
     "attn_selftest_bounded_wait": (I, [P]),
@@ -719,6 +721,48 @@ def attn_fwd_scoremod(q, k, v, causal: bool, scale: float | None = None, softcap
     if st:
         _check("attn_fwd_scoremod", st)
     return out, lse
+
+
+def attn_bwd_scoremod_workspace_size(B: int, Hq: int, Nq: int) -> int:
+    return int(load_library().attn_bwd_scoremod_workspace_size(B, Hq, Nq))
+
+
+def _workspace(t, need, device):
+    """The caller's uint8 workspace (its size is checked by the library) or a new one: tensor, address, bytes."""
+    if t is None:
+        t = _t.empty(need if need > 16 else 16, dtype=_t.uint8, device=device)
+        return t, t.data_ptr(), t.numel()
+    return t, _in(t, "workspace", _t.uint8, 1, device), t.numel()
+
+
+def attn_bwd_scoremod(q, k, v, o, lse, dout, causal: bool, scale: float | None = None, softcap: float = 0.0,
+                      alibi_slopes=None, key_begin=None, key_end=None, kv_lens=None, dq=None, dk=None, dv=None,
+                      workspace=None, stream=None):
+    """Backward of attn_fwd_scoremod: q, o, dout [B,Hq,Nq,d] and k, v [B,Hkv,Nkv,d] bf16, lse [B,Hq,Nq]
+    fp32 from the forward, the modification as in the forward call.  Returns (dq, dk, dv) bf16.
+    workspace: optional uint8 tensor of attn_bwd_scoremod_workspace_size(B, Hq, Nq) bytes."""
+    device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d = _dense_inputs(q, k, v)
+    bf = _t.bfloat16
+    op, lp = _in(o, "o", bf, 4, device), _in(lse, "lse", _t.float32, 3, device)
+    gp = _in(dout, "dout", bf, 4, device)
+    if o.shape != q.shape or dout.shape != q.shape or lse.shape != q.shape[:3]:
+        raise ValueError("o and dout must match q, lse must be [B, Hq, Nq]")
+    mod = _scoremod_inputs(device, B, Hq, Nq, alibi_slopes, key_begin, key_end, kv_lens)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attn_bwd_scoremod(q, k, v, o, lse, dout, causal, scale, softcap, alibi_slopes, key_begin, key_end,
+                                     kv_lens, dq, dk, dv, workspace)
+    dq, dqp = _output(dq, "dq", bf, q.shape, device)
+    dk, dkp = _output(dk, "dk", bf, k.shape, device)
+    dv, dvp = _output(dv, "dv", bf, k.shape, device)
+    lib = load_library()
+    workspace, wp, wn = _workspace(workspace, lib.attn_bwd_scoremod_workspace_size(B, Hq, Nq), device)
+    st = lib.attn_bwd_scoremod(qp, kp, vp, op, lp, gp, dqp, dkp, dvp, B, Hq, Hkv, Nq, Nkv, d, int(bool(causal)),
+                               d ** -0.5 if scale is None else scale, softcap, *mod, wp, wn, _current_stream(device))
+    if st:
+        _check("attn_bwd_scoremod", st)
+    return dq, dk, dv
 
 
 def attn_selftest_bounded_wait(stream=None) -> None:

@@ -454,6 +454,39 @@ ATTN_API int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_p
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+ATTN_API size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Nq) {
+    return attn::bwd_scoremod_workspace_bytes(B, Hq, Nq);
+}
+
+ATTN_API int attn_bwd_scoremod(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                               const void *dout, void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Nq, int Nkv,
+                               int d, int causal, float scale, float softcap, const float *alibi_slopes,
+                               const int32_t *key_begin, const int32_t *key_end, const int32_t *kv_lens,
+                               void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+    if (!o || !lse || !dout || !dk || !dv) return ATTN_ERR_INVALID_ARG;
+    int st = prefill_checks(q, k, v, dq, nullptr, B, Hq, Hkv, Nq, Nkv, d, causal, scale, kv_lens);
+    if (st == ATTN_OK) st = scoremod_checks(softcap, alibi_slopes, key_begin, key_end);
+    if (st != ATTN_OK) return st;
+    const uint64_t kv_ctas = ((uint64_t)Nkv + 127) / 128 * (uint64_t)B * (uint64_t)Hkv;
+    if (kv_ctas > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(o) || !aligned16(dout) || !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
+        return ATTN_ERR_MISALIGNED;
+    const size_t need = attn::bwd_scoremod_workspace_bytes(B, Hq, Nq);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    attn::BwdArgs a{q,  k,  v,      o, dout, lse, dq, dk, dv, static_cast<float *>(workspace), kv_lens, status,
+                    B,  Hq, Hkv, Nq, Nkv, d, causal, scale};
+    a.softcap = softcap;
+    a.slopes = alibi_slopes;
+    a.key_begin = key_begin;
+    a.key_end = key_end;
+    a.spans = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + attn::bwd_workspace_bytes(B, Hq, Nq));
+    cudaError_t e = attn::launch_bwd_scoremod(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 namespace {
 // Strides {batch, head, token} of a [B, H, N, d] input, in elements: the caller's (dims of size one
 // count as 0), or those of a contiguous tensor.  Rows are read as 16-byte vectors.

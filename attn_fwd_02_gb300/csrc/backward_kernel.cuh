@@ -1,0 +1,1073 @@
+// backward_kernel.cuh -- attention backward on the sm_103a tensor cores; instantiated by backward.cu and,
+// for modified scores, by backward_scoremod.cu.
+//
+// The method (gpu-inference blog, section 02 "FlashAttention-2 in Triton"): the backward keeps
+// no probability matrix; it recomputes the probabilities tile by tile from the log-sum-exp the
+// forward saved, and it is split into three kernels: a pass that computes the row term
+// D_i = dO_i . O_i, a dK/dV kernel and a dQ kernel.  With P = exp(s - LSE) on the valid keys
+// (s = scale q.k), dP = dO V^T and dS = P * (dP - D):
+//     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K.
+//
+// GB300 mapping of the two tile kernels (d in {32, 64, 80, 96, 128}):
+//   * One CTA owns a 128-row tile of what it accumulates (dK and dV of 128 keys, or dQ of 128
+//     queries) in TMEM, and streams the other side's 128-row tiles through a 2-slot TMA ring
+//     (128-byte swizzled boxes of 128 rows x 64 columns).
+//   * 10 warps.  Warps 0-7 are two compute warpgroups: thread r of warpgroup w owns TMEM lane r
+//     (row r of the CTA's own tile) and columns 64w .. 64w+63 of each 128 x 128 score tile.
+//     Warp 8 loads; warp 9 owns the TMEM and one of its threads issues every MMA.
+//   * dK/dV: S^T = K Q^T and dP^T = V dO^T land in TMEM with lane = key.  The warpgroups write
+//     P^T and dS^T (bf16 pairs) back over the columns they read, where dV += P^T dO and
+//     dK += dS^T Q take them as the A operand straight from TMEM.  Each Q or dO tile is the
+//     K-major B operand of a score product and the MN-major B operand of an accumulation.
+//     TMEM: S^T 128 | dP^T 128 | dV d | dK d columns.
+//   * dQ: S = Q K^T and dP = dO V^T with lane = query; dS (bf16) over dP feeds dQ += dS K.
+//     TMEM: S 128 | dP 128 | dQ d columns.
+//   * Modified scores (MOD: s = cap tanh(scale q.k / cap) - slope |distance| on an interval of keys per
+//     query): P = exp(s - LSE) as before, and dS, the gradient of the modified score, times 1 - tanh^2
+//     is that of scale q.k.  P times that factor takes the place of P in registers once P itself is
+//     packed, so the cap holds no further registers.  Key tiles visit the query tiles from the first to
+//     the last whose intervals meet them (the row-term kernel also writes each query tile's interval).
+//   * Issue order per step j.  dK/dV: dV(j), S^T(j+1), then dK(j), dP^T(j+1).  dQ: S(j+1),
+//     then dQ(j), dP(j+1).  The tensor core computes the next scores while the warpgroups turn
+//     dP(j) into dS(j), and the next dP while they turn S(j+1) into P(j+1).  The MMAs of one
+//     thread run in issue order, so a product that overwrites a TMEM buffer never overtakes the
+//     earlier product that reads the same columns as its operand.
+#pragma once
+
+#include <cmath>
+
+#include "launch.h"
+#include "scoremod.cuh"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kT = 128;  // rows of every tile (queries or keys)
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kStages = 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBoxBytes = 128 * 64 * 2;  // one 128-row x 64-column bf16 box
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kFull = 0xffffffffu;
+// Tiles are padded to 64 (d <= 64) or 128 columns of 64-column TMA boxes, which read zeros past d:
+// the score products run over d/16 k-steps and the accumulations over N = d columns, so the padding
+// costs shared memory only.  Accumulators in TMEM sit at padded column offsets.
+template <int D> constexpr int kBPad = D <= 64 ? 64 : 128;
+template <int D> constexpr int kBBoxes = kBPad<D> / 64;
+// dQ columns of the first warpgroup (the second takes the rest): halves in multiples of 16
+template <int D> constexpr int kDqSplit = ((D / 16 + 1) / 2) * 16;
+
+struct BwdParams {
+    const float *lse, *dterm;
+    __nv_bfloat16 *dq, *dk, *dv;
+    const int32_t *kv_lens;
+    int *status;
+    int B, Hq, Hkv, group, Nq, Nkv, causal;
+    int units_per_head;   // query tiles (dQ kernel) or key tiles (dK/dV kernel) of one head
+    int heads_per_chunk;  // heads whose streamed operands share L2 at a time
+    float scale, scale_log2;
+    // modified scores (MOD): see the forward; spans [B, query tiles] holds the union {lo, hi} of the
+    // intervals of a query tile's rows
+    const int32_t *key_begin, *key_end;
+    const float *slopes;
+    float cap_in, cap_out;
+    int2 *spans;
+};
+
+// Keys lo <= j < hi that query `row` of sequence b sees (none past the last query).
+__device__ __forceinline__ int2 bwd_row_span(const BwdParams &p, int b, int row, int kv_end) {
+    if (row >= p.Nq) return make_int2(0, 0);
+    const size_t at = (size_t)b * p.Nq + row;
+    int2 s;
+    s.x = p.key_begin ? max(p.key_begin[at], 0) : 0;
+    s.y = p.key_end ? min(p.key_end[at], kv_end) : kv_end;
+    if (p.causal) s.y = min(s.y, row + p.Nkv - p.Nq + 1);
+    return s;
+}
+
+// CTA order (as in the forward): heads in chunks small enough that the chunk's streamed tiles
+// stay in L2; inside a chunk, unit levels in order (level 0 = the heaviest unit of a head
+// under the causal mask) across the chunk's heads.
+__device__ __forceinline__ void unit_of(const BwdParams &p, int n_heads, int &head, int &level) {
+    const int per_chunk = p.heads_per_chunk * p.units_per_head;
+    const int chunk = (int)(blockIdx.x / per_chunk);
+    const int h0 = chunk * p.heads_per_chunk;
+    const int heads = min(p.heads_per_chunk, n_heads - h0);
+    const int in_chunk = (int)(blockIdx.x % per_chunk);
+    level = in_chunk / heads;
+    head = h0 + in_chunk % heads;
+}
+
+__device__ __forceinline__ int kv_end_for(const BwdParams &p, int b) {
+    return p.kv_lens ? min(max(p.kv_lens[b], 0), p.Nkv) : p.Nkv;
+}
+
+// 128 x 128 score tile: D[tmem] = A B^T over the head dimension (both operands K-major tiles).
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, const __nv_bfloat16 *a, const __nv_bfloat16 *b) {
+    constexpr uint32_t id = idesc_bf16_f32(kT, kT, false, false);
+    const uint64_t da = sdesc_sw128(smem_u32(a), 16, 1024), db = sdesc_sw128(smem_u32(b), 16, 1024);
+    static_assert(kBoxBytes == 16384, "k-step layout of the grouped issue");
+    tc_mma_ss_ksteps<D / 16>(d_tmem, da, db, id, 0u);
+}
+
+// 128 x d accumulation: D[tmem] (+)= A[tmem] B, A = 128 x 128 bf16 written by the two warpgroups
+// (columns 0-31 and 64-95 of a_tmem hold the bf16 pairs of k-indices 0-63 and 64-127), B = a
+// 128-row tile read MN-major (k-index = tile row).
+template <int D>
+__device__ __forceinline__ void mma_accum(uint32_t d_tmem, uint32_t a_tmem, const __nv_bfloat16 *b, bool first) {
+    constexpr uint32_t id = idesc_bf16_f32(kT, D, false, true);
+    const uint64_t db = sdesc_sw128(smem_u32(b), kBoxBytes, 1024);
+    static_assert(kT / 16 == 8, "one group of eight k-steps");
+    tc_mma_ts_k8_halves(d_tmem, a_tmem, db, id, first ? 0u : 1u);
+}
+
+// The bias -slope |d| (log2 domain) over a row of 64 columns at distances d = d0 + Step c (Step 1:
+// columns are queries, -1: columns are keys); nonneg, nonpos: d has one sign over the whole tile, and the
+// bias is linear in the column.
+template <int Step>
+struct Distance {
+    float sl, base, d0;
+    bool linear;
+    __device__ __forceinline__ Distance(float slope, int d, bool nonneg, bool nonpos) {
+        const float sign = nonneg ? -slope : slope;
+        linear = nonneg || nonpos;
+        d0 = (float)d;
+        base = linear ? sign * d0 : -slope;
+        sl = sign * (float)Step;
+    }
+    __device__ __forceinline__ float add(int c, float e) const {
+        return linear ? fmaf(sl, (float)c, e + base) : fmaf(base, fabsf(d0 + (float)(Step * c)), e);
+    }
+};
+
+// 64 TMEM columns of this thread's lane -> registers.
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&x)[2][32]) {
+    tmem_ld32(taddr, x[0]);
+    tmem_ld32(taddr + 32, x[1]);
+    tmem_wait_ld(x[0]);
+    tmem_wait_ld(x[1]);
+}
+
+// Writes NCOLS (a multiple of 16) columns of this thread's row of an fp32 TMEM accumulator,
+// times `mul`, as bf16 to dst (`store` false skips the write).  Zeros if !have.
+template <int NCOLS>
+__device__ __forceinline__ void store_rows(uint32_t tacc, bool have, bool store, float mul, __nv_bfloat16 *dst) {
+    static_assert(NCOLS % 16 == 0, "16-column steps");
+#pragma unroll
+    for (int cc = 0; cc < NCOLS / 32; ++cc) {
+        uint32_t v[32];
+        if (have) {
+            tmem_ld32(tacc + cc * 32, v);
+            tmem_wait_ld(v);
+        }
+        if (store) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = have ? pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul) : 0u;
+            uint4 *o = reinterpret_cast<uint4 *>(dst + cc * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+    }
+    if constexpr (NCOLS % 32 != 0) {  // the last 16 columns
+        constexpr int c0 = NCOLS / 32 * 32;
+        uint32_t v[16];
+        if (have) {
+            tmem_ld16(tacc + c0, v);
+            tmem_wait_ld16(v);
+        }
+        if (store) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                pk[i] = have ? pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul) : 0u;
+            uint4 *o = reinterpret_cast<uint4 *>(dst + c0);
+            o[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            o[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+    }
+}
+
+// ================================================================== row term D = rowsum(dO * O)
+// kTpr threads per row (d / 8 rounded up to a power of two), one 16-byte load of O and of dO each
+// for the threads whose 8 columns lie inside d, then a shuffle reduction.
+template <int D> constexpr int kRowThreads = D / 8 <= 4 ? 4 : (D / 8 <= 8 ? 8 : 16);
+template <int D>
+__device__ __forceinline__ void rowdot(const __nv_bfloat16 *o, const __nv_bfloat16 *dout, float *dterm,
+                                       long long rows) {
+    constexpr int kTpr = kRowThreads<D>;
+    const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long row = gid / kTpr;
+    const int part = (int)(gid % kTpr);
+    float acc = 0.f;
+    if (row < rows && part * 8 < D) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(o + row * D + part * 8);
+        const uint4 b = *reinterpret_cast<const uint4 *>(dout + row * D + part * 8);
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 fa = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&av[i]));
+            const float2 fb = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&bv[i]));
+            acc = fmaf(fa.x, fb.x, acc);
+            acc = fmaf(fa.y, fb.y, acc);
+        }
+    }
+#pragma unroll
+    for (int off = kTpr / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(kFull, acc, off);
+    if (row < rows && part == 0) dterm[row] = acc;
+}
+template <int D>
+__global__ void __launch_bounds__(256) bwd_rowdot_kernel(const __nv_bfloat16 *o, const __nv_bfloat16 *dout,
+                                                         float *dterm, long long rows) {
+    rowdot<D>(o, dout, dterm, rows);
+}
+
+// The row term and, in the blocks after the first row_blocks, the intervals of two query tiles each.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_rowdot_spans_kernel(const __nv_bfloat16 *o, const __nv_bfloat16 *dout,
+                                                               float *dterm, long long rows, int row_blocks,
+                                                               const BwdParams p, int n_qt) {
+    if ((int)blockIdx.x < row_blocks) {
+        rowdot<D>(o, dout, dterm, rows);
+        return;
+    }
+    __shared__ int2 part[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long tile = ((long long)blockIdx.x - row_blocks) * 2 + warp / 4;
+    int2 s = make_int2(0, 0);
+    if (tile < (long long)p.B * n_qt) {
+        const int b = (int)(tile / n_qt), qt = (int)(tile % n_qt);
+        s = bwd_row_span(p, b, qt * kT + ((int)threadIdx.x & 127), kv_end_for(p, b));
+    }
+    const bool some = s.x < s.y;
+    const int lo = __reduce_min_sync(kFull, some ? s.x : 0x7fffffff), hi = __reduce_max_sync(kFull, some ? s.y : 0);
+    if (lane == 0) part[warp] = make_int2(lo, hi);
+    __syncthreads();
+    if ((threadIdx.x & 127) == 0 && tile < (long long)p.B * n_qt) {
+        int2 u = part[warp];
+        for (int w = 1; w < 4; ++w) u = make_int2(min(u.x, part[warp + w].x), max(u.y, part[warp + w].y));
+        p.spans[tile] = u;
+    }
+}
+
+// ================================================================== dK / dV
+// MOD: a streamed query tile's intervals, slope and whether every row sees all the CTA's keys
+template <bool MOD> struct QuerySpans {};
+template <> struct QuerySpans<true> {
+    int4 lo[kStages][kT / 4], hi[kStages][kT / 4];
+    float slope2[kStages];
+    int inside[kStages];
+    int first, last;  // query tiles that see one of the CTA's keys
+};
+
+template <int D>
+struct alignas(1024) DkvTiles {
+    __nv_bfloat16 k[kT * kBPad<D>];              // the CTA's 128 keys (kBBoxes boxes)
+    __nv_bfloat16 v[kT * kBPad<D>];
+    __nv_bfloat16 q[kStages][kT * kBPad<D>];     // streamed query tiles
+    __nv_bfloat16 dout[kStages][kT * kBPad<D>];  // and their upstream gradients
+    float nlse2[kStages][kT];             // minus the log2-domain LSE of each streamed query (0 past Nq)
+    float dterm[kStages][kT];             // row term D of each streamed query (0 past Nq)
+    uint64_t kv_full;
+    uint64_t u_full[kStages], u_empty[kStages];
+    uint64_t s_full, p_full, dp_full, ds_full, acc_done, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int D, bool MOD> struct DkvSmem : DkvTiles<D>, QuerySpans<MOD> {};
+__device__ __forceinline__ float sm_slope(const QuerySpans<false> &, int) { return 0.f; }
+__device__ __forceinline__ float sm_slope(const QuerySpans<true> &s, int slot) { return s.slope2[slot]; }
+
+// Query tiles a key tile [k0, k0+128) must visit: queries i >= k0 - delta can see its keys
+// under the causal mask (query i sees key j iff j <= i + delta).
+__device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_end, int delta, int &qi_start,
+                                           int &nqt) {
+    const int n_qt = (p.Nq + kT - 1) / kT;
+    qi_start = 0;
+    nqt = 0;
+    if (k0 >= kv_end) return;
+    if (p.causal) {
+        const int first = k0 - delta;
+        if (first >= p.Nq) return;
+        qi_start = first > 0 ? first / kT : 0;
+    }
+    nqt = n_qt - qi_start;
+}
+
+template <int D, bool MOD>
+__device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const BwdParams &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
+                              const CUtensorMap *tmK, const CUtensorMap *tmV, int b, int hkv, int bh_kv, int k0,
+                              int qi_start, int nqt, int n, WaitCtx wc) {
+    constexpr int kBoxes = kBBoxes<D>;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        prefetch_tensormap(tmQ);
+        prefetch_tensormap(tmdO);
+        mbar_arrive_expect_tx(&sm.kv_full, 2 * kBoxes * kBoxBytes);
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) {
+            tma_load_3d(sm.k + i * (kT * 64), tmK, &sm.kv_full, i * 64, k0, bh_kv);
+            tma_load_3d(sm.v + i * (kT * 64), tmV, &sm.kv_full, i * 64, k0, bh_kv);
+        }
+    }
+    // the row statistics of unit u's 128 queries, four per lane (plain loads, zeros past Nq); they
+    // are loaded one unit ahead so their latency hides behind the ring wait
+    auto load_stats = [&](int u, float (&l4)[4], float (&d4)[4]) {
+        const int bh_q = b * p.Hq + hkv * p.group + u / nqt;
+        const int q0 = (qi_start + u % nqt) * kT;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int row = q0 + lane * 4 + t;
+            l4[t] = 0.f;
+            d4[t] = 0.f;
+            if (row < p.Nq) {
+                l4[t] = p.lse[(size_t)bh_q * p.Nq + row];
+                d4[t] = p.dterm[(size_t)bh_q * p.Nq + row];
+            }
+        }
+    };
+    float l4n[4], d4n[4];
+    load_stats(0, l4n, d4n);
+    int2 s4n[4] = {};
+    float slope_n = 0.f;
+    const int kv_end = kv_end_for(p, b);
+    auto load_spans = [&](int u) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + u % nqt) * kT + lane * 4 + t, kv_end);
+        slope_n = p.slopes ? p.slopes[hkv * p.group + u / nqt] * kLog2e : 0.f;
+    };
+    if constexpr (MOD) load_spans(0);
+    int fills = 0;
+    for (int u = 0; u < n; ++u) {
+        const int slot = u % kStages, use = u / kStages;
+        if (use > 0 && !__all_sync(kFull, mbar_wait(&sm.u_empty[slot], (uint32_t)((use - 1) & 1), wc, 60))) break;
+        const int g = u / nqt, qi = qi_start + u % nqt;
+        const int bh_q = b * p.Hq + hkv * p.group + g;
+        const int q0 = qi * kT;
+        *reinterpret_cast<float4 *>(&sm.nlse2[slot][lane * 4]) =
+            make_float4(l4n[0] * -kLog2e, l4n[1] * -kLog2e, l4n[2] * -kLog2e, l4n[3] * -kLog2e);
+        *reinterpret_cast<float4 *>(&sm.dterm[slot][lane * 4]) = make_float4(d4n[0], d4n[1], d4n[2], d4n[3]);
+        if (u + 1 < n) load_stats(u + 1, l4n, d4n);
+        if constexpr (MOD) {
+            sm.lo[slot][lane] = make_int4(s4n[0].x, s4n[1].x, s4n[2].x, s4n[3].x);
+            sm.hi[slot][lane] = make_int4(s4n[0].y, s4n[1].y, s4n[2].y, s4n[3].y);
+            bool all = true;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) all = all && s4n[t].x <= k0 && s4n[t].y >= k0 + kT;
+            all = __all_sync(kFull, all);
+            if (lane == 0) {
+                sm.inside[slot] = all ? 1 : 0;
+                sm.slope2[slot] = slope_n;
+            }
+            if (u + 1 < n) load_spans(u + 1);
+        }
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.u_full[slot], 2 * kBoxes * kBoxBytes);
+#pragma unroll
+            for (int i = 0; i < kBoxes; ++i) {
+                tma_load_3d(sm.q[slot] + i * (kT * 64), tmQ, &sm.u_full[slot], i * 64, q0, bh_q);
+                tma_load_3d(sm.dout[slot] + i * (kT * 64), tmdO, &sm.u_full[slot], i * 64, q0, bh_q);
+            }
+        } else {
+            mbar_arrive(&sm.u_full[slot]);
+        }
+        ++fills;
+    }
+    if (lane == 0 && *wc.abort_flag) {
+        // unwinding: let every copy still in flight land before the CTA exits
+        WaitCtx drain{nullptr, wc.status};
+        (void)mbar_wait(&sm.kv_full, 0, drain, 61);
+        for (int f = (fills > kStages ? fills - kStages : 0); f < fills; ++f)
+            (void)mbar_wait(&sm.u_full[f % kStages], (uint32_t)((f / kStages) & 1), drain, 62);
+    }
+}
+
+template <int D, bool MOD>
+__device__ void dkdv_mma(DkvSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
+    const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + kBPad<D>;
+    bool ok = mbar_wait(&sm.kv_full, 0, wc, 63) && mbar_wait(&sm.u_full[0], 0, wc, 64);
+    if (ok) {
+        tc_fence_after_sync();
+        mma_scores<D>(tS, sm.k, sm.q[0]);
+        tc_commit(&sm.s_full);
+        mma_scores<D>(tdP, sm.v, sm.dout[0]);
+        tc_commit(&sm.dp_full);
+        for (int j = 0; j < n; ++j) {
+            const int slot = j % kStages;
+            if (!(ok = mbar_wait(&sm.p_full, (uint32_t)(j & 1), wc, 65))) break;
+            tc_fence_after_sync();
+            mma_accum<D>(tdV, tS, sm.dout[slot], j == 0);  // dV += P^T dO
+            if (j + 1 < n) {
+                const int u = j + 1;
+                if (!(ok = mbar_wait(&sm.u_full[u % kStages], (uint32_t)((u / kStages) & 1), wc, 66))) break;
+                mma_scores<D>(tS, sm.k, sm.q[u % kStages]);  // S^T(j+1), after dV(j) read P^T(j)
+                tc_commit(&sm.s_full);
+            }
+            if (!(ok = mbar_wait(&sm.ds_full, (uint32_t)(j & 1), wc, 67))) break;
+            tc_fence_after_sync();
+            mma_accum<D>(tdK, tdP, sm.q[slot], j == 0);  // dK += dS^T Q
+            tc_commit(&sm.u_empty[slot]);
+            if (j == n - 1) tc_commit(&sm.acc_done);
+            if (j + 1 < n) {
+                mma_scores<D>(tdP, sm.v, sm.dout[(j + 1) % kStages]);  // dP^T(j+1), after dK(j) read dS^T(j)
+                tc_commit(&sm.dp_full);
+            }
+        }
+    }
+    tc_commit(&sm.drain);
+    WaitCtx drain{nullptr, wc.status};
+    (void)mbar_wait(&sm.drain, 0, drain, 68);
+}
+
+template <int D, bool MOD>
+__device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem, int w, int bh_kv, int k0,
+                             int kv_end, int delta, int qi_start, int nqt, int n, WaitCtx wc) {
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
+    const uint32_t tS = lane_base + (uint32_t)(w * 64);
+    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * 64);
+    const int key = k0 + r;
+    const bool key_ok = key < kv_end;
+    // with the cap, x becomes tanh and c2 its factor cap * log2(e)
+    const float cmul = (MOD && p.cap_in > 0.f) ? p.cap_out : p.scale_log2;
+    const uint64_t c2 = f32x2_pack(cmul, cmul);
+    [[maybe_unused]] const TanhPoly capped(1.f);
+    [[maybe_unused]] const uint64_t in2 = f32x2_pack(p.cap_in, p.cap_in);
+    [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+        const int slot = j % kStages;
+        const int col0 = (qi_start + j % nqt) * kT + w * 64;  // query of this half's column 0
+        // valid columns lo <= c < hi: query < Nq, key < kv_end, and key <= query + delta if causal
+        int lo = 0, hi = min(64, p.Nq - col0);
+        if (p.causal) lo = max(0, key - delta - col0);
+        if (!key_ok) hi = 0;
+        bool need_mask = lo > 0 || hi < 64;
+
+        // The columns' statistics are read before the score waits so that their latency hides
+        // behind them.  The producer wrote them before arriving on the unit's full barrier; waiting
+        // on that barrier (without arriving) orders these reads after its writes.  The slot cannot
+        // be refilled before this step ends (the refill waits for dK(j), which needs this step's dS).
+        if (!__all_sync(kFull, mbar_wait(&sm.u_full[slot], (uint32_t)((j / kStages) & 1), wc, 73))) {
+            ok = false;
+            break;
+        }
+        if constexpr (MOD) need_mask = sm.inside[slot] == 0;
+        float4 L4[16];
+        const float4 *l2 = reinterpret_cast<const float4 *>(sm.nlse2[slot] + w * 64);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) L4[i] = l2[i];
+        if (!__all_sync(kFull, mbar_wait(&sm.s_full, (uint32_t)(j & 1), wc, 70))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        uint32_t x[2][32];
+        load64(tS, x);
+        [[maybe_unused]] bool far = false;
+        if constexpr (MOD)
+            if (p.cap_in > 0.f) far = __any_sync(kFull, abs_max(x) * p.cap_in > 1.f);
+        // column c is the query at position col0 + c + delta; under the causal mask the keys after it are
+        // masked, so the linear form serves there too
+        const int first = col0 + delta;
+        [[maybe_unused]] const Distance<1> dist(MOD ? sm_slope(sm, slot) : 0.f, first - key,
+                                                p.causal || first >= k0 + kT - 1, first + 63 <= k0);
+        // P^T = 2^(s * scale * log2e - lse2): bf16 pairs over the scores, fp32 kept in x
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 L = L4[(h * 32 + i) / 4];
+                uint64_t x01 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+                uint64_t x23 = f32x2_pack(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
+                [[maybe_unused]] float g[4];  // 1 - tanh^2
+                if constexpr (MOD) {
+                    if (p.cap_in > 0.f) {
+                        x01 = capped(f32x2_mul(x01, in2), far);
+                        x23 = capped(f32x2_mul(x23, in2), far);
+                        f32x2_unpack(f32x2_fma(f32x2_mul(x01, minus1), x01, one), g[0], g[1]);
+                        f32x2_unpack(f32x2_fma(f32x2_mul(x23, minus1), x23, one), g[2], g[3]);
+                    }
+                }
+                const uint64_t e01 = f32x2_fma(x01, c2, f32x2_pack(L.x, L.y));
+                const uint64_t e23 = f32x2_fma(x23, c2, f32x2_pack(L.z, L.w));
+                float e[4];
+                f32x2_unpack(e01, e[0], e[1]);
+                f32x2_unpack(e23, e[2], e[3]);
+                if constexpr (MOD) {
+                    if (p.slopes)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) e[t] = dist.add(h * 32 + i + t, e[t]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float pv = ex2_approx(e[t]);
+                    if constexpr (!MOD) {
+                        if (need_mask) {
+                            const int c = h * 32 + i + t;
+                            pv = (c >= lo && c < hi) ? pv : 0.f;
+                        }
+                    }
+                    x[h][i + t] = __float_as_uint(pv);
+                }
+                if constexpr (MOD) {
+                    if (need_mask) {  // the columns' intervals, four queries at a time
+                        const int4 a = sm.lo[slot][w * 16 + (h * 32 + i) / 4], z = sm.hi[slot][w * 16 + (h * 32 + i) / 4];
+                        const int al[4] = {a.x, a.y, a.z, a.w}, zl[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (key < al[t] || key >= zl[t]) x[h][i + t] = 0u;
+                    }
+                }
+                pk[i / 2] = pack_bf16x2(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+                pk[i / 2 + 1] = pack_bf16x2(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
+                if constexpr (MOD) {
+                    if (p.cap_in > 0.f)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)  // a masked weight stays 0
+                            if (!need_mask || x[h][i + t] != 0u)
+                                x[h][i + t] = __float_as_uint(__uint_as_float(x[h][i + t]) * g[t]);
+                }
+            }
+            tmem_st16(tS + (uint32_t)(h * 16), pk);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sm.p_full);
+
+        float4 D4[16];
+        const float4 *dd = reinterpret_cast<const float4 *>(sm.dterm[slot] + w * 64);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) D4[i] = dd[i];
+        if (!__all_sync(kFull, mbar_wait(&sm.dp_full, (uint32_t)(j & 1), wc, 71))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        uint32_t y[2][32];
+        load64(tdP, y);
+        // dS^T = P^T * (dP^T - D): bf16 pairs over dP^T
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 Dv = D4[(h * 32 + i) / 4];
+                float s0 = __uint_as_float(x[h][i]) * (__uint_as_float(y[h][i]) - Dv.x);
+                float s1 = __uint_as_float(x[h][i + 1]) * (__uint_as_float(y[h][i + 1]) - Dv.y);
+                float s2 = __uint_as_float(x[h][i + 2]) * (__uint_as_float(y[h][i + 2]) - Dv.z);
+                float s3 = __uint_as_float(x[h][i + 3]) * (__uint_as_float(y[h][i + 3]) - Dv.w);
+                if constexpr (MOD) {
+                    if (need_mask) {  // dP of a masked key may be anything
+                        s0 = x[h][i] ? s0 : 0.f;
+                        s1 = x[h][i + 1] ? s1 : 0.f;
+                        s2 = x[h][i + 2] ? s2 : 0.f;
+                        s3 = x[h][i + 3] ? s3 : 0.f;
+                    }
+                }
+                pk[i / 2] = pack_bf16x2(s0, s1);
+                pk[i / 2 + 1] = pack_bf16x2(s2, s3);
+            }
+            tmem_st16(tdP + (uint32_t)(h * 16), pk);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sm.ds_full);
+    }
+
+    if (ok && n > 0) {
+        if (!__all_sync(kFull, mbar_wait(&sm.acc_done, 0, wc, 72))) ok = false;
+        else tc_fence_after_sync();
+    }
+    if (!ok) return;
+    // warpgroup 0 writes dV, warpgroup 1 writes dK (times scale); rows past Nkv are not stored
+    const bool store = key < p.Nkv;
+    __nv_bfloat16 *dst = (w == 0 ? p.dv : p.dk) + ((size_t)bh_kv * p.Nkv + (store ? key : 0)) * D;
+    store_rows<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, w == 0 ? 1.f : p.scale, dst);
+}
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    DkvSmem<D, MOD> &sm =
+        *reinterpret_cast<DkvSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    int bh_kv, level;
+    unit_of(p, p.B * p.Hkv, bh_kv, level);
+    const int b = bh_kv / p.Hkv, hkv = bh_kv % p.Hkv;
+    const int k0 = level * kT;  // level 0 = key tile 0, seen by the most queries when causal
+    const int kv_end = kv_end_for(p, b);
+    const int delta = p.Nkv - p.Nq;
+    int qi_start = 0, nqt = 0;
+    if constexpr (MOD) {
+        if (threadIdx.x == 0) {
+            sm.first = 0x7fffffff;
+            sm.last = -1;
+        }
+        __syncthreads();
+        const int n_qt = (p.Nq + kT - 1) / kT;
+        int first = 0x7fffffff, last = -1;
+        for (int qi = threadIdx.x; qi < n_qt; qi += kThreads) {
+            const int2 s = p.spans[(size_t)b * n_qt + qi];
+            if (s.x < k0 + kT && s.y > k0) {
+                first = min(first, qi);
+                last = qi;
+            }
+        }
+        if (last >= 0) {
+            atomicMin(&sm.first, first);
+            atomicMax(&sm.last, last);
+        }
+    } else {
+        dkdv_range(p, k0, kv_end, delta, qi_start, nqt);
+    }
+
+    if (threadIdx.x == 0) {
+        mbar_init(&sm.kv_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.u_full[s], 32);
+            mbar_init(&sm.u_empty[s], 1);
+        }
+        mbar_init(&sm.s_full, 1);
+        mbar_init(&sm.p_full, 256);
+        mbar_init(&sm.dp_full, 1);
+        mbar_init(&sm.ds_full, 256);
+        mbar_init(&sm.acc_done, 1);
+        mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    WaitCtx wc{&sm.abort_flag, p.status};
+    if constexpr (MOD) {
+        if (sm.last >= 0) {
+            qi_start = sm.first;
+            nqt = sm.last - sm.first + 1;
+        }
+    }
+    const int n = nqt * p.group;  // steps: every query tile of every query head of the group
+
+    if (warp == kProducerWarp) {
+        if (n > 0) dkdv_producer<D, MOD>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, n, wc);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0 && n > 0) dkdv_mma<D, MOD>(sm, tmem, n, wc);
+    } else {
+        dkdv_compute<D, MOD>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, n, wc);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ================================================================== dQ
+template <bool MOD> struct KeySpan {};
+template <> struct KeySpan<true> {
+    int lo[4], hi[4];  // per warp of the first warpgroup: the union of its rows' intervals
+};
+template <int D>
+struct alignas(1024) DqTiles {
+    __nv_bfloat16 q[kT * kBPad<D>];  // the CTA's 128 queries
+    __nv_bfloat16 dout[kT * kBPad<D>];
+    __nv_bfloat16 k[kStages][kT * kBPad<D>];  // streamed key tiles
+    __nv_bfloat16 v[kStages][kT * kBPad<D>];
+    uint64_t qd_full;
+    uint64_t u_full[kStages], u_empty[kStages];
+    uint64_t s_full, s_free, dp_full, ds_full, acc_done, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int D, bool MOD> struct DqSmem : DqTiles<D>, KeySpan<MOD> {};
+
+template <int D, bool MOD>
+__device__ void dq_producer(DqSmem<D, MOD> &sm, const CUtensorMap *tmQ, const CUtensorMap *tmdO, const CUtensorMap *tmK,
+                            const CUtensorMap *tmV, int bh, int bh_kv, int q0, int n, int j0, WaitCtx wc) {
+    constexpr int kBoxes = kBBoxes<D>;
+    prefetch_tensormap(tmK);
+    prefetch_tensormap(tmV);
+    mbar_arrive_expect_tx(&sm.qd_full, 2 * kBoxes * kBoxBytes);
+#pragma unroll
+    for (int i = 0; i < kBoxes; ++i) {
+        tma_load_3d(sm.q + i * (kT * 64), tmQ, &sm.qd_full, i * 64, q0, bh);
+        tma_load_3d(sm.dout + i * (kT * 64), tmdO, &sm.qd_full, i * 64, q0, bh);
+    }
+    int fills = 0;
+    for (int u = 0; u < n; ++u) {
+        const int slot = u % kStages, use = u / kStages;
+        if (use > 0 && !mbar_wait(&sm.u_empty[slot], (uint32_t)((use - 1) & 1), wc, 80)) break;
+        mbar_arrive_expect_tx(&sm.u_full[slot], 2 * kBoxes * kBoxBytes);
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i) {
+            tma_load_3d(sm.k[slot] + i * (kT * 64), tmK, &sm.u_full[slot], i * 64, (j0 + u) * kT, bh_kv);
+            tma_load_3d(sm.v[slot] + i * (kT * 64), tmV, &sm.u_full[slot], i * 64, (j0 + u) * kT, bh_kv);
+        }
+        ++fills;
+    }
+    if (*wc.abort_flag) {
+        WaitCtx drain{nullptr, wc.status};
+        (void)mbar_wait(&sm.qd_full, 0, drain, 81);
+        for (int f = (fills > kStages ? fills - kStages : 0); f < fills; ++f)
+            (void)mbar_wait(&sm.u_full[f % kStages], (uint32_t)((f / kStages) & 1), drain, 82);
+    }
+}
+
+template <int D, bool MOD>
+__device__ void dq_mma(DqSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
+    const uint32_t tS = tmem, tdP = tmem + 128, tdQ = tmem + 256;
+    bool ok = mbar_wait(&sm.qd_full, 0, wc, 83) && mbar_wait(&sm.u_full[0], 0, wc, 84);
+    if (ok) {
+        tc_fence_after_sync();
+        mma_scores<D>(tS, sm.q, sm.k[0]);
+        tc_commit(&sm.s_full);
+        mma_scores<D>(tdP, sm.dout, sm.v[0]);
+        tc_commit(&sm.dp_full);
+        for (int j = 0; j < n; ++j) {
+            const int slot = j % kStages;
+            if (j + 1 < n) {
+                const int u = j + 1;
+                if (!(ok = mbar_wait(&sm.s_free, (uint32_t)(j & 1), wc, 85))) break;
+                if (!(ok = mbar_wait(&sm.u_full[u % kStages], (uint32_t)((u / kStages) & 1), wc, 86))) break;
+                tc_fence_after_sync();
+                mma_scores<D>(tS, sm.q, sm.k[u % kStages]);  // S(j+1): the warpgroups have read S(j)
+                tc_commit(&sm.s_full);
+            }
+            if (!(ok = mbar_wait(&sm.ds_full, (uint32_t)(j & 1), wc, 87))) break;
+            tc_fence_after_sync();
+            mma_accum<D>(tdQ, tdP, sm.k[slot], j == 0);  // dQ += dS K
+            tc_commit(&sm.u_empty[slot]);
+            if (j == n - 1) tc_commit(&sm.acc_done);
+            if (j + 1 < n) {
+                mma_scores<D>(tdP, sm.dout, sm.v[(j + 1) % kStages]);  // dP(j+1), after dQ(j) read dS(j)
+                tc_commit(&sm.dp_full);
+            }
+        }
+    }
+    tc_commit(&sm.drain);
+    WaitCtx drain{nullptr, wc.status};
+    (void)mbar_wait(&sm.drain, 0, drain, 88);
+}
+
+template <int D, bool MOD>
+__device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
+                           int delta, int n, int j0, int2 span, WaitCtx wc) {
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
+    const uint32_t tS = lane_base + (uint32_t)(w * 64);
+    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * 64);
+    const int row = q0 + r;
+    const bool row_ok = row < p.Nq;
+    const float lse2 = row_ok ? p.lse[(size_t)bh * p.Nq + row] * kLog2e : 0.f;
+    const float drow = row_ok ? p.dterm[(size_t)bh * p.Nq + row] : 0.f;
+    // keys < lim are valid for this row
+    int lim = row_ok ? kv_end : 0;
+    if (p.causal) lim = min(lim, row + delta + 1);
+    if constexpr (MOD) lim = span.y;
+    const float cmul = (MOD && p.cap_in > 0.f) ? p.cap_out : p.scale_log2;
+    const uint64_t c2 = f32x2_pack(cmul, cmul);
+    [[maybe_unused]] const TanhPoly capped(1.f);
+    [[maybe_unused]] const uint64_t in2 = f32x2_pack(p.cap_in, p.cap_in);
+    [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
+    [[maybe_unused]] const float slope2 = (MOD && p.slopes) ? p.slopes[bh % p.Hq] * kLog2e : 0.f;
+    const uint64_t nl2 = f32x2_pack(-lse2, -lse2);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+        const int key0 = (j0 + j) * kT + w * 64;
+        const int nvalid = lim - key0;  // columns c < nvalid are valid
+        bool need_mask = nvalid < 64;
+        [[maybe_unused]] int lo = 0;  // (MOD) and columns from lo on
+        if constexpr (MOD) {
+            lo = span.x - key0;
+            need_mask = __any_sync(kFull, need_mask || lo > 0);
+        }
+        if (!__all_sync(kFull, mbar_wait(&sm.s_full, (uint32_t)(j & 1), wc, 90))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        uint32_t x[2][32];
+        load64(tS, x);
+        tc_fence_before_sync();
+        mbar_arrive(&sm.s_free);
+        [[maybe_unused]] bool far = false;
+        if constexpr (MOD)
+            if (p.cap_in > 0.f) far = __any_sync(kFull, abs_max(x) * p.cap_in > 1.f);
+        const int at = q0 + delta;  // position of the tile's first query
+        [[maybe_unused]] const Distance<-1> dist(slope2, row + delta - key0, p.causal || key0 + 63 <= at,
+                                                 key0 >= at + kT - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                uint64_t x2 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+                [[maybe_unused]] float g0 = 1.f, g1 = 1.f;  // 1 - tanh^2
+                if constexpr (MOD) {
+                    if (p.cap_in > 0.f) {
+                        x2 = capped(f32x2_mul(x2, in2), far);
+                        f32x2_unpack(f32x2_fma(f32x2_mul(x2, minus1), x2, one), g0, g1);
+                    }
+                }
+                const uint64_t e2 = f32x2_fma(x2, c2, nl2);
+                float e0, e1;
+                f32x2_unpack(e2, e0, e1);
+                if constexpr (MOD) {
+                    if (p.slopes) {
+                        e0 = dist.add(h * 32 + i, e0);
+                        e1 = dist.add(h * 32 + i + 1, e1);
+                    }
+                }
+                float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                if constexpr (MOD) {
+                    if (p.cap_in > 0.f) {
+                        p0 *= g0;
+                        p1 *= g1;
+                    }
+                }
+                if (need_mask) {
+                    const int c = h * 32 + i;
+                    p0 = c < nvalid && (!MOD || c >= lo) ? p0 : 0.f;
+                    p1 = c + 1 < nvalid && (!MOD || c + 1 >= lo) ? p1 : 0.f;
+                }
+                x[h][i] = __float_as_uint(p0);
+                x[h][i + 1] = __float_as_uint(p1);
+            }
+
+        if (!__all_sync(kFull, mbar_wait(&sm.dp_full, (uint32_t)(j & 1), wc, 91))) {
+            ok = false;
+            break;
+        }
+        tc_fence_after_sync();
+        uint32_t y[2][32];
+        load64(tdP, y);
+        // dS = P * (dP - D): bf16 pairs over dP
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float s0 = __uint_as_float(x[h][i]) * (__uint_as_float(y[h][i]) - drow);
+                float s1 = __uint_as_float(x[h][i + 1]) * (__uint_as_float(y[h][i + 1]) - drow);
+                if constexpr (MOD) {
+                    if (need_mask) {  // dP of a masked key may be anything
+                        s0 = x[h][i] ? s0 : 0.f;
+                        s1 = x[h][i + 1] ? s1 : 0.f;
+                    }
+                }
+                pk[i / 2] = pack_bf16x2(s0, s1);
+            }
+            tmem_st16(tdP + (uint32_t)(h * 16), pk);
+        }
+        if constexpr (MOD) {
+            // K rows past the sequence's keys may hold anything: dS is 0 there, and dS K needs finite values
+            // (S(j) has been read, and the tile stays until dQ(j) completes)
+            const int rows0 = kv_end - (j0 + j) * kT;
+            if (rows0 < kT && kv_end < p.Nkv) {
+                uint4 *tile = reinterpret_cast<uint4 *>(sm.k[j % kStages]);
+                for (int box = 0; box < kBBoxes<D>; ++box)
+                    for (int i = rows0 * 8 + (int)threadIdx.x; i < kT * 8; i += 256)
+                        tile[box * (kT * 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&sm.ds_full);
+    }
+
+    if (ok && n > 0) {
+        if (!__all_sync(kFull, mbar_wait(&sm.acc_done, 0, wc, 92))) ok = false;
+        else tc_fence_after_sync();
+    }
+    if (!ok) return;
+    // warpgroup 0 writes columns 0 .. kDqSplit - 1 of dQ, warpgroup 1 the rest (times scale)
+    __nv_bfloat16 *dst = p.dq + ((size_t)bh * p.Nq + (row_ok ? row : 0)) * D + (w ? kDqSplit<D> : 0);
+    if (w == 0) store_rows<kDqSplit<D>>(lane_base + 256u, n > 0, row_ok, p.scale, dst);
+    else store_rows<D - kDqSplit<D>>(lane_base + 256u + (uint32_t)kDqSplit<D>, n > 0, row_ok, p.scale, dst);
+}
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    DqSmem<D, MOD> &sm = *reinterpret_cast<DqSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    int bh, level;
+    unit_of(p, p.B * p.Hq, bh, level);
+    const int qt = p.units_per_head - 1 - level;  // level 0 = the last query tile (most keys if causal)
+    const int b = bh / p.Hq;
+    const int bh_kv = b * p.Hkv + (bh % p.Hq) / p.group;
+    const int q0 = qt * kT;
+    const int kv_end = kv_end_for(p, b);
+    const int delta = p.Nkv - p.Nq;
+    int limit = kv_end;
+    if (p.causal) limit = min(limit, min(q0 + kT, p.Nq) + delta);
+    int n = limit > 0 ? (limit + kT - 1) / kT : 0;
+    int j0 = 0;  // MOD: the first key tile that a row of the CTA sees
+    int2 span = make_int2(0, 0);
+    if constexpr (MOD) {
+        if (warp < 8) {
+            span = bwd_row_span(p, b, q0 + ((int)threadIdx.x & 127), kv_end);
+            const int lo = __reduce_min_sync(kFull, span.x < span.y ? span.x : 0x7fffffff);
+            const int hi = __reduce_max_sync(kFull, span.x < span.y ? span.y : 0);
+            if (warp < 4 && lane == 0) {
+                sm.lo[warp] = lo;
+                sm.hi[warp] = hi;
+            }
+        }
+    }
+
+    if (threadIdx.x == 0) {
+        mbar_init(&sm.qd_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.u_full[s], 1);
+            mbar_init(&sm.u_empty[s], 1);
+        }
+        mbar_init(&sm.s_full, 1);
+        mbar_init(&sm.s_free, 256);
+        mbar_init(&sm.dp_full, 1);
+        mbar_init(&sm.ds_full, 256);
+        mbar_init(&sm.acc_done, 1);
+        mbar_init(&sm.drain, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    WaitCtx wc{&sm.abort_flag, p.status};
+    if constexpr (MOD) {
+        const int lo = min(min(sm.lo[0], sm.lo[1]), min(sm.lo[2], sm.lo[3]));
+        const int hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
+        j0 = hi > 0 ? lo / kT : 0;
+        n = hi > 0 ? (hi + kT - 1) / kT - j0 : 0;
+    }
+
+    if (warp == kProducerWarp) {
+        if (lane == 0 && n > 0) dq_producer<D, MOD>(sm, &tmQ, &tmdO, &tmK, &tmV, bh, bh_kv, q0, n, j0, wc);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0 && n > 0) dq_mma<D, MOD>(sm, tmem, n, wc);
+    } else {
+        dq_compute<D, MOD>(sm, p, tmem, warp >> 2, bh, q0, kv_end, delta, n, j0, span, wc);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+int heads_per_chunk(double bytes_per_head, int n_heads) {
+    // about 48 MB of streamed tiles per chunk: the chunk finishing and the one starting fit in
+    // the 126 MB L2 together
+    int h = (int)(48.0e6 / bytes_per_head);
+    return h < 1 ? 1 : (h > n_heads ? n_heads : h);
+}
+
+template <int D, bool MOD>
+cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
+    const long long rows = (long long)a.B * a.Hq * a.Nq;
+    CUtensorMap tq, tdo, tk, tv;
+    const int BHq = a.B * a.Hq, BHkv = a.B * a.Hkv;
+    if (!encode_qkv_map(&tq, a.q, BHq, a.Nq, D) || !encode_qkv_map(&tdo, a.dout, BHq, a.Nq, D) ||
+        !encode_qkv_map(&tk, a.k, BHkv, a.Nkv, D) || !encode_qkv_map(&tv, a.v, BHkv, a.Nkv, D))
+        return cudaErrorInvalidValue;
+    BwdParams p;
+    p.lse = a.lse;
+    p.dterm = a.dterm;
+    p.dq = reinterpret_cast<__nv_bfloat16 *>(a.dq);
+    p.dk = reinterpret_cast<__nv_bfloat16 *>(a.dk);
+    p.dv = reinterpret_cast<__nv_bfloat16 *>(a.dv);
+    p.kv_lens = a.kv_lens;
+    p.status = a.status;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.group = a.Hq / a.Hkv;
+    p.Nq = a.Nq;
+    p.Nkv = a.Nkv;
+    p.causal = a.causal;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * kLog2e;
+    p.key_begin = a.key_begin;
+    p.key_end = a.key_end;
+    p.slopes = a.slopes;
+    p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    p.cap_out = a.softcap * kLog2e;
+    p.spans = a.spans;
+
+    {
+        const int row_blocks = (int)((rows * kRowThreads<D> + 255) / 256);
+        const __nv_bfloat16 *o = reinterpret_cast<const __nv_bfloat16 *>(a.o);
+        const __nv_bfloat16 *dout = reinterpret_cast<const __nv_bfloat16 *>(a.dout);
+        if constexpr (MOD) {
+            const int n_qt = (a.Nq + kT - 1) / kT;
+            const int span_blocks = (int)(((long long)a.B * n_qt + 1) / 2);
+            bwd_rowdot_spans_kernel<D><<<row_blocks + span_blocks, 256, 0, stream>>>(o, dout, a.dterm, rows, row_blocks,
+                                                                                    p, n_qt);
+        } else {
+            bwd_rowdot_kernel<D><<<row_blocks, 256, 0, stream>>>(o, dout, a.dterm, rows);
+        }
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+
+    // dK/dV: one CTA per (batch, key/value head, key tile); streams Q and dO of the group's heads
+    {
+        BwdParams pk = p;
+        pk.units_per_head = (a.Nkv + kT - 1) / kT;
+        pk.heads_per_chunk = heads_per_chunk(2.0 * p.group * a.Nq * D * 2.0, BHkv);
+        const size_t smem = sizeof(DkvSmem<D, MOD>) + 1024;
+        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dkdv_kernel<D, MOD>), (int)smem);
+        if (e != cudaSuccess) return e;
+        const unsigned grid = (unsigned)((size_t)pk.units_per_head * BHkv);
+        bwd_dkdv_kernel<D, MOD><<<grid, kThreads, smem, stream>>>(tq, tdo, tk, tv, pk);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    // dQ: one CTA per (batch, query head, query tile); streams K and V of its key/value head
+    {
+        BwdParams pq = p;
+        pq.units_per_head = (a.Nq + kT - 1) / kT;
+        pq.heads_per_chunk = heads_per_chunk(2.0 * a.Nkv * D * 2.0 / p.group, BHq);
+        const size_t smem = sizeof(DqSmem<D, MOD>) + 1024;
+        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dq_kernel<D, MOD>), (int)smem);
+        if (e != cudaSuccess) return e;
+        const unsigned grid = (unsigned)((size_t)pq.units_per_head * BHq);
+        bwd_dq_kernel<D, MOD><<<grid, kThreads, smem, stream>>>(tq, tdo, tk, tv, pq);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace attn

@@ -56,6 +56,11 @@ struct BwdArgs {
     int *status;
     int B, Hq, Hkv, Nq, Nkv, d, causal;
     float scale;
+    // modified scores (launch_bwd_scoremod), as in PrefillArgs; spans: the rest of the workspace
+    float softcap = 0.f;
+    const float *slopes = nullptr;
+    const int32_t *key_begin = nullptr, *key_end = nullptr;
+    int2 *spans = nullptr;
 };
 
 // Per-device facts looked up once (host-side caches shared by the launchers): the SM count
@@ -79,6 +84,8 @@ cudaError_t launch_prefill_scoremod(const PrefillArgs &a, cudaStream_t stream);
 // Backward: the row term D, then the dK/dV kernel and the dQ kernel.
 cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t stream);
 size_t bwd_workspace_bytes(int B, int Hq, int Nq);
+cudaError_t launch_bwd_scoremod(const BwdArgs &a, cudaStream_t stream);
+size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Nq);
 
 // Writes new tokens' K/V into their pages (token t of sequence b goes to position
 // start_pos[b] + t).  Positions past the table's capacity are skipped.

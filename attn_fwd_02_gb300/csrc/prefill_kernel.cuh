@@ -44,6 +44,7 @@
 #include <cmath>
 
 #include "launch.h"
+#include "scoremod.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -656,11 +657,6 @@ __device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r) {
 
 // Modified scores (kContigMod): x = log2(e) (cap tanh(scale raw / cap) - slope |pos - key|), or without
 // the cap x = log2(e) (scale raw - slope |pos - key|), in place on the raw scores of a row.
-//
-// tanh(u) = u P(u^2) with a polynomial fitted to tanh(u) / u over |u| <= 1 (iterated weighted least
-// squares, relative error 6e-7 and 7e-7 with the roundings of fp32): eight packed operations per two
-// scores, no special-function unit.  Rows with a larger |u| take the exponential form 1 - 2 / (1 +
-// e^(2|u|)) there, whose cancellation is harmless from |u| = 1 on (a warp decides as one).
 struct ScoreMod {
     bool cap = false, bias = false;
     float c = 0.f, cin = 0.f, cout = 0.f, slope2 = 0.f;
@@ -681,17 +677,10 @@ struct ScoreMod {
     __device__ __forceinline__ void apply_cap(uint32_t (&s)[H][2][32]) const {
         float big = 0.f;
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) big = fmaxf(big, fabsf(__uint_as_float(s[h][cc][i])));
+        for (int h = 0; h < H; ++h) big = fmaxf(big, abs_max(s[h]));
         const bool far = __any_sync(0xffffffffu, big * cin > 1.f);
+        const TanhPoly capped(cout);
         const uint64_t in2 = f32x2_pack(cin, cin);
-        uint64_t a[6];
-        constexpr float kP[6] = {0.999999414f, -0.333290424f, 0.13281434f, -0.0516056762f, 0.0167431162f, -0.00306706033f};
-#pragma unroll
-        for (int i = 0; i < 6; ++i) a[i] = f32x2_pack(kP[i] * cout, kP[i] * cout);
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -700,19 +689,8 @@ struct ScoreMod {
                 for (int i = 0; i < 32; i += 2) {
                     const uint64_t u =
                         f32x2_mul(f32x2_pack(__uint_as_float(s[h][cc][i]), __uint_as_float(s[h][cc][i + 1])), in2);
-                    const uint64_t z = f32x2_mul(u, u);
-                    uint64_t t = f32x2_fma(z, a[5], a[4]);
-#pragma unroll
-                    for (int k = 3; k >= 0; --k) t = f32x2_fma(z, t, a[k]);
-                    t = f32x2_mul(t, u);
                     float t0, t1;
-                    f32x2_unpack(t, t0, t1);
-                    if (far) {
-                        float u0, u1;
-                        f32x2_unpack(u, u0, u1);
-                        t0 = fabsf(u0) > 1.f ? copysignf(tanh_large(fabsf(u0)) * cout, u0) : t0;
-                        t1 = fabsf(u1) > 1.f ? copysignf(tanh_large(fabsf(u1)) * cout, u1) : t1;
-                    }
+                    f32x2_unpack(capped(u, far), t0, t1);
                     s[h][cc][i] = __float_as_uint(t0);
                     s[h][cc][i + 1] = __float_as_uint(t1);
                 }

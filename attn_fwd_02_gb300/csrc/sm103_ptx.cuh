@@ -446,10 +446,6 @@ __device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// tanh(u) for u >= 1 as 1 - 2 / (1 + e^(2u)) (relative error below 1e-6 there; 1 once e^(2u) overflows).
-__device__ __forceinline__ float tanh_large(float u) {
-    return 1.f - __fdividef(2.f, 1.f + ex2_approx(u * 2.885390082f));
-}
 __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

@@ -357,6 +357,24 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *o, const f
              size_t workspace_bytes, attn_stream_t stream);
 
 /*
+ * Backward of attn_fwd_scoremod: as attn_bwd for the modified scores.  With t_ij = tanh(scale <q_i, k_j> /
+ * cap) the gradient of the modified score, dS = P * (dP - D), times 1 - t_ij^2 is that of scale <q_i, k_j>:
+ *     dV = P^T dO,   dK = scale (dS (1 - t^2))^T Q,   dQ = scale (dS (1 - t^2)) K
+ * (without the cap the factor is 1; the slopes and the intervals get no gradient).
+ *   lse, o: attn_fwd_scoremod's for the same inputs and modification; dout finite
+ *   workspace: at least attn_bwd_scoremod_workspace_size(B, Hq, Nq) bytes, 16-byte aligned
+ * Rows of k and v past kv_lens[b] may hold anything; dk and dv get zeros there.  Other arguments as
+ * attn_bwd and attn_fwd_scoremod.
+ */
+size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Nq);
+
+int attn_bwd_scoremod(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                      const void *dout, void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Nq, int Nkv,
+                      int d, int causal, float scale, float softcap, const float *alibi_slopes,
+                      const int32_t *key_begin, const int32_t *key_end, const int32_t *kv_lens, void *workspace,
+                      size_t workspace_bytes, attn_stream_t stream);
+
+/*
  * paged_attn_decode for callers that cannot allocate device memory.  The pages
  * describe no such variant; it exists for callers such as code running inside
  * a memory pool or allocator callback (where a nested cudaMalloc is not

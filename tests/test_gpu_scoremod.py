@@ -146,3 +146,114 @@ def test_other_stream_and_captured_graph(lib):
     want = lib.attn_fwd_scoremod(q, k, v, True, softcap=20.0)
     torch.cuda.synchronize()
     assert torch.equal(cap[0], want[0])
+
+
+# Gradients.  P and dS are rounded once to bf16 (2^-8 of each) before the products that sum them in fp32, and
+# each gradient is rounded once.  D = dO . O is taken from the bf16 O (2^-8 of each O), which moves dP - D by
+# at most 2^-8 |dO| . |O|; the scores' error of 2e-4 moves P by 2e-4 of itself.  Element by element, with the
+# sums over absolute values of the definition in 64 bits:
+#   dV: (2^-8 + 4e-4) P^T |dO|,   dQ, dK: scale (((2^-8 + 4e-4) |dS| + 2^-8 P (|dO| . |O|)) g + 4e-4 |dP - D| P)
+#   summed against |K|, |Q| (g = 1 - t^2), each plus 2^-8 of the gradient, 2 % for the cross terms.
+def grad_bounds(q, k, v, dout, o64, w, t, scale, grads):
+    B, H, Nq, d = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    rep = H // Hkv
+    k64, v64 = (x.double().nan_to_num(0.0, 0.0, 0.0).repeat_interleave(rep, 1) for x in (k, v))
+    g = dout.double()
+    dp = g @ v64.transpose(2, 3) - (g * o64).sum(-1, keepdim=True)
+    fac = torch.ones_like(w) if t is None else 1 - t * t
+    ds = w * dp.abs() * fac
+    slack = w * (g.abs() * o64.abs()).sum(-1, keepdim=True) * fac
+    m = scale * ((2.0 ** -8 + 8e-4) * ds + 2.0 ** -8 * slack)
+    fold = lambda x: x.view(B, Hkv, rep, Nkv, d).sum(2)  # noqa: E731
+    out = (m @ k64.abs(), fold(m.transpose(2, 3) @ q.double().abs()),
+           fold((2.0 ** -8 + 4e-4) * (w.transpose(2, 3) @ g.abs())))
+    return [1.02 * (b + 2.0 ** -8 * x.abs()) + 1e-9 for b, x in zip(out, grads)]
+
+
+BWD_SIZES = [(2, 2, 2, 1, 1, 32), (1, 3, 1, 65, 64, 64), (2, 4, 2, 300, 300, 80), (1, 2, 1, 129, 517, 96),
+             (3, 2, 2, 257, 256, 128), (1, 4, 2, 640, 640, 64)]
+
+
+@pytest.mark.parametrize("mod", MODS, ids=["plain", "cap5", "bias", "cap30_bias"])
+@pytest.mark.parametrize("kind", MASKS)
+@pytest.mark.parametrize("size", BWD_SIZES, ids=["x".join(map(str, s)) for s in BWD_SIZES])
+def test_backward(lib, size, kind, mod):
+    B, H, Hkv, Nq, Nkv, d = size
+    q, k, v = rand(1, B, H, Nq, d, by=2.0), rand(2, B, Hkv, Nkv, d), rand(3, B, Hkv, Nkv, d)
+    dout = rand(4, B, H, Nq, d)
+    cap, bias = mod
+    m = masks(kind, B, Nq, Nkv)
+    sl = slopes_of(H) if bias else None
+    if m["kv_lens"] is not None:
+        for b in range(B):
+            n = int(m["kv_lens"][b])
+            k[b, :, n:], v[b, :, n:] = float("nan"), float("inf")
+    scale = d ** -0.5
+    kw = dict(softcap=cap, alibi_slopes=cuda(sl), key_begin=cuda(m["key_begin"]), key_end=cuda(m["key_end"]),
+              kv_lens=cuda(m["kv_lens"]))
+    qc, kc, vc = q.cuda(), k.cuda(), v.cuda()
+    o, lse = lib.attn_fwd_scoremod(qc, kc, vc, m["causal"], scale, **kw)
+    outs = [torch.full(x.shape, float("nan"), dtype=torch.bfloat16, device="cuda") for x in (q, k, v)]
+    lib.attn_bwd_scoremod(qc, kc, vc, o, lse, dout.cuda(), m["causal"], scale, dq=outs[0], dk=outs[1], dv=outs[2], **kw)
+    torch.cuda.synchronize()
+    assert lib.attn_check_device_status() == 0
+    ref = (m["causal"], scale, cap, sl, m["key_begin"], m["key_end"], m["kv_lens"])
+    want = backward(q, k, v, dout, *ref)
+    o64, _, w, t = forward(q, k, v, *ref)
+    for name, got, x, tol in zip(("dq", "dk", "dv"), outs, want, grad_bounds(q, k, v, dout, o64, w, t, scale, want)):
+        err = (got.cpu().double() - x).abs()
+        assert torch.isfinite(got).all(), name
+        assert (err <= tol).all(), (name, float(err.max()), float((err / tol).max()))
+
+
+def test_backward_of_a_plain_call_equals_the_plain_backward(lib):
+    q, k, v, g = (rand(20 + i, 2, h, 500, 128).cuda() for i, h in enumerate((4, 2, 2, 4)))
+    for causal in (False, True):
+        o, lse = lib.attn_fwd_gqa(q, k, v, causal)
+        a = lib.attn_bwd(q, k, v, o, lse, g, causal)
+        b = lib.attn_bwd_scoremod(q, k, v, o, lse, g, causal)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_gradients_match_differences():
+    """The formula of the backward (and its 64-bit restatement) against central differences of the forward."""
+    torch.manual_seed(0)
+    B, H, Hkv, Nq, Nkv, d = 1, 2, 1, 5, 7, 32
+    q, k, v = (torch.randn(B, h, n, d, dtype=torch.float64) for h, n in ((H, Nq), (Hkv, Nkv), (Hkv, Nkv)))
+    g = torch.randn(B, H, Nq, d, dtype=torch.float64)
+    kb, ke = documents(B, Nq, Nkv, [3, 4])
+    args = (False, 0.3, 2.0, slopes_of(H), kb, ke, torch.tensor([6]))
+    got = backward(q, k, v, g, *args)
+    loss = lambda: float((forward(q, k, v, *args)[0] * g).sum())  # noqa: E731
+    for x, dx in zip((q, k, v), got):
+        flat, dflat = x.view(-1), dx.reshape(-1)
+        for i in range(0, flat.numel(), 13):
+            old, h = float(flat[i]), 1e-5
+            flat[i] = old + h
+            up = loss()
+            flat[i] = old - h
+            down = loss()
+            flat[i] = old
+            assert abs((up - down) / (2 * h) - float(dflat[i])) <= 1e-7
+
+
+def test_backward_on_another_stream_captured_and_repeated(lib):
+    q, k, v, g = (rand(30 + i, 1, h, 400, 64).cuda() for i, h in enumerate((4, 2, 2, 4)))
+    kb, ke = (t.cuda() for t in documents(1, 400, 400, [77, 130]))
+    kw = dict(softcap=20.0, key_begin=kb, key_end=ke)
+    o, lse = lib.attn_fwd_scoremod(q, k, v, True, **kw)
+    want = lib.attn_bwd_scoremod(q, k, v, o, lse, g, True, **kw)
+    again = lib.attn_bwd_scoremod(q, k, v, o, lse, g, True, **kw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = lib.attn_bwd_scoremod(q, k, v, o, lse, g, True, stream=side, **kw)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, l2 = lib.attn_fwd_scoremod(q, k, v, True, **kw)
+        cap = lib.attn_bwd_scoremod(q, k, v, o2, l2, g, True, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c, e in zip(want, again, other, cap):
+        assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, e)
