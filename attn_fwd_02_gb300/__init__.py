@@ -25,6 +25,12 @@ from .binding import (  # noqa: F401
     paged_attn_decode_fp8,
     paged_attn_decode_gqa,
     paged_attn_decode_noalloc,
+    paged_attn_decode_scoremod,
+    paged_attn_decode_scoremod_fp8,
+    paged_attn_decode_scoremod_workspace_size,
+    paged_attn_decode_shared,
+    paged_attn_decode_shared_fp8,
+    paged_attn_decode_shared_workspace_size,
     paged_attn_prefill,
     paged_attn_prefill_fp8,
     paged_kv_append,

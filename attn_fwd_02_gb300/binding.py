@@ -49,6 +49,12 @@ SIGNATURES = {
     "attn_fwd_scoremod": (I, [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P]),
     "attn_bwd_scoremod_workspace_size": (Z, [I, I, I]),
     "attn_bwd_scoremod": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P, Z, P]),
+    "paged_attn_decode_scoremod_workspace_size": (Z, [I, I, I, I, I, I]),
+    "paged_attn_decode_scoremod": (I, [P, P, P, P, P, I, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P]),
+    "paged_attn_decode_scoremod_fp8": (I, [P, P, P, F, F, P, P, I, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P]),
+    "paged_attn_decode_shared_workspace_size": (Z, [I, I, I, I, I, I, I]),
+    "paged_attn_decode_shared": (I, [P, P, P, P, P, P, I, I, P, P, I, I, I, I, I, I, F, P, Z, P]),
+    "paged_attn_decode_shared_fp8": (I, [P, P, P, F, F, P, P, P, I, I, P, P, I, I, I, I, I, I, F, P, Z, P]),
     "attn_check_device_status": (I, [P]),
     "attn_last_device_status": (I, []),
     "attn_selftest_bounded_wait": (I, [P]),
@@ -763,6 +769,130 @@ def attn_bwd_scoremod(q, k, v, o, lse, dout, causal: bool, scale: float | None =
     if st:
         _check("attn_bwd_scoremod", st)
     return dq, dk, dv
+
+
+def paged_attn_decode_scoremod_workspace_size(B: int, H: int, Hkv: int, d: int, max_pages_per_seq: int,
+                                              page_size: int = 16) -> int:
+    return int(load_library().paged_attn_decode_scoremod_workspace_size(B, H, Hkv, d, max_pages_per_seq, page_size))
+
+
+def paged_attn_decode_shared_workspace_size(B: int, H: int, Hkv: int, d: int, max_pages_per_seq: int,
+                                            group_size: int, page_size: int = 16) -> int:
+    return int(load_library().paged_attn_decode_shared_workspace_size(B, H, Hkv, d, max_pages_per_seq, group_size,
+                                                                      page_size))
+
+
+def _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens):
+    """Addresses and sizes of a decode batch over a paged cache, on one device."""
+    torch = _torch()
+    qp = _in(q, "q", torch.bfloat16, 3)
+    device = q.device
+    kp, vp = _in(k_pages, "k_pages", page_dtype, 4, device), _in(v_pages, "v_pages", page_dtype, 4, device)
+    table, ctx = _in(page_table, "page_table", torch.int32, 2, device), _in(ctx_lens, "ctx_lens", torch.int32, 1, device)
+    B, H, d = q.shape
+    num_pages, Hkv, page_size, dk = k_pages.shape
+    if dk != d or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d] matching q")
+    Bt, max_pages = page_table.shape
+    if Bt != B or ctx_lens.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages] and ctx_lens [B]")
+    return device, (qp, kp, vp, table, ctx), (B, H, Hkv, d, max_pages, num_pages), page_size
+
+
+def _decode_outputs(out, lse, return_lse, B, H, d, device):
+    out, op = _output(out, "out", _t.bfloat16, (B, H, d), device)
+    lp = None
+    if lse is not None or return_lse:
+        lse, lp = _output(lse, "lse", _t.float32, (B, H), device)
+    return out, op, lse, lp
+
+
+def _decode_scoremod(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes,
+                     key_begin, out, lse, workspace, return_lse, stream):
+    device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens)
+    B, H, Hkv, d, max_pages, num_pages = sizes
+    slopes = _optional(alibi_slopes, "alibi_slopes", _t.float32, (H,), device)
+    begin = _optional(key_begin, "key_begin", _t.int32, (B,), device)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return _decode_scoremod(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap,
+                                    alibi_slopes, key_begin, out, lse, workspace, return_lse, None)
+    out, op, lse, lp = _decode_outputs(out, lse, return_lse, B, H, d, device)
+    lib = load_library()
+    workspace, wp, wn = _workspace(
+        workspace, lib.paged_attn_decode_scoremod_workspace_size(B, H, Hkv, d, max_pages, ps), device)
+    st = getattr(lib, fn)(qp, kp, vp, *scales, table, ctx_p, ps, op, lp, *sizes, d ** -0.5 if scale is None else scale,
+                          softcap, slopes, begin, wp, wn, _current_stream(device))
+    if st:
+        _check(fn, st)
+    return out, lse
+
+
+def paged_attn_decode_scoremod(q, k_pages, v_pages, page_table, ctx_lens, scale: float | None = None,
+                               softcap: float = 0.0, alibi_slopes=None, key_begin=None, out=None, lse=None,
+                               workspace=None, return_lse: bool = True, stream=None):
+    """Paged decode with modified scores: softcap * tanh(scale q.k / softcap) - alibi_slopes[h] * distance over
+    the cached tokens key_begin[b] <= j < ctx_lens[b].  q [B,H,d] bf16; k_pages/v_pages [P,Hkv,16,d] bf16;
+    page_table [B,max_pages], ctx_lens [B] int32; alibi_slopes [H] fp32 and key_begin [B] int32 optional;
+    softcap 0 is none.  Returns (o, lse)."""
+    return _decode_scoremod("paged_attn_decode_scoremod", _torch().bfloat16, (), q, k_pages, v_pages, page_table,
+                            ctx_lens, scale, softcap, alibi_slopes, key_begin, out, lse, workspace, return_lse, stream)
+
+
+def paged_attn_decode_scoremod_fp8(q, k_pages, v_pages, k_scale: float, v_scale: float, page_table, ctx_lens,
+                                   scale: float | None = None, softcap: float = 0.0, alibi_slopes=None,
+                                   key_begin=None, out=None, lse=None, workspace=None, return_lse: bool = True,
+                                   stream=None):
+    """paged_attn_decode_scoremod over an e4m3 cache (k_pages, v_pages uint8 codes [P,Hkv,16,d])."""
+    return _decode_scoremod("paged_attn_decode_scoremod_fp8", _torch().uint8, (float(k_scale), float(v_scale)), q,
+                            k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes, key_begin, out, lse,
+                            workspace, return_lse, stream)
+
+
+def _decode_shared(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, shared_pages, group_size, scale,
+                   out, lse, workspace, return_lse, stream):
+    device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens)
+    B, H, Hkv, d, max_pages, num_pages = sizes
+    if group_size <= 0 or B % group_size:
+        raise ValueError(f"the batch of {B} must be whole groups of group_size = {group_size} sequences")
+    shared = _optional(shared_pages, "shared_pages", _t.int32, (B // group_size,), device)
+    if shared is None:
+        raise TypeError("shared_pages must be a torch.Tensor")
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return _decode_shared(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, shared_pages,
+                                  group_size, scale, out, lse, workspace, return_lse, None)
+    out, op, lse, lp = _decode_outputs(out, lse, return_lse, B, H, d, device)
+    lib = load_library()
+    workspace, wp, wn = _workspace(
+        workspace, lib.paged_attn_decode_shared_workspace_size(B, H, Hkv, d, max_pages, group_size, ps), device)
+    st = getattr(lib, fn)(qp, kp, vp, *scales, table, ctx_p, shared, group_size, ps, op, lp, *sizes,
+                          d ** -0.5 if scale is None else scale, wp, wn, _current_stream(device))
+    if st:
+        _check(fn, st)
+    return out, lse
+
+
+def paged_attn_decode_shared(q, k_pages, v_pages, page_table, ctx_lens, shared_pages, group_size: int,
+                             scale: float | None = None, out=None, lse=None, workspace=None, return_lse: bool = True,
+                             stream=None):
+    """Paged decode of groups of group_size consecutive sequences that share their first pages, which are read
+    once per group: q [B,H,d] bf16; k_pages/v_pages [P,Hkv,16,d] bf16; page_table [B,max_pages], ctx_lens [B]
+    int32; shared_pages [B/group_size] int32, the number of shared page-table entries of each group (taken from
+    its first sequence's row).  Returns (o, lse)."""
+    return _decode_shared("paged_attn_decode_shared", _torch().bfloat16, (), q, k_pages, v_pages, page_table, ctx_lens,
+                          shared_pages, group_size, scale, out, lse, workspace, return_lse, stream)
+
+
+def paged_attn_decode_shared_fp8(q, k_pages, v_pages, k_scale: float, v_scale: float, page_table, ctx_lens,
+                                 shared_pages, group_size: int, scale: float | None = None, out=None, lse=None,
+                                 workspace=None, return_lse: bool = True, stream=None):
+    """paged_attn_decode_shared over an e4m3 cache (k_pages, v_pages uint8 codes [P,Hkv,16,d])."""
+    return _decode_shared("paged_attn_decode_shared_fp8", _torch().uint8, (float(k_scale), float(v_scale)), q, k_pages,
+                          v_pages, page_table, ctx_lens, shared_pages, group_size, scale, out, lse, workspace,
+                          return_lse, stream)
 
 
 def attn_selftest_bounded_wait(stream=None) -> None:

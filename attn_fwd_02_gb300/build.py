@@ -24,7 +24,8 @@ ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden,-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
-SOURCES = ["abi.cu", "prefill.cu", "prefill_scoremod.cu", "decode.cu", "kvcache.cu", "backward.cu", "backward_scoremod.cu", "append_rope.cu"]
+SOURCES = ["abi.cu", "prefill.cu", "prefill_scoremod.cu", "decode.cu", "kvcache.cu", "backward.cu", "backward_scoremod.cu", "append_rope.cu",
+           "decode_scoremod.cu", "decode_shared.cu"]
 
 
 def nvcc() -> str:

@@ -179,6 +179,19 @@ bool encode_qkv_map(CUtensorMap *m, const void *ptr, int BH, int N, int D, int b
     return r == CUDA_SUCCESS;
 }
 
+bool encode_q_heads_map(CUtensorMap *m, const void *ptr, int B, int H, int D, int heads, int seqs) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)seqs};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_page_map_u8(CUtensorMap *m, const void *ptr, int rows, int page_rows, int D, bool swizzle) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
@@ -572,6 +585,102 @@ ATTN_API int paged_attn_decode_gqa(const void *q, const void *k_pages, const voi
                        max_pages_per_seq, num_pages, scale, Hkv};
     cudaError_t e = attn::launch_decode(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+ATTN_API size_t paged_attn_decode_scoremod_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq,
+                                                          int page_size) {
+    return attn::decode_scoremod_workspace_bytes(B, H, Hkv, d, max_pages_per_seq, page_size);
+}
+
+ATTN_API size_t paged_attn_decode_shared_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq,
+                                                        int group_size, int page_size) {
+    return attn::decode_shared_workspace_bytes(B, H, Hkv, d, max_pages_per_seq, group_size, page_size);
+}
+
+namespace {
+// Decode with modified scores (k_scale, v_scale 1 for a bf16 cache).
+int decode_scoremod(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stream) {
+    int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
+                               a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
+    if (st == ATTN_OK) st = scoremod_checks(a.softcap, a.slopes, a.key_begin, nullptr);
+    if (st != ATTN_OK) return st;
+    if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn::decode_scoremod_workspace_bytes(a.B, a.H, a.Hkv, a.d, a.max_pages, a.page_size);
+    if (!a.workspace || !aligned16(a.workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    st = device_setup(&a.status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_decode_scoremod(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int decode_shared(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stream) {
+    if (!a.shared_pages || a.group_size <= 0) return ATTN_ERR_INVALID_ARG;
+    int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
+                               a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
+    if (st != ATTN_OK) return st;
+    if (a.B % a.group_size != 0) return ATTN_ERR_INVALID_ARG;
+    if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned4(a.shared_pages)) return ATTN_ERR_MISALIGNED;
+    const size_t need = attn::decode_shared_workspace_bytes(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size, a.page_size);
+    if (!a.workspace || !aligned16(a.workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    st = device_setup(&a.status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_decode_shared(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+}  // namespace
+
+ATTN_API int paged_attn_decode_scoremod(const void *q, const void *k_pages, const void *v_pages,
+                                        const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o,
+                                        float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                                        float scale, float softcap, const float *alibi_slopes,
+                                        const int32_t *key_begin, void *workspace, size_t workspace_bytes,
+                                        attn_stream_t stream) {
+    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv};
+    a.softcap = softcap;
+    a.slopes = alibi_slopes;
+    a.key_begin = key_begin;
+    return decode_scoremod(a, workspace_bytes, stream);
+}
+
+ATTN_API int paged_attn_decode_scoremod_fp8(const void *q, const void *k_pages, const void *v_pages, float k_scale,
+                                            float v_scale, const int32_t *page_table, const int32_t *ctx_lens,
+                                            int page_size, void *o, float *lse, int B, int H, int Hkv, int d,
+                                            int max_pages_per_seq, int num_pages, float scale, float softcap,
+                                            const float *alibi_slopes, const int32_t *key_begin, void *workspace,
+                                            size_t workspace_bytes, attn_stream_t stream) {
+    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale};
+    a.softcap = softcap;
+    a.slopes = alibi_slopes;
+    a.key_begin = key_begin;
+    return decode_scoremod(a, workspace_bytes, stream);
+}
+
+ATTN_API int paged_attn_decode_shared(const void *q, const void *k_pages, const void *v_pages,
+                                      const int32_t *page_table, const int32_t *ctx_lens,
+                                      const int32_t *shared_pages, int group_size, int page_size, void *o, float *lse,
+                                      int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale,
+                                      void *workspace, size_t workspace_bytes, attn_stream_t stream) {
+    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv};
+    a.shared_pages = shared_pages;
+    a.group_size = group_size;
+    return decode_shared(a, workspace_bytes, stream);
+}
+
+ATTN_API int paged_attn_decode_shared_fp8(const void *q, const void *k_pages, const void *v_pages, float k_scale,
+                                          float v_scale, const int32_t *page_table, const int32_t *ctx_lens,
+                                          const int32_t *shared_pages, int group_size, int page_size, void *o,
+                                          float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq,
+                                          int num_pages, float scale, void *workspace, size_t workspace_bytes,
+                                          attn_stream_t stream) {
+    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale};
+    a.shared_pages = shared_pages;
+    a.group_size = group_size;
+    return decode_shared(a, workspace_bytes, stream);
 }
 
 ATTN_API int paged_attn_decode(const void *q, const void *k_pages, const void *v_pages, const int32_t *page_table,

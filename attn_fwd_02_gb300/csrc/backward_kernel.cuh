@@ -69,16 +69,22 @@ struct BwdParams {
     int units_per_head;   // query tiles (dQ kernel) or key tiles (dK/dV kernel) of one head
     int heads_per_chunk;  // heads whose streamed operands share L2 at a time
     float scale, scale_log2;
-    // modified scores (MOD): see the forward; spans [B, query tiles] holds the union {lo, hi} of the
-    // intervals of a query tile's rows
+};
+// With modified scores (see the forward's parameters); spans [B, query tiles] holds the union {lo, hi} of
+// the intervals of a query tile's rows.  A type of its own: the plain kernels' registers depend on the
+// size of their parameters (spilled bytes of the dK/dV kernel 20 / 12 without these fields, 56 / 76 with).
+struct BwdModParams : BwdParams {
     const int32_t *key_begin, *key_end;
     const float *slopes;
     float cap_in, cap_out;
     int2 *spans;
 };
+template <bool MOD> struct ParamsOf { using type = BwdParams; };
+template <> struct ParamsOf<true> { using type = BwdModParams; };
+template <bool MOD> using Params = typename ParamsOf<MOD>::type;
 
 // Keys lo <= j < hi that query `row` of sequence b sees (none past the last query).
-__device__ __forceinline__ int2 bwd_row_span(const BwdParams &p, int b, int row, int kv_end) {
+__device__ __forceinline__ int2 bwd_row_span(const BwdModParams &p, int b, int row, int kv_end) {
     if (row >= p.Nq) return make_int2(0, 0);
     const size_t at = (size_t)b * p.Nq + row;
     int2 s;
@@ -142,6 +148,15 @@ struct Distance {
     __device__ __forceinline__ float add(int c, float e) const {
         return linear ? fmaf(sl, (float)c, e + base) : fmaf(base, fabsf(d0 + (float)(Step * c)), e);
     }
+};
+
+// The cap as the compute warpgroups use it: u = raw * in goes into tanh (0: no cap), and the score in the
+// log2 domain is tanh * mul, or raw * mul without the cap.
+struct CapOf {
+    float in, mul;
+    __device__ __forceinline__ explicit CapOf(const BwdParams &p) : in(0.f), mul(p.scale_log2) {}
+    __device__ __forceinline__ explicit CapOf(const BwdModParams &p)
+        : in(p.cap_in), mul(p.cap_in > 0.f ? p.cap_out : p.scale_log2) {}
 };
 
 // 64 TMEM columns of this thread's lane -> registers.
@@ -231,7 +246,7 @@ __global__ void __launch_bounds__(256) bwd_rowdot_kernel(const __nv_bfloat16 *o,
 template <int D>
 __global__ void __launch_bounds__(256) bwd_rowdot_spans_kernel(const __nv_bfloat16 *o, const __nv_bfloat16 *dout,
                                                                float *dterm, long long rows, int row_blocks,
-                                                               const BwdParams p, int n_qt) {
+                                                               const BwdModParams p, int n_qt) {
     if ((int)blockIdx.x < row_blocks) {
         rowdot<D>(o, dout, dterm, rows);
         return;
@@ -300,7 +315,7 @@ __device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_en
 }
 
 template <int D, bool MOD>
-__device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const BwdParams &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
+__device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const Params<MOD> &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
                               const CUtensorMap *tmK, const CUtensorMap *tmV, int b, int hkv, int bh_kv, int k0,
                               int qi_start, int nqt, int n, WaitCtx wc) {
     constexpr int kBoxes = kBBoxes<D>;
@@ -337,9 +352,11 @@ __device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const BwdParams &p, const CUt
     float slope_n = 0.f;
     const int kv_end = kv_end_for(p, b);
     auto load_spans = [&](int u) {
+        if constexpr (MOD) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + u % nqt) * kT + lane * 4 + t, kv_end);
-        slope_n = p.slopes ? p.slopes[hkv * p.group + u / nqt] * kLog2e : 0.f;
+            for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + u % nqt) * kT + lane * 4 + t, kv_end);
+            slope_n = p.slopes ? p.slopes[hkv * p.group + u / nqt] * kLog2e : 0.f;
+        }
     };
     if constexpr (MOD) load_spans(0);
     int fills = 0;
@@ -425,7 +442,7 @@ __device__ void dkdv_mma(DkvSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) 
 }
 
 template <int D, bool MOD>
-__device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem, int w, int bh_kv, int k0,
+__device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tmem, int w, int bh_kv, int k0,
                              int kv_end, int delta, int qi_start, int nqt, int n, WaitCtx wc) {
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
@@ -434,10 +451,10 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t t
     const int key = k0 + r;
     const bool key_ok = key < kv_end;
     // with the cap, x becomes tanh and c2 its factor cap * log2(e)
-    const float cmul = (MOD && p.cap_in > 0.f) ? p.cap_out : p.scale_log2;
-    const uint64_t c2 = f32x2_pack(cmul, cmul);
+    const CapOf cap(p);
+    const uint64_t c2 = f32x2_pack(cap.mul, cap.mul);
     [[maybe_unused]] const TanhPoly capped(1.f);
-    [[maybe_unused]] const uint64_t in2 = f32x2_pack(p.cap_in, p.cap_in);
+    [[maybe_unused]] const uint64_t in2 = f32x2_pack(cap.in, cap.in);
     [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -471,12 +488,12 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t t
         load64(tS, x);
         [[maybe_unused]] bool far = false;
         if constexpr (MOD)
-            if (p.cap_in > 0.f) far = __any_sync(kFull, abs_max(x) * p.cap_in > 1.f);
+            if (cap.in > 0.f) far = __any_sync(kFull, abs_max(x) * cap.in > 1.f);
         // column c is the query at position col0 + c + delta; under the causal mask the keys after it are
         // masked, so the linear form serves there too
-        const int first = col0 + delta;
-        [[maybe_unused]] const Distance<1> dist(MOD ? sm_slope(sm, slot) : 0.f, first - key,
-                                                p.causal || first >= k0 + kT - 1, first + 63 <= k0);
+        const int first = MOD ? col0 + delta : 0;
+        [[maybe_unused]] const Distance<1> dist(sm_slope(sm, slot), MOD ? first - key : 0,
+                                                MOD && (p.causal || first >= k0 + kT - 1), MOD && first + 63 <= k0);
         // P^T = 2^(s * scale * log2e - lse2): bf16 pairs over the scores, fp32 kept in x
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -488,7 +505,7 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t t
                 uint64_t x23 = f32x2_pack(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
                 [[maybe_unused]] float g[4];  // 1 - tanh^2
                 if constexpr (MOD) {
-                    if (p.cap_in > 0.f) {
+                    if (cap.in > 0.f) {
                         x01 = capped(f32x2_mul(x01, in2), far);
                         x23 = capped(f32x2_mul(x23, in2), far);
                         f32x2_unpack(f32x2_fma(f32x2_mul(x01, minus1), x01, one), g[0], g[1]);
@@ -528,7 +545,7 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const BwdParams &p, uint32_t t
                 pk[i / 2] = pack_bf16x2(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
                 pk[i / 2 + 1] = pack_bf16x2(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
                 if constexpr (MOD) {
-                    if (p.cap_in > 0.f)
+                    if (cap.in > 0.f)
 #pragma unroll
                         for (int t = 0; t < 4; ++t)  // a masked weight stays 0
                             if (!need_mask || x[h][i + t] != 0u)
@@ -596,7 +613,7 @@ template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const BwdParams p) {
+                    const Params<MOD> p) {
     extern __shared__ uint8_t smem_raw[];
     DkvSmem<D, MOD> &sm =
         *reinterpret_cast<DkvSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -631,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         dkdv_range(p, k0, kv_end, delta, qi_start, nqt);
     }
+    int n = nqt * p.group;  // steps: every query tile of every query head of the group
 
     if (threadIdx.x == 0) {
         mbar_init(&sm.kv_full, 1);
@@ -661,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             qi_start = sm.first;
             nqt = sm.last - sm.first + 1;
         }
+        n = nqt * p.group;
     }
-    const int n = nqt * p.group;  // steps: every query tile of every query head of the group
 
     if (warp == kProducerWarp) {
         if (n > 0) dkdv_producer<D, MOD>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, n, wc);
@@ -768,7 +786,7 @@ __device__ void dq_mma(DqSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
 }
 
 template <int D, bool MOD>
-__device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
+__device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
                            int delta, int n, int j0, int2 span, WaitCtx wc) {
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
@@ -782,12 +800,13 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem
     int lim = row_ok ? kv_end : 0;
     if (p.causal) lim = min(lim, row + delta + 1);
     if constexpr (MOD) lim = span.y;
-    const float cmul = (MOD && p.cap_in > 0.f) ? p.cap_out : p.scale_log2;
-    const uint64_t c2 = f32x2_pack(cmul, cmul);
+    const CapOf cap(p);
+    const uint64_t c2 = f32x2_pack(cap.mul, cap.mul);
     [[maybe_unused]] const TanhPoly capped(1.f);
-    [[maybe_unused]] const uint64_t in2 = f32x2_pack(p.cap_in, p.cap_in);
+    [[maybe_unused]] const uint64_t in2 = f32x2_pack(cap.in, cap.in);
     [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
-    [[maybe_unused]] const float slope2 = (MOD && p.slopes) ? p.slopes[bh % p.Hq] * kLog2e : 0.f;
+    [[maybe_unused]] float slope2 = 0.f;
+    if constexpr (MOD) slope2 = p.slopes ? p.slopes[bh % p.Hq] * kLog2e : 0.f;
     const uint64_t nl2 = f32x2_pack(-lse2, -lse2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -810,7 +829,7 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem
         mbar_arrive(&sm.s_free);
         [[maybe_unused]] bool far = false;
         if constexpr (MOD)
-            if (p.cap_in > 0.f) far = __any_sync(kFull, abs_max(x) * p.cap_in > 1.f);
+            if (cap.in > 0.f) far = __any_sync(kFull, abs_max(x) * cap.in > 1.f);
         const int at = q0 + delta;  // position of the tile's first query
         [[maybe_unused]] const Distance<-1> dist(slope2, row + delta - key0, p.causal || key0 + 63 <= at,
                                                  key0 >= at + kT - 1);
@@ -821,7 +840,7 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem
                 uint64_t x2 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
                 [[maybe_unused]] float g0 = 1.f, g1 = 1.f;  // 1 - tanh^2
                 if constexpr (MOD) {
-                    if (p.cap_in > 0.f) {
+                    if (cap.in > 0.f) {
                         x2 = capped(f32x2_mul(x2, in2), far);
                         f32x2_unpack(f32x2_fma(f32x2_mul(x2, minus1), x2, one), g0, g1);
                     }
@@ -837,7 +856,7 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const BwdParams &p, uint32_t tmem
                 }
                 float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
                 if constexpr (MOD) {
-                    if (p.cap_in > 0.f) {
+                    if (cap.in > 0.f) {
                         p0 *= g0;
                         p1 *= g1;
                     }
@@ -908,7 +927,7 @@ template <int D, bool MOD>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const BwdParams p) {
+                  const Params<MOD> p) {
     extern __shared__ uint8_t smem_raw[];
     DqSmem<D, MOD> &sm = *reinterpret_cast<DqSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1000,7 +1019,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     if (!encode_qkv_map(&tq, a.q, BHq, a.Nq, D) || !encode_qkv_map(&tdo, a.dout, BHq, a.Nq, D) ||
         !encode_qkv_map(&tk, a.k, BHkv, a.Nkv, D) || !encode_qkv_map(&tv, a.v, BHkv, a.Nkv, D))
         return cudaErrorInvalidValue;
-    BwdParams p;
+    Params<MOD> p;
     p.lse = a.lse;
     p.dterm = a.dterm;
     p.dq = reinterpret_cast<__nv_bfloat16 *>(a.dq);
@@ -1017,12 +1036,14 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     p.causal = a.causal;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
-    p.key_begin = a.key_begin;
-    p.key_end = a.key_end;
-    p.slopes = a.slopes;
-    p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-    p.cap_out = a.softcap * kLog2e;
-    p.spans = a.spans;
+    if constexpr (MOD) {
+        p.key_begin = a.key_begin;
+        p.key_end = a.key_end;
+        p.slopes = a.slopes;
+        p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+        p.cap_out = a.softcap * kLog2e;
+        p.spans = a.spans;
+    }
 
     {
         const int row_blocks = (int)((rows * kRowThreads<D> + 255) / 256);
@@ -1042,7 +1063,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
 
     // dK/dV: one CTA per (batch, key/value head, key tile); streams Q and dO of the group's heads
     {
-        BwdParams pk = p;
+        Params<MOD> pk = p;
         pk.units_per_head = (a.Nkv + kT - 1) / kT;
         pk.heads_per_chunk = heads_per_chunk(2.0 * p.group * a.Nq * D * 2.0, BHkv);
         const size_t smem = sizeof(DkvSmem<D, MOD>) + 1024;
@@ -1055,7 +1076,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     }
     // dQ: one CTA per (batch, query head, query tile); streams K and V of its key/value head
     {
-        BwdParams pq = p;
+        Params<MOD> pq = p;
         pq.units_per_head = (a.Nq + kT - 1) / kT;
         pq.heads_per_chunk = heads_per_chunk(2.0 * a.Nkv * D * 2.0 / p.group, BHq);
         const size_t smem = sizeof(DqSmem<D, MOD>) + 1024;

@@ -32,6 +32,7 @@
 #include <mutex>
 
 #include "launch.h"
+#include "mma_sync.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -39,13 +40,8 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// Programmatic dependent launch: the chunk merge is launched while the split kernel drains.
-// Each split CTA signals once its partial is written (launch_dependents); the merge's blocks
-// wait for the split grid's completion, with its memory visible, before reading (wait).
-__device__ __forceinline__ void griddep_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The chunk merge is launched while the split kernel drains: each split CTA signals once its partial is
+// written, and the merge's blocks wait for the split grid's completion before reading.
 // Ring slots per warp: 3 page blocks for a bf16 cache and one query head per CTA (4 KB each at
 // d = 128: 96 KB per CTA, 2 CTAs per SM); 2 when the arithmetic per byte is higher -- an e4m3
 // cache (half the bytes per token; 2 KB blocks, 32 KB per CTA, 7 CTAs per SM) or several query
@@ -608,47 +604,6 @@ __global__ void __launch_bounds__(kWarps * 32) decode_split_kernel(const DecodeA
 // grows by more than 2^8).  The page blocks arrive by TMA in 128-byte-swizzled boxes of 16 rows x
 // 64 columns (the 16-byte chunk c of row r sits at chunk c ^ (r & 7)), so the eight rows of every
 // ldmatrix read fall in different banks.
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// d (+)= a b: a 16x16 bf16 (row-major fragment), b 16x8 bf16 (column-major fragment), d 16x8 fp32.
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The same product over f16 fragments.
-__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Byte permute: byte i of the result is byte (sel >> 4i) & 7 of {hi:lo}.
-__device__ __forceinline__ uint32_t prmt(uint32_t lo, uint32_t hi, uint32_t sel) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(lo), "r"(hi), "r"(sel));
-    return r;
-}
-
-// Byte offset of the 16-byte chunk holding column col (a multiple of 8) of row r in a page block
-// stored as 128-byte-swizzled boxes of 16 rows x 64 bf16 columns.
-__device__ __forceinline__ uint32_t swz_off(int r, int col) {
-    return (uint32_t)((col >> 6) * (16 * 128) + r * 128 + ((((col & 63) >> 3) ^ (r & 7)) << 4));
-}
-
 // An e4m3 cache takes the same path with f16 products.  Each page block arrives by TMA as one
 // 128-byte-swizzled box of 16 rows x 128 codes, and ldmatrix hands every lane its codes in
 // fragment order, so they are widened in registers (one conversion per two codes, exact) with no

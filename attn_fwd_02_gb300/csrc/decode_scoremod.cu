@@ -1,0 +1,39 @@
+// decode_scoremod.cu -- paged decode with modified scores: s = cap tanh(scale q.k / cap) - slope (ctx - 1 -
+// j) over the cached tokens key_begin <= j < ctx.  Splits of 64 pages; pages before key_begin are not read.
+#include "decode_rows.cuh"
+
+namespace attn {
+
+size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size) {
+    if (decode_workspace_bytes(B, H, Hkv, d, max_pages, page_size) == 0) return 0;  // unsupported sizes
+    const size_t splits = ((size_t)max_pages + kRowChunkPages - 1) / kRowChunkPages;
+    return (size_t)B * H * splits * (size_t)(d + 4) * sizeof(float);
+}
+
+cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream) {
+    RowsParams p{};
+    p.q = a.q;
+    p.page_table = a.page_table;
+    p.ctx_lens = a.ctx_lens;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.ws = static_cast<float *>(a.workspace);
+    p.status = a.status;
+    p.B = a.B;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.group = a.H / a.Hkv;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.n_splits = p.ws_splits = (a.max_pages + kRowChunkPages - 1) / kRowChunkPages;
+    const float kscale = a.scale * (a.kv_fp8 ? a.k_scale : 1.f);
+    p.c = kscale * kRowLog2e;
+    p.v_scale = a.v_scale;
+    p.cap_in = a.softcap > 0.f ? kscale / a.softcap : 0.f;
+    p.cap_out = a.softcap * kRowLog2e;
+    p.slopes = a.slopes;
+    p.key_begin = a.key_begin;
+    return launch_rows<true>(p, a.d, a.k_pages, a.v_pages, a.kv_fp8 != 0, false, stream);
+}
+
+}  // namespace attn

@@ -1,0 +1,145 @@
+// decode_shared.cu -- paged decode of a batch whose groups of sequences share their first pages.
+//
+// The shared pages are read once per (group, key/value head) instead of once per sequence: the query
+// heads of all the group's sequences are the rows of the prefill kernel's 128-row tcgen05 tiles (a form
+// without a causal mask), split along the keys so that the CTAs fill the GPU.  Each sequence's own pages
+// go through the rows kernel, which may start as the first kernel's CTAs leave, and one merge joins the
+// partial results.
+#include "decode_rows.cuh"
+#include "prefill_kernel.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kSms = 152;
+
+// How a batch is cut.  Groups of more than 128 query heads per key/value head do not fit a tile, and
+// groups of one sequence share nothing: their pages all count as the sequences' own (prefix_splits 0).
+struct SharedPlan {
+    int group, seqs_per_tile, units, prefix_splits, own_splits;
+};
+SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
+    SharedPlan pl{};
+    pl.group = H / Hkv;
+    if (S > 1 && pl.group <= 128) {
+        pl.seqs_per_tile = 128 / pl.group;
+        const int qt = d <= 64 ? Cfg<64>::QT : Cfg<128>::QT;
+        pl.units = (S + pl.seqs_per_tile * qt - 1) / (pl.seqs_per_tile * qt);
+        // splits: whole waves of CTAs; a split costs about three key tiles on top of its share
+        const long long ctas = (long long)(B / S) * Hkv * pl.units;
+        const int bn = d <= 64 ? Cfg<64>::BN : Cfg<128>::BN, per_sm = d <= 64 ? 3 : 1;
+        const int tiles = (max_pages * kPageTokens + bn - 1) / bn;
+        double best = 1e30;
+        for (int n = 1; n <= 64 && n <= tiles; ++n) {
+            const double waves = (double)((ctas * n + kSms * per_sm - 1) / (kSms * per_sm));
+            const double cost = waves * ((tiles + n - 1) / n + 3);
+            if (cost < best) {
+                best = cost;
+                pl.prefix_splits = n;
+            }
+        }
+    }
+    const int rgroups = pl.group <= 8 ? 1 : (pl.group + 15) / 16;
+    const long long rows = (long long)B * Hkv * rgroups;
+    const long long want = (2LL * kSms * 6 + rows - 1) / rows, most = (max_pages + 31) / 32;
+    pl.own_splits = (int)(want < most ? want : most);
+    return pl;
+}
+
+// Query heads [B, H, D] in boxes of 64 columns x `group` heads x `seqs` sequences.
+template <int D, int M>
+cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, cudaStream_t stream) {
+    CUtensorMap tq, tk, tv;
+    const int pool = a.num_pages * a.Hkv;
+    bool ok = encode_q_heads_map(&tq, a.q, a.B, a.H, D, pl.group, pl.seqs_per_tile);
+    if constexpr (kIsE4m3<M>)
+        ok = ok && encode_page_map_u8(&tk, a.k_pages, pool, kPageTokens, D, false) &&
+             encode_page_map_u8(&tv, a.v_pages, pool, kPageTokens, D, false);
+    else
+        ok = ok && encode_qkv_map(&tk, a.k_pages, pool, kPageTokens, D, kPageTokens) &&
+             encode_qkv_map(&tv, a.v_pages, pool, kPageTokens, D, kPageTokens);
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t e = check_register_split<D, M>();
+    if (e != cudaSuccess) return e;
+    PrefillSharedParams p{};
+    p.status = a.status;
+    p.B = a.B;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.group = pl.group;
+    p.Nkv = a.max_pages * kPageTokens + 1;  // every page is a tile's own rows: a ragged end is always cleared
+    p.n_units = pl.units;
+    p.heads_per_chunk = a.B * a.H;
+    p.page_table = a.page_table;
+    p.ctx_lens = a.ctx_lens;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.scale_log2 = a.scale * kLog2e * (kIsE4m3<M> ? a.k_scale : 1.f);
+    p.o_scale = kIsE4m3<M> ? a.v_scale : 1.f;
+    p.shared_pages = a.shared_pages;
+    p.S = a.group_size;
+    p.seqs_per_tile = pl.seqs_per_tile;
+    p.n_splits = pl.prefix_splits;
+    p.ws_splits = pl.prefix_splits + pl.own_splits;
+    p.ws = static_cast<float *>(a.workspace);
+    const size_t smem = sizeof(PrefillSmem<D, M>) + 1024;
+    e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(prefill_kernel<D, M>), (int)smem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((size_t)(a.B / a.group_size) * a.Hkv * pl.units * pl.prefix_splits);
+    prefill_kernel<D, M><<<grid, Occ<D, M>::kThreads, smem, stream>>>(tq, tk, tv, tq, p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_shared_prefix_d(const DecodeArgs &a, const SharedPlan &pl, cudaStream_t stream) {
+    return a.kv_fp8 ? launch_shared_prefix<D, kSharedE4m3>(a, pl, stream)
+                    : launch_shared_prefix<D, kSharedBf16>(a, pl, stream);
+}
+
+}  // namespace
+
+size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int S, int page_size) {
+    if (S <= 0 || B % S != 0 || decode_workspace_bytes(B, H, Hkv, d, max_pages, page_size) == 0) return 0;
+    const SharedPlan pl = shared_plan(B, H, Hkv, d, max_pages, S);
+    return (size_t)B * H * (pl.prefix_splits + pl.own_splits) * (size_t)(d + 4) * sizeof(float);
+}
+
+cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream) {
+    const SharedPlan pl = shared_plan(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size);
+    if (pl.prefix_splits > 0) {
+        cudaError_t e;
+        switch (a.d) {
+            case 32: e = launch_shared_prefix_d<32>(a, pl, stream); break;
+            case 64: e = launch_shared_prefix_d<64>(a, pl, stream); break;
+            case 80: e = launch_shared_prefix_d<80>(a, pl, stream); break;
+            case 96: e = launch_shared_prefix_d<96>(a, pl, stream); break;
+            case 128: e = launch_shared_prefix_d<128>(a, pl, stream); break;
+            default: e = cudaErrorInvalidValue;
+        }
+        if (e != cudaSuccess) return e;
+    }
+    RowsParams p{};
+    p.q = a.q;
+    p.page_table = a.page_table;
+    p.ctx_lens = a.ctx_lens;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.ws = static_cast<float *>(a.workspace);
+    p.status = a.status;
+    p.B = a.B;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.group = pl.group;
+    p.max_pages = a.max_pages;
+    p.num_pages = a.num_pages;
+    p.n_splits = pl.own_splits;
+    p.ws_first = pl.prefix_splits;
+    p.ws_splits = pl.prefix_splits + pl.own_splits;
+    p.c = a.scale * kRowLog2e * (a.kv_fp8 ? a.k_scale : 1.f);
+    p.v_scale = a.v_scale;
+    p.shared_pages = a.shared_pages;
+    p.S = pl.prefix_splits > 0 ? a.group_size : 0;
+    return launch_rows<false>(p, a.d, a.k_pages, a.v_pages, a.kv_fp8 != 0, pl.prefix_splits > 0, stream);
+}
+
+}  // namespace attn

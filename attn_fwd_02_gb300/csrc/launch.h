@@ -45,6 +45,13 @@ struct DecodeArgs {
     // e4m3 cache: pages hold FP8 codes, value = e4m3(code) * k_scale (keys) or * v_scale (values)
     int kv_fp8 = 0;
     float k_scale = 1.f, v_scale = 1.f;
+    // launch_decode_shared: groups of group_size sequences share their first shared_pages[b / group_size] pages
+    const int32_t *shared_pages = nullptr;
+    int group_size = 0;
+    // launch_decode_scoremod: cap (0: none), slopes [H], first visible token [B] (null: none)
+    float softcap = 0.f;
+    const float *slopes = nullptr;
+    const int32_t *key_begin = nullptr;
 };
 
 struct BwdArgs {
@@ -75,6 +82,9 @@ bool encode_qkv_map(CUtensorMap *m, const void *ptr, int BH, int N, int D, int b
 // [rows, page_rows, D] one-byte (e4m3) page blocks, one box of page_rows x 128 bytes per block,
 // with the 128-byte swizzle or none; the bytes of a box past D are read as zeros.
 bool encode_page_map_u8(CUtensorMap *m, const void *ptr, int rows, int page_rows, int D, bool swizzle = true);
+
+// Query heads of a decode batch, [B, H, D] bf16, in swizzled boxes of 64 columns x heads x seqs rows.
+bool encode_q_heads_map(CUtensorMap *m, const void *ptr, int B, int H, int D, int heads, int seqs);
 
 // Encodes the TMA descriptors and launches the prefill kernel.
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
@@ -122,6 +132,12 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 // Workspace bytes the decode needs for H query heads over Hkv cache heads (0 if the sizes are
 // unsupported).
 size_t decode_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
+
+// Decode with modified scores, and decode of a batch whose groups share their first pages.
+cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream);
+size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
+cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream);
+size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int S, int page_size);
 
 // Same kernels with the chunk partials in the library's static scratch array
 // (no workspace from the caller); see decode.cu.

@@ -1,7 +1,7 @@
 // prefill_kernel.cuh -- FlashAttention-style prefill forward on the sm_103a tensor cores.  The forms of
 // the kernel (KvMode) are instantiated by the translation units that include this file: prefill.cu
-// (contiguous K/V and the chunked prefill over pages) and prefill_scoremod.cu (modified scores and
-// per-query key intervals).
+// (contiguous K/V and the chunked prefill over pages), prefill_scoremod.cu (modified scores and per-query
+// key intervals) and decode_shared.cu (the shared pages of a decode batch).
 //
 // The method (NanoInfer README, Flash Attention bullets; gpu-inference blog,
 // section 02; llm-kernel-lib README, kernel 1; Kernel-Inference-Engine README,
@@ -106,13 +106,16 @@ constexpr int kPageTokens = 16;            // tokens per page of the paged KV ca
 // Where K/V come from (a compile-time parameter of the kernel, so that each form carries only
 // its own code): contiguous [B, Hkv, Nkv, d] tensors; bf16 pages of a paged KV cache; e4m3 pages,
 // widened to f16 in shared memory before the products; or contiguous tensors with modified scores (a
-// tanh cap, a distance bias) and an interval of visible keys per query (kContigMod).
-enum KvMode : int { kContig = 0, kPagedBf16 = 1, kPagedE4m3 = 2, kContigMod = 3 };
-template <int M> constexpr bool kIsPaged = (M == kPagedBf16 || M == kPagedE4m3);
-template <int M> constexpr bool kIsE4m3 = (M == kPagedE4m3);
+// tanh cap, a distance bias) and an interval of visible keys per query (kContigMod); or the pages that a
+// group of sequences shares in a decode step, split along the keys, with the group's query heads of one
+// key/value head as the rows and unnormalised partial results (kSharedBf16, kSharedE4m3).
+enum KvMode : int { kContig = 0, kPagedBf16 = 1, kPagedE4m3 = 2, kContigMod = 3, kSharedBf16 = 4, kSharedE4m3 = 5 };
+template <int M> constexpr bool kIsShared = (M == kSharedBf16 || M == kSharedE4m3);
+template <int M> constexpr bool kIsPaged = (M == kPagedBf16 || M == kPagedE4m3 || kIsShared<M>);
+template <int M> constexpr bool kIsE4m3 = (M == kPagedE4m3 || M == kSharedE4m3);
 template <int M> constexpr bool kIsMod = (M == kContigMod);
 // Forms whose tiles start at the first key that a row of the CTA sees, with rows limited to intervals.
-template <int M> constexpr bool kHasSpan = kIsMod<M>;
+template <int M> constexpr bool kHasSpan = (kIsMod<M> || kIsShared<M>);
 
 // CTAs per SM and the register split per KV mode.  e4m3 pages at d <= 64: the two converter warps
 // (the non-softmax warpgroup's idle pair) need more than the 32 registers that four CTAs per SM
@@ -143,6 +146,7 @@ template <> struct Occ<32, kPagedE4m3> {
     static constexpr uint32_t kRegsSoftmax = 2 * kLaunch - kRegsOther;
 };
 template <> struct Occ<64, kPagedE4m3> : Occ<32, kPagedE4m3> {};
+template <int D> struct Occ<D, kSharedE4m3> : Occ<D, kPagedE4m3> {};
 static_assert(128 * (Occ<64, kPagedE4m3>::kRegsSoftmax + Occ<64, kPagedE4m3>::kRegsOther) <=
                   256 * Occ<64, kPagedE4m3>::kLaunch,
               "e4m3 d<=64 register split");
@@ -164,13 +168,31 @@ struct PrefillParams {
     int heads_per_chunk;                 // heads whose K/V share L2 at a time (see the CTA order)
     float scale_log2;                    // scale * log2(e) (times the key scale of e4m3 pages)
     float o_scale;                       // multiplies O in the epilogue (the value scale of e4m3 pages)
-    // kContigMod: keys key_begin[b, i] <= j < key_end[b, i] are visible to query i (null: no limit);
+};
+// kContigMod: a type of its own, so that the other forms' parameters stay as they are (their registers
+// depend on them).
+struct PrefillModParams : PrefillParams {
+    // keys key_begin[b, i] <= j < key_end[b, i] are visible to query i (null: no limit);
     // score = cap tanh(scale q.k / cap) - slope[h] |distance| (cap_in = scale / cap, 0: no cap;
     // cap_out = cap * log2(e); slopes null: no bias)
     const int32_t *key_begin, *key_end;
     const float *slopes;
     float cap_in, cap_out;
 };
+
+// kSharedBf16, kSharedE4m3: the batch is groups of S consecutive sequences; the rows of a 128-row tile are
+// seqs_per_tile sequences times the `group` query heads of one key/value head.  Split `split` of n_splits
+// takes its share of the key tiles and writes {O (unnormalised), m, l} per row to ws.
+struct PrefillSharedParams : PrefillParams {
+    const int32_t *shared_pages;  // [B / S]
+    int S, seqs_per_tile, n_splits, ws_splits;
+    float *ws;                    // [B, H, ws_splits, d + 4], the first n_splits of each row
+};
+template <int M> struct ParamsOf { using type = PrefillParams; };
+template <> struct ParamsOf<kSharedBf16> { using type = PrefillSharedParams; };
+template <> struct ParamsOf<kSharedE4m3> { using type = PrefillSharedParams; };
+template <> struct ParamsOf<kContigMod> { using type = PrefillModParams; };
+template <int M> using Params = typename ParamsOf<M>::type;
 
 // The key tiles of a CTA's query tiles in the forms with intervals: tiles j0 + begin[t] ..
 // j0 + n[t] - 1 of query tile t (counted from j0, the CTA's first).
@@ -278,27 +300,38 @@ __device__ int producer_start(PrefillSmem<D, M> &sm, const PrefillParams &p, con
 }
 
 template <int D, int M>
-__device__ void run_producer(PrefillSmem<D, M> &sm, const PrefillParams &p, const CUtensorMap *tmQ,
+__device__ void run_producer(PrefillSmem<D, M> &sm, const Params<M> &p, const CUtensorMap *tmQ,
                              const CUtensorMap *tmK, const CUtensorMap *tmV, int b, int bh, int bh_kv, int q0,
-                             int n_all, int u_begin, int j0, WaitCtx wc) {
+                             int n_all, int u_begin, int j0, int kv_end, WaitCtx wc) {
     constexpr int kBoxes = kPad<D> / 64;
     if (u_begin == 0) {  // Q not yet issued (paged modes)
         prefetch_tensormap(tmQ);
         prefetch_tensormap(tmK);
         prefetch_tensormap(tmV);
-        mbar_arrive_expect_tx(&sm.q_full, Cfg<D>::QT * kBoxes * kBoxBytes);
+        if constexpr (kIsShared<M>) {
+            // q0: the unit's first sequence of the group; a tile is one box of seqs_per_tile x group rows
+            const int tiles = q0 + p.seqs_per_tile < p.S ? Cfg<D>::QT : 1;
+            mbar_arrive_expect_tx(&sm.q_full, tiles * kBoxes * p.seqs_per_tile * p.group * 128);
+            for (int t = 0; t < tiles; ++t)
 #pragma unroll
-        for (int t = 0; t < Cfg<D>::QT; ++t)
+                for (int i = 0; i < kBoxes; ++i)
+                    tma_load_3d(sm.q[t] + i * (kBM * 64), tmQ, &sm.q_full, i * 64, bh_kv % p.Hkv * p.group,
+                                b + q0 + t * p.seqs_per_tile);
+        } else {
+            mbar_arrive_expect_tx(&sm.q_full, Cfg<D>::QT * kBoxes * kBoxBytes);
 #pragma unroll
-            for (int i = 0; i < kBoxes; ++i)
-                tma_load_3d(sm.q[t] + i * (kBM * 64), tmQ, &sm.q_full, i * 64, q0 + t * kBM, bh);
+            for (int t = 0; t < Cfg<D>::QT; ++t)
+#pragma unroll
+                for (int i = 0; i < kBoxes; ++i)
+                    tma_load_3d(sm.q[t] + i * (kBM * 64), tmQ, &sm.q_full, i * 64, q0 + t * kBM, bh);
+        }
     }
     // paged modes: the page ids of each tile (-1 past the sequence's last page), fetched one
     // ring unit ahead of their use, so the global loads stay in flight across the ring wait
     constexpr int kBN = kBNd<D>;
     constexpr int kTilePages = kBN / kPageTokens;
     const int kvh = bh_kv % p.Hkv;
-    const int pages_used = kIsPaged<M> ? (kv_end_of(p, b) + kPageTokens - 1) / kPageTokens : 0;
+    const int pages_used = kIsPaged<M> ? (kv_end + kPageTokens - 1) / kPageTokens : 0;
     auto fetch_ids = [&](int tile, int (&ids)[kTilePages]) {
 #pragma unroll
         for (int pg = 0; pg < kTilePages; ++pg) {
@@ -309,7 +342,7 @@ __device__ void run_producer(PrefillSmem<D, M> &sm, const PrefillParams &p, cons
     int ids_prev[kTilePages], ids_cur[kTilePages], ids_next[kTilePages];
 #pragma unroll
     for (int pg = 0; pg < kTilePages; ++pg) ids_prev[pg] = ids_cur[pg] = ids_next[pg] = -1;
-    if constexpr (kIsPaged<M>) fetch_ids(0, ids_next);
+    if constexpr (kIsPaged<M>) fetch_ids(j0, ids_next);
 
     // K/V by TMA into the ring slots.  Paged: pool row (page * Hkv + head) of each page of a tile;
     // pages past the sequence's last page, or with an id outside the pool (an unmapped page, whose
@@ -361,7 +394,7 @@ __device__ void run_producer(PrefillSmem<D, M> &sm, const PrefillParams &p, cons
                 ids_prev[pg] = ids_cur[pg];
                 ids_cur[pg] = ids_next[pg];
             }
-            if (u + 1 < n_all) fetch_ids(u + 1, ids_next);
+            if (u + 1 < n_all) fetch_ids(j0 + u + 1, ids_next);
             if (has_k) load_tile(sm.k[slot], tmK, full, ids_cur);
             if (has_v) load_tile(sm.v[slot], tmV, full, ids_prev);
         }
@@ -420,8 +453,8 @@ template <int D> constexpr int kConverters = Occ<D, kPagedE4m3>::kThreads - (Cfg
 // the async proxy and arrive (one lane per warp) on the unit's V barrier; then K(u) and the unit's
 // full barrier.  Each completes when every converter warp has arrived (unit 0 has no V and the
 // last unit no K: the arrivals keep the barriers' phases in step).
-template <int D>
-__device__ void run_convert(PrefillSmem<D, kPagedE4m3> &sm, int n_all, int ct, WaitCtx wc) {
+template <int D, int M>
+__device__ void run_convert(PrefillSmem<D, M> &sm, int n_all, int ct, WaitCtx wc) {
     constexpr int kCW = kConverters<D> / 32;
     const int cw = ct >> 5, lane = ct & 31;
     for (int u = 0; u <= n_all; ++u) {
@@ -662,7 +695,7 @@ struct ScoreMod {
     float c = 0.f, cin = 0.f, cout = 0.f, slope2 = 0.f;
     int pos = 0;  // the row's position among the keys
 
-    __device__ __forceinline__ void init(const PrefillParams &p, int h, int pos_) {
+    __device__ __forceinline__ void init(const PrefillModParams &p, int h, int pos_) {
         cap = p.cap_in > 0.f;
         bias = p.slopes != nullptr;
         c = p.scale_log2;
@@ -730,7 +763,7 @@ struct ScoreMod {
 };
 
 template <int D, int M>
-__device__ void run_softmax(PrefillSmem<D, M> &sm, const PrefillParams &p, const CUtensorMap *tmO, uint32_t tmem,
+__device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUtensorMap *tmO, uint32_t tmem,
                             int t, int bh, int q0, int n_tiles, int n_all, int kv_end, int delta, int j0, int begin,
                             RowSpan span, WaitCtx wc) {
     const int r = threadIdx.x & 127;  // query row in the tile = TMEM lane
@@ -777,12 +810,12 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const PrefillParams &p, const
         return (lane < kBN / kPageTokens && lp < pages_used) ? table[lp] : 0;
     };
     int next_id = 0;
-    if constexpr (kPaged) next_id = table_entry(0);
+    if constexpr (kPaged) next_id = table_entry(j0 + begin);
     for (int j = begin; j < n_tiles; ++j) {
         uint32_t unmapped = 0;
         if constexpr (kPaged) {
             const int id = next_id;
-            if (j + 1 < n_tiles) next_id = table_entry(j + 1);
+            if (j + 1 < n_tiles) next_id = table_entry(j0 + j + 1);
             unmapped = __ballot_sync(0xffffffffu, id < 0 || id >= p.num_pages);
         }
         // every decision that guards a .sync.aligned tcgen05 instruction is warp-uniform
@@ -861,7 +894,7 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const PrefillParams &p, const
             // until the product that this warpgroup's P starts.
             if (key0 + kBN > kv_end && kv_end < p.Nkv) {
                 const int u = j + 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm.u_full[u % kStagesOf<D>],
+                if (!__all_sync(0xffffffffu, mbar_wait(kIsE4m3<M> ? &sm.v_full[u % kStagesOf<D>] : &sm.u_full[u % kStagesOf<D>],
                                                        (uint32_t)((u / kStagesOf<D>) & 1), wc, 26 + t))) {
                     ok = false;
                     break;
@@ -887,6 +920,30 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const PrefillParams &p, const
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, wc, 24))) ok = false;
     }
     if (!ok) return;
+    if constexpr (kIsShared<M>) {
+        // partial result of this row: O (times the value scale), the reference max and l
+        const int sub = r / p.group;  // sequence of the tile
+        const int s = q0 + t * p.seqs_per_tile + sub;
+        const bool mine = sub < p.seqs_per_tile && s < p.S;
+        const size_t head = (size_t)bh + (size_t)(mine ? s : 0) * p.H + r % p.group;  // bh: first sequence, first head
+        float *w = p.ws + (head * p.ws_splits + blockIdx.x % p.n_splits) * (D + 4);
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t ov[16];
+            if (n_tiles > begin) {
+                tmem_ld16(tO + cc * 16, ov);
+                tmem_wait_ld16(ov);
+                if (mine)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4 *>(w + cc * 16 + i) =
+                            make_float4(__uint_as_float(ov[i]) * p.o_scale, __uint_as_float(ov[i + 1]) * p.o_scale,
+                                        __uint_as_float(ov[i + 2]) * p.o_scale, __uint_as_float(ov[i + 3]) * p.o_scale);
+            }
+        }
+        if (mine) *reinterpret_cast<float2 *>(w + D) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
+        return;
+    }
     const bool have = (n_tiles > 0) && (l > 0.f);
     const float inv_l = have ? (kIsE4m3<M> ? p.o_scale : 1.f) / l : 0.f;
     uint8_t *stage = reinterpret_cast<uint8_t *>(sm.q[t]) + r * 128;
@@ -942,7 +999,7 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const PrefillParams &p, const
 }
 
 // Keys that query `row` of sequence b sees (none past the last query).
-__device__ __forceinline__ RowSpan row_span(const PrefillParams &p, int b, int row, int kv_end, int delta) {
+__device__ __forceinline__ RowSpan row_span(const PrefillModParams &p, int b, int row, int kv_end, int delta) {
     RowSpan s;
     if (row >= p.Nq) return s;
     const size_t at = (size_t)b * p.Nq + row;
@@ -956,7 +1013,7 @@ template <int D, int M>
 __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks))
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                   const PrefillParams p) {
+                   const Params<M> p) {
     extern __shared__ uint8_t smem_raw[];
     PrefillSmem<D, M> &sm =
         *reinterpret_cast<PrefillSmem<D, M> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -967,22 +1024,37 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
     // all its heads (the last query rows, which see the most keys under the causal mask).
     // The hardware dispatches CTAs in index order, so this is a longest-first schedule per
     // chunk: no heavy unit is left to start at the end of the launch.
-    const int BH = p.B * p.H;
-    const int per_chunk = p.heads_per_chunk * p.n_units;
-    const int chunk = (int)(blockIdx.x / per_chunk);
-    const int h0 = chunk * p.heads_per_chunk;
-    const int heads = min(p.heads_per_chunk, BH - h0);  // the last chunk may be smaller
-    const int in_chunk = (int)(blockIdx.x % per_chunk);
-    const int level = in_chunk / heads;  // 0 = heaviest unit of a head
-    const int bh = h0 + in_chunk % heads;
-    const int unit = p.n_units - 1 - level;
-    // key/value head of this query head (grouped-query attention; = bh for multi-head)
-    const int bh_kv = (bh / p.H) * p.Hkv + (bh % p.H) / p.group;
-    const int b = bh / p.H;
-    const int q0 = unit * (kBM * Cfg<D>::QT);
+    int bh, bh_kv, b, q0;
+    if constexpr (kIsShared<M>) {
+        // CTA = (group and key/value head, unit of sequences, split), splits innermost.  The kernel that
+        // takes the sequences' own pages may start as these CTAs leave room.
+        griddep_launch_dependents();
+        const int rest = (int)(blockIdx.x / p.n_splits);
+        bh_kv = rest / p.n_units;  // group * Hkv + key/value head
+        b = bh_kv / p.Hkv * p.S;   // the group's first sequence: its page table, its rows
+        bh = b * p.H + bh_kv % p.Hkv * p.group;
+        q0 = rest % p.n_units * (Cfg<D>::QT * p.seqs_per_tile);
+    } else {
+        const int BH = p.B * p.H;
+        const int per_chunk = p.heads_per_chunk * p.n_units;
+        const int chunk = (int)(blockIdx.x / per_chunk);
+        const int h0 = chunk * p.heads_per_chunk;
+        const int heads = min(p.heads_per_chunk, BH - h0);  // the last chunk may be smaller
+        const int in_chunk = (int)(blockIdx.x % per_chunk);
+        const int level = in_chunk / heads;  // 0 = heaviest unit of a head
+        bh = h0 + in_chunk % heads;
+        const int unit = p.n_units - 1 - level;
+        // key/value head of this query head (grouped-query attention; = bh for multi-head)
+        bh_kv = (bh / p.H) * p.Hkv + (bh % p.H) / p.group;
+        b = bh / p.H;
+        q0 = unit * (kBM * Cfg<D>::QT);
+    }
     // keys of this sequence and the causal offset (query i sits at key position i + delta)
     int kv_end, delta;
-    if constexpr (kIsPaged<M>) {
+    if constexpr (kIsShared<M>) {
+        kv_end = min(max(p.shared_pages[bh_kv / p.Hkv], 0), p.max_pages) * kPageTokens;
+        delta = 0;
+    } else if constexpr (kIsPaged<M>) {
         kv_end = kv_end_of(p, b);
         delta = kv_end - p.Nq;
     } else {
@@ -996,7 +1068,13 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
     if constexpr (kHasSpan<M>) {
         // this softmax thread's interval of keys, and the union over its warp
         if (warp < 4 * Cfg<D>::QT) {
-            rs = row_span(p, b, q0 + (int)threadIdx.x, kv_end, delta);
+            if constexpr (kIsShared<M>) {
+                const int row = (int)threadIdx.x & 127, sub = row / p.group;
+                const int s = q0 + (warp >> 2) * p.seqs_per_tile + sub;
+                if (sub < p.seqs_per_tile && s < p.S) rs.hi = min(max(p.ctx_lens[b + s], 0), kv_end);
+            } else {
+                rs = row_span(p, b, q0 + (int)threadIdx.x, kv_end, delta);
+            }
             const int lo = __reduce_min_sync(0xffffffffu, rs.lo < rs.hi ? rs.lo : 0x7fffffff);
             const int hi = __reduce_max_sync(0xffffffffu, rs.lo < rs.hi ? rs.hi : 0);
             if (lane == 0) {
@@ -1062,6 +1140,24 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
             span.j0 = min(span.j0, first[t]);
         }
         if (span.j0 == 0x7fffffff) span.j0 = 0;
+        if constexpr (kIsShared<M>) {
+            // the keys that some row sees, and this split's share of their tiles
+            kv_end = 0;
+#pragma unroll
+            for (int t = 0; t < Cfg<D>::QT; ++t)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) kv_end = max(kv_end, sm.hi[4 * t + w]);
+            const int tiles = (kv_end + kBNd<D> - 1) / kBNd<D>;
+            const int split = (int)(blockIdx.x % p.n_splits);
+            span.j0 = (int)((long long)tiles * split / p.n_splits);
+            const int end = (int)((long long)tiles * (split + 1) / p.n_splits);
+#pragma unroll
+            for (int t = 0; t < Cfg<D>::QT; ++t) {
+                first[t] = span.j0;
+                last[t] = min(last[t], end);
+                if (last[t] <= first[t]) last[t] = 0;
+            }
+        }
 #pragma unroll
         for (int t = 0; t < Cfg<D>::QT; ++t) {
             span.begin[t] = last[t] > 0 ? first[t] - span.j0 : 0;
@@ -1074,12 +1170,12 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
         if constexpr (Cfg<D>::kSplitRegs) setmaxnreg_dec<Occ<D, M>::kRegsOther>();
         if (warp == Cfg<D>::kProducerWarp) {
             if (lane == 0 && n_all > 0)
-                run_producer<D, M>(sm, p, &tmQ, &tmK, &tmV, b, bh, bh_kv, q0, n_all, u_begin, span.j0, wc);
+                run_producer<D, M>(sm, p, &tmQ, &tmK, &tmV, b, bh, bh_kv, q0, n_all, u_begin, span.j0, kv_end, wc);
         } else if (warp == Cfg<D>::kMmaWarp) {
             if (lane == 0 && n_all > 0) run_mma<D, M>(sm, tmem, n, span.begin, n_all, wc);
         } else if constexpr (kIsE4m3<M>) {
             // the warps after the MMA issuer's convert e4m3 tiles into the ring
-            if (n_all > 0) run_convert<D>(sm, n_all, (int)threadIdx.x - (Cfg<D>::kMmaWarp + 1) * 32, wc);
+            if (n_all > 0) run_convert<D, M>(sm, n_all, (int)threadIdx.x - (Cfg<D>::kMmaWarp + 1) * 32, wc);
         }
     } else {
         if constexpr (Cfg<D>::kSplitRegs) setmaxnreg_inc<Occ<D, M>::kRegsSoftmax>();
@@ -1130,7 +1226,7 @@ cudaError_t launch_prefill_dm(const PrefillArgs &a, cudaStream_t stream) {
     if (!ok_maps) return cudaErrorInvalidValue;
     cudaError_t e = check_register_split<D, M>();
     if (e != cudaSuccess) return e;
-    PrefillParams p;
+    Params<M> p;
     p.o = reinterpret_cast<__nv_bfloat16 *>(a.o);
     p.lse = a.lse;
     p.kv_lens = a.kv_lens;
@@ -1146,11 +1242,13 @@ cudaError_t launch_prefill_dm(const PrefillArgs &a, cudaStream_t stream) {
     p.ctx_lens = a.ctx_lens;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
-    p.key_begin = a.key_begin;
-    p.key_end = a.key_end;
-    p.slopes = a.slopes;
-    p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-    p.cap_out = a.softcap * kLog2e;
+    if constexpr (kIsMod<M>) {
+        p.key_begin = a.key_begin;
+        p.key_end = a.key_end;
+        p.slopes = a.slopes;
+        p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+        p.cap_out = a.softcap * kLog2e;
+    }
     p.k8 = static_cast<const uint8_t *>(a.k);
     p.v8 = static_cast<const uint8_t *>(a.v);
     p.n_units = (a.Nq + kBM * Cfg<D>::QT - 1) / (kBM * Cfg<D>::QT);

@@ -205,6 +205,63 @@ int paged_attn_decode_gqa(const void *q, const void *k_pages, const void *v_page
                           attn_stream_t stream);
 
 /*
+ * Paged decode with modified scores (paged_attn_decode_gqa with the modification of attn_fwd_scoremod for
+ * one query at position ctx_lens[b] - 1):
+ *     s_j = cap tanh(scale <q, k_j> / cap) - slope[h] (ctx_lens[b] - 1 - j)      (softcap cap > 0)
+ *     s_j = scale <q, k_j> - slope[h] (ctx_lens[b] - 1 - j)                      (softcap 0)
+ * over the cached tokens key_begin[b] <= j < ctx_lens[b].
+ *   softcap 0, or finite and positive; alibi_slopes [H] fp32 or NULL; key_begin [B] int32 (clamped) or NULL
+ *   workspace: at least paged_attn_decode_scoremod_workspace_size(...) bytes, 16-byte aligned
+ * Pages wholly before key_begin are not read, and slots of the first page before it may hold anything.
+ * A sequence that sees no token gets O = 0 and LSE = -inf.  Other arguments as paged_attn_decode_gqa;
+ * _fp8: over an e4m3 cache, as paged_attn_decode_fp8.
+ */
+size_t paged_attn_decode_scoremod_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq,
+                                                 int page_size);
+
+int paged_attn_decode_scoremod(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o,
+                               float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages,
+                               float scale, float softcap, const float *alibi_slopes, const int32_t *key_begin,
+                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+int paged_attn_decode_scoremod_fp8(const void *q, const void *k_pages, const void *v_pages, float k_scale,
+                                   float v_scale, const int32_t *page_table, const int32_t *ctx_lens,
+                                   int page_size, void *o, float *lse, int B, int H, int Hkv, int d,
+                                   int max_pages_per_seq, int num_pages, float scale, float softcap,
+                                   const float *alibi_slopes, const int32_t *key_begin, void *workspace,
+                                   size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * Paged decode of a batch whose groups of sequences share their first pages (samples of one prompt, users
+ * behind one system prompt or document): paged_attn_decode_gqa, with the shared pages read once per group.
+ *   group_size    the batch is B / group_size groups of consecutive sequences (B % group_size == 0); pad a
+ *                 shorter group with sequences of ctx_lens 0
+ *   shared_pages  [B / group_size] int32 (device, clamped to [0, max_pages_per_seq]): the first
+ *                 shared_pages[g] entries of page_table are the same for every sequence of group g, and
+ *                 are read from the row of its FIRST sequence (b = g * group_size); those entries of its
+ *                 other rows are not read
+ * Sequence b still attends to its first ctx_lens[b] tokens, which may end inside the shared pages.  The
+ * later pages of each sequence are its own.  Unmapped ids, empty sequences, o and lse as in
+ * paged_attn_decode_gqa.  workspace: at least paged_attn_decode_shared_workspace_size(...) bytes, 16-byte
+ * aligned.  _fp8: over an e4m3 cache, as paged_attn_decode_fp8.
+ */
+size_t paged_attn_decode_shared_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq,
+                                               int group_size, int page_size);
+
+int paged_attn_decode_shared(const void *q, const void *k_pages, const void *v_pages,
+                             const int32_t *page_table, const int32_t *ctx_lens, const int32_t *shared_pages,
+                             int group_size, int page_size, void *o, float *lse, int B, int H, int Hkv, int d,
+                             int max_pages_per_seq, int num_pages, float scale, void *workspace,
+                             size_t workspace_bytes, attn_stream_t stream);
+
+int paged_attn_decode_shared_fp8(const void *q, const void *k_pages, const void *v_pages, float k_scale,
+                                 float v_scale, const int32_t *page_table, const int32_t *ctx_lens,
+                                 const int32_t *shared_pages, int group_size, int page_size, void *o, float *lse,
+                                 int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale,
+                                 void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
  * Chunked prefill over the paged KV cache (a prefill step writing into, then
  * attending over, a KV cache kept in pages: inference-kernel-cookbook README,
  * recipes 02 and 03).  Sequence b holds ctx_lens[b] tokens (device int32 [B],
