@@ -232,9 +232,14 @@ ATTN_API int attn_fwd(const void *q, const void *k, const void *v, void *o, floa
 }
 
 namespace {
-// The score modification's arguments: softcap 0 (none) or finite and positive, 4-byte aligned arrays.
-int scoremod_checks(float softcap, const float *alibi_slopes, const int32_t *key_begin, const int32_t *key_end) {
-    if (!(softcap >= 0.f) || !(softcap < 3.0e38f)) return ATTN_ERR_INVALID_ARG;
+// The score modification's arguments: softcap 0 (none), or positive with factors that fp32 holds (cap and
+// score factor / cap at most 2^100; `factor` is the scale, times the key scale of an e4m3 cache); 4-byte
+// aligned arrays.
+int scoremod_checks(float factor, float softcap, const float *alibi_slopes, const int32_t *key_begin,
+                    const int32_t *key_end) {
+    constexpr float kMost = 1.2676506e30f;  // 2^100
+    if (!(softcap >= 0.f) || !(softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
+    if (softcap > 0.f && !(factor / softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
     if (!aligned4(alibi_slopes) || !aligned4(key_begin) || !aligned4(key_end)) return ATTN_ERR_MISALIGNED;
     return ATTN_OK;
 }
@@ -245,7 +250,7 @@ ATTN_API int attn_fwd_scoremod(const void *q, const void *k, const void *v, void
                                const float *alibi_slopes, const int32_t *key_begin, const int32_t *key_end,
                                const int32_t *kv_lens, attn_stream_t stream) {
     int st = prefill_checks(q, k, v, o, lse, B, Hq, Hkv, Nq, Nkv, d, causal, scale, kv_lens);
-    if (st == ATTN_OK) st = scoremod_checks(softcap, alibi_slopes, key_begin, key_end);
+    if (st == ATTN_OK) st = scoremod_checks(scale, softcap, alibi_slopes, key_begin, key_end);
     if (st != ATTN_OK) return st;
     int *status = nullptr;
     st = device_setup(&status);
@@ -478,7 +483,7 @@ ATTN_API int attn_bwd_scoremod(const void *q, const void *k, const void *v, cons
                                void *workspace, size_t workspace_bytes, attn_stream_t stream) {
     if (!o || !lse || !dout || !dk || !dv) return ATTN_ERR_INVALID_ARG;
     int st = prefill_checks(q, k, v, dq, nullptr, B, Hq, Hkv, Nq, Nkv, d, causal, scale, kv_lens);
-    if (st == ATTN_OK) st = scoremod_checks(softcap, alibi_slopes, key_begin, key_end);
+    if (st == ATTN_OK) st = scoremod_checks(scale, softcap, alibi_slopes, key_begin, key_end);
     if (st != ATTN_OK) return st;
     const uint64_t kv_ctas = ((uint64_t)Nkv + 127) / 128 * (uint64_t)B * (uint64_t)Hkv;
     if (kv_ctas > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
@@ -602,9 +607,10 @@ namespace {
 int decode_scoremod(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stream) {
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
-    if (st == ATTN_OK) st = scoremod_checks(a.softcap, a.slopes, a.key_begin, nullptr);
     if (st != ATTN_OK) return st;
     if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
+    st = scoremod_checks(a.scale * a.k_scale, a.softcap, a.slopes, a.key_begin, nullptr);
+    if (st != ATTN_OK) return st;
     const size_t need = attn::decode_scoremod_workspace_bytes(a.B, a.H, a.Hkv, a.d, a.max_pages, a.page_size);
     if (!a.workspace || !aligned16(a.workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     st = device_setup(&a.status);

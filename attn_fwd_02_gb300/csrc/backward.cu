@@ -5,11 +5,11 @@ namespace attn {
 
 cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t stream) {
     switch (a.d) {
-        case 32: return launch_bwd_d<32, false>(a, stream);
-        case 64: return launch_bwd_d<64, false>(a, stream);
-        case 80: return launch_bwd_d<80, false>(a, stream);
-        case 96: return launch_bwd_d<96, false>(a, stream);
-        case 128: return launch_bwd_d<128, false>(a, stream);
+        case 32: return launch_bwd_d<32, kPlain>(a, stream);
+        case 64: return launch_bwd_d<64, kPlain>(a, stream);
+        case 80: return launch_bwd_d<80, kPlain>(a, stream);
+        case 96: return launch_bwd_d<96, kPlain>(a, stream);
+        case 128: return launch_bwd_d<128, kPlain>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }

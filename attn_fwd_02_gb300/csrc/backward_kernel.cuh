@@ -22,8 +22,8 @@
 //     TMEM: S^T 128 | dP^T 128 | dV d | dK d columns.
 //   * dQ: S = Q K^T and dP = dO V^T with lane = query; dS (bf16) over dP feeds dQ += dS K.
 //     TMEM: S 128 | dP 128 | dQ d columns.
-//   * Modified scores (MOD: s = cap tanh(scale q.k / cap) - slope |distance| on an interval of keys per
-//     query): P = exp(s - LSE) as before, and dS, the gradient of the modified score, times 1 - tanh^2
+//   * Modified scores (forms F >= 0: an interval of keys per query and, bit 0, the cap, bit 1, the distance
+//     bias of s = cap tanh(scale q.k / cap) - slope |distance|): P = exp(s - LSE) as before, and dS, the gradient of the modified score, times 1 - tanh^2
 //     is that of scale q.k.  P times that factor takes the place of P in registers once P itself is
 //     packed, so the cap holds no further registers.  Key tiles visit the query tiles from the first to
 //     the last whose intervals meet them (the row-term kernel also writes each query tile's interval).
@@ -45,6 +45,15 @@ namespace {
 
 constexpr int kT = 128;  // rows of every tile (queries or keys)
 constexpr int kThreads = 320;
+// Forms: plain scores, or modified ones (kMod .. kMod + 3).  The modified forms hold more per score: they
+// launch a third warpgroup whose idle warps give their registers to the compute warpgroups (setmaxnreg:
+// 128 x (2 x 216 + 64) of the 384 x 168 at launch; with 320 threads the dK/dV kernel spilled 528 bytes).
+constexpr int kPlain = -1, kMod = 0;
+template <int F> constexpr bool kIsMod = (F >= kMod);
+template <int F> constexpr bool kHasCap = (F > 0 && (F & 1) != 0);
+template <int F> constexpr bool kHasBias = (F > 0 && (F & 2) != 0);
+template <int F> constexpr int kThreadsOf = kIsMod<F> ? 384 : kThreads;
+constexpr uint32_t kRegsCompute = 216, kRegsOther = 64;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kStages = 2;
@@ -81,7 +90,7 @@ struct BwdModParams : BwdParams {
 };
 template <bool MOD> struct ParamsOf { using type = BwdParams; };
 template <> struct ParamsOf<true> { using type = BwdModParams; };
-template <bool MOD> using Params = typename ParamsOf<MOD>::type;
+template <int F> using Params = typename ParamsOf<kIsMod<F>>::type;
 
 // Keys lo <= j < hi that query `row` of sequence b sees (none past the last query).
 __device__ __forceinline__ int2 bwd_row_span(const BwdModParams &p, int b, int row, int kv_end) {
@@ -138,7 +147,7 @@ template <int Step>
 struct Distance {
     float sl, base, d0;
     bool linear;
-    __device__ __forceinline__ Distance(float slope, int d, bool nonneg, bool nonpos) {
+    __device__ __forceinline__ void set(float slope, int d, bool nonneg, bool nonpos) {
         const float sign = nonneg ? -slope : slope;
         linear = nonneg || nonpos;
         d0 = (float)d;
@@ -150,14 +159,16 @@ struct Distance {
     }
 };
 
-// The cap as the compute warpgroups use it: u = raw * in goes into tanh (0: no cap), and the score in the
-// log2 domain is tanh * mul, or raw * mul without the cap.
-struct CapOf {
-    float in, mul;
-    __device__ __forceinline__ explicit CapOf(const BwdParams &p) : in(0.f), mul(p.scale_log2) {}
-    __device__ __forceinline__ explicit CapOf(const BwdModParams &p)
-        : in(p.cap_in), mul(p.cap_in > 0.f ? p.cap_out : p.scale_log2) {}
-};
+// The cap's scale / cap (0 without it), and the factor that takes the raw scores -- with the cap their tanh
+// -- to the log2 domain.
+template <int F> __device__ __forceinline__ float cap_in_of(const Params<F> &p) {
+    if constexpr (kHasCap<F>) return p.cap_in;
+    else return 0.f;
+}
+template <int F> __device__ __forceinline__ float score_factor(const Params<F> &p) {
+    if constexpr (kHasCap<F>) return p.cap_out;
+    else return p.scale_log2;
+}
 
 // 64 TMEM columns of this thread's lane -> registers.
 __device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&x)[2][32]) {
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(256) bwd_rowdot_spans_kernel(const __nv_bfloat
 }
 
 // ================================================================== dK / dV
-// MOD: a streamed query tile's intervals, slope and whether every row sees all the CTA's keys
+// Modified forms: a streamed query tile's intervals, slope and whether every row sees all the CTA's keys
 template <bool MOD> struct QuerySpans {};
 template <> struct QuerySpans<true> {
     int4 lo[kStages][kT / 4], hi[kStages][kT / 4];
@@ -294,9 +305,7 @@ struct alignas(1024) DkvTiles {
     uint32_t tmem_base;
     int abort_flag;
 };
-template <int D, bool MOD> struct DkvSmem : DkvTiles<D>, QuerySpans<MOD> {};
-__device__ __forceinline__ float sm_slope(const QuerySpans<false> &, int) { return 0.f; }
-__device__ __forceinline__ float sm_slope(const QuerySpans<true> &s, int slot) { return s.slope2[slot]; }
+template <int D, int F> struct DkvSmem : DkvTiles<D>, QuerySpans<kIsMod<F>> {};
 
 // Query tiles a key tile [k0, k0+128) must visit: queries i >= k0 - delta can see its keys
 // under the causal mask (query i sees key j iff j <= i + delta).
@@ -314,8 +323,8 @@ __device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_en
     nqt = n_qt - qi_start;
 }
 
-template <int D, bool MOD>
-__device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const Params<MOD> &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
+template <int D, int F>
+__device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
                               const CUtensorMap *tmK, const CUtensorMap *tmV, int b, int hkv, int bh_kv, int k0,
                               int qi_start, int nqt, int n, WaitCtx wc) {
     constexpr int kBoxes = kBBoxes<D>;
@@ -352,13 +361,13 @@ __device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const Params<MOD> &p, const C
     float slope_n = 0.f;
     const int kv_end = kv_end_for(p, b);
     auto load_spans = [&](int u) {
-        if constexpr (MOD) {
+        if constexpr (kIsMod<F>) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + u % nqt) * kT + lane * 4 + t, kv_end);
             slope_n = p.slopes ? p.slopes[hkv * p.group + u / nqt] * kLog2e : 0.f;
         }
     };
-    if constexpr (MOD) load_spans(0);
+    if constexpr (kIsMod<F>) load_spans(0);
     int fills = 0;
     for (int u = 0; u < n; ++u) {
         const int slot = u % kStages, use = u / kStages;
@@ -370,7 +379,7 @@ __device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const Params<MOD> &p, const C
             make_float4(l4n[0] * -kLog2e, l4n[1] * -kLog2e, l4n[2] * -kLog2e, l4n[3] * -kLog2e);
         *reinterpret_cast<float4 *>(&sm.dterm[slot][lane * 4]) = make_float4(d4n[0], d4n[1], d4n[2], d4n[3]);
         if (u + 1 < n) load_stats(u + 1, l4n, d4n);
-        if constexpr (MOD) {
+        if constexpr (kIsMod<F>) {
             sm.lo[slot][lane] = make_int4(s4n[0].x, s4n[1].x, s4n[2].x, s4n[3].x);
             sm.hi[slot][lane] = make_int4(s4n[0].y, s4n[1].y, s4n[2].y, s4n[3].y);
             bool all = true;
@@ -404,8 +413,8 @@ __device__ void dkdv_producer(DkvSmem<D, MOD> &sm, const Params<MOD> &p, const C
     }
 }
 
-template <int D, bool MOD>
-__device__ void dkdv_mma(DkvSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
+template <int D, int F>
+__device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
     const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + kBPad<D>;
     bool ok = mbar_wait(&sm.kv_full, 0, wc, 63) && mbar_wait(&sm.u_full[0], 0, wc, 64);
     if (ok) {
@@ -441,8 +450,8 @@ __device__ void dkdv_mma(DkvSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) 
     (void)mbar_wait(&sm.drain, 0, drain, 68);
 }
 
-template <int D, bool MOD>
-__device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tmem, int w, int bh_kv, int k0,
+template <int D, int F>
+__device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh_kv, int k0,
                              int kv_end, int delta, int qi_start, int nqt, int n, WaitCtx wc) {
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
@@ -451,11 +460,10 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
     const int key = k0 + r;
     const bool key_ok = key < kv_end;
     // with the cap, x becomes tanh and c2 its factor cap * log2(e)
-    const CapOf cap(p);
-    const uint64_t c2 = f32x2_pack(cap.mul, cap.mul);
-    [[maybe_unused]] const TanhPoly capped(1.f);
-    [[maybe_unused]] const uint64_t in2 = f32x2_pack(cap.in, cap.in);
-    [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
+    // with the cap, the scores become tanh in place and the factor to the log2 domain is cap * log2(e)
+    [[maybe_unused]] const TanhCap cap(cap_in_of<F>(p), 1.f);
+    const float to_log2 = score_factor<F>(p);
+    const uint64_t c2 = f32x2_pack(to_log2, to_log2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
         const int slot = j % kStages;
@@ -474,7 +482,7 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
             ok = false;
             break;
         }
-        if constexpr (MOD) need_mask = sm.inside[slot] == 0;
+        if constexpr (kIsMod<F>) need_mask = sm.inside[slot] == 0;
         float4 L4[16];
         const float4 *l2 = reinterpret_cast<const float4 *>(sm.nlse2[slot] + w * 64);
 #pragma unroll
@@ -486,14 +494,14 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
         tc_fence_after_sync();
         uint32_t x[2][32];
         load64(tS, x);
-        [[maybe_unused]] bool far = false;
-        if constexpr (MOD)
-            if (cap.in > 0.f) far = __any_sync(kFull, abs_max(x) * cap.in > 1.f);
+        if constexpr (kHasCap<F>) cap.apply(cap.tier(fmaxf(max64_of(x), -min64(x))), x);
         // column c is the query at position col0 + c + delta; under the causal mask the keys after it are
         // masked, so the linear form serves there too
-        const int first = MOD ? col0 + delta : 0;
-        [[maybe_unused]] const Distance<1> dist(sm_slope(sm, slot), MOD ? first - key : 0,
-                                                MOD && (p.causal || first >= k0 + kT - 1), MOD && first + 63 <= k0);
+        [[maybe_unused]] Distance<1> dist;
+        if constexpr (kHasBias<F>) {
+            const int first = col0 + delta;
+            dist.set(sm.slope2[slot], first - key, p.causal || first >= k0 + kT - 1, first + 63 <= k0);
+        }
         // P^T = 2^(s * scale * log2e - lse2): bf16 pairs over the scores, fp32 kept in x
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -501,31 +509,27 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 const float4 L = L4[(h * 32 + i) / 4];
-                uint64_t x01 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
-                uint64_t x23 = f32x2_pack(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
+                const uint64_t x01 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+                const uint64_t x23 = f32x2_pack(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
                 [[maybe_unused]] float g[4];  // 1 - tanh^2
-                if constexpr (MOD) {
-                    if (cap.in > 0.f) {
-                        x01 = capped(f32x2_mul(x01, in2), far);
-                        x23 = capped(f32x2_mul(x23, in2), far);
-                        f32x2_unpack(f32x2_fma(f32x2_mul(x01, minus1), x01, one), g[0], g[1]);
-                        f32x2_unpack(f32x2_fma(f32x2_mul(x23, minus1), x23, one), g[2], g[3]);
-                    }
+                if constexpr (kHasCap<F>) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        g[t] = fmaf(-__uint_as_float(x[h][i + t]), __uint_as_float(x[h][i + t]), 1.f);
                 }
                 const uint64_t e01 = f32x2_fma(x01, c2, f32x2_pack(L.x, L.y));
                 const uint64_t e23 = f32x2_fma(x23, c2, f32x2_pack(L.z, L.w));
                 float e[4];
                 f32x2_unpack(e01, e[0], e[1]);
                 f32x2_unpack(e23, e[2], e[3]);
-                if constexpr (MOD) {
-                    if (p.slopes)
+                if constexpr (kHasBias<F>) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) e[t] = dist.add(h * 32 + i + t, e[t]);
+                    for (int t = 0; t < 4; ++t) e[t] = dist.add(h * 32 + i + t, e[t]);
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float pv = ex2_approx(e[t]);
-                    if constexpr (!MOD) {
+                    if constexpr (!kIsMod<F>) {
                         if (need_mask) {
                             const int c = h * 32 + i + t;
                             pv = (c >= lo && c < hi) ? pv : 0.f;
@@ -533,7 +537,7 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
                     }
                     x[h][i + t] = __float_as_uint(pv);
                 }
-                if constexpr (MOD) {
+                if constexpr (kIsMod<F>) {
                     if (need_mask) {  // the columns' intervals, four queries at a time
                         const int4 a = sm.lo[slot][w * 16 + (h * 32 + i) / 4], z = sm.hi[slot][w * 16 + (h * 32 + i) / 4];
                         const int al[4] = {a.x, a.y, a.z, a.w}, zl[4] = {z.x, z.y, z.z, z.w};
@@ -544,12 +548,12 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
                 }
                 pk[i / 2] = pack_bf16x2(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
                 pk[i / 2 + 1] = pack_bf16x2(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
-                if constexpr (MOD) {
-                    if (cap.in > 0.f)
+                if constexpr (kHasCap<F>) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t)  // a masked weight stays 0
-                            if (!need_mask || x[h][i + t] != 0u)
-                                x[h][i + t] = __float_as_uint(__uint_as_float(x[h][i + t]) * g[t]);
+                    for (int t = 0; t < 4; ++t) {
+                        const float pg = __uint_as_float(x[h][i + t]) * g[t];
+                        x[h][i + t] = need_mask && x[h][i + t] == 0u ? 0u : __float_as_uint(pg);  // masked: stays 0
+                    }
                 }
             }
             tmem_st16(tS + (uint32_t)(h * 16), pk);
@@ -580,7 +584,7 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
                 float s1 = __uint_as_float(x[h][i + 1]) * (__uint_as_float(y[h][i + 1]) - Dv.y);
                 float s2 = __uint_as_float(x[h][i + 2]) * (__uint_as_float(y[h][i + 2]) - Dv.z);
                 float s3 = __uint_as_float(x[h][i + 3]) * (__uint_as_float(y[h][i + 3]) - Dv.w);
-                if constexpr (MOD) {
+                if constexpr (kIsMod<F>) {
                     if (need_mask) {  // dP of a masked key may be anything
                         s0 = x[h][i] ? s0 : 0.f;
                         s1 = x[h][i + 1] ? s1 : 0.f;
@@ -609,14 +613,14 @@ __device__ void dkdv_compute(DkvSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t
     store_rows<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, w == 0 ? 1.f : p.scale, dst);
 }
 
-template <int D, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int F>
+__global__ void __launch_bounds__(kThreadsOf<F>, 1)
     bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const Params<MOD> p) {
+                    const Params<F> p) {
     extern __shared__ uint8_t smem_raw[];
-    DkvSmem<D, MOD> &sm =
-        *reinterpret_cast<DkvSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    DkvSmem<D, F> &sm =
+        *reinterpret_cast<DkvSmem<D, F> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     int bh_kv, level;
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kv_end = kv_end_for(p, b);
     const int delta = p.Nkv - p.Nq;
     int qi_start = 0, nqt = 0;
-    if constexpr (MOD) {
+    if constexpr (kIsMod<F>) {
         if (threadIdx.x == 0) {
             sm.first = 0x7fffffff;
             sm.last = -1;
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         const int n_qt = (p.Nq + kT - 1) / kT;
         int first = 0x7fffffff, last = -1;
-        for (int qi = threadIdx.x; qi < n_qt; qi += kThreads) {
+        for (int qi = threadIdx.x; qi < n_qt; qi += kThreadsOf<F>) {
             const int2 s = p.spans[(size_t)b * n_qt + qi];
             if (s.x < k0 + kT && s.y > k0) {
                 first = min(first, qi);
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
     WaitCtx wc{&sm.abort_flag, p.status};
-    if constexpr (MOD) {
+    if constexpr (kIsMod<F>) {
         if (sm.last >= 0) {
             qi_start = sm.first;
             nqt = sm.last - sm.first + 1;
@@ -682,12 +686,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         n = nqt * p.group;
     }
 
-    if (warp == kProducerWarp) {
-        if (n > 0) dkdv_producer<D, MOD>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, n, wc);
-    } else if (warp == kMmaWarp) {
-        if (lane == 0 && n > 0) dkdv_mma<D, MOD>(sm, tmem, n, wc);
+    // (each role inside the branch that sets its registers: code after a join gets the smaller limit)
+    if (warp >= kProducerWarp) {
+        if constexpr (kIsMod<F>) setmaxnreg_dec<kRegsOther>();
+        if (warp == kProducerWarp) {
+            if (n > 0) dkdv_producer<D, F>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, n, wc);
+        } else if (warp == kMmaWarp) {
+            if (lane == 0 && n > 0) dkdv_mma<D, F>(sm, tmem, n, wc);
+        }
     } else {
-        dkdv_compute<D, MOD>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, n, wc);
+        if constexpr (kIsMod<F>) setmaxnreg_inc<kRegsCompute>();
+        dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, n, wc);
     }
 
     tc_fence_before_sync();
@@ -715,10 +724,10 @@ struct alignas(1024) DqTiles {
     uint32_t tmem_base;
     int abort_flag;
 };
-template <int D, bool MOD> struct DqSmem : DqTiles<D>, KeySpan<MOD> {};
+template <int D, int F> struct DqSmem : DqTiles<D>, KeySpan<kIsMod<F>> {};
 
-template <int D, bool MOD>
-__device__ void dq_producer(DqSmem<D, MOD> &sm, const CUtensorMap *tmQ, const CUtensorMap *tmdO, const CUtensorMap *tmK,
+template <int D, int F>
+__device__ void dq_producer(DqSmem<D, F> &sm, const CUtensorMap *tmQ, const CUtensorMap *tmdO, const CUtensorMap *tmK,
                             const CUtensorMap *tmV, int bh, int bh_kv, int q0, int n, int j0, WaitCtx wc) {
     constexpr int kBoxes = kBBoxes<D>;
     prefetch_tensormap(tmK);
@@ -749,8 +758,8 @@ __device__ void dq_producer(DqSmem<D, MOD> &sm, const CUtensorMap *tmQ, const CU
     }
 }
 
-template <int D, bool MOD>
-__device__ void dq_mma(DqSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
+template <int D, int F>
+__device__ void dq_mma(DqSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
     const uint32_t tS = tmem, tdP = tmem + 128, tdQ = tmem + 256;
     bool ok = mbar_wait(&sm.qd_full, 0, wc, 83) && mbar_wait(&sm.u_full[0], 0, wc, 84);
     if (ok) {
@@ -785,8 +794,8 @@ __device__ void dq_mma(DqSmem<D, MOD> &sm, uint32_t tmem, int n, WaitCtx wc) {
     (void)mbar_wait(&sm.drain, 0, drain, 88);
 }
 
-template <int D, bool MOD>
-__device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
+template <int D, int F>
+__device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
                            int delta, int n, int j0, int2 span, WaitCtx wc) {
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
@@ -799,22 +808,20 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tm
     // keys < lim are valid for this row
     int lim = row_ok ? kv_end : 0;
     if (p.causal) lim = min(lim, row + delta + 1);
-    if constexpr (MOD) lim = span.y;
-    const CapOf cap(p);
-    const uint64_t c2 = f32x2_pack(cap.mul, cap.mul);
-    [[maybe_unused]] const TanhPoly capped(1.f);
-    [[maybe_unused]] const uint64_t in2 = f32x2_pack(cap.in, cap.in);
-    [[maybe_unused]] const uint64_t one = f32x2_pack(1.f, 1.f), minus1 = f32x2_pack(-1.f, -1.f);
+    if constexpr (kIsMod<F>) lim = span.y;
+    [[maybe_unused]] const TanhCap cap(cap_in_of<F>(p), 1.f);
+    const float to_log2 = score_factor<F>(p);
+    const uint64_t c2 = f32x2_pack(to_log2, to_log2);
     [[maybe_unused]] float slope2 = 0.f;
-    if constexpr (MOD) slope2 = p.slopes ? p.slopes[bh % p.Hq] * kLog2e : 0.f;
+    if constexpr (kHasBias<F>) slope2 = p.slopes[bh % p.Hq] * kLog2e;
     const uint64_t nl2 = f32x2_pack(-lse2, -lse2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
         const int key0 = (j0 + j) * kT + w * 64;
         const int nvalid = lim - key0;  // columns c < nvalid are valid
         bool need_mask = nvalid < 64;
-        [[maybe_unused]] int lo = 0;  // (MOD) and columns from lo on
-        if constexpr (MOD) {
+        [[maybe_unused]] int lo = 0;  // modified forms: and columns from lo on
+        if constexpr (kIsMod<F>) {
             lo = span.x - key0;
             need_mask = __any_sync(kFull, need_mask || lo > 0);
         }
@@ -827,44 +834,33 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tm
         load64(tS, x);
         tc_fence_before_sync();
         mbar_arrive(&sm.s_free);
-        [[maybe_unused]] bool far = false;
-        if constexpr (MOD)
-            if (cap.in > 0.f) far = __any_sync(kFull, abs_max(x) * cap.in > 1.f);
-        const int at = q0 + delta;  // position of the tile's first query
-        [[maybe_unused]] const Distance<-1> dist(slope2, row + delta - key0, p.causal || key0 + 63 <= at,
-                                                 key0 >= at + kT - 1);
+        if constexpr (kHasCap<F>) cap.apply(cap.tier(fmaxf(max64_of(x), -min64(x))), x);
+        [[maybe_unused]] Distance<-1> dist;
+        if constexpr (kHasBias<F>) {
+            const int at = q0 + delta;  // position of the tile's first query
+            dist.set(slope2, row + delta - key0, p.causal || key0 + 63 <= at, key0 >= at + kT - 1);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                uint64_t x2 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
-                [[maybe_unused]] float g0 = 1.f, g1 = 1.f;  // 1 - tanh^2
-                if constexpr (MOD) {
-                    if (cap.in > 0.f) {
-                        x2 = capped(f32x2_mul(x2, in2), far);
-                        f32x2_unpack(f32x2_fma(f32x2_mul(x2, minus1), x2, one), g0, g1);
-                    }
-                }
+                const uint64_t x2 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
                 const uint64_t e2 = f32x2_fma(x2, c2, nl2);
                 float e0, e1;
                 f32x2_unpack(e2, e0, e1);
-                if constexpr (MOD) {
-                    if (p.slopes) {
-                        e0 = dist.add(h * 32 + i, e0);
-                        e1 = dist.add(h * 32 + i + 1, e1);
-                    }
+                if constexpr (kHasBias<F>) {
+                    e0 = dist.add(h * 32 + i, e0);
+                    e1 = dist.add(h * 32 + i + 1, e1);
                 }
                 float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
-                if constexpr (MOD) {
-                    if (cap.in > 0.f) {
-                        p0 *= g0;
-                        p1 *= g1;
-                    }
+                if constexpr (kHasCap<F>) {  // times 1 - tanh^2
+                    p0 *= fmaf(-__uint_as_float(x[h][i]), __uint_as_float(x[h][i]), 1.f);
+                    p1 *= fmaf(-__uint_as_float(x[h][i + 1]), __uint_as_float(x[h][i + 1]), 1.f);
                 }
                 if (need_mask) {
                     const int c = h * 32 + i;
-                    p0 = c < nvalid && (!MOD || c >= lo) ? p0 : 0.f;
-                    p1 = c + 1 < nvalid && (!MOD || c + 1 >= lo) ? p1 : 0.f;
+                    p0 = c < nvalid && (!kIsMod<F> || c >= lo) ? p0 : 0.f;
+                    p1 = c + 1 < nvalid && (!kIsMod<F> || c + 1 >= lo) ? p1 : 0.f;
                 }
                 x[h][i] = __float_as_uint(p0);
                 x[h][i + 1] = __float_as_uint(p1);
@@ -885,7 +881,7 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tm
             for (int i = 0; i < 32; i += 2) {
                 float s0 = __uint_as_float(x[h][i]) * (__uint_as_float(y[h][i]) - drow);
                 float s1 = __uint_as_float(x[h][i + 1]) * (__uint_as_float(y[h][i + 1]) - drow);
-                if constexpr (MOD) {
+                if constexpr (kIsMod<F>) {
                     if (need_mask) {  // dP of a masked key may be anything
                         s0 = x[h][i] ? s0 : 0.f;
                         s1 = x[h][i + 1] ? s1 : 0.f;
@@ -895,7 +891,7 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tm
             }
             tmem_st16(tdP + (uint32_t)(h * 16), pk);
         }
-        if constexpr (MOD) {
+        if constexpr (kIsMod<F>) {
             // K rows past the sequence's keys may hold anything: dS is 0 there, and dS K needs finite values
             // (S(j) has been read, and the tile stays until dQ(j) completes)
             const int rows0 = kv_end - (j0 + j) * kT;
@@ -923,13 +919,13 @@ __device__ void dq_compute(DqSmem<D, MOD> &sm, const Params<MOD> &p, uint32_t tm
     else store_rows<D - kDqSplit<D>>(lane_base + 256u + (uint32_t)kDqSplit<D>, n > 0, row_ok, p.scale, dst);
 }
 
-template <int D, bool MOD>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int F>
+__global__ void __launch_bounds__(kThreadsOf<F>, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const Params<MOD> p) {
+                  const Params<F> p) {
     extern __shared__ uint8_t smem_raw[];
-    DqSmem<D, MOD> &sm = *reinterpret_cast<DqSmem<D, MOD> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    DqSmem<D, F> &sm = *reinterpret_cast<DqSmem<D, F> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     int bh, level;
@@ -943,9 +939,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int limit = kv_end;
     if (p.causal) limit = min(limit, min(q0 + kT, p.Nq) + delta);
     int n = limit > 0 ? (limit + kT - 1) / kT : 0;
-    int j0 = 0;  // MOD: the first key tile that a row of the CTA sees
+    int j0 = 0;  // modified forms: the first key tile that a row of the CTA sees
     int2 span = make_int2(0, 0);
-    if constexpr (MOD) {
+    if constexpr (kIsMod<F>) {
         if (warp < 8) {
             span = bwd_row_span(p, b, q0 + ((int)threadIdx.x & 127), kv_end);
             const int lo = __reduce_min_sync(kFull, span.x < span.y ? span.x : 0x7fffffff);
@@ -981,19 +977,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
     WaitCtx wc{&sm.abort_flag, p.status};
-    if constexpr (MOD) {
+    if constexpr (kIsMod<F>) {
         const int lo = min(min(sm.lo[0], sm.lo[1]), min(sm.lo[2], sm.lo[3]));
         const int hi = max(max(sm.hi[0], sm.hi[1]), max(sm.hi[2], sm.hi[3]));
         j0 = hi > 0 ? lo / kT : 0;
         n = hi > 0 ? (hi + kT - 1) / kT - j0 : 0;
     }
 
-    if (warp == kProducerWarp) {
-        if (lane == 0 && n > 0) dq_producer<D, MOD>(sm, &tmQ, &tmdO, &tmK, &tmV, bh, bh_kv, q0, n, j0, wc);
-    } else if (warp == kMmaWarp) {
-        if (lane == 0 && n > 0) dq_mma<D, MOD>(sm, tmem, n, wc);
+    if (warp >= kProducerWarp) {
+        if constexpr (kIsMod<F>) setmaxnreg_dec<kRegsOther>();
+        if (warp == kProducerWarp) {
+            if (lane == 0 && n > 0) dq_producer<D, F>(sm, &tmQ, &tmdO, &tmK, &tmV, bh, bh_kv, q0, n, j0, wc);
+        } else if (warp == kMmaWarp) {
+            if (lane == 0 && n > 0) dq_mma<D, F>(sm, tmem, n, wc);
+        }
     } else {
-        dq_compute<D, MOD>(sm, p, tmem, warp >> 2, bh, q0, kv_end, delta, n, j0, span, wc);
+        if constexpr (kIsMod<F>) setmaxnreg_inc<kRegsCompute>();
+        dq_compute<D, F>(sm, p, tmem, warp >> 2, bh, q0, kv_end, delta, n, j0, span, wc);
     }
 
     tc_fence_before_sync();
@@ -1011,7 +1011,18 @@ int heads_per_chunk(double bytes_per_head, int n_heads) {
     return h < 1 ? 1 : (h > n_heads ? n_heads : h);
 }
 
-template <int D, bool MOD>
+// The register split draws on the launch allocation; a larger one would wait forever.
+template <int F>
+cudaError_t check_register_split(const void *kernel) {
+    if (!kIsMod<F>) return cudaSuccess;
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    return (long)fa.numRegs * kThreadsOf<F> >= 128L * (2 * kRegsCompute + kRegsOther) ? cudaSuccess
+                                                                                     : cudaErrorInvalidConfiguration;
+}
+
+template <int D, int F>
 cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     const long long rows = (long long)a.B * a.Hq * a.Nq;
     CUtensorMap tq, tdo, tk, tv;
@@ -1019,7 +1030,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     if (!encode_qkv_map(&tq, a.q, BHq, a.Nq, D) || !encode_qkv_map(&tdo, a.dout, BHq, a.Nq, D) ||
         !encode_qkv_map(&tk, a.k, BHkv, a.Nkv, D) || !encode_qkv_map(&tv, a.v, BHkv, a.Nkv, D))
         return cudaErrorInvalidValue;
-    Params<MOD> p;
+    Params<F> p;
     p.lse = a.lse;
     p.dterm = a.dterm;
     p.dq = reinterpret_cast<__nv_bfloat16 *>(a.dq);
@@ -1036,7 +1047,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     p.causal = a.causal;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
-    if constexpr (MOD) {
+    if constexpr (kIsMod<F>) {
         p.key_begin = a.key_begin;
         p.key_end = a.key_end;
         p.slopes = a.slopes;
@@ -1049,7 +1060,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         const int row_blocks = (int)((rows * kRowThreads<D> + 255) / 256);
         const __nv_bfloat16 *o = reinterpret_cast<const __nv_bfloat16 *>(a.o);
         const __nv_bfloat16 *dout = reinterpret_cast<const __nv_bfloat16 *>(a.dout);
-        if constexpr (MOD) {
+        if constexpr (kIsMod<F>) {
             const int n_qt = (a.Nq + kT - 1) / kT;
             const int span_blocks = (int)(((long long)a.B * n_qt + 1) / 2);
             bwd_rowdot_spans_kernel<D><<<row_blocks + span_blocks, 256, 0, stream>>>(o, dout, a.dterm, rows, row_blocks,
@@ -1063,27 +1074,31 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
 
     // dK/dV: one CTA per (batch, key/value head, key tile); streams Q and dO of the group's heads
     {
-        Params<MOD> pk = p;
+        Params<F> pk = p;
         pk.units_per_head = (a.Nkv + kT - 1) / kT;
         pk.heads_per_chunk = heads_per_chunk(2.0 * p.group * a.Nq * D * 2.0, BHkv);
-        const size_t smem = sizeof(DkvSmem<D, MOD>) + 1024;
-        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dkdv_kernel<D, MOD>), (int)smem);
+        const size_t smem = sizeof(DkvSmem<D, F>) + 1024;
+        static const cudaError_t split = check_register_split<F>(reinterpret_cast<const void *>(bwd_dkdv_kernel<D, F>));
+        if (split != cudaSuccess) return split;
+        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dkdv_kernel<D, F>), (int)smem);
         if (e != cudaSuccess) return e;
         const unsigned grid = (unsigned)((size_t)pk.units_per_head * BHkv);
-        bwd_dkdv_kernel<D, MOD><<<grid, kThreads, smem, stream>>>(tq, tdo, tk, tv, pk);
+        bwd_dkdv_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pk);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     // dQ: one CTA per (batch, query head, query tile); streams K and V of its key/value head
     {
-        Params<MOD> pq = p;
+        Params<F> pq = p;
         pq.units_per_head = (a.Nq + kT - 1) / kT;
         pq.heads_per_chunk = heads_per_chunk(2.0 * a.Nkv * D * 2.0 / p.group, BHq);
-        const size_t smem = sizeof(DqSmem<D, MOD>) + 1024;
-        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dq_kernel<D, MOD>), (int)smem);
+        const size_t smem = sizeof(DqSmem<D, F>) + 1024;
+        static const cudaError_t split = check_register_split<F>(reinterpret_cast<const void *>(bwd_dq_kernel<D, F>));
+        if (split != cudaSuccess) return split;
+        cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dq_kernel<D, F>), (int)smem);
         if (e != cudaSuccess) return e;
         const unsigned grid = (unsigned)((size_t)pq.units_per_head * BHq);
-        bwd_dq_kernel<D, MOD><<<grid, kThreads, smem, stream>>>(tq, tdo, tk, tv, pq);
+        bwd_dq_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pq);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

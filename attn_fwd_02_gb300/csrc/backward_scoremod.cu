@@ -3,13 +3,24 @@
 
 namespace attn {
 
+namespace {
+
+template <int D>
+cudaError_t launch_scoremod_d(const BwdArgs &a, cudaStream_t stream) {
+    const bool cap = a.softcap > 0.f && a.scale / a.softcap > 0.f, bias = a.slopes != nullptr;
+    if (cap) return bias ? launch_bwd_d<D, kMod + 3>(a, stream) : launch_bwd_d<D, kMod + 1>(a, stream);
+    return bias ? launch_bwd_d<D, kMod + 2>(a, stream) : launch_bwd_d<D, kMod>(a, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_bwd_scoremod(const BwdArgs &a, cudaStream_t stream) {
     switch (a.d) {
-        case 32: return launch_bwd_d<32, true>(a, stream);
-        case 64: return launch_bwd_d<64, true>(a, stream);
-        case 80: return launch_bwd_d<80, true>(a, stream);
-        case 96: return launch_bwd_d<96, true>(a, stream);
-        case 128: return launch_bwd_d<128, true>(a, stream);
+        case 32: return launch_scoremod_d<32>(a, stream);
+        case 64: return launch_scoremod_d<64>(a, stream);
+        case 80: return launch_scoremod_d<80>(a, stream);
+        case 96: return launch_scoremod_d<96>(a, stream);
+        case 128: return launch_scoremod_d<128>(a, stream);
         default: return cudaErrorInvalidValue;
     }
 }

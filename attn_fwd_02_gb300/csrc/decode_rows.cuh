@@ -324,12 +324,17 @@ __global__ void __launch_bounds__(kRowWarps * 32)
                 for (int i = 0; i < 4; ++i) sc[nt][i] += sc2[nt][i];
                 if constexpr (MOD) {
                     if (cin > 0.f) {
-                        const TanhPoly capped(a.cap_out);
+                        const TanhCap cap(cin, a.cap_out);
                         const float big = fmaxf(fmaxf(fabsf(sc[nt][0]), fabsf(sc[nt][1])),
                                                 fmaxf(fabsf(sc[nt][2]), fabsf(sc[nt][3])));
-                        const bool far = __any_sync(0xffffffffu, big * cin > 1.f);
-                        f32x2_unpack(capped(f32x2_pack(sc[nt][0] * cin, sc[nt][1] * cin), far), sc[nt][0], sc[nt][1]);
-                        f32x2_unpack(capped(f32x2_pack(sc[nt][2] * cin, sc[nt][3] * cin), far), sc[nt][2], sc[nt][3]);
+                        const uint64_t s01 = f32x2_pack(sc[nt][0], sc[nt][1]), s23 = f32x2_pack(sc[nt][2], sc[nt][3]);
+                        if (__any_sync(0xffffffffu, big * cin > 1.f)) {
+                            f32x2_unpack(cap.eval<2>(s01), sc[nt][0], sc[nt][1]);
+                            f32x2_unpack(cap.eval<2>(s23), sc[nt][2], sc[nt][3]);
+                        } else {
+                            f32x2_unpack(cap.eval<1>(s01), sc[nt][0], sc[nt][1]);
+                            f32x2_unpack(cap.eval<1>(s23), sc[nt][2], sc[nt][3]);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sc[nt][i] *= c;

@@ -105,15 +105,18 @@ constexpr int kPageTokens = 16;            // tokens per page of the paged KV ca
 
 // Where K/V come from (a compile-time parameter of the kernel, so that each form carries only
 // its own code): contiguous [B, Hkv, Nkv, d] tensors; bf16 pages of a paged KV cache; e4m3 pages,
-// widened to f16 in shared memory before the products; or contiguous tensors with modified scores (a
-// tanh cap, a distance bias) and an interval of visible keys per query (kContigMod); or the pages that a
+// widened to f16 in shared memory before the products; contiguous tensors with an interval of visible keys
+// per query and, bit 0, a tanh cap and, bit 1, a distance bias of the scores (kMod .. kMod + 3: forms of
+// their own, since the registers of one kernel for all spilled); or the pages that a
 // group of sequences shares in a decode step, split along the keys, with the group's query heads of one
 // key/value head as the rows and unnormalised partial results (kSharedBf16, kSharedE4m3).
-enum KvMode : int { kContig = 0, kPagedBf16 = 1, kPagedE4m3 = 2, kContigMod = 3, kSharedBf16 = 4, kSharedE4m3 = 5 };
+enum KvMode : int { kContig = 0, kPagedBf16 = 1, kPagedE4m3 = 2, kSharedBf16 = 4, kSharedE4m3 = 5, kMod = 8 };
 template <int M> constexpr bool kIsShared = (M == kSharedBf16 || M == kSharedE4m3);
 template <int M> constexpr bool kIsPaged = (M == kPagedBf16 || M == kPagedE4m3 || kIsShared<M>);
 template <int M> constexpr bool kIsE4m3 = (M == kPagedE4m3 || M == kSharedE4m3);
-template <int M> constexpr bool kIsMod = (M == kContigMod);
+template <int M> constexpr bool kIsMod = (M >= kMod);
+template <int M> constexpr bool kHasCap = (kIsMod<M> && (M & 1) != 0);
+template <int M> constexpr bool kHasBias = (kIsMod<M> && (M & 2) != 0);
 // Forms whose tiles start at the first key that a row of the CTA sees, with rows limited to intervals.
 template <int M> constexpr bool kHasSpan = (kIsMod<M> || kIsShared<M>);
 
@@ -169,7 +172,7 @@ struct PrefillParams {
     float scale_log2;                    // scale * log2(e) (times the key scale of e4m3 pages)
     float o_scale;                       // multiplies O in the epilogue (the value scale of e4m3 pages)
 };
-// kContigMod: a type of its own, so that the other forms' parameters stay as they are (their registers
+// kMod forms: a type of its own, so that the other forms' parameters stay as they are (their registers
 // depend on them).
 struct PrefillModParams : PrefillParams {
     // keys key_begin[b, i] <= j < key_end[b, i] are visible to query i (null: no limit);
@@ -189,9 +192,12 @@ struct PrefillSharedParams : PrefillParams {
     float *ws;                    // [B, H, ws_splits, d + 4], the first n_splits of each row
 };
 template <int M> struct ParamsOf { using type = PrefillParams; };
+template <> struct ParamsOf<kMod> { using type = PrefillModParams; };
+template <> struct ParamsOf<kMod + 1> { using type = PrefillModParams; };
+template <> struct ParamsOf<kMod + 2> { using type = PrefillModParams; };
+template <> struct ParamsOf<kMod + 3> { using type = PrefillModParams; };
 template <> struct ParamsOf<kSharedBf16> { using type = PrefillSharedParams; };
 template <> struct ParamsOf<kSharedE4m3> { using type = PrefillSharedParams; };
-template <> struct ParamsOf<kContigMod> { using type = PrefillModParams; };
 template <int M> using Params = typename ParamsOf<M>::type;
 
 // The key tiles of a CTA's query tiles in the forms with intervals: tiles j0 + begin[t] ..
@@ -598,13 +604,23 @@ __device__ __forceinline__ void mask_pages(uint32_t (&s)[H][2][32], uint32_t bad
                 if ((bad >> (h * 4 + cc * 2 + (i >> 4))) & 1u) s[h][cc][i] = __float_as_uint(-INFINITY);
 }
 
-// Scores at positions outside lo <= i < hi (relative to the first of the 64 held) become -inf.
-__device__ __forceinline__ void mask_span(uint32_t (&s)[2][32], int lo, int hi) {
+// Scores at positions < first (relative to the first of the 64 held) become -inf.
+__device__ __forceinline__ void mask_below(uint32_t (&s)[2][32], int first) {
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (cc * 32 + i < lo || cc * 32 + i >= hi) s[cc][i] = __float_as_uint(-INFINITY);
+            if (cc * 32 + i < first) s[cc][i] = __float_as_uint(-INFINITY);
+}
+
+// The cap's factors (0 in the forms without it).
+template <int M> __device__ __forceinline__ float cap_in_of(const Params<M> &p) {
+    if constexpr (kHasCap<M>) return p.cap_in;
+    else return 0.f;
+}
+template <int M> __device__ __forceinline__ float cap_out_of(const Params<M> &p) {
+    if constexpr (kHasCap<M>) return p.cap_out;
+    else return 0.f;
 }
 
 // Rows first .. kBN - 1 of a key or value tile become zero (all 128 threads of a warpgroup; each box
@@ -688,53 +704,14 @@ __device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r) {
     return __uint_as_float((uint32_t)(127 + sh) << 23);
 }
 
-// Modified scores (kContigMod): x = log2(e) (cap tanh(scale raw / cap) - slope |pos - key|), or without
-// the cap x = log2(e) (scale raw - slope |pos - key|), in place on the raw scores of a row.
-struct ScoreMod {
-    bool cap = false, bias = false;
-    float c = 0.f, cin = 0.f, cout = 0.f, slope2 = 0.f;
+// The distance bias of a row: -slope |pos - key| (log2 domain), added to `mul` times the scores in place.
+struct DistanceBias {
+    float slope2 = 0.f;
     int pos = 0;  // the row's position among the keys
-
-    __device__ __forceinline__ void init(const PrefillModParams &p, int h, int pos_) {
-        cap = p.cap_in > 0.f;
-        bias = p.slopes != nullptr;
-        c = p.scale_log2;
-        cin = p.cap_in;
-        cout = p.cap_out;
-        slope2 = bias ? p.slopes[h] * kLog2e : 0.f;
-        pos = pos_;
-    }
-    __device__ __forceinline__ bool any() const { return cap || bias; }
-
-    template <int H>
-    __device__ __forceinline__ void apply_cap(uint32_t (&s)[H][2][32]) const {
-        float big = 0.f;
-#pragma unroll
-        for (int h = 0; h < H; ++h) big = fmaxf(big, abs_max(s[h]));
-        const bool far = __any_sync(0xffffffffu, big * cin > 1.f);
-        const TanhPoly capped(cout);
-        const uint64_t in2 = f32x2_pack(cin, cin);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const uint64_t u =
-                        f32x2_mul(f32x2_pack(__uint_as_float(s[h][cc][i]), __uint_as_float(s[h][cc][i + 1])), in2);
-                    float t0, t1;
-                    f32x2_unpack(capped(u, far), t0, t1);
-                    s[h][cc][i] = __float_as_uint(t0);
-                    s[h][cc][i + 1] = __float_as_uint(t1);
-                }
-    }
 
     // key0: the tile's first key; row0: the position of the tile's first row.
     template <int H>
-    __device__ __forceinline__ void apply(uint32_t (&s)[H][2][32], int key0, bool causal, int row0) const {
-        if (cap) apply_cap<H>(s);
-        if (!bias) return;
-        const float mul = cap ? 1.f : c;
+    __device__ __forceinline__ void apply(uint32_t (&s)[H][2][32], float mul, int key0, bool causal, int row0) const {
         const float d0 = (float)(pos - key0);
         // all keys of the tile at or before the rows (under the causal mask the later ones are masked),
         // or all after them: the distance is linear in the key
@@ -787,11 +764,14 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
             mbar_arrive(&sm.q_conv[t]);
         }
     }
-    ScoreMod mod;
-    if constexpr (kIsMod<M>) {
-        mod.init(p, bh % p.H, row + delta);
-        if (mod.any()) c = 1.f;  // the modified scores are in the log2 domain already
+    // modified scores are brought to the log2 domain before the maximum, with the cap or the bias
+    [[maybe_unused]] const TanhCap cap(cap_in_of<M>(p), cap_out_of<M>(p));
+    [[maybe_unused]] DistanceBias bias;
+    if constexpr (kHasBias<M>) {
+        bias.slope2 = p.slopes[bh % p.H] * kLog2e;
+        bias.pos = row + delta;
     }
+    if constexpr (kHasCap<M> || kHasBias<M>) c = 1.f;
     const uint64_t c2 = f32x2_pack(c, c);
 
     float m_ref = -INFINITY;  // reference max (log2 domain) shared by l and O
@@ -829,7 +809,11 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
         // that straddle the causal diagonal or the key-padding length.
         const int key0 = (j0 + j) * kBN;
         bool need_mask = (key0 + kBN > kv_end) || (p.causal && key0 + kBN - 1 > qs + delta);
-        if constexpr (kHasSpan<M>) need_mask = __any_sync(0xffffffffu, span.lo > key0 || span.hi < key0 + kBN);
+        bool need_lo = false;  // forms with intervals: some row's interval starts inside the tile
+        if constexpr (kHasSpan<M>) {
+            need_mask = __any_sync(0xffffffffu, span.hi < key0 + kBN);
+            if constexpr (kIsMod<M>) need_lo = __any_sync(0xffffffffu, span.lo > key0);
+        }
         int nvalid = kBN;
         if (!kHasSpan<M> && need_mask) {
             int lim = kv_end;
@@ -847,18 +831,48 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
             tmem_wait_ld(s[h][0]);
             tmem_wait_ld(s[h][1]);
         }
-        if constexpr (kIsMod<M>) mod.template apply<kHalves>(s, key0, p.causal != 0, qs + delta);
-        if (need_mask) {
+        [[maybe_unused]] float raw_max = 0.f;
+        [[maybe_unused]] int tier = 0;
+        if constexpr (kHasCap<M>) {
+            raw_max = max64_of(s[0]);
+            float raw_min = min64(s[0]);
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                if constexpr (kHasSpan<M>) mask_span(s[h], span.lo - key0 - 64 * h, span.hi - key0 - 64 * h);
-                else mask_chunks(s[h], nvalid - 64 * h);
+            for (int h = 1; h < kHalves; ++h) {
+                raw_max = fmaxf(raw_max, max64_of(s[h]));
+                raw_min = fminf(raw_min, min64(s[h]));
+            }
+            tier = cap.tier(fmaxf(raw_max, -raw_min));
+            if (tier == 0) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) cap.template apply_tier<0>(s[h]);
+            } else if (tier == 1) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) cap.template apply_tier<1>(s[h]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) cap.template apply_tier<2>(s[h]);
             }
         }
-        if (kPaged && unmapped) mask_pages<kHalves>(s, unmapped);
-        float mx = max64(s[0]);
+        if constexpr (kHasBias<M>)
+            bias.template apply<kHalves>(s, kHasCap<M> ? 1.f : p.scale_log2, key0, p.causal != 0, qs + delta);
+        if (need_mask) {
+            if constexpr (kHasSpan<M>) nvalid = span.hi - key0;
 #pragma unroll
-        for (int h = 1; h < kHalves; ++h) mx = fmaxf(mx, max64(s[h]));
+            for (int h = 0; h < kHalves; ++h) mask_chunks(s[h], nvalid - 64 * h);
+        }
+        if (kIsMod<M> && need_lo) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) mask_below(s[h], span.lo - key0 - 64 * h);
+        }
+        if (kPaged && unmapped) mask_pages<kHalves>(s, unmapped);
+        float mx;
+        if (kHasCap<M> && !kHasBias<M> && !need_mask && !need_lo) {
+            mx = cap.one(tier, raw_max);  // the cap is monotone
+        } else {
+            mx = max64(s[0]);
+#pragma unroll
+            for (int h = 1; h < kHalves; ++h) mx = fmaxf(mx, max64(s[h]));
+        }
         const float m_cand = mx * c;  // -inf stays -inf (c > 0)
         const bool resc = m_cand > m_ref + kRescaleThreshold;
         float alpha = 1.f;

@@ -436,6 +436,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Packed pairs of fp32 (one 64-bit register holds {lo, hi}): one instruction does two lanes' worth.
 __device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
     uint64_t r;

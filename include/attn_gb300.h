@@ -129,7 +129,7 @@ int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *ls
  *     s_ij = scale <q_i, k_j> - slope[h] |p_i - j|                       (softcap 0: no cap)
  *     J    = { j : key_begin[b, i] <= j < key_end[b, i], 0 <= j < kv_lens[b], j <= p_i if causal }
  * and O, LSE as in attn_fwd_gqa over these scores and keys (no visible key: O = 0, LSE = -inf).
- *   softcap       0, or finite and positive
+ *   softcap       0, or positive; it and scale / softcap at most 2^100
  *   alibi_slopes  [Hq] fp32 (device), finite; NULL: no distance bias
  *   key_begin, key_end [B, Nq] int32 (device): any values, clamped; NULL: 0 and Nkv
  * The intervals say documents packed into a row (begin and end of the query's document), a prefix that
@@ -210,7 +210,7 @@ int paged_attn_decode_gqa(const void *q, const void *k_pages, const void *v_page
  *     s_j = cap tanh(scale <q, k_j> / cap) - slope[h] (ctx_lens[b] - 1 - j)      (softcap cap > 0)
  *     s_j = scale <q, k_j> - slope[h] (ctx_lens[b] - 1 - j)                      (softcap 0)
  * over the cached tokens key_begin[b] <= j < ctx_lens[b].
- *   softcap 0, or finite and positive; alibi_slopes [H] fp32 or NULL; key_begin [B] int32 (clamped) or NULL
+ *   softcap 0, or positive (it and scale / softcap at most 2^100); alibi_slopes [H] fp32 or NULL; key_begin [B] int32 (clamped) or NULL
  *   workspace: at least paged_attn_decode_scoremod_workspace_size(...) bytes, 16-byte aligned
  * Pages wholly before key_begin are not read, and slots of the first page before it may hold anything.
  * A sequence that sees no token gets O = 0 and LSE = -inf.  Other arguments as paged_attn_decode_gqa;
