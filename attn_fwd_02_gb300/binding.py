@@ -47,7 +47,7 @@ SIGNATURES = {
     "paged_kv_append_rope": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
     "paged_kv_append_rope_fp8": (I, [P, P, P, P, P, P, P, P, P, F, F, P, I, I, I, P, P, P, I, I, I, I, I, I, I, I, P]),
     "attn_fwd_scoremod": (I, [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P]),
-    "attn_bwd_scoremod_workspace_size": (Z, [I, I, I]),
+    "attn_bwd_scoremod_workspace_size": (Z, [I, I, I, I, I, I]),
     "attn_bwd_scoremod": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, P, P, P, Z, P]),
     "paged_attn_decode_scoremod_workspace_size": (Z, [I, I, I, I, I, I]),
     "paged_attn_decode_scoremod": (I, [P, P, P, P, P, I, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P]),
@@ -729,8 +729,8 @@ def attn_fwd_scoremod(q, k, v, causal: bool, scale: float | None = None, softcap
     return out, lse
 
 
-def attn_bwd_scoremod_workspace_size(B: int, Hq: int, Nq: int) -> int:
-    return int(load_library().attn_bwd_scoremod_workspace_size(B, Hq, Nq))
+def attn_bwd_scoremod_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, Nkv: int, d: int) -> int:
+    return int(load_library().attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d))
 
 
 def _workspace(t, need, device):
@@ -746,7 +746,7 @@ def attn_bwd_scoremod(q, k, v, o, lse, dout, causal: bool, scale: float | None =
                       workspace=None, stream=None):
     """Backward of attn_fwd_scoremod: q, o, dout [B,Hq,Nq,d] and k, v [B,Hkv,Nkv,d] bf16, lse [B,Hq,Nq]
     fp32 from the forward, the modification as in the forward call.  Returns (dq, dk, dv) bf16.
-    workspace: optional uint8 tensor of attn_bwd_scoremod_workspace_size(B, Hq, Nq) bytes."""
+    workspace: optional uint8 tensor of attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d) bytes."""
     device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d = _dense_inputs(q, k, v)
     bf = _t.bfloat16
     op, lp = _in(o, "o", bf, 4, device), _in(lse, "lse", _t.float32, 3, device)
@@ -763,7 +763,7 @@ def attn_bwd_scoremod(q, k, v, o, lse, dout, causal: bool, scale: float | None =
     dk, dkp = _output(dk, "dk", bf, k.shape, device)
     dv, dvp = _output(dv, "dv", bf, k.shape, device)
     lib = load_library()
-    workspace, wp, wn = _workspace(workspace, lib.attn_bwd_scoremod_workspace_size(B, Hq, Nq), device)
+    workspace, wp, wn = _workspace(workspace, lib.attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d), device)
     st = lib.attn_bwd_scoremod(qp, kp, vp, op, lp, gp, dqp, dkp, dvp, B, Hq, Hkv, Nq, Nkv, d, int(bool(causal)),
                                d ** -0.5 if scale is None else scale, softcap, *mod, wp, wn, _current_stream(device))
     if st:

@@ -472,8 +472,9 @@ ATTN_API int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_p
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-ATTN_API size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Nq) {
-    return attn::bwd_scoremod_workspace_bytes(B, Hq, Nq);
+ATTN_API size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Hkv, int Nq, int Nkv, int d) {
+    size_t offsets[2];
+    return attn::bwd_scoremod_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d, offsets);
 }
 
 ATTN_API int attn_bwd_scoremod(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -489,7 +490,8 @@ ATTN_API int attn_bwd_scoremod(const void *q, const void *k, const void *v, cons
     if (kv_ctas > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(o) || !aligned16(dout) || !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
         return ATTN_ERR_MISALIGNED;
-    const size_t need = attn::bwd_scoremod_workspace_bytes(B, Hq, Nq);
+    size_t offsets[2];
+    const size_t need = attn::bwd_scoremod_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d, offsets);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     int *status = nullptr;
     st = device_setup(&status);
@@ -500,7 +502,8 @@ ATTN_API int attn_bwd_scoremod(const void *q, const void *k, const void *v, cons
     a.slopes = alibi_slopes;
     a.key_begin = key_begin;
     a.key_end = key_end;
-    a.spans = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + attn::bwd_workspace_bytes(B, Hq, Nq));
+    a.spans = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + offsets[0]);
+    a.kv_parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + offsets[1]);
     cudaError_t e = attn::launch_bwd_scoremod(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -87,6 +87,8 @@ struct BwdModParams : BwdParams {
     const float *slopes;
     float cap_in, cap_out;
     int2 *spans;
+    int kv_splits;    // CTAs per key tile of the dK/dV kernel, each with a share of the query tiles
+    float *kv_parts;  // their sums [split][dV, dK][B, Hkv, Nkv, d] (kv_splits > 1)
 };
 template <bool MOD> struct ParamsOf { using type = BwdParams; };
 template <> struct ParamsOf<true> { using type = BwdModParams; };
@@ -106,12 +108,12 @@ __device__ __forceinline__ int2 bwd_row_span(const BwdModParams &p, int b, int r
 // CTA order (as in the forward): heads in chunks small enough that the chunk's streamed tiles
 // stay in L2; inside a chunk, unit levels in order (level 0 = the heaviest unit of a head
 // under the causal mask) across the chunk's heads.
-__device__ __forceinline__ void unit_of(const BwdParams &p, int n_heads, int &head, int &level) {
+__device__ __forceinline__ void unit_of(const BwdParams &p, int n_heads, unsigned unit, int &head, int &level) {
     const int per_chunk = p.heads_per_chunk * p.units_per_head;
-    const int chunk = (int)(blockIdx.x / per_chunk);
+    const int chunk = (int)(unit / per_chunk);
     const int h0 = chunk * p.heads_per_chunk;
     const int heads = min(p.heads_per_chunk, n_heads - h0);
-    const int in_chunk = (int)(blockIdx.x % per_chunk);
+    const int in_chunk = (int)(unit % per_chunk);
     level = in_chunk / heads;
     head = h0 + in_chunk % heads;
 }
@@ -219,6 +221,26 @@ __device__ __forceinline__ void store_rows(uint32_t tacc, bool have, bool store,
     }
 }
 
+// The same columns as fp32.
+template <int NCOLS>
+__device__ __forceinline__ void store_rows_f32(uint32_t tacc, bool have, bool store, float *dst) {
+#pragma unroll
+    for (int cc = 0; cc < NCOLS / 16; ++cc) {
+        uint32_t v[16];
+        if (have) {
+            tmem_ld16(tacc + cc * 16, v);
+            tmem_wait_ld16(v);
+        }
+        if (store)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4 *>(dst + cc * 16 + i) =
+                    have ? make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                                       __uint_as_float(v[i + 3]))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
 // ================================================================== row term D = rowsum(dO * O)
 // kTpr threads per row (d / 8 rounded up to a power of two), one 16-byte load of O and of dO each
 // for the threads whose 8 columns lie inside d, then a shuffle reduction.
@@ -307,6 +329,11 @@ struct alignas(1024) DkvTiles {
 };
 template <int D, int F> struct DkvSmem : DkvTiles<D>, QuerySpans<kIsMod<F>> {};
 
+template <int F> __device__ __forceinline__ unsigned splits_of(const Params<F> &p) {
+    if constexpr (kIsMod<F>) return (unsigned)p.kv_splits;
+    else return 1u;
+}
+
 // Query tiles a key tile [k0, k0+128) must visit: queries i >= k0 - delta can see its keys
 // under the causal mask (query i sees key j iff j <= i + delta).
 __device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_end, int delta, int &qi_start,
@@ -326,7 +353,7 @@ __device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_en
 template <int D, int F>
 __device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUtensorMap *tmQ, const CUtensorMap *tmdO,
                               const CUtensorMap *tmK, const CUtensorMap *tmV, int b, int hkv, int bh_kv, int k0,
-                              int qi_start, int nqt, int n, WaitCtx wc) {
+                              int qi_start, int nqt, int u0, int n, WaitCtx wc) {
     constexpr int kBoxes = kBBoxes<D>;
     const int lane = threadIdx.x & 31;
     if (lane == 0) {
@@ -342,8 +369,8 @@ __device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUten
     // the row statistics of unit u's 128 queries, four per lane (plain loads, zeros past Nq); they
     // are loaded one unit ahead so their latency hides behind the ring wait
     auto load_stats = [&](int u, float (&l4)[4], float (&d4)[4]) {
-        const int bh_q = b * p.Hq + hkv * p.group + u / nqt;
-        const int q0 = (qi_start + u % nqt) * kT;
+        const int bh_q = b * p.Hq + hkv * p.group + (u0 + u) / nqt;
+        const int q0 = (qi_start + (u0 + u) % nqt) * kT;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int row = q0 + lane * 4 + t;
@@ -363,8 +390,8 @@ __device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUten
     auto load_spans = [&](int u) {
         if constexpr (kIsMod<F>) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + u % nqt) * kT + lane * 4 + t, kv_end);
-            slope_n = p.slopes ? p.slopes[hkv * p.group + u / nqt] * kLog2e : 0.f;
+            for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + (u0 + u) % nqt) * kT + lane * 4 + t, kv_end);
+            slope_n = p.slopes ? p.slopes[hkv * p.group + (u0 + u) / nqt] * kLog2e : 0.f;
         }
     };
     if constexpr (kIsMod<F>) load_spans(0);
@@ -372,7 +399,7 @@ __device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUten
     for (int u = 0; u < n; ++u) {
         const int slot = u % kStages, use = u / kStages;
         if (use > 0 && !__all_sync(kFull, mbar_wait(&sm.u_empty[slot], (uint32_t)((use - 1) & 1), wc, 60))) break;
-        const int g = u / nqt, qi = qi_start + u % nqt;
+        const int g = (u0 + u) / nqt, qi = qi_start + (u0 + u) % nqt;
         const int bh_q = b * p.Hq + hkv * p.group + g;
         const int q0 = qi * kT;
         *reinterpret_cast<float4 *>(&sm.nlse2[slot][lane * 4]) =
@@ -452,7 +479,7 @@ __device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
 
 template <int D, int F>
 __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh_kv, int k0,
-                             int kv_end, int delta, int qi_start, int nqt, int n, WaitCtx wc) {
+                             int kv_end, int delta, int qi_start, int nqt, int u0, int n, WaitCtx wc) {
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
     const uint32_t tS = lane_base + (uint32_t)(w * 64);
@@ -467,7 +494,7 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
     bool ok = true;
     for (int j = 0; j < n; ++j) {
         const int slot = j % kStages;
-        const int col0 = (qi_start + j % nqt) * kT + w * 64;  // query of this half's column 0
+        const int col0 = (qi_start + (u0 + j) % nqt) * kT + w * 64;  // query of this half's column 0
         // valid columns lo <= c < hi: query < Nq, key < kv_end, and key <= query + delta if causal
         int lo = 0, hi = min(64, p.Nq - col0);
         if (p.causal) lo = max(0, key - delta - col0);
@@ -609,6 +636,15 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
     if (!ok) return;
     // warpgroup 0 writes dV, warpgroup 1 writes dK (times scale); rows past Nkv are not stored
     const bool store = key < p.Nkv;
+    if constexpr (kIsMod<F>) {
+        if (p.kv_splits > 1) {  // a part of the queries: fp32 sums, added up by the reduction kernel
+            const size_t rows = (size_t)p.B * p.Hkv * p.Nkv;
+            const size_t part = (size_t)(blockIdx.x % p.kv_splits) * 2 + (w == 0 ? 0 : 1);
+            float *out = p.kv_parts + (part * rows + (size_t)bh_kv * p.Nkv + (store ? key : 0)) * D;
+            store_rows_f32<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, out);
+            return;
+        }
+    }
     __nv_bfloat16 *dst = (w == 0 ? p.dv : p.dk) + ((size_t)bh_kv * p.Nkv + (store ? key : 0)) * D;
     store_rows<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, w == 0 ? 1.f : p.scale, dst);
 }
@@ -624,37 +660,22 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     int bh_kv, level;
-    unit_of(p, p.B * p.Hkv, bh_kv, level);
+    unit_of(p, p.B * p.Hkv, kIsMod<F> ? blockIdx.x / splits_of<F>(p) : blockIdx.x, bh_kv, level);
     const int b = bh_kv / p.Hkv, hkv = bh_kv % p.Hkv;
     const int k0 = level * kT;  // level 0 = key tile 0, seen by the most queries when causal
     const int kv_end = kv_end_for(p, b);
     const int delta = p.Nkv - p.Nq;
     int qi_start = 0, nqt = 0;
-    if constexpr (kIsMod<F>) {
-        if (threadIdx.x == 0) {
-            sm.first = 0x7fffffff;
-            sm.last = -1;
-        }
-        __syncthreads();
-        const int n_qt = (p.Nq + kT - 1) / kT;
-        int first = 0x7fffffff, last = -1;
-        for (int qi = threadIdx.x; qi < n_qt; qi += kThreadsOf<F>) {
-            const int2 s = p.spans[(size_t)b * n_qt + qi];
-            if (s.x < k0 + kT && s.y > k0) {
-                first = min(first, qi);
-                last = qi;
-            }
-        }
-        if (last >= 0) {
-            atomicMin(&sm.first, first);
-            atomicMax(&sm.last, last);
-        }
-    } else {
+    if constexpr (!kIsMod<F>) {
         dkdv_range(p, k0, kv_end, delta, qi_start, nqt);
     }
     int n = nqt * p.group;  // steps: every query tile of every query head of the group
 
     if (threadIdx.x == 0) {
+        if constexpr (kIsMod<F>) {
+            sm.first = 0x7fffffff;
+            sm.last = -1;
+        }
         mbar_init(&sm.kv_full, 1);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sm.u_full[s], 32);
@@ -678,25 +699,45 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
     WaitCtx wc{&sm.abort_flag, p.status};
+    int u0 = 0;  // first of the CTA's steps
     if constexpr (kIsMod<F>) {
+        // the row-term kernel's results are complete from here on; the dQ kernel may start as CTAs leave
+        griddep_wait();
+        griddep_launch_dependents();
+        const int n_qt = (p.Nq + kT - 1) / kT;
+        int first = 0x7fffffff, last = -1;
+        for (int qi = threadIdx.x; qi < n_qt; qi += kThreadsOf<F>) {
+            const int2 s = p.spans[(size_t)b * n_qt + qi];
+            if (s.x < k0 + kT && s.y > k0) {
+                first = min(first, qi);
+                last = qi;
+            }
+        }
+        if (last >= 0) {
+            atomicMin(&sm.first, first);
+            atomicMax(&sm.last, last);
+        }
+        __syncthreads();
         if (sm.last >= 0) {
             qi_start = sm.first;
             nqt = sm.last - sm.first + 1;
         }
-        n = nqt * p.group;
+        const int all = nqt * p.group, split = (int)(blockIdx.x % p.kv_splits);
+        u0 = (int)((long long)all * split / p.kv_splits);
+        n = (int)((long long)all * (split + 1) / p.kv_splits) - u0;
     }
 
     // (each role inside the branch that sets its registers: code after a join gets the smaller limit)
     if (warp >= kProducerWarp) {
         if constexpr (kIsMod<F>) setmaxnreg_dec<kRegsOther>();
         if (warp == kProducerWarp) {
-            if (n > 0) dkdv_producer<D, F>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, n, wc);
+            if (n > 0) dkdv_producer<D, F>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, u0, n, wc);
         } else if (warp == kMmaWarp) {
             if (lane == 0 && n > 0) dkdv_mma<D, F>(sm, tmem, n, wc);
         }
     } else {
         if constexpr (kIsMod<F>) setmaxnreg_inc<kRegsCompute>();
-        dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, n, wc);
+        dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, u0, n, wc);
     }
 
     tc_fence_before_sync();
@@ -929,7 +970,7 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     int bh, level;
-    unit_of(p, p.B * p.Hq, bh, level);
+    unit_of(p, p.B * p.Hq, blockIdx.x, bh, level);
     const int qt = p.units_per_head - 1 - level;  // level 0 = the last query tile (most keys if causal)
     const int b = bh / p.Hq;
     const int bh_kv = b * p.Hkv + (bh % p.Hq) / p.group;
@@ -1002,6 +1043,38 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
+    // modified forms: this grid may have started before the dK/dV grid ended; its completion includes that
+    if constexpr (kIsMod<F>) griddep_wait();
+}
+
+// dV and dK [rows, D] from the splits' sums: four columns per thread, in the splits' order.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_reduce_kernel(const float4 *parts, uint2 *dv, uint2 *dk, long long rows,
+                                                         int splits, float scale) {
+    const long long n4 = rows * (D / 4), i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * n4) return;
+    const bool is_k = i >= n4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+        const float4 v = parts[(long long)s * 2 * n4 + i];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const float f = is_k ? scale : 1.f;
+    (is_k ? dk : dv)[is_k ? i - n4 : i] =
+        make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+}
+
+// Splits of the dK/dV kernel of the modified forms: one CTA per key tile leaves the GPU empty for short
+// sequences with few key/value heads, so the steps of a key tile (query tiles x query heads) are shared
+// out until there are about two CTAs per SM, down to two steps each.
+int dkdv_splits(int B, int Hkv, int group, int Nq, int Nkv) {
+    const long long ctas = (long long)B * Hkv * ((Nkv + kT - 1) / kT);
+    const long long steps = (long long)group * ((Nq + kT - 1) / kT);
+    if (ctas >= 152 || steps < 4) return 1;
+    long long n = (2 * 152 + ctas - 1) / ctas;
+    if (n > steps / 2) n = steps / 2;
+    return (int)(n > 16 ? 16 : n);
 }
 
 int heads_per_chunk(double bytes_per_head, int n_heads) {
@@ -1054,6 +1127,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
         p.cap_out = a.softcap * kLog2e;
         p.spans = a.spans;
+        p.kv_splits = dkdv_splits(a.B, a.Hkv, p.group, a.Nq, a.Nkv);
+        p.kv_parts = a.kv_parts;
     }
 
     {
@@ -1083,8 +1158,13 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dkdv_kernel<D, F>), (int)smem);
         if (e != cudaSuccess) return e;
         const unsigned grid = (unsigned)((size_t)pk.units_per_head * BHkv);
-        bwd_dkdv_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pk);
-        e = cudaGetLastError();
+        if constexpr (kIsMod<F>) {
+            e = launch_dependent(bwd_dkdv_kernel<D, F>, dim3(grid * p.kv_splits), kThreadsOf<F>, smem, stream, tq, tdo, tk,
+                                 tv, pk);
+        } else {
+            bwd_dkdv_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pk);
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
     }
     // dQ: one CTA per (batch, query head, query tile); streams K and V of its key/value head
@@ -1098,9 +1178,23 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(bwd_dq_kernel<D, F>), (int)smem);
         if (e != cudaSuccess) return e;
         const unsigned grid = (unsigned)((size_t)pq.units_per_head * BHq);
-        bwd_dq_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pq);
-        e = cudaGetLastError();
+        if constexpr (kIsMod<F>) {
+            e = launch_dependent(bwd_dq_kernel<D, F>, dim3(grid), kThreadsOf<F>, smem, stream, tq, tdo, tk, tv, pq);
+        } else {
+            bwd_dq_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pq);
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
+    }
+    if constexpr (kIsMod<F>) {
+        if (p.kv_splits > 1) {
+            const long long kv_rows = (long long)a.B * a.Hkv * a.Nkv;
+            bwd_reduce_kernel<D><<<(unsigned)((kv_rows * (D / 2) + 255) / 256), 256, 0, stream>>>(
+                reinterpret_cast<const float4 *>(p.kv_parts), reinterpret_cast<uint2 *>(p.dv),
+                reinterpret_cast<uint2 *>(p.dk), kv_rows, p.kv_splits, a.scale);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
     }
     return cudaSuccess;
 }

@@ -25,10 +25,14 @@ cudaError_t launch_bwd_scoremod(const BwdArgs &a, cudaStream_t stream) {
     }
 }
 
-// The row term, then {lo, hi} of each query tile's keys.
-size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Nq) {
+// The row term, then {lo, hi} of each query tile's keys, then the dK/dV sums of the splits.
+size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d, size_t (&offsets)[2]) {
     const size_t dterm = bwd_workspace_bytes(B, Hq, Nq);
-    return dterm == 0 ? 0 : dterm + (size_t)B * (((size_t)Nq + kT - 1) / kT) * sizeof(int2);
+    if (dterm == 0 || Hkv <= 0 || Hq % Hkv != 0 || Nkv <= 0 || d <= 0) return 0;
+    offsets[0] = dterm;
+    offsets[1] = (dterm + (size_t)B * (((size_t)Nq + kT - 1) / kT) * sizeof(int2) + 255) & ~(size_t)255;
+    const int splits = dkdv_splits(B, Hkv, Hq / Hkv, Nq, Nkv);
+    return offsets[1] + (splits > 1 ? (size_t)splits * 2 * B * Hkv * Nkv * d * sizeof(float) : 0);
 }
 
 }  // namespace attn

@@ -45,13 +45,13 @@ struct RowsParams {
     float cap_in, cap_out;
     const float *slopes;       // [H], may be null
     const int32_t *key_begin;  // [B], may be null
+    int chunk_pages;           // pages per split
 };
 
 namespace {
 
 constexpr int kRowWarps = 4;
 constexpr int kRowPS = 16;
-constexpr int kRowChunkPages = 64;  // pages per split of the decode with modified scores
 constexpr float kRowLog2e = 1.4426950408889634f;
 constexpr float kRowLn2 = 0.6931471805599453f;
 // Ring slots (page blocks of K and V in flight) per warp.
@@ -92,8 +92,8 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
     const int pages = (r.hi + kRowPS - 1) / kRowPS;
     if constexpr (MOD) {
         r.lo = a.key_begin ? min(max(a.key_begin[b], 0), r.hi) : 0;
-        r.p0 = max(split * kRowChunkPages, r.lo / kRowPS);
-        r.p1 = r.lo < r.hi ? min((split + 1) * kRowChunkPages, pages) : 0;
+        r.p0 = max(split * a.chunk_pages, r.lo / kRowPS);
+        r.p1 = r.lo < r.hi ? min((split + 1) * a.chunk_pages, pages) : 0;
     } else {
         r.lo = 0;
         const int base = a.S > 0 ? min(max(a.shared_pages[b / a.S], 0), a.max_pages) : 0;
@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
     int s0 = 0, s1 = a.ws_first + a.n_splits;
     if constexpr (MOD) {  // only the splits with a visible page were written
         const PageRange r = rows_range<true>(a, b, 0);
-        s0 = r.lo / (kRowChunkPages * kRowPS);
-        s1 = r.lo < r.hi ? (r.hi + kRowChunkPages * kRowPS - 1) / (kRowChunkPages * kRowPS) : 0;
+        s0 = r.lo / (a.chunk_pages * kRowPS);
+        s1 = r.lo < r.hi ? (r.hi + a.chunk_pages * kRowPS - 1) / (a.chunk_pages * kRowPS) : 0;
     }
     const float *ws = a.ws + (size_t)row * a.ws_splits * (D + 4);
     float M = -INFINITY, L = 0.f;
@@ -522,15 +522,21 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
         L = L * al + ls;
         acc.x *= al, acc.y *= al, acc.z *= al, acc.w *= al;
         const int n = min(32, s1 - base);
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-            const float ms = __shfl_sync(0xffffffffu, ml.x, s), wt = __shfl_sync(0xffffffffu, w, s);
-            if (ms != -INFINITY && 4 * lane < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(ws + (size_t)(base + s) * (D + 4) + 4 * lane);
-                acc.x = fmaf(v.x, wt, acc.x);
-                acc.y = fmaf(v.y, wt, acc.y);
-                acc.z = fmaf(v.z, wt, acc.z);
-                acc.w = fmaf(v.w, wt, acc.w);
+        const uint32_t some = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+        for (int s = 0; s < n; s += 8) {  // eight partials' columns in flight
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 4 * lane < D && ((some >> (s + i)) & 1u)
+                           ? *reinterpret_cast<const float4 *>(ws + (size_t)(base + s + i) * (D + 4) + 4 * lane)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wt = __shfl_sync(0xffffffffu, w, s + i);
+                acc.x = fmaf(v[i].x, wt, acc.x);
+                acc.y = fmaf(v[i].y, wt, acc.y);
+                acc.z = fmaf(v[i].z, wt, acc.z);
+                acc.w = fmaf(v[i].w, wt, acc.w);
             }
         }
     }
@@ -540,22 +546,6 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
         *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + (size_t)row * D + 4 * lane) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (lane == 0 && a.lse) a.lse[row] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
-}
-
-// Launches a kernel that may start while the one before it on the stream drains (it waits by itself).
-template <class K, class... A>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // The rows kernel (dependent: it may overlap the grid before it) and the merge.

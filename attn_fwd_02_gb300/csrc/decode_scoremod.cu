@@ -1,12 +1,26 @@
 // decode_scoremod.cu -- paged decode with modified scores: s = cap tanh(scale q.k / cap) - slope (ctx - 1 -
-// j) over the cached tokens key_begin <= j < ctx.  Splits of 64 pages; pages before key_begin are not read.
+// j) over the cached tokens key_begin <= j < ctx.  Pages before key_begin are not read.
 #include "decode_rows.cuh"
 
 namespace attn {
+namespace {
+
+// Pages per split: 64 (1024 tokens) where that fills the GPU several times over, down to 8 for small
+// batches, whose latency is that of one split's pages.
+int chunk_pages_for(int B, int H, int Hkv, int max_pages) {
+    const int group = H / Hkv;
+    const long long rows = (long long)B * Hkv * (group <= 8 ? 1 : (group + 15) / 16);
+    int chunk = 64;
+    while (chunk > 8 && rows * ((max_pages + chunk - 1) / chunk) < 4 * 152) chunk /= 2;
+    return chunk;
+}
+
+}  // namespace
 
 size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size) {
     if (decode_workspace_bytes(B, H, Hkv, d, max_pages, page_size) == 0) return 0;  // unsupported sizes
-    const size_t splits = ((size_t)max_pages + kRowChunkPages - 1) / kRowChunkPages;
+    const size_t chunk = (size_t)chunk_pages_for(B, H, Hkv, max_pages);
+    const size_t splits = ((size_t)max_pages + chunk - 1) / chunk;
     return (size_t)B * H * splits * (size_t)(d + 4) * sizeof(float);
 }
 
@@ -25,7 +39,8 @@ cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream) {
     p.group = a.H / a.Hkv;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
-    p.n_splits = p.ws_splits = (a.max_pages + kRowChunkPages - 1) / kRowChunkPages;
+    p.chunk_pages = chunk_pages_for(a.B, a.H, a.Hkv, a.max_pages);
+    p.n_splits = p.ws_splits = (a.max_pages + p.chunk_pages - 1) / p.chunk_pages;
     const float kscale = a.scale * (a.kv_fp8 ? a.k_scale : 1.f);
     p.c = kscale * kRowLog2e;
     p.v_scale = a.v_scale;

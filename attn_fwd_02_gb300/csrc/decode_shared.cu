@@ -41,7 +41,7 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
     }
     const int rgroups = pl.group <= 8 ? 1 : (pl.group + 15) / 16;
     const long long rows = (long long)B * Hkv * rgroups;
-    const long long want = (2LL * kSms * 6 + rows - 1) / rows, most = (max_pages + 31) / 32;
+    const long long want = (4LL * kSms + rows - 1) / rows, most = (max_pages + 31) / 32;
     pl.own_splits = (int)(want < most ? want : most);
     return pl;
 }

@@ -68,6 +68,7 @@ struct BwdArgs {
     const float *slopes = nullptr;
     const int32_t *key_begin = nullptr, *key_end = nullptr;
     int2 *spans = nullptr;
+    float *kv_parts = nullptr;
 };
 
 // Per-device facts looked up once (host-side caches shared by the launchers): the SM count
@@ -83,6 +84,23 @@ bool encode_qkv_map(CUtensorMap *m, const void *ptr, int BH, int N, int D, int b
 // with the 128-byte swizzle or none; the bytes of a box past D are read as zeros.
 bool encode_page_map_u8(CUtensorMap *m, const void *ptr, int rows, int page_rows, int D, bool swizzle = true);
 
+// Launches a kernel that may start while the one before it on the stream drains (griddepcontrol.wait in
+// the kernel orders it after that one's completion).
+template <class K, class... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Query heads of a decode batch, [B, H, D] bf16, in swizzled boxes of 64 columns x heads x seqs rows.
 bool encode_q_heads_map(CUtensorMap *m, const void *ptr, int B, int H, int D, int heads, int seqs);
 
@@ -95,7 +113,8 @@ cudaError_t launch_prefill_scoremod(const PrefillArgs &a, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdArgs &a, cudaStream_t stream);
 size_t bwd_workspace_bytes(int B, int Hq, int Nq);
 cudaError_t launch_bwd_scoremod(const BwdArgs &a, cudaStream_t stream);
-size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Nq);
+// Bytes of its workspace; offsets: where the query tiles' intervals and the dK/dV sums start in it.
+size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d, size_t (&offsets)[2]);
 
 // Writes new tokens' K/V into their pages (token t of sequence b goes to position
 // start_pos[b] + t).  Positions past the table's capacity are skipped.

@@ -419,11 +419,11 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *o, const f
  *     dV = P^T dO,   dK = scale (dS (1 - t^2))^T Q,   dQ = scale (dS (1 - t^2)) K
  * (without the cap the factor is 1; the slopes and the intervals get no gradient).
  *   lse, o: attn_fwd_scoremod's for the same inputs and modification; dout finite
- *   workspace: at least attn_bwd_scoremod_workspace_size(B, Hq, Nq) bytes, 16-byte aligned
+ *   workspace: at least attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d) bytes, 16-byte aligned
  * Rows of k and v past kv_lens[b] may hold anything; dk and dv get zeros there.  Other arguments as
  * attn_bwd and attn_fwd_scoremod.
  */
-size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Nq);
+size_t attn_bwd_scoremod_workspace_size(int B, int Hq, int Hkv, int Nq, int Nkv, int d);
 
 int attn_bwd_scoremod(const void *q, const void *k, const void *v, const void *o, const float *lse,
                       const void *dout, void *dq, void *dk, void *dv, int B, int Hq, int Hkv, int Nq, int Nkv,
