@@ -272,17 +272,11 @@ __device__ __forceinline__ int tiles_for(const PrefillParams &p, int qs, int kv_
 }
 
 // ------------------------------------------------------------------ producer
-// Contiguous K/V: the loads that need no ring wait -- Q and the first kStages units -- issued by
-// the producer thread before the CTA's start-up barrier, so they overlap the TMEM allocation and
-// the other warps' start (at d = 64 this took the start of a CTA from about 5000 to 4200 cycles
-// and the decoder workload's span from 28.4 to 25.1 us in a timestamped copy).  Returns the first
-// unit left for run_producer.
+// Descriptors into the cache, and the load of the CTA's query tiles.
 template <int D, int M>
-__device__ int producer_start(PrefillSmem<D, M> &sm, const PrefillParams &p, const CUtensorMap *tmQ,
-                              const CUtensorMap *tmK, const CUtensorMap *tmV, int bh, int bh_kv, int q0, int n_all) {
-    static_assert(M == kContig, "contiguous K/V only");
+__device__ __forceinline__ void issue_q(PrefillSmem<D, M> &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                                        const CUtensorMap *tmV, int bh, int q0) {
     constexpr int kBoxes = kPad<D> / 64;
-    constexpr int kBN = kBNd<D>;
     prefetch_tensormap(tmQ);
     prefetch_tensormap(tmK);
     prefetch_tensormap(tmV);
@@ -292,14 +286,29 @@ __device__ int producer_start(PrefillSmem<D, M> &sm, const PrefillParams &p, con
 #pragma unroll
         for (int i = 0; i < kBoxes; ++i)
             tma_load_3d(sm.q[t] + i * (kBM * 64), tmQ, &sm.q_full, i * 64, q0 + t * kBM, bh);
+}
+
+// Contiguous K/V: the loads that need no ring wait -- Q and the first kStages units -- issued by
+// the producer thread before the CTA's start-up barrier, so they overlap the TMEM allocation and
+// the other warps' start (at d = 64 this took the start of a CTA from about 5000 to 4200 cycles
+// and the decoder workload's span from 28.4 to 25.1 us in a timestamped copy).  Returns the first
+// unit left for run_producer.
+template <int D, int M>
+__device__ int producer_start(PrefillSmem<D, M> &sm, const PrefillParams &p, const CUtensorMap *tmQ,
+                              const CUtensorMap *tmK, const CUtensorMap *tmV, int bh, int bh_kv, int q0, int n_all,
+                              int j0) {
+    static_assert(!kIsPaged<M>, "contiguous K/V only");
+    constexpr int kBoxes = kPad<D> / 64;
+    constexpr int kBN = kBNd<D>;
+    if constexpr (!kIsMod<M>) issue_q<D, M>(sm, tmQ, tmK, tmV, bh, q0);
     const int first = n_all + 1 < kStagesOf<D> ? n_all + 1 : kStagesOf<D>;
     for (int u = 0; u < first; ++u) {
         const bool has_k = u < n_all, has_v = u > 0;
         mbar_arrive_expect_tx(&sm.u_full[u], ((has_k ? 1 : 0) + (has_v ? 1 : 0)) * kBoxes * kKvBoxBytes<D>);
 #pragma unroll
         for (int i = 0; i < kBoxes; ++i) {
-            if (has_k) tma_load_3d(sm.k[u] + i * (kBN * 64), tmK, &sm.u_full[u], i * 64, u * kBN, bh_kv);
-            if (has_v) tma_load_3d(sm.v[u] + i * (kBN * 64), tmV, &sm.u_full[u], i * 64, (u - 1) * kBN, bh_kv);
+            if (has_k) tma_load_3d(sm.k[u] + i * (kBN * 64), tmK, &sm.u_full[u], i * 64, (j0 + u) * kBN, bh_kv);
+            if (has_v) tma_load_3d(sm.v[u] + i * (kBN * 64), tmV, &sm.u_full[u], i * 64, (j0 + u - 1) * kBN, bh_kv);
         }
     }
     return first;
@@ -930,7 +939,7 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
     if (ok && n_tiles > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done[t], 0, wc, 22 + t))) ok = false;
         else tc_fence_after_sync();
-    } else if (ok && n_all > 0) {
+    } else if (ok && (kIsMod<M> || n_all > 0)) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, wc, 24))) ok = false;
     }
     if (!ok) return;
@@ -1007,7 +1016,8 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
             for (int i = 0; i < kPad<D> / 64; ++i)
                 if (i * 64 < D) tma_store_3d(tmO, reinterpret_cast<const uint8_t *>(sm.q[t]) + i * (kBM * 128), i * 64, qs, bh);
             bulk_commit_group();
-            bulk_wait_group_all();
+            if constexpr (kIsMod<M>) bulk_wait_group_read_all();
+            else bulk_wait_group_all();
         }
     }
 }
@@ -1126,7 +1136,30 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
         sm.abort_flag = 0;
         fence_mbar_init();
         if constexpr (M == kContig) {
-            if (n_all > 0) u_begin = producer_start<D, M>(sm, p, &tmQ, &tmK, &tmV, bh, bh_kv, q0, n_all);
+            if (n_all > 0) u_begin = producer_start<D, M>(sm, p, &tmQ, &tmK, &tmV, bh, bh_kv, q0, n_all, 0);
+        }
+        // intervals: the queries are loaded before it is known whether they see a key (run_softmax waits
+        // for them in any case)
+        if constexpr (kIsMod<M>) issue_q<D, M>(sm, &tmQ, &tmK, &tmV, bh, q0);
+    }
+    if constexpr (kIsMod<M>) {
+        // The producer warp finds the CTA's key tiles by itself, so that their first loads do not wait for
+        // the start-up barrier.
+        if (warp == Cfg<D>::kProducerWarp) {
+            int lo = 0x7fffffff, hi = 0;
+#pragma unroll
+            for (int i = 0; i < Cfg<D>::QT * kBM / 32; ++i) {
+                const RowSpan s = row_span(p, b, q0 + i * 32 + lane, kv_end, delta);
+                lo = min(lo, s.lo < s.hi ? s.lo : 0x7fffffff);
+                hi = max(hi, s.lo < s.hi ? s.hi : 0);
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (lane == 0 && hi > 0) {
+                const int first = lo / kBNd<D>;
+                u_begin = producer_start<D, M>(sm, p, &tmQ, &tmK, &tmV, bh, bh_kv, q0,
+                                               (hi + kBNd<D> - 1) / kBNd<D> - first, first);
+            }
         }
     }
     if (warp == Cfg<D>::kMmaWarp) {
