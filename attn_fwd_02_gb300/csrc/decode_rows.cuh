@@ -105,7 +105,7 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
 }
 
 template <int D, bool FP8, int NT, bool MOD>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, 4)
     decode_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const RowsParams a) {
     constexpr int kSl = kRowSlots<FP8>;
