@@ -522,15 +522,28 @@ def paged_kv_append(k_new, v_new, k_pages, v_pages, page_table, start_pos, strea
 
 
 def _torch():
-    """torch, imported at the first call (the module itself loads without it)."""
-    global _t
+    """torch, imported at the first call (the module itself loads without it), and with it the compiled
+    marshalling if it was built against this torch."""
+    global _t, _fast
     if _t is None:
         import torch
+        lib = load_library()
+        try:
+            from . import _fastcall
+        except ImportError:
+            _fastcall = None
+        if _fastcall is not None and _fastcall.torch_version == torch.__version__.split("+")[0]:
+            address = {n: ctypes.cast(getattr(lib, n), P).value for n in SIGNATURES}
+            if _fastcall.bind(address):
+                _fast = _fastcall
         _t = torch
     return _t
 
 
 _t = None
+# Compiled marshalling (csrc/fastcall.cpp): each function takes the call's arguments and returns its
+# result, the library's status, or None for a call that goes through the checks below.
+_fast = None
 
 
 def _in(t, name, dtype, ndim, device=None):
@@ -551,7 +564,7 @@ def _elsewhere(device, stream):
     """Context that makes ``stream`` (None: the device's current stream) and its device current, or
     None if they already are.  Tensors allocated inside belong to that stream, so the allocator does
     not hand their memory to another stream's work while the call still uses it."""
-    torch = _t
+    torch = _torch()
     if stream is None:
         return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     if stream.device != device:
@@ -641,6 +654,15 @@ def _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_
     return q_out
 
 
+def _appended(fn, r):
+    """The compiled append's answer: q_out, False (no query), or a status."""
+    if r is False:
+        return None
+    if r.__class__ is int:
+        _check(fn, r)
+    return r
+
+
 def paged_kv_append_rope(q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos, interleaved: bool = False,
                          new_lens=None, q_out=None, stream=None):
     """Rotates new tokens' queries and keys to their positions and appends keys and values to the
@@ -650,6 +672,11 @@ def paged_kv_append_rope(q, k_new, v_new, k_pages, v_pages, cos_sin, page_table,
     optional [B] int32, the tokens past it being padding, of which nothing is written (allocated
     q_out rows of padding are uninitialised).  Returns q_out [B,H,Nnew,d] bf16, contiguous (q itself
     may be given if contiguous)."""
+    if _fast is not None and stream is None:
+        r = _fast.append_rope(None, q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos, interleaved,
+                              new_lens, q_out)
+        if r is not None:
+            return _appended("paged_kv_append_rope", r)
     return _append_rope("paged_kv_append_rope", q, k_new, v_new, k_pages, v_pages, _torch().bfloat16, (), cos_sin,
                         page_table, start_pos, interleaved, new_lens, q_out, stream)
 
@@ -657,6 +684,11 @@ def paged_kv_append_rope(q, k_new, v_new, k_pages, v_pages, cos_sin, page_table,
 def paged_kv_append_rope_fp8(q, k_new, v_new, k_pages, v_pages, k_scale: float, v_scale: float, cos_sin, page_table,
                              start_pos, interleaved: bool = False, new_lens=None, q_out=None, stream=None):
     """paged_kv_append_rope into an e4m3 cache (k_pages, v_pages uint8 [P,Hkv,16,d])."""
+    if _fast is not None and stream is None:
+        r = _fast.append_rope((k_scale, v_scale), q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos,
+                              interleaved, new_lens, q_out)
+        if r is not None:
+            return _appended("paged_kv_append_rope_fp8", r)
     return _append_rope("paged_kv_append_rope_fp8", q, k_new, v_new, k_pages, v_pages, _torch().uint8,
                         (float(k_scale), float(v_scale)), cos_sin, page_table, start_pos, interleaved, new_lens,
                         q_out, stream)
@@ -710,6 +742,13 @@ def attn_fwd_scoremod(q, k, v, causal: bool, scale: float | None = None, softcap
     over the keys key_begin[b,i] <= j < key_end[b,i] (and kv_lens, causal).  q [B,Hq,Nq,d], k/v
     [B,Hkv,Nkv,d] bf16; alibi_slopes [Hq] fp32; key_begin, key_end [B,Nq] int32; kv_lens [B] int32, all
     optional CUDA tensors; softcap 0 is none.  Returns (o, lse)."""
+    if _fast is not None and stream is None:
+        r = _fast.fwd_scoremod(q, k, v, causal, scale, softcap, alibi_slopes, key_begin, key_end, kv_lens, out, lse,
+                               return_lse)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("attn_fwd_scoremod", r)
     device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d = _dense_inputs(q, k, v)
     mod = _scoremod_inputs(device, B, Hq, Nq, alibi_slopes, key_begin, key_end, kv_lens)
     ctx = _elsewhere(device, stream)
@@ -747,6 +786,13 @@ def attn_bwd_scoremod(q, k, v, o, lse, dout, causal: bool, scale: float | None =
     """Backward of attn_fwd_scoremod: q, o, dout [B,Hq,Nq,d] and k, v [B,Hkv,Nkv,d] bf16, lse [B,Hq,Nq]
     fp32 from the forward, the modification as in the forward call.  Returns (dq, dk, dv) bf16.
     workspace: optional uint8 tensor of attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d) bytes."""
+    if _fast is not None and stream is None:
+        r = _fast.bwd_scoremod(q, k, v, o, lse, dout, causal, scale, softcap, alibi_slopes, key_begin, key_end, kv_lens,
+                               dq, dk, dv, workspace)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("attn_bwd_scoremod", r)
     device, qp, kp, vp, B, Hq, Hkv, Nq, Nkv, d = _dense_inputs(q, k, v)
     bf = _t.bfloat16
     op, lp = _in(o, "o", bf, 4, device), _in(lse, "lse", _t.float32, 3, device)
@@ -809,6 +855,13 @@ def _decode_outputs(out, lse, return_lse, B, H, d, device):
 
 def _decode_scoremod(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes,
                      key_begin, out, lse, workspace, return_lse, stream):
+    if _fast is not None and stream is None:
+        r = _fast.decode_scoremod(scales or None, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap,
+                                  alibi_slopes, key_begin, out, lse, workspace, return_lse)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(fn, r)
     device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens)
     B, H, Hkv, d, max_pages, num_pages = sizes
     slopes = _optional(alibi_slopes, "alibi_slopes", _t.float32, (H,), device)
@@ -852,6 +905,13 @@ def paged_attn_decode_scoremod_fp8(q, k_pages, v_pages, k_scale: float, v_scale:
 
 def _decode_shared(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, shared_pages, group_size, scale,
                    out, lse, workspace, return_lse, stream):
+    if _fast is not None and stream is None:
+        r = _fast.decode_shared(scales or None, q, k_pages, v_pages, page_table, ctx_lens, shared_pages, group_size,
+                                scale, out, lse, workspace, return_lse)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(fn, r)
     device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens)
     B, H, Hkv, d, max_pages, num_pages = sizes
     if group_size <= 0 or B % group_size:

@@ -5,20 +5,26 @@
 Each translation unit under csrc/ compiles in parallel to an object file under
 _build/, then nvcc links them into attn_fwd_02_gb300/libattn_gb300.so with the
 CUDA runtime linked statically (the library loads without a GPU present).
+g++ also compiles csrc/fastcall.cpp, the binding's compiled argument marshalling, into
+_fastcall.so against the installed torch; where that is not possible (no Python or torch
+headers), the binding marshals in Python alone, with the same results.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libattn_gb300.so")
+FAST_SRC, FAST_OUT = os.path.join(CSRC, "fastcall.cpp"), os.path.join(HERE, "_fastcall.so")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -59,14 +65,42 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_fastcall() -> str | None:
+    header = os.path.join(ROOT, "include", "attn_gb300.h")
+    if os.path.exists(FAST_OUT) and os.path.getmtime(FAST_OUT) >= max(map(os.path.getmtime, (FAST_SRC, header))):
+        return FAST_OUT
+    spec = importlib.util.find_spec("torch")
+    torch = spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else ""
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    inc = [os.path.dirname(header), os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+    tmp = FAST_OUT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{i}" for i in inc), FAST_SRC,
+           "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr if r.returncode else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        sys.stderr.write(f"fastcall.cpp was not compiled (the binding marshals in Python):\n{why[-2000:]}\n")
+        return None
+    os.replace(tmp, FAST_OUT)
+    return FAST_OUT
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for f in os.listdir(BUILD):
             if f.endswith(".o"):
                 os.remove(os.path.join(BUILD, f))
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        if os.path.exists(FAST_OUT):
+            os.remove(FAST_OUT)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(_compile_fastcall)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        fast.result()
     if os.path.exists(OUT) and os.path.getmtime(OUT) >= max(os.path.getmtime(o) for o in objs) and not force:
         return OUT
     tmp = OUT + f".tmp{os.getpid()}"
