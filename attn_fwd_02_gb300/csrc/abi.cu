@@ -132,7 +132,7 @@ cudaError_t ensure_max_dynamic_smem(const void *kernel, int bytes) {
         int dev;
         int bytes;
     };
-    static Entry done[256];
+    static Entry done[512];
     static int n_done = 0;
     static std::mutex mu;
     int dev = -1;
@@ -143,7 +143,7 @@ cudaError_t ensure_max_dynamic_smem(const void *kernel, int bytes) {
         if (done[i].fn == kernel && done[i].dev == dev && done[i].bytes >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (n_done < 256) done[n_done++] = Entry{kernel, dev, bytes};
+    if (n_done < 512) done[n_done++] = Entry{kernel, dev, bytes};
     return cudaSuccess;
 }
 
@@ -238,6 +238,7 @@ namespace {
 int scoremod_checks(float factor, float softcap, const float *alibi_slopes, const int32_t *key_begin,
                     const int32_t *key_end) {
     constexpr float kMost = 1.2676506e30f;  // 2^100
+    if (!(factor > 0.f) || !(factor < 3.0e38f)) return ATTN_ERR_INVALID_ARG;
     if (!(softcap >= 0.f) || !(softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
     if (softcap > 0.f && !(factor / softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
     if (!aligned4(alibi_slopes) || !aligned4(key_begin) || !aligned4(key_end)) return ATTN_ERR_MISALIGNED;
@@ -611,6 +612,7 @@ int decode_scoremod(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t st
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
     if (st != ATTN_OK) return st;
+    if ((uint64_t)a.B * (uint64_t)a.H > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
     if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
     st = scoremod_checks(a.scale * a.k_scale, a.softcap, a.slopes, a.key_begin, nullptr);
     if (st != ATTN_OK) return st;
@@ -627,8 +629,9 @@ int decode_shared(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stre
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
     if (st != ATTN_OK) return st;
-    if (a.B % a.group_size != 0) return ATTN_ERR_INVALID_ARG;
-    if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (a.B % a.group_size != 0 || (uint64_t)a.B * (uint64_t)a.H > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
+    if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale) || !finite_positive(a.scale * a.k_scale))
+        return ATTN_ERR_INVALID_ARG;
     if (!aligned4(a.shared_pages)) return ATTN_ERR_MISALIGNED;
     const size_t need = attn::decode_shared_workspace_bytes(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size, a.page_size);
     if (!a.workspace || !aligned16(a.workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
@@ -764,10 +767,10 @@ ATTN_API int attn_last_device_status(void) {
 ATTN_API const char *attn_status_string(int status) {
     switch (status) {
         case ATTN_OK: return "ok";
-        case ATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or oversized dimension, bad scale)";
+        case ATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or oversized dimension, bad scale or cap)";
         case ATTN_ERR_UNSUPPORTED: return "unsupported (head dim 32, 64, 80, 96 or 128; 64 or 128 for the backward; page size 16; device sm_103)";
         case ATTN_ERR_MISALIGNED: return "misaligned pointer (tensors need 16-byte alignment)";
-        case ATTN_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than paged_attn_decode_workspace_size() (decode) or attn_bwd_workspace_size() (backward)";
+        case ATTN_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than the call's *_workspace_size() (paged_attn_decode_workspace_size(), attn_bwd_workspace_size() and so on)";
         case ATTN_ERR_CUDA: return "CUDA runtime error or launch failure";
         case ATTN_ERR_DEVICE_TIMEOUT: return "a bounded in-kernel wait ran out; results of the affected calls are invalid, and calls launch nothing until attn_check_device_status() clears it";
         case ATTN_ERR_SCRATCH_LIMIT: return "sizes need more decode scratch than the 12 MiB static array of paged_attn_decode_noalloc (use paged_attn_decode with a workspace)";

@@ -102,7 +102,7 @@ __device__ __forceinline__ int2 bwd_row_span(const BwdModParams &p, int b, int r
     s.x = p.key_begin ? max(p.key_begin[at], 0) : 0;
     s.y = p.key_end ? min(p.key_end[at], kv_end) : kv_end;
     if (p.causal) s.y = min(s.y, row + p.Nkv - p.Nq + 1);
-    return s;
+    return s.x < s.y ? s : make_int2(0, 0);  // (the bounds given may be any int)
 }
 
 // CTA order (as in the forward): heads in chunks small enough that the chunk's streamed tiles

@@ -548,17 +548,18 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
     if (lane == 0 && a.lse) a.lse[row] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
 }
 
+// Page boxes of the rows kernel over a pool of `pool` page blocks.
+template <int D>
+bool encode_rows_maps(bool fp8, const void *k_pages, const void *v_pages, int pool, CUtensorMap &tk, CUtensorMap &tv) {
+    return fp8 ? (encode_page_map_u8(&tk, k_pages, pool, kRowPS, D) && encode_page_map_u8(&tv, v_pages, pool, kRowPS, D))
+               : (encode_qkv_map(&tk, k_pages, pool, kRowPS, D, kRowPS) &&
+                  encode_qkv_map(&tv, v_pages, pool, kRowPS, D, kRowPS));
+}
+
 // The rows kernel (dependent: it may overlap the grid before it) and the merge.
 template <int D, bool FP8, int NT, bool MOD>
-cudaError_t launch_rows_n(const RowsParams &p, const void *k_pages, const void *v_pages, bool dependent,
+cudaError_t launch_rows_n(const RowsParams &p, const CUtensorMap &tk, const CUtensorMap &tv, bool dependent,
                           cudaStream_t stream) {
-    CUtensorMap tk{}, tv{};
-    const int pool = p.num_pages * p.Hkv;
-    const bool ok = FP8 ? (encode_page_map_u8(&tk, k_pages, pool, kRowPS, D) &&
-                           encode_page_map_u8(&tv, v_pages, pool, kRowPS, D))
-                        : (encode_qkv_map(&tk, k_pages, pool, kRowPS, D, kRowPS) &&
-                           encode_qkv_map(&tv, v_pages, pool, kRowPS, D, kRowPS));
-    if (!ok) return cudaErrorInvalidValue;
     const size_t smem = sizeof(RowsSmem<D, FP8, NT>) + 1024;
     auto kernel = decode_rows_kernel<D, FP8, NT, MOD>;
     cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem);
@@ -577,26 +578,14 @@ cudaError_t launch_rows_n(const RowsParams &p, const void *k_pages, const void *
 
 // Up to 8 query heads per key/value head take one n-tile of 8; larger groups take 16 heads per CTA.
 template <int D, bool MOD>
-cudaError_t launch_rows_d(RowsParams p, const void *k_pages, const void *v_pages, bool fp8, bool dependent,
+cudaError_t launch_rows_d(RowsParams p, const CUtensorMap &tk, const CUtensorMap &tv, bool fp8, bool dependent,
                           cudaStream_t stream) {
     p.rgroups = p.group <= 8 ? 1 : (p.group + 15) / 16;
     if (fp8)
-        return p.group <= 8 ? launch_rows_n<D, true, 1, MOD>(p, k_pages, v_pages, dependent, stream)
-                            : launch_rows_n<D, true, 2, MOD>(p, k_pages, v_pages, dependent, stream);
-    return p.group <= 8 ? launch_rows_n<D, false, 1, MOD>(p, k_pages, v_pages, dependent, stream)
-                        : launch_rows_n<D, false, 2, MOD>(p, k_pages, v_pages, dependent, stream);
-}
-template <bool MOD>
-cudaError_t launch_rows(const RowsParams &p, int d, const void *k_pages, const void *v_pages, bool fp8, bool dependent,
-                        cudaStream_t stream) {
-    switch (d) {
-        case 32: return launch_rows_d<32, MOD>(p, k_pages, v_pages, fp8, dependent, stream);
-        case 64: return launch_rows_d<64, MOD>(p, k_pages, v_pages, fp8, dependent, stream);
-        case 80: return launch_rows_d<80, MOD>(p, k_pages, v_pages, fp8, dependent, stream);
-        case 96: return launch_rows_d<96, MOD>(p, k_pages, v_pages, fp8, dependent, stream);
-        case 128: return launch_rows_d<128, MOD>(p, k_pages, v_pages, fp8, dependent, stream);
-        default: return cudaErrorInvalidValue;
-    }
+        return p.group <= 8 ? launch_rows_n<D, true, 1, MOD>(p, tk, tv, dependent, stream)
+                            : launch_rows_n<D, true, 2, MOD>(p, tk, tv, dependent, stream);
+    return p.group <= 8 ? launch_rows_n<D, false, 1, MOD>(p, tk, tv, dependent, stream)
+                        : launch_rows_n<D, false, 2, MOD>(p, tk, tv, dependent, stream);
 }
 
 }  // namespace

@@ -15,6 +15,13 @@ int chunk_pages_for(int B, int H, int Hkv, int max_pages) {
     return chunk;
 }
 
+template <int D>
+cudaError_t launch_decode_scoremod_d(const DecodeArgs &a, const RowsParams &p, cudaStream_t stream) {
+    CUtensorMap tk, tv;
+    if (!encode_rows_maps<D>(a.kv_fp8 != 0, a.k_pages, a.v_pages, a.num_pages * a.Hkv, tk, tv)) return cudaErrorInvalidValue;
+    return launch_rows_d<D, true>(p, tk, tv, a.kv_fp8 != 0, false, stream);
+}
+
 }  // namespace
 
 size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size) {
@@ -48,7 +55,14 @@ cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream) {
     p.cap_out = a.softcap * kRowLog2e;
     p.slopes = a.slopes;
     p.key_begin = a.key_begin;
-    return launch_rows<true>(p, a.d, a.k_pages, a.v_pages, a.kv_fp8 != 0, false, stream);
+    switch (a.d) {
+        case 32: return launch_decode_scoremod_d<32>(a, p, stream);
+        case 64: return launch_decode_scoremod_d<64>(a, p, stream);
+        case 80: return launch_decode_scoremod_d<80>(a, p, stream);
+        case 96: return launch_decode_scoremod_d<96>(a, p, stream);
+        case 128: return launch_decode_scoremod_d<128>(a, p, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace attn

@@ -29,15 +29,20 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
         const long long ctas = (long long)(B / S) * Hkv * pl.units;
         const int bn = d <= 64 ? Cfg<64>::BN : Cfg<128>::BN, per_sm = d <= 64 ? 3 : 1;
         const int tiles = (max_pages * kPageTokens + bn - 1) / bn;
-        double best = 1e30;
-        for (int n = 1; n <= 64 && n <= tiles; ++n) {
-            const double waves = (double)((ctas * n + kSms * per_sm - 1) / (kSms * per_sm));
-            const double cost = waves * ((tiles + n - 1) / n + 3);
-            if (cost < best) {
+        const long long slots = (long long)kSms * per_sm;
+        long long best = -1;
+        for (long long waves = 1; waves <= 4; ++waves) {  // the most splits that fit this many waves
+            long long n = waves * slots / ctas;
+            if (n < 1) continue;
+            n = n > 64 ? 64 : n;
+            n = n > tiles ? tiles : n;
+            const long long cost = waves * ((tiles + n - 1) / n + 3);
+            if (best < 0 || cost < best) {
                 best = cost;
-                pl.prefix_splits = n;
+                pl.prefix_splits = (int)n;
             }
         }
+        if (best < 0) pl.prefix_splits = 1;
     }
     const int rgroups = pl.group <= 8 ? 1 : (pl.group + 15) / 16;
     const long long rows = (long long)B * Hkv * rgroups;
@@ -48,16 +53,18 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
 
 // Query heads [B, H, D] in boxes of 64 columns x `group` heads x `seqs` sequences.
 template <int D, int M>
-cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, cudaStream_t stream) {
+cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, const CUtensorMap &bf16_k,
+                                 const CUtensorMap &bf16_v, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     const int pool = a.num_pages * a.Hkv;
     bool ok = encode_q_heads_map(&tq, a.q, a.B, a.H, D, pl.group, pl.seqs_per_tile);
-    if constexpr (kIsE4m3<M>)
+    if constexpr (kIsE4m3<M>) {
         ok = ok && encode_page_map_u8(&tk, a.k_pages, pool, kPageTokens, D, false) &&
              encode_page_map_u8(&tv, a.v_pages, pool, kPageTokens, D, false);
-    else
-        ok = ok && encode_qkv_map(&tk, a.k_pages, pool, kPageTokens, D, kPageTokens) &&
-             encode_qkv_map(&tv, a.v_pages, pool, kPageTokens, D, kPageTokens);
+    } else {  // the page boxes of the rows kernel
+        tk = bf16_k;
+        tv = bf16_v;
+    }
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e = check_register_split<D, M>();
     if (e != cudaSuccess) return e;
@@ -91,9 +98,15 @@ cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, cuda
 }
 
 template <int D>
-cudaError_t launch_shared_prefix_d(const DecodeArgs &a, const SharedPlan &pl, cudaStream_t stream) {
-    return a.kv_fp8 ? launch_shared_prefix<D, kSharedE4m3>(a, pl, stream)
-                    : launch_shared_prefix<D, kSharedBf16>(a, pl, stream);
+cudaError_t launch_decode_shared_d(const DecodeArgs &a, const SharedPlan &pl, const RowsParams &rows, cudaStream_t stream) {
+    CUtensorMap tk, tv;
+    if (!encode_rows_maps<D>(a.kv_fp8 != 0, a.k_pages, a.v_pages, a.num_pages * a.Hkv, tk, tv)) return cudaErrorInvalidValue;
+    if (pl.prefix_splits > 0) {
+        const cudaError_t e = a.kv_fp8 ? launch_shared_prefix<D, kSharedE4m3>(a, pl, tk, tv, stream)
+                                       : launch_shared_prefix<D, kSharedBf16>(a, pl, tk, tv, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_rows_d<D, false>(rows, tk, tv, a.kv_fp8 != 0, pl.prefix_splits > 0, stream);
 }
 
 }  // namespace
@@ -106,18 +119,6 @@ size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages
 
 cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream) {
     const SharedPlan pl = shared_plan(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size);
-    if (pl.prefix_splits > 0) {
-        cudaError_t e;
-        switch (a.d) {
-            case 32: e = launch_shared_prefix_d<32>(a, pl, stream); break;
-            case 64: e = launch_shared_prefix_d<64>(a, pl, stream); break;
-            case 80: e = launch_shared_prefix_d<80>(a, pl, stream); break;
-            case 96: e = launch_shared_prefix_d<96>(a, pl, stream); break;
-            case 128: e = launch_shared_prefix_d<128>(a, pl, stream); break;
-            default: e = cudaErrorInvalidValue;
-        }
-        if (e != cudaSuccess) return e;
-    }
     RowsParams p{};
     p.q = a.q;
     p.page_table = a.page_table;
@@ -139,7 +140,14 @@ cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream) {
     p.v_scale = a.v_scale;
     p.shared_pages = a.shared_pages;
     p.S = pl.prefix_splits > 0 ? a.group_size : 0;
-    return launch_rows<false>(p, a.d, a.k_pages, a.v_pages, a.kv_fp8 != 0, pl.prefix_splits > 0, stream);
+    switch (a.d) {
+        case 32: return launch_decode_shared_d<32>(a, pl, p, stream);
+        case 64: return launch_decode_shared_d<64>(a, pl, p, stream);
+        case 80: return launch_decode_shared_d<80>(a, pl, p, stream);
+        case 96: return launch_decode_shared_d<96>(a, pl, p, stream);
+        case 128: return launch_decode_shared_d<128>(a, pl, p, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace attn

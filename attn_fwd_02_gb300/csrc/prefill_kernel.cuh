@@ -918,7 +918,7 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
             if (key0 + kBN > kv_end && kv_end < p.Nkv) {
                 const int u = j + 1;
                 if (!__all_sync(0xffffffffu, mbar_wait(kIsE4m3<M> ? &sm.v_full[u % kStagesOf<D>] : &sm.u_full[u % kStagesOf<D>],
-                                                       (uint32_t)((u / kStagesOf<D>) & 1), wc, 26 + t))) {
+                                                       (uint32_t)((u / kStagesOf<D>) & 1), wc, 28 + t))) {
                     ok = false;
                     break;
                 }
@@ -1030,6 +1030,7 @@ __device__ __forceinline__ RowSpan row_span(const PrefillModParams &p, int b, in
     s.lo = p.key_begin ? max(p.key_begin[at], 0) : 0;
     s.hi = p.key_end ? min(p.key_end[at], kv_end) : kv_end;
     if (p.causal) s.hi = min(s.hi, row + delta + 1);
+    if (s.lo >= s.hi) s.lo = s.hi = 0;  // nothing (the bounds given may be any int)
     return s;
 }
 

@@ -23,18 +23,20 @@ __device__ __forceinline__ float tanh_large(float u) {
 struct TanhCap {
     float in, out;
     uint64_t n0, n1, n2;  // near coefficients, as packed pairs
+    bool near_ok;         // they are all well inside the normal range of fp32
 
     __device__ __forceinline__ TanhCap(float in_, float out_) : in(in_), out(out_) {
         const float a = in * out, s = in * in;
         n0 = f32x2_pack(0.999999604f * a, 0.999999604f * a);
         n1 = f32x2_pack(-0.333219082f * a * s, -0.333219082f * a * s);
         n2 = f32x2_pack(0.128416134f * a * s * s, 0.128416134f * a * s * s);
+        const float most = fmaxf(a, a * s * s), least = fminf(a, a * s * s);
+        near_ok = most < 1e36f && least > 1e-36f;
     }
-    // 0 near, 1 mid, 2 far for a warp whose lanes hold scores up to `big` in absolute value.  (A factor
-    // so small that its powers leave the normal range of fp32 takes the mid form.)
+    // 0 near, 1 mid, 2 far for a warp whose lanes hold scores up to `big` in absolute value.
     __device__ __forceinline__ int tier(float big) const {
         const float u = big * in;
-        if (in >= 9.5367431640625e-7f && !__any_sync(0xffffffffu, u > 0.25f)) return 0;
+        if (near_ok && !__any_sync(0xffffffffu, u > 0.25f)) return 0;
         return __any_sync(0xffffffffu, u > 1.f) ? 2 : 1;
     }
     template <int T>

@@ -64,7 +64,10 @@ def masks(kind, B, Nq, Nkv):
         kw["key_begin"], kw["key_end"] = documents(B, Nq, Nkv, [90, 40])
         kw["kv_lens"] = torch.tensor([Nkv // 2, 0, 1, Nkv][:B] + [Nkv] * (B - 4), dtype=torch.int32)
         kw["key_end"][:, ::5] = -7
+        kw["key_end"][:, 3::11] = -2**31
+        kw["key_begin"][:, 1::11] = -2**31
         kw["key_begin"][:, ::7] = 2**31 - 1
+        kw["key_end"][:, 4::13] = 2**31 - 1
     return kw
 
 
@@ -126,6 +129,25 @@ def test_large_scores_meet_the_cap(lib):
         # raw scores reach 30 * 3 * 4 sqrt(d) / sqrt(d) = 400: off by 128 * 2^-23 * scale * sum |q k| <= 9e-3
         # before the cap, whose slope 1 - tanh^2 only shrinks that; all weights move by twice it at most
         assert ((o.cpu().double() - want).abs() <= o_bound(w, v, want) + 1.8e-2 * (w @ v.double().abs())).all()
+
+
+@pytest.mark.parametrize("cap, scale", [(1e-3, 0.1), (1e-6, 1e-3), (1e6, 0.1), (1e20, 0.1), (1e-20, 0.1), (30.0, 1e-20),
+                                        (1e-12, 1e-12), (2.0 ** 100, 0.1)])
+def test_extreme_caps(lib, cap, scale):
+    q, k, v = rand(13, 1, 2, 150, 64), rand(14, 1, 2, 150, 64), rand(15, 1, 2, 150, 64)
+    q[0, 0, 3] = 0  # scores of exactly zero
+    q, k, v, g = q.cuda(), k.cuda(), v.cuda(), rand(16, 1, 2, 150, 64).cuda()
+    o, lse = lib.attn_fwd_scoremod(q, k, v, True, scale, softcap=cap)
+    want, wl, w, t = forward(q, k, v, True, scale, cap)
+    assert (lse.cpu().double() - wl).abs().max() <= LSE_MAX
+    assert ((o.cpu().double() - want).abs() <= o_bound(w, v.cpu(), want)).all()
+    got = lib.attn_bwd_scoremod(q, k, v, o, lse, g, True, scale, softcap=cap)
+    ref = backward(q, k, v, g, True, scale, cap)
+    # 1 - t^2 where tanh saturates: t is off by at most 2^-22, so the factor by 2^-21
+    slack = scale * 2.0 ** -21 * 64
+    for x, y, tol in zip(got, ref, grad_bounds(q.cpu(), k.cpu(), v.cpu(), g.cpu(), want, w, t, scale, ref)):
+        assert torch.isfinite(x).all()
+        assert ((x.cpu().double() - y).abs() <= tol + slack * 150).all()
 
 
 def test_other_stream_and_captured_graph(lib):
