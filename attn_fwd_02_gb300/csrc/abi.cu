@@ -608,7 +608,7 @@ ATTN_API size_t paged_attn_decode_shared_workspace_size(int B, int H, int Hkv, i
 
 namespace {
 // Decode with modified scores (k_scale, v_scale 1 for a bf16 cache).
-int decode_scoremod(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stream) {
+int decode_scoremod(attn::DecodeMoreArgs a, size_t workspace_bytes, attn_stream_t stream) {
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
     if (st != ATTN_OK) return st;
@@ -624,7 +624,7 @@ int decode_scoremod(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t st
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-int decode_shared(attn::DecodeArgs a, size_t workspace_bytes, attn_stream_t stream) {
+int decode_shared(attn::DecodeMoreArgs a, size_t workspace_bytes, attn_stream_t stream) {
     if (!a.shared_pages || a.group_size <= 0) return ATTN_ERR_INVALID_ARG;
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
@@ -648,8 +648,8 @@ ATTN_API int paged_attn_decode_scoremod(const void *q, const void *k_pages, cons
                                         float scale, float softcap, const float *alibi_slopes,
                                         const int32_t *key_begin, void *workspace, size_t workspace_bytes,
                                         attn_stream_t stream) {
-    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
-                       max_pages_per_seq, num_pages, scale, Hkv};
+    attn::DecodeMoreArgs a{{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv}};
     a.softcap = softcap;
     a.slopes = alibi_slopes;
     a.key_begin = key_begin;
@@ -662,8 +662,8 @@ ATTN_API int paged_attn_decode_scoremod_fp8(const void *q, const void *k_pages, 
                                             int max_pages_per_seq, int num_pages, float scale, float softcap,
                                             const float *alibi_slopes, const int32_t *key_begin, void *workspace,
                                             size_t workspace_bytes, attn_stream_t stream) {
-    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
-                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale};
+    attn::DecodeMoreArgs a{{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale}};
     a.softcap = softcap;
     a.slopes = alibi_slopes;
     a.key_begin = key_begin;
@@ -675,8 +675,8 @@ ATTN_API int paged_attn_decode_shared(const void *q, const void *k_pages, const 
                                       const int32_t *shared_pages, int group_size, int page_size, void *o, float *lse,
                                       int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale,
                                       void *workspace, size_t workspace_bytes, attn_stream_t stream) {
-    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
-                       max_pages_per_seq, num_pages, scale, Hkv};
+    attn::DecodeMoreArgs a{{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv}};
     a.shared_pages = shared_pages;
     a.group_size = group_size;
     return decode_shared(a, workspace_bytes, stream);
@@ -688,8 +688,8 @@ ATTN_API int paged_attn_decode_shared_fp8(const void *q, const void *k_pages, co
                                           float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq,
                                           int num_pages, float scale, void *workspace, size_t workspace_bytes,
                                           attn_stream_t stream) {
-    attn::DecodeArgs a{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
-                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale};
+    attn::DecodeMoreArgs a{{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv, 1, k_scale, v_scale}};
     a.shared_pages = shared_pages;
     a.group_size = group_size;
     return decode_shared(a, workspace_bytes, stream);

@@ -16,7 +16,7 @@ int chunk_pages_for(int B, int H, int Hkv, int max_pages) {
 }
 
 template <int D>
-cudaError_t launch_decode_scoremod_d(const DecodeArgs &a, const RowsParams &p, cudaStream_t stream) {
+cudaError_t launch_decode_scoremod_d(const DecodeMoreArgs &a, const RowsParams &p, cudaStream_t stream) {
     CUtensorMap tk, tv;
     if (!encode_rows_maps<D>(a.kv_fp8 != 0, a.k_pages, a.v_pages, a.num_pages * a.Hkv, tk, tv)) return cudaErrorInvalidValue;
     return launch_rows_d<D, true>(p, tk, tv, a.kv_fp8 != 0, false, stream);
@@ -31,7 +31,7 @@ size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pag
     return (size_t)B * H * splits * (size_t)(d + 4) * sizeof(float);
 }
 
-cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream) {
+cudaError_t launch_decode_scoremod(const DecodeMoreArgs &a, cudaStream_t stream) {
     RowsParams p{};
     p.q = a.q;
     p.page_table = a.page_table;

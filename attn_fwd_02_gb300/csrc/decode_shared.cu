@@ -53,7 +53,7 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
 
 // Query heads [B, H, D] in boxes of 64 columns x `group` heads x `seqs` sequences.
 template <int D, int M>
-cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, const CUtensorMap &bf16_k,
+cudaError_t launch_shared_prefix(const DecodeMoreArgs &a, const SharedPlan &pl, const CUtensorMap &bf16_k,
                                  const CUtensorMap &bf16_v, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     const int pool = a.num_pages * a.Hkv;
@@ -98,7 +98,7 @@ cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedPlan &pl, cons
 }
 
 template <int D>
-cudaError_t launch_decode_shared_d(const DecodeArgs &a, const SharedPlan &pl, const RowsParams &rows, cudaStream_t stream) {
+cudaError_t launch_decode_shared_d(const DecodeMoreArgs &a, const SharedPlan &pl, const RowsParams &rows, cudaStream_t stream) {
     CUtensorMap tk, tv;
     if (!encode_rows_maps<D>(a.kv_fp8 != 0, a.k_pages, a.v_pages, a.num_pages * a.Hkv, tk, tv)) return cudaErrorInvalidValue;
     if (pl.prefix_splits > 0) {
@@ -117,7 +117,7 @@ size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages
     return (size_t)B * H * (pl.prefix_splits + pl.own_splits) * (size_t)(d + 4) * sizeof(float);
 }
 
-cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream) {
+cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
     const SharedPlan pl = shared_plan(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size);
     RowsParams p{};
     p.q = a.q;

@@ -45,6 +45,10 @@ struct DecodeArgs {
     // e4m3 cache: pages hold FP8 codes, value = e4m3(code) * k_scale (keys) or * v_scale (values)
     int kv_fp8 = 0;
     float k_scale = 1.f, v_scale = 1.f;
+};
+
+// Of the further decode calls (apart from DecodeArgs, which is the decode kernels' parameter itself).
+struct DecodeMoreArgs : DecodeArgs {
     // launch_decode_shared: groups of group_size sequences share their first shared_pages[b / group_size] pages
     const int32_t *shared_pages = nullptr;
     int group_size = 0;
@@ -153,9 +157,9 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 size_t decode_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
 
 // Decode with modified scores, and decode of a batch whose groups share their first pages.
-cudaError_t launch_decode_scoremod(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_scoremod(const DecodeMoreArgs &a, cudaStream_t stream);
 size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
-cudaError_t launch_decode_shared(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream);
 size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int S, int page_size);
 
 // Same kernels with the chunk partials in the library's static scratch array

@@ -346,7 +346,8 @@ __device__ void run_producer(PrefillSmem<D, M> &sm, const Params<M> &p, const CU
     constexpr int kBN = kBNd<D>;
     constexpr int kTilePages = kBN / kPageTokens;
     const int kvh = bh_kv % p.Hkv;
-    const int pages_used = kIsPaged<M> ? (kv_end + kPageTokens - 1) / kPageTokens : 0;
+    const int pages_used =
+        kIsPaged<M> ? ((kIsShared<M> ? kv_end : kv_end_of(p, b)) + kPageTokens - 1) / kPageTokens : 0;
     auto fetch_ids = [&](int tile, int (&ids)[kTilePages]) {
 #pragma unroll
         for (int pg = 0; pg < kTilePages; ++pg) {
@@ -488,7 +489,7 @@ __device__ void run_convert(PrefillSmem<D, M> &sm, int n_all, int ct, WaitCtx wc
 
 // ------------------------------------------------------------------ MMA issuer
 template <int D, int M>
-__device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQTilesMax], const int (&begin)[kQTilesMax],
+__device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQTilesMax], int begin0, int begin1,
                         int n_all, WaitCtx wc) {
     constexpr int kBN = kBNd<D>;
     // e4m3 pages: Q, K and V are f16 in shared memory and P is packed as f16, so both products run
@@ -511,6 +512,12 @@ __device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQT
     // issued in groups from single asm statements (the second 64-column box of a 128-row tile
     // starts 16 KB on, which the grouped issue assumes)
     static_assert(kPad<D> == 64 || kBN * 128 == 16384, "k-step layout of the grouped issue");
+    // first tile of query tile t (a constant in the forms without intervals: as an array element it cost the
+    // plain form 1 % of its rate)
+    auto first = [&](int t) {
+        if constexpr (kHasSpan<M>) return t ? begin1 : begin0;
+        else return 0;
+    };
     auto issue_S = [&](int t, int j) {
         const uint64_t a = dq + (t ? kQTile : 0);
         const uint64_t b = dk + (uint64_t)(j % kStagesOf<D>) * kKvTile;  // K(j) sits in slot j % S
@@ -524,8 +531,8 @@ __device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQT
         const uint64_t b = dv + (uint64_t)((j + 1) % kStagesOf<D>) * kKvTile;  // V(j) sits in slot (j + 1) % S
         const uint32_t tP = tmem + p_col<D>(t);
         const uint32_t tO = tmem + o_col<D>(t);
-        if constexpr (kBN == 128) tc_mma_ts_k8(tO, tP, b, idPV, j > begin[t] ? 1u : 0u);
-        else tc_mma_ts_k4(tO, tP, b, idPV, j > begin[t] ? 1u : 0u);
+        if constexpr (kBN == 128) tc_mma_ts_k8(tO, tP, b, idPV, j > first(t) ? 1u : 0u);
+        else tc_mma_ts_k4(tO, tP, b, idPV, j > first(t) ? 1u : 0u);
     };
 
     // The data waits below (Q, ring units) need no tcgen05 fence: TMA writes and the MMA's
@@ -538,7 +545,7 @@ __device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQT
     if (ok) {
         tc_fence_after_sync();
         for (int t = 0; t < Cfg<D>::QT; ++t)
-            if (n[t] > 0 && begin[t] == 0) issue_S(t, 0);
+            if (n[t] > 0 && first(t) == 0) issue_S(t, 0);
         tc_commit(&sm.u_empty[0]);
         for (int j = 0; j < n_all && ok; ++j) {
             const int u = j + 1;  // unit with V(j) and K(j+1)
@@ -550,13 +557,13 @@ __device__ void run_mma(PrefillSmem<D, M> &sm, uint32_t tmem, const int (&n)[kQT
             bool k_ready = !kIsE4m3<M>;
             // P over S: PV_t(j) must be issued before S_t(j+1) overwrites its buffer
             for (int t = 0; t < Cfg<D>::QT; ++t) {
-                if (j < n[t] && j >= begin[t]) {
-                    if (!(ok = mbar_wait(&sm.p_full[t], (uint32_t)((j - begin[t]) & 1), wc, 12 + 8 * t))) break;
+                if (j < n[t] && (!kHasSpan<M> || j >= first(t))) {
+                    if (!(ok = mbar_wait(&sm.p_full[t], (uint32_t)((j - first(t)) & 1), wc, 12 + 8 * t))) break;
                     tc_fence_after_sync();
                     issue_PV(t, j);
                     if (j == n[t] - 1) tc_commit(&sm.o_done[t]);
                 }
-                if (j + 1 < n[t] && j + 1 >= begin[t]) {
+                if (j + 1 < n[t] && (!kHasSpan<M> || j + 1 >= first(t))) {
                     if (!k_ready) {
                         if (!(ok = mbar_wait(&sm.u_full[u % kStagesOf<D>], ph, wc, 15))) break;
                         k_ready = true;
@@ -622,6 +629,10 @@ __device__ __forceinline__ void mask_below(uint32_t (&s)[2][32], int first) {
             if (cc * 32 + i < first) s[cc][i] = __float_as_uint(-INFINITY);
 }
 
+// In the place of the cap or the bias in the forms without it.
+struct Without {
+    __device__ __forceinline__ explicit Without(float = 0.f, float = 0.f) {}
+};
 // The cap's factors (0 in the forms without it).
 template <int M> __device__ __forceinline__ float cap_in_of(const Params<M> &p) {
     if constexpr (kHasCap<M>) return p.cap_in;
@@ -752,6 +763,7 @@ template <int D, int M>
 __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUtensorMap *tmO, uint32_t tmem,
                             int t, int bh, int q0, int n_tiles, int n_all, int kv_end, int delta, int j0, int begin,
                             RowSpan span, WaitCtx wc) {
+    if constexpr (!kHasSpan<M>) j0 = begin = 0;  // (constants here keep the plain forms' code as it was)
     const int r = threadIdx.x & 127;  // query row in the tile = TMEM lane
     const int wq = (threadIdx.x >> 5) & 3;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
@@ -774,8 +786,8 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
         }
     }
     // modified scores are brought to the log2 domain before the maximum, with the cap or the bias
-    [[maybe_unused]] const TanhCap cap(cap_in_of<M>(p), cap_out_of<M>(p));
-    [[maybe_unused]] DistanceBias bias;
+    const std::conditional_t<kHasCap<M>, TanhCap, Without> cap(cap_in_of<M>(p), cap_out_of<M>(p));
+    std::conditional_t<kHasBias<M>, DistanceBias, Without> bias;
     if constexpr (kHasBias<M>) {
         bias.slope2 = p.slopes[bh % p.H] * kLog2e;
         bias.pos = row + delta;
@@ -875,9 +887,14 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
         }
         if (kPaged && unmapped) mask_pages<kHalves>(s, unmapped);
         float mx;
-        if (kHasCap<M> && !kHasBias<M> && !need_mask && !need_lo) {
-            mx = cap.one(tier, raw_max);  // the cap is monotone
-        } else {
+        bool have_max = false;
+        if constexpr (kHasCap<M> && !kHasBias<M>) {
+            if (!need_mask && !need_lo) {
+                mx = cap.one(tier, raw_max);  // the cap is monotone
+                have_max = true;
+            }
+        }
+        if (!have_max) {
             mx = max64(s[0]);
 #pragma unroll
             for (int h = 1; h < kHalves; ++h) mx = fmaxf(mx, max64(s[h]));
@@ -1220,7 +1237,7 @@ __global__ void __launch_bounds__((Occ<D, M>::kThreads), (Occ<D, M>::kMinBlocks)
             if (lane == 0 && n_all > 0)
                 run_producer<D, M>(sm, p, &tmQ, &tmK, &tmV, b, bh, bh_kv, q0, n_all, u_begin, span.j0, kv_end, wc);
         } else if (warp == Cfg<D>::kMmaWarp) {
-            if (lane == 0 && n_all > 0) run_mma<D, M>(sm, tmem, n, span.begin, n_all, wc);
+            if (lane == 0 && n_all > 0) run_mma<D, M>(sm, tmem, n, span.begin[0], span.begin[1], n_all, wc);
         } else if constexpr (kIsE4m3<M>) {
             // the warps after the MMA issuer's convert e4m3 tiles into the ring
             if (n_all > 0) run_convert<D, M>(sm, n_all, (int)threadIdx.x - (Cfg<D>::kMmaWarp + 1) * 32, wc);
