@@ -233,12 +233,13 @@ ATTN_API int attn_fwd(const void *q, const void *k, const void *v, void *o, floa
 
 namespace {
 // The score modification's arguments: softcap 0 (none), or positive with factors that fp32 holds (cap and
-// score factor / cap at most 2^100; `factor` is the scale, times the key scale of an e4m3 cache); 4-byte
-// aligned arrays.
+// score factor / cap at most 2^100, the factor at least 2^-100 with slopes; `factor` is the scale, times the
+// key scale of an e4m3 cache); 4-byte aligned arrays.
 int scoremod_checks(float factor, float softcap, const float *alibi_slopes, const int32_t *key_begin,
                     const int32_t *key_end) {
     constexpr float kMost = 1.2676506e30f;  // 2^100
     if (!(factor > 0.f) || !(factor < 3.0e38f)) return ATTN_ERR_INVALID_ARG;
+    if (alibi_slopes && !(factor >= 1.f / kMost)) return ATTN_ERR_INVALID_ARG;  // slopes are divided by it
     if (!(softcap >= 0.f) || !(softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
     if (softcap > 0.f && !(factor / softcap <= kMost)) return ATTN_ERR_INVALID_ARG;
     if (!aligned4(alibi_slopes) || !aligned4(key_begin) || !aligned4(key_end)) return ATTN_ERR_MISALIGNED;

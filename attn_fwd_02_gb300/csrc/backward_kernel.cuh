@@ -1051,6 +1051,7 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
 template <int D>
 __global__ void __launch_bounds__(256) bwd_reduce_kernel(const float4 *parts, uint2 *dv, uint2 *dk, long long rows,
                                                          int splits, float scale) {
+    griddep_wait();  // (launched as the dQ grid, whose end includes the dK/dV grid's, drains)
     const long long n4 = rows * (D / 4), i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= 2 * n4) return;
     const bool is_k = i >= n4;
@@ -1191,10 +1192,10 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     if constexpr (kIsMod<F>) {
         if (p.kv_splits > 1) {
             const long long kv_rows = (long long)a.B * a.Hkv * a.Nkv;
-            bwd_reduce_kernel<D><<<(unsigned)((kv_rows * (D / 2) + 255) / 256), 256, 0, stream>>>(
+            const cudaError_t e = launch_dependent(
+                bwd_reduce_kernel<D>, dim3((unsigned)((kv_rows * (D / 2) + 255) / 256)), 256, 0, stream,
                 reinterpret_cast<const float4 *>(p.kv_parts), reinterpret_cast<uint2 *>(p.dv),
-                reinterpret_cast<uint2 *>(p.dk), kv_rows, p.kv_splits, a.scale);
-            const cudaError_t e = cudaGetLastError();
+                reinterpret_cast<uint2 *>(p.dk), kv_rows, (int)p.kv_splits, a.scale);
             if (e != cudaSuccess) return e;
         }
     }

@@ -7,8 +7,8 @@
 //   far                the exponential form 1 - 2 / (1 + e^(2|u|)) where |u| > 1 (its cancellation is
 //                      harmless from there on), the six terms elsewhere.
 // The polynomials are fits of tanh(u) / u in u^2 by iterated weighted least squares.  A warp takes the
-// tier that its largest |u| needs, as one.  Measured on a causal forward of 16 heads x 8192, d = 128: the
-// exponential form for every score 784 us, mid alone 587 us.
+// tier that its largest |u| needs, as one.  Measured on a causal forward of 16 heads x 8192, d = 128: no cap
+// 212 us, scores in the near tier 270, in the far one 561.
 #pragma once
 
 #include "sm103_ptx.cuh"
