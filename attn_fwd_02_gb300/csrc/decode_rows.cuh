@@ -38,9 +38,10 @@ struct RowsParams {
     int n_splits, ws_splits, ws_first;  // this kernel writes partials ws_first .. ws_first + n_splits - 1
     float c;                            // scale * log2(e) (times the key scale of an e4m3 cache)
     float v_scale;
-    // own pages behind shared ones: the first shared_pages[b / S] pages are not read here (S 0: none)
+    // groups of S sequences: the first shared_pages[b / S] pages are those of the group's first row of the
+    // table; own_only: they are not read here
     const int32_t *shared_pages;
-    int S;
+    int S, own_only;
     // modified scores: cap_in (0: none) = scale * key scale / cap, cap_out = cap * log2(e)
     float cap_in, cap_out;
     const float *slopes;       // [H], may be null
@@ -85,6 +86,9 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 struct PageRange {
     int p0, p1, lo, hi;
 };
+__device__ __forceinline__ int shared_pages_of(const RowsParams &a, int b) {
+    return min(max(a.shared_pages[b / a.S], 0), a.max_pages);
+}
 template <bool MOD>
 __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int split) {
     PageRange r;
@@ -96,7 +100,7 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
         r.p1 = r.lo < r.hi ? min((split + 1) * a.chunk_pages, pages) : 0;
     } else {
         r.lo = 0;
-        const int base = a.S > 0 ? min(max(a.shared_pages[b / a.S], 0), a.max_pages) : 0;
+        const int base = a.own_only ? shared_pages_of(a, b) : 0;
         const long long n = max(pages - base, 0);
         r.p0 = base + (int)(n * split / a.n_splits);
         r.p1 = base + (int)(n * (split + 1) / a.n_splits);
@@ -157,10 +161,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
     // Page ids, 32 of this warp's pages at a time (lane l: page k0 + l); bit k % 32 of mapped: page k's id
     // lies in the pool (an unmapped page holds no token)
     const int32_t *table = a.page_table + (size_t)b * a.max_pages + pr.p0 + warp;
+    // shared pages (not own_only): the entries of the group's first row, `back` before this row's
+    const int shared = !MOD && !a.own_only ? shared_pages_of(a, b) - pr.p0 - warp : 0;
+    const size_t back = !MOD ? (size_t)(b % a.S) * a.max_pages : 0;
     int my_pid = -1;
     uint32_t mapped = 0;
     auto issue = [&](int k) {
-        if ((k & 31) == 0) my_pid = k + lane < nk ? table[kRowWarps * (k + lane)] : -1;
+        if ((k & 31) == 0) {
+            const int at = kRowWarps * (k + lane);
+            my_pid = k + lane < nk ? (!MOD && at < shared ? table - back : table)[at] : -1;
+        }
         const int pid = __shfl_sync(0xffffffffu, my_pid, k & 31);
         const bool ok = pid >= 0 && pid < a.num_pages;
         mapped = (mapped & ~(1u << (k & 31))) | ((ok ? 1u : 0u) << (k & 31));

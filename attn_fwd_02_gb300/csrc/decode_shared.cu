@@ -13,15 +13,23 @@ namespace {
 
 constexpr int kSms = 152;
 
-// How a batch is cut.  Groups of more than 128 query heads per key/value head do not fit a tile, and
-// groups of one sequence share nothing: their pages all count as the sequences' own (prefix_splits 0).
+// How a batch is cut.  prefix_splits 0: the shared pages are read once per sequence by the rows kernel, as
+// its own ones: groups of one sequence share nothing, groups of more than 128 query heads per key/value head
+// do not fit a tile, and while the repeated reads are few they come from L2 and cost less than the first
+// kernel's start and the merge of its parts.  Both ways, us (bf16 unless said; repeated reads by the table's
+// capacity, bytes (S - 1) / S of the batch's cache): 5 MB 9.1 / 6.1 (once per group / per sequence), 36 MB 14.3 /
+// 11.8, 56 MB 29.0 / 17.8, e4m3 54 MB 23.6 / 18.1, 99 MB 22.2 / 18.9, 108 MB 12.9 / 17.5, 129 MB 15.9 / 19.2,
+// 140 MB 15.3 / 18.9.
+constexpr double kRepeatedBytes = 100e6;
+
 struct SharedPlan {
     int group, seqs_per_tile, units, prefix_splits, own_splits;
 };
-SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
+SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S, bool fp8) {
     SharedPlan pl{};
     pl.group = H / Hkv;
-    if (S > 1 && pl.group <= 128) {
+    const double repeated = 2.0 * (B - B / S) * Hkv * max_pages * kPageTokens * d * (fp8 ? 1 : 2);
+    if (pl.group <= 128 && repeated > kRepeatedBytes) {
         pl.seqs_per_tile = 128 / pl.group;
         const int qt = d <= 64 ? Cfg<64>::QT : Cfg<128>::QT;
         pl.units = (S + pl.seqs_per_tile * qt - 1) / (pl.seqs_per_tile * qt);
@@ -46,7 +54,7 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S) {
     }
     const int rgroups = pl.group <= 8 ? 1 : (pl.group + 15) / 16;
     const long long rows = (long long)B * Hkv * rgroups;
-    const long long want = (4LL * kSms + rows - 1) / rows, most = (max_pages + 31) / 32;
+    const long long want = (4LL * kSms + rows - 1) / rows, most = (max_pages + 7) / 8;
     pl.own_splits = (int)(want < most ? want : most);
     return pl;
 }
@@ -113,12 +121,14 @@ cudaError_t launch_decode_shared_d(const DecodeMoreArgs &a, const SharedPlan &pl
 
 size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int S, int page_size) {
     if (S <= 0 || B % S != 0 || decode_workspace_bytes(B, H, Hkv, d, max_pages, page_size) == 0) return 0;
-    const SharedPlan pl = shared_plan(B, H, Hkv, d, max_pages, S);
-    return (size_t)B * H * (pl.prefix_splits + pl.own_splits) * (size_t)(d + 4) * sizeof(float);
+    // (the larger of the two cache types' plans)
+    const SharedPlan a = shared_plan(B, H, Hkv, d, max_pages, S, false), b = shared_plan(B, H, Hkv, d, max_pages, S, true);
+    const int parts = a.prefix_splits + a.own_splits, parts8 = b.prefix_splits + b.own_splits;
+    return (size_t)B * H * (parts > parts8 ? parts : parts8) * (size_t)(d + 4) * sizeof(float);
 }
 
 cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
-    const SharedPlan pl = shared_plan(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size);
+    const SharedPlan pl = shared_plan(a.B, a.H, a.Hkv, a.d, a.max_pages, a.group_size, a.kv_fp8 != 0);
     RowsParams p{};
     p.q = a.q;
     p.page_table = a.page_table;
@@ -139,7 +149,8 @@ cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
     p.c = a.scale * kRowLog2e * (a.kv_fp8 ? a.k_scale : 1.f);
     p.v_scale = a.v_scale;
     p.shared_pages = a.shared_pages;
-    p.S = pl.prefix_splits > 0 ? a.group_size : 0;
+    p.S = a.group_size;
+    p.own_only = pl.prefix_splits > 0;
     switch (a.d) {
         case 32: return launch_decode_shared_d<32>(a, pl, p, stream);
         case 64: return launch_decode_shared_d<64>(a, pl, p, stream);

@@ -234,7 +234,8 @@ int paged_attn_decode_scoremod_fp8(const void *q, const void *k_pages, const voi
 
 /*
  * Paged decode of a batch whose groups of sequences share their first pages (samples of one prompt, users
- * behind one system prompt or document): paged_attn_decode_gqa, with the shared pages read once per group.
+ * behind one system prompt or document): paged_attn_decode_gqa, with the shared pages read once per group
+ * (or once per sequence, from L2, where that is faster: small batches).
  *   group_size    the batch is B / group_size groups of consecutive sequences (B % group_size == 0); pad a
  *                 shorter group with sequences of ctx_lens 0
  *   shared_pages  [B / group_size] int32 (device, clamped to [0, max_pages_per_seq]): the first

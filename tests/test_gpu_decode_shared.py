@@ -18,6 +18,12 @@ def lib():
     return binding
 
 
+def wide(H, Hkv, d, S, shared, ctx):
+    """Spare columns that bring the repeated reads, by the table's capacity, past what is left to L2 (100 MB)."""
+    B = len(ctx)
+    return 1 + int(1.1e8 / (2 * max(1, B - B // S) * Hkv * 16 * d))
+
+
 def make(H, Hkv, d, S, shared, ctx, fp8, seed, spare=1):
     """shared: pages of each group; ctx: tokens of each sequence.  Returns the call's tensors and full tables."""
     G, B = len(shared), len(ctx)
@@ -76,13 +82,12 @@ CASES = [  # H, Hkv, d, S, shared pages per group, contexts
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("once", [False, True], ids=["per_sequence", "per_group"])
 @pytest.mark.parametrize("case", CASES, ids=[f"H{c[0]}kv{c[1]}d{c[2]}S{c[3]}G{len(c[4])}" for c in CASES])
-def test_matches_the_definition(lib, case, fp8):
+def test_matches_the_definition(lib, case, once, fp8):
     H, Hkv, d, S, shared, ctx = case
-    x = make(H, Hkv, d, S, shared, ctx, fp8, 3)
+    x = make(H, Hkv, d, S, shared, ctx, fp8, 3, spare=wide(H, Hkv, d, S, shared, ctx) if once else 1)
     B = len(ctx)
-    if S == 1 or H // Hkv > 128:
-        x["table"] = x["full"]
     o = torch.full((B, H, d), float("nan"), dtype=torch.bfloat16, device="cuda")
     lse = torch.full((B, H), float("nan"), device="cuda")
     run(lib, x, fp8, out=o, lse=lse)
@@ -91,9 +96,10 @@ def test_matches_the_definition(lib, case, fp8):
     R.check(o.cpu(), lse.cpu(), *R.decode(x["q"], x["k"], x["v"], x["full"], ctx, d ** -0.5, fp8))
 
 
+@pytest.mark.parametrize("once", [False, True], ids=["per_sequence", "per_group"])
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
-def test_unmapped_shared_pages_and_clamped_counts(lib, fp8):
-    x = make(4, 2, 64, 2, [10, 3, 2], [200, 190, 60, 77, 0, 0], fp8, 4)
+def test_unmapped_shared_pages_and_clamped_counts(lib, fp8, once):
+    x = make(4, 2, 64, 2, [10, 3, 2], [200, 190, 60, 77, 0, 0], fp8, 4, spare=12000 if once else 1)
     for t in (x["table"], x["full"]):
         t[0:2, 4] = -1
         t[2:4, 0] = 10**6
@@ -108,8 +114,10 @@ def test_unmapped_shared_pages_and_clamped_counts(lib, fp8):
     R.check(out[0].cpu(), out[1].cpu(), *R.decode(y["q"], y["k"], y["v"], y["full"], y["ctx"].tolist(), 64 ** -0.5, fp8))
 
 
-def test_other_stream_graph_and_repeats(lib):
-    x = make(8, 2, 128, 4, [30, 12], [500 + 9 * i for i in range(4)] + [200 + 30 * i for i in range(4)], False, 6)
+@pytest.mark.parametrize("once", [False, True], ids=["per_sequence", "per_group"])
+def test_other_stream_graph_and_repeats(lib, once):
+    x = make(8, 2, 128, 4, [30, 12], [500 + 9 * i for i in range(4)] + [200 + 30 * i for i in range(4)], False, 6,
+             spare=3000 if once else 1)
     want = run(lib, x, False)
     a = [x[n].cuda() for n in ("q", "k", "v", "table", "ctx", "shared")]
     need = lib.paged_attn_decode_shared_workspace_size(8, 8, 2, 128, x["table"].shape[1], 4)
