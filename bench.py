@@ -43,11 +43,15 @@ PROFILE_TRAFFIC = os.path.join(ROOT, "profiles", "ncu_traffic.txt")
 # Traffic entries of profiles/ncu_traffic.txt: key -> source files whose hash the entry was taken on.
 # Each key stands for one kernel on the workload its bench line times.
 KERNEL_SOURCES = {
-    "prefill_kernel": ["attn_fwd_02_gb300/csrc/prefill.cu", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
-    "decode_split_kernel": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
-    "decode_split_kernel_e4m3": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
-    "decode_gqa_mma_kernel": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
-    "decode_gqa_mma_kernel_e4m3": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
+    "prefill_kernel": ["attn_fwd_02_gb300/csrc/prefill_kernel.cuh", "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
+    "decode_split_kernel": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/mma_sync.cuh",
+                            "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
+    "decode_split_kernel_e4m3": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/mma_sync.cuh",
+                                 "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
+    "decode_gqa_mma_kernel": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/mma_sync.cuh",
+                              "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
+    "decode_gqa_mma_kernel_e4m3": ["attn_fwd_02_gb300/csrc/decode.cu", "attn_fwd_02_gb300/csrc/mma_sync.cuh",
+                                   "attn_fwd_02_gb300/csrc/sm103_ptx.cuh"],
 }
 
 PREFILL_BY_NAME = {
