@@ -1,10 +1,15 @@
 // decode_shared.cu -- paged decode of a batch whose groups of sequences share their first pages.
 //
-// The shared pages are read once per (group, key/value head) instead of once per sequence: the query
-// heads of all the group's sequences are the rows of the prefill kernel's 128-row tcgen05 tiles (a form
-// without a causal mask), split along the keys so that the CTAs fill the GPU.  Each sequence's own pages
-// go through the rows kernel, which may start as the first kernel's CTAs leave, and one merge joins the
-// partial results.
+// Where the sequences' repeated reads of the shared pages would be many (shared_plan), they are read once
+// per (group, key/value head): the query heads of all the group's sequences are the rows of the prefill
+// kernel's 128-row tcgen05 tiles (a form without a causal mask), split along the keys so that the CTAs fill
+// the GPU.  Each sequence's own pages go through the rows kernel, which may start as the first kernel's
+// CTAs leave, and one merge joins the partial results.  Elsewhere the rows kernel reads the shared pages
+// too.  Measured (32 query and 8 key/value heads, d 128): 32 sequences behind one prompt of 8192 tokens
+// 29.2 us, of which the shared pages' kernel takes about 18 and the rows kernel 16, overlapping; 128 sequences
+// in two groups behind documents of up to 16384 tokens over an e4m3 cache 70.7 us (47 and 31).  Both kernels are
+// bound by latency, not bandwidth (15 to 52 % of it): a few key tiles per CTA in the first, a page's chain in the
+// second.
 #include "decode_rows.cuh"
 #include "prefill_kernel.cuh"
 

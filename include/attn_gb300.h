@@ -210,7 +210,8 @@ int paged_attn_decode_gqa(const void *q, const void *k_pages, const void *v_page
  *     s_j = cap tanh(scale <q, k_j> / cap) - slope[h] (ctx_lens[b] - 1 - j)      (softcap cap > 0)
  *     s_j = scale <q, k_j> - slope[h] (ctx_lens[b] - 1 - j)                      (softcap 0)
  * over the cached tokens key_begin[b] <= j < ctx_lens[b].
- *   softcap 0, or positive (it and scale / softcap at most 2^100); alibi_slopes [H] fp32 or NULL; key_begin [B] int32 (clamped) or NULL
+ *   softcap 0, or positive; alibi_slopes [H] fp32 (finite) or NULL; key_begin [B] int32 (clamped) or NULL.
+ *     Bounds as in attn_fwd_scoremod, of scale * k_scale in place of scale over an e4m3 cache
  *   workspace: at least paged_attn_decode_scoremod_workspace_size(...) bytes, 16-byte aligned
  * Pages wholly before key_begin are not read, and slots of the first page before it may hold anything.
  * A sequence that sees no token gets O = 0 and LSE = -inf.  Other arguments as paged_attn_decode_gqa;
