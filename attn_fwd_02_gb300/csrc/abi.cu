@@ -147,6 +147,26 @@ cudaError_t ensure_max_dynamic_smem(const void *kernel, int bytes) {
     return cudaSuccess;
 }
 
+cudaError_t ensure_large_clusters(const void *kernel) {
+    struct Entry {
+        const void *fn;
+        int dev;
+    };
+    static Entry done[512];
+    static int n_done = 0;
+    static std::mutex mu;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n_done; ++i)
+        if (done[i].fn == kernel && done[i].dev == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (n_done < 512) done[n_done++] = Entry{kernel, dev};
+    return cudaSuccess;
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

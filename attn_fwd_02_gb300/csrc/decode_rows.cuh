@@ -1,5 +1,6 @@
 // decode_rows.cuh -- paged decode with the query heads as the columns of the products: the kernel of the
-// decode with modified scores and of a batch's own pages behind shared ones, and the merge of partials.
+// decode with modified scores and of a batch's own pages behind shared ones, and the merge of partials, which
+// the splits of a row do themselves where they fit a cluster (cluster_splits).
 //
 // One query per sequence attends over its pages.  A CTA takes a range of pages of one (sequence,
 // key/value head) for up to 8 NT of the query heads that share the head; its four warps take every
@@ -46,7 +47,8 @@ struct RowsParams {
     float cap_in, cap_out;
     const float *slopes;       // [H], may be null
     const int32_t *key_begin;  // [B], may be null
-    int chunk_pages;           // pages per split
+    int chunk_pages;           // pages per split (0: even shares of the pages)
+    int cluster;               // the splits of a row are the CTAs of one cluster, which merges them itself
 };
 
 namespace {
@@ -57,6 +59,7 @@ constexpr float kRowLog2e = 1.4426950408889634f;
 constexpr float kRowLn2 = 0.6931471805599453f;
 // Ring slots (page blocks of K and V in flight) per warp.
 template <bool FP8> constexpr int kRowSlots = 2;
+constexpr int kRowCluster = 16;  // most splits of a row that one cluster merges
 template <int D, bool FP8> constexpr int kRowBoxes = FP8 ? 1 : (D + 63) / 64;  // 128-byte-row boxes per block
 template <int D, bool FP8> constexpr int kRowBlock = kRowBoxes<D, FP8> * kRowPS * 128;
 
@@ -69,6 +72,7 @@ struct RowsSmem {
             float o[kRowWarps][8 * NT][D];
             float m[kRowWarps][8 * NT];
             float l[kRowWarps][8 * NT];
+            float2 ml[8 * NT];  // of the CTA (whose O is then in o[0])
         } red;
     } u;
     uint64_t full[kRowWarps][kRowSlots<FP8>];
@@ -80,6 +84,22 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
+}
+
+// Barrier over the cluster's threads, ordering their shared-memory accesses.
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The same shared-memory address in CTA `rank` of the cluster, and a load from there.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 
 // Pages [p0, p1) of this split, and the tokens lo <= t < hi among them that the query sees.
@@ -96,8 +116,15 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
     const int pages = (r.hi + kRowPS - 1) / kRowPS;
     if constexpr (MOD) {
         r.lo = a.key_begin ? min(max(a.key_begin[b], 0), r.hi) : 0;
-        r.p0 = max(split * a.chunk_pages, r.lo / kRowPS);
-        r.p1 = r.lo < r.hi ? min((split + 1) * a.chunk_pages, pages) : 0;
+        if (a.chunk_pages == 0) {
+            const int base = r.lo / kRowPS;
+            const long long n = max(pages - base, 0);
+            r.p0 = base + (int)(n * split / a.n_splits);
+            r.p1 = r.lo < r.hi ? base + (int)(n * (split + 1) / a.n_splits) : 0;
+        } else {
+            r.p0 = max(split * a.chunk_pages, r.lo / kRowPS);
+            r.p1 = r.lo < r.hi ? min((split + 1) * a.chunk_pages, pages) : 0;
+        }
     } else {
         r.lo = 0;
         const int base = a.own_only ? shared_pages_of(a, b) : 0;
@@ -131,7 +158,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
     const PageRange pr = rows_range<MOD>(a, b, split);
     float *ws = a.ws + (((size_t)b * a.H + h0) * a.ws_splits + a.ws_first + split) * (D + 4);
     const size_t ws_row = (size_t)a.ws_splits * (D + 4);
-    if (pr.p0 >= pr.p1) {  // nothing here (uniform over the CTA)
+    if (pr.p0 >= pr.p1 && !a.cluster) {  // nothing here (uniform over the CTA)
         if (!MOD) {
             if ((int)threadIdx.x < rows) {
                 ws[threadIdx.x * ws_row + D] = -INFINITY;
@@ -469,6 +496,62 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
             }
         }
     __syncthreads();
+    if (a.cluster) {
+        // the CTA's state, over the first warp's
+        for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
+            const int r = e / D, dd = e % D;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, sm.u.red.m[w][r]);
+            float L = 0.f, O = 0.f;
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kRowWarps; ++w) {
+                    const float wgt = ex2_approx(sm.u.red.m[w][r] - M);
+                    L += sm.u.red.l[w][r] * wgt;
+                    O += sm.u.red.o[w][r][dd] * wgt;
+                }
+            }
+            sm.u.red.o[0][r][dd] = O;
+            if (dd == 0) sm.u.red.ml[r] = make_float2(M, L);
+        }
+        cluster_sync_all();
+        // the cluster's: the rows' pairs of columns are shared out over its threads
+        const uint32_t ml0 = smem_u32(sm.u.red.ml), o0 = smem_u32(sm.u.red.o[0]);
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.o) + ((size_t)b * a.H + h0) * D;
+        for (int e = split * kRowWarps * 32 + threadIdx.x; e < rows * (D / 2); e += a.n_splits * kRowWarps * 32) {
+            const int r = e / (D / 2), pair = e % (D / 2);
+            float2 ml[kRowCluster], ov[kRowCluster];
+#pragma unroll
+            for (int c0 = 0; c0 < kRowCluster; ++c0) {
+                ml[c0] = make_float2(-INFINITY, 0.f), ov[c0] = make_float2(0.f, 0.f);
+                if (c0 < a.n_splits) {
+                    ml[c0] = cluster_load2(cluster_map(ml0 + r * 8, c0));
+                    ov[c0] = cluster_load2(cluster_map(o0 + (r * D + 2 * pair) * 4, c0));
+                }
+            }
+            float M = -INFINITY;
+#pragma unroll
+            for (int c0 = 0; c0 < kRowCluster; ++c0) M = fmaxf(M, ml[c0].x);
+            float L = 0.f;
+            float2 O = make_float2(0.f, 0.f);
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int c0 = 0; c0 < kRowCluster; ++c0) {
+                    const float wgt = ex2_approx(ml[c0].x - M);  // 0 for an empty one, whose O is 0
+                    L = fmaf(ml[c0].y, wgt, L);
+                    O.x = fmaf(ov[c0].x, wgt, O.x);
+                    O.y = fmaf(ov[c0].y, wgt, O.y);
+                }
+            }
+            const bool any = L > 0.f;
+            const float inv = any ? (FP8 ? a.v_scale : 1.f) / L : 0.f;
+            *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(O.x * inv, O.y * inv);
+            if (pair == 0 && a.lse) a.lse[(size_t)b * a.H + h0 + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its state
+        return;
+    }
     if (!sm.abort_flag) {
         for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
             const int r = e / D, dd = e % D;
@@ -558,6 +641,30 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
     if (lane == 0 && a.lse) a.lse[row] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
 }
 
+// Splits of a row (a sequence's heads that one CTA takes) for the form whose splits are one cluster: it merges
+// them through distributed shared memory, without the workspace and the second launch.  0: splits through the
+// workspace.  The clusters are to be resident all at once (clusters of more than 4 leave some slots unused); a
+// row that outruns its share is cut finer through the workspace, and so is a long context of so few rows that
+// the clusters leave SMs empty.  Both ways, us (32 query heads, d 128 unless said; cluster / workspace):
+//   1 sequence, 8 key/value heads    8 pages 4.8 / 6.4, 97 6.8 / 7.1, 262 8.8 / 9.6, 1000 16.3 / 24.1
+//   the same, 2 key/value heads      51 pages 7.5 / 9.0, 262 11.4 / 11.4, 1000 22.5 / 19.8
+//   8 sequences, 8 heads (6 splits)  22 pages 6.4 / 7.3, 250 15.6 / 20.8, 497 34.4 / 36.7; all in flight or not:
+//                                    62 pages 8.2 with 6 splits, 12.9 with 8
+//   32 sequences, 8 heads, e4m3 (2)  63 pages 13.2 / 17.1, 250 38.4 / 44.7, 497 70.6 / 71.2
+//   the same in bf16 (1 split)       63 pages 17.0 / 19.1, 123 37.1 / 36.6, 497 125.9 / 118.2
+//   128 sequences, 12 heads, d 64    7 pages 14.1 / 12.2 (not resident at once)
+inline int cluster_splits(int B, int H, int Hkv, int d, int max_pages, bool fp8) {
+    const int group = H / Hkv;
+    const long long rows = (long long)B * Hkv * (group <= 8 ? 1 : (group + 15) / 16);
+    const long long slots = 152 * (d > 64 && !fp8 ? 3 : 4);  // by shared memory, and by registers
+    long long n = slots * 95 / 100 / rows;
+    if (n > 4) n = slots * 85 / 100 / rows > 4 ? slots * 85 / 100 / rows : 4;
+    if (n > kRowCluster) n = kRowCluster;
+    if (n > (max_pages + kRowWarps - 1) / kRowWarps) n = (max_pages + kRowWarps - 1) / kRowWarps;
+    if (max_pages > 32 * kRowWarps * n || (max_pages > 256 && rows * n < 128)) return 0;
+    return (int)n;
+}
+
 // Page boxes of the rows kernel over a pool of `pool` page blocks.
 template <int D>
 bool encode_rows_maps(bool fp8, const void *k_pages, const void *v_pages, int pool, CUtensorMap &tk, CUtensorMap &tv) {
@@ -566,7 +673,26 @@ bool encode_rows_maps(bool fp8, const void *k_pages, const void *v_pages, int po
                   encode_qkv_map(&tv, v_pages, pool, kRowPS, D, kRowPS));
 }
 
-// The rows kernel (dependent: it may overlap the grid before it) and the merge.
+// Launches a kernel with the CTAs of each blockIdx.y, blockIdx.z as one cluster.
+template <class K, class... A>
+cudaError_t launch_cluster(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The rows kernel (dependent: it may overlap the grid before it) and the merge, or one kernel whose
+// clusters merge.
 template <int D, bool FP8, int NT, bool MOD>
 cudaError_t launch_rows_n(const RowsParams &p, const CUtensorMap &tk, const CUtensorMap &tv, bool dependent,
                           cudaStream_t stream) {
@@ -575,6 +701,11 @@ cudaError_t launch_rows_n(const RowsParams &p, const CUtensorMap &tk, const CUte
     cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(p.n_splits, p.Hkv * p.rgroups, p.B);
+    if (p.cluster) {
+        if (p.n_splits > 8) e = ensure_large_clusters(reinterpret_cast<const void *>(kernel));
+        if (e != cudaSuccess) return e;
+        return launch_cluster(kernel, grid, kRowWarps * 32, smem, stream, tk, tv, p);
+    }
     if (dependent) {
         e = launch_dependent(kernel, grid, kRowWarps * 32, smem, stream, tk, tv, p);
     } else {

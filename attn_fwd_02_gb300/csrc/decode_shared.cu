@@ -21,11 +21,13 @@ constexpr int kSms = 152;
 // How a batch is cut.  prefix_splits 0: the shared pages are read once per sequence by the rows kernel, as
 // its own ones: groups of one sequence share nothing, groups of more than 128 query heads per key/value head
 // do not fit a tile, and while the repeated reads are few they come from L2 and cost less than the first
-// kernel's start and the merge of its parts.  Both ways, us (bf16 unless said; repeated reads by the table's
-// capacity, bytes (S - 1) / S of the batch's cache): 5 MB 9.1 / 6.1 (once per group / per sequence), 36 MB 14.3 /
-// 11.8, 56 MB 29.0 / 17.8, e4m3 54 MB 23.6 / 18.1, 99 MB 22.2 / 18.9, 108 MB 12.9 / 17.5, 129 MB 15.9 / 19.2,
-// 140 MB 15.3 / 18.9.
-constexpr double kRepeatedBytes = 100e6;
+// kernel's start and the merge of its parts; the more so where clusters merge the rows kernel's splits.  Repeated
+// reads by the table's capacity, MB, and us once per group / once per sequence:
+//   by clusters   97 15.6 / 12.7, 129 16.0 / 14.4, 140 15.1 / 16.1, 198 27.7 / 22.1, 192 18.4 / 18.8, e4m3 122
+//                 23.7 / 21.8, 181 27.6 / 29.1, 239 31.7 / 40.5, 461 26.8 / 48.2
+//   by workspace  34 12.4 / 10.8, 59 12.3 / 13.1, 67 15.7 / 15.3, 83 18.6 / 18.3, 91 16.2 / 17.0, 116 16.5 / 18.9,
+//                 e4m3 87 21.7 / 19.0, 153 23.6 / 25.5
+constexpr double kRepeatedBytesCluster = 180e6, kRepeatedBytes = 80e6;
 
 struct SharedPlan {
     int group, seqs_per_tile, units, prefix_splits, own_splits;
@@ -34,7 +36,8 @@ SharedPlan shared_plan(int B, int H, int Hkv, int d, int max_pages, int S, bool 
     SharedPlan pl{};
     pl.group = H / Hkv;
     const double repeated = 2.0 * (B - B / S) * Hkv * max_pages * kPageTokens * d * (fp8 ? 1 : 2);
-    if (pl.group <= 128 && repeated > kRepeatedBytes) {
+    const bool clusters = cluster_splits(B, H, Hkv, d, max_pages, fp8) > 0;
+    if (pl.group <= 128 && repeated > (clusters ? kRepeatedBytesCluster : kRepeatedBytes)) {
         pl.seqs_per_tile = 128 / pl.group;
         const int qt = d <= 64 ? Cfg<64>::QT : Cfg<128>::QT;
         pl.units = (S + pl.seqs_per_tile * qt - 1) / (pl.seqs_per_tile * qt);
@@ -156,6 +159,10 @@ cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
     p.shared_pages = a.shared_pages;
     p.S = a.group_size;
     p.own_only = pl.prefix_splits > 0;
+    if (const int n = p.own_only ? 0 : cluster_splits(a.B, a.H, a.Hkv, a.d, a.max_pages, a.kv_fp8 != 0)) {
+        p.n_splits = n;
+        p.cluster = 1;
+    }
     switch (a.d) {
         case 32: return launch_decode_shared_d<32>(a, pl, p, stream);
         case 64: return launch_decode_shared_d<64>(a, pl, p, stream);

@@ -80,6 +80,8 @@ struct BwdArgs {
 // function and device; cudaFuncSetAttribute is not free on every call).
 cudaError_t current_sm_count(int *sms);
 cudaError_t ensure_max_dynamic_smem(const void *kernel, int bytes);
+// Allows clusters of more than 8 CTAs (once per kernel and device).
+cudaError_t ensure_large_clusters(const void *kernel);
 
 // TMA descriptor of a bf16 [BH, N, D] tensor viewed as 3-D (innermost first) with boxes of
 // 64 x box_rows x 1 and the 128-byte swizzle; rows past N read as zeros.

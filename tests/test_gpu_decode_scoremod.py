@@ -49,6 +49,11 @@ def run(lib, x, fp8, **kw):
     return lib.paged_attn_decode_scoremod(q, k, v, table, ctx, **kw)
 
 
+# A narrow table is cut into clusters of CTAs, which merge among themselves; one this wide into splits that go
+# through the workspace.
+WIDE = 2100
+FORMS = dict(argvalues=[2, WIDE], ids=["cluster", "workspace"])
+
 SHAPES = [  # B, H, Hkv, d, contexts
     (1, 1, 1, 32, [1]), (4, 4, 4, 64, [0, 16, 17, 1025]), (3, 14, 2, 80, [333, 15, 2000]), (2, 12, 1, 96, [1024, 70]),
     (2, 16, 1, 128, [3000, 129]), (2, 40, 2, 128, [513, 900]), (3, 32, 8, 128, [4097, 1, 640]), (1, 6, 2, 32, [2600]),
@@ -58,12 +63,13 @@ SHAPES = [  # B, H, Hkv, d, contexts
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("mod", [(0.0, False, 0), (5.0, False, 0), (0.0, True, 100), (30.0, True, 33)],
                          ids=["plain", "cap5", "bias_window", "cap30_bias_window"])
+@pytest.mark.parametrize("spare", **FORMS)
 @pytest.mark.parametrize("shape", SHAPES, ids=[f"B{s[0]}H{s[1]}kv{s[2]}d{s[3]}" for s in SHAPES])
-def test_matches_the_definition(lib, shape, mod, fp8):
+def test_matches_the_definition(lib, shape, spare, mod, fp8):
     B, H, Hkv, d, ctx = shape
     cap, bias, window = mod
     begin = [c - window for c in ctx] if window else None
-    x = make(B, H, Hkv, d, ctx, fp8, 3, begin)
+    x = make(B, H, Hkv, d, ctx, fp8, 3, begin, spare)
     sl = slopes_of(H) if bias else None
     kb = None if begin is None else torch.tensor(begin, dtype=torch.int32)
     o = torch.full((B, H, d), float("nan"), dtype=torch.bfloat16, device="cuda")
@@ -75,10 +81,11 @@ def test_matches_the_definition(lib, shape, mod, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
-def test_unmapped_pages_and_odd_intervals(lib, fp8):
+@pytest.mark.parametrize("spare", [0, WIDE], ids=["cluster", "workspace"])
+def test_unmapped_pages_and_odd_intervals(lib, fp8, spare):
     ctx = [200, 300, 64, 500, 5000, 50]
     begin = [200, 2**31 - 1, -5, 250, 10, 50]  # nothing left, nothing left, all, a page's middle, nothing left
-    x = make(6, 4, 2, 64, ctx, fp8, 5, spare=0)
+    x = make(6, 4, 2, 64, ctx, fp8, 5, spare=spare)
     x[3][0, 1], x[3][3, 20], x[3][2, 0] = -1, 10**6, -7
     x[3][5, :] = x[1].shape[0]  # no page mapped at all
     out = run(lib, x, fp8, softcap=10.0, alibi_slopes=slopes_of(4), key_begin=torch.tensor(begin, dtype=torch.int32))
@@ -105,8 +112,18 @@ def test_huge_queries_over_e4m3_pages(lib):
     R.check(out[0].cpu(), out[1].cpu(), *R.decode(x[0], x[1], x[2], x[3], [40, 90], scale, True, 20.0))
 
 
-def test_other_stream_graph_and_workspace(lib):
-    x = make(3, 8, 2, 64, [300, 17, 1500], False, 8)
+def test_many_rows_with_few_splits(lib):
+    # 64 x 8 rows of CTAs: one CTA each over an e4m3 cache, two per row at half the batch
+    for B in (32, 64):
+        ctx = [(b * 97) % 1200 for b in range(B)]
+        x = make(B, 8, 8, 32, ctx, True, 9)
+        out = run(lib, x, True, softcap=20.0)
+        R.check(out[0].cpu(), out[1].cpu(), *R.decode(x[0], x[1], x[2], x[3], ctx, 32 ** -0.5, True, 20.0))
+
+
+@pytest.mark.parametrize("spare", **FORMS)
+def test_other_stream_graph_and_workspace(lib, spare):
+    x = make(3, 8, 2, 64, [300, 17, 1500], False, 8, spare=spare)
     want = run(lib, x, False, softcap=20.0)
     side = torch.cuda.Stream()
     q, k, v, table, ctx = (t.cuda() for t in x)
