@@ -14,7 +14,8 @@
 //     (128-byte swizzled boxes of 128 rows x 64 columns).
 //   * 10 warps.  Warps 0-7 are two compute warpgroups: thread r of warpgroup w owns TMEM lane r
 //     (row r of the CTA's own tile) and columns 64w .. 64w+63 of each 128 x 128 score tile.
-//     Warp 8 loads; warp 9 owns the TMEM and one of its threads issues every MMA.
+//     Warp 8 loads; warp 9 owns the TMEM and one of its threads issues every MMA.  (Capped scores: four
+//     warpgroups of 32 columns, then those two warps.)
 //   * dK/dV: S^T = K Q^T and dP^T = V dO^T land in TMEM with lane = key.  The warpgroups write
 //     P^T and dS^T (bf16 pairs) back over the columns they read, where dV += P^T dO and
 //     dK += dS^T Q take them as the A operand straight from TMEM.  Each Q or dO tile is the
@@ -23,8 +24,8 @@
 //   * dQ: S = Q K^T and dP = dO V^T with lane = query; dS (bf16) over dP feeds dQ += dS K.
 //     TMEM: S 128 | dP 128 | dQ d columns.
 //   * Modified scores (forms F >= 0: an interval of keys per query and, bit 0, the cap, bit 1, the distance
-//     bias of s = cap tanh(scale q.k / cap) - slope |distance|): P = exp(s - LSE) as before, and dS, the gradient of the modified score, times 1 - tanh^2
-//     is that of scale q.k.  P times that factor takes the place of P in registers once P itself is
+//     bias of s = cap tanh(scale q.k / cap) - slope |distance|): P = exp(s - LSE) as before, and dS, the
+//     gradient of the modified score, times 1 - tanh^2 is that of scale q.k.  P times that factor takes the place of P in registers once P itself is
 //     packed, so the cap holds no further registers.  Key tiles visit the query tiles from the first to
 //     the last whose intervals meet them (the row-term kernel also writes each query tile's interval).
 //   * Issue order per step j.  dK/dV: dV(j), S^T(j+1), then dK(j), dP^T(j+1).  dQ: S(j+1),
@@ -44,18 +45,25 @@ namespace attn {
 namespace {
 
 constexpr int kT = 128;  // rows of every tile (queries or keys)
-constexpr int kThreads = 320;
-// Forms: plain scores, or modified ones (kMod .. kMod + 3).  The modified forms hold more per score: they
-// launch a third warpgroup whose idle warps give their registers to the compute warpgroups (setmaxnreg:
-// 128 x (2 x 216 + 64) of the 384 x 168 at launch; with 320 threads the dK/dV kernel spilled 528 bytes).
+// Forms: plain scores, or modified ones (kMod .. kMod + 3).
 constexpr int kPlain = -1, kMod = 0;
 template <int F> constexpr bool kIsMod = (F >= kMod);
 template <int F> constexpr bool kHasCap = (F > 0 && (F & 1) != 0);
 template <int F> constexpr bool kHasBias = (F > 0 && (F & 2) != 0);
-template <int F> constexpr int kThreadsOf = kIsMod<F> ? 384 : kThreads;
+// Compute warpgroups, and the columns of a score tile that each takes.  The capped forms do the most per score and
+// take four of 32 columns, whose warps hide one another's latency; the others two of 64.  Measured (causal, 16
+// heads x 8192, the whole backward, four / two): d 128 cap 1049 / 1080 us, cap and bias 1151 / 1217, no cap 964 /
+// 930, bias 1057 / 1018; d 64 cap 889 / 949, both 984 / 1123, no cap 775 / 722, bias 902 / 854.
+template <int F> constexpr int kGroups = kHasCap<F> ? 4 : 2;
+template <int F> constexpr int kCols = kT / kGroups<F>;
+// Two groups of a modified form hold more per thread than the plain form's: a third warpgroup is launched whose
+// idle warps give it their registers (setmaxnreg: 128 x (2 x 216 + 64) of the 384 x 168 at launch; with 320 threads
+// the dK/dV kernel spilled 528 bytes).
+template <int F> constexpr bool kSplitRegs = kIsMod<F> && kGroups<F> == 2;
+template <int F> constexpr int kThreadsOf = 128 * kGroups<F> + (kSplitRegs<F> ? 128 : 64);
 constexpr uint32_t kRegsCompute = 216, kRegsOther = 64;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+template <int F> constexpr int kProducerWarp = 4 * kGroups<F>;
+template <int F> constexpr int kMmaWarp = kProducerWarp<F> + 1;
 constexpr int kStages = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBoxBytes = 128 * 64 * 2;  // one 128-row x 64-column bf16 box
@@ -131,15 +139,33 @@ __device__ __forceinline__ void mma_scores(uint32_t d_tmem, const __nv_bfloat16 
     tc_mma_ss_ksteps<D / 16>(d_tmem, da, db, id, 0u);
 }
 
-// 128 x d accumulation: D[tmem] (+)= A[tmem] B, A = 128 x 128 bf16 written by the two warpgroups
-// (columns 0-31 and 64-95 of a_tmem hold the bf16 pairs of k-indices 0-63 and 64-127), B = a
-// 128-row tile read MN-major (k-index = tile row).
-template <int D>
+// tc_mma_ts_k8_halves for A in four groups of two k-steps, 32 columns apart.
+#define ATTN_TS_QUARTER(COLS, STEP)                                                                   \
+    "add.u32 ta, %1, " #COLS ";\n\tadd.s64 rb, %2, " #STEP                                            \
+    ";\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [ta], rb, %3, q;\n\t"
+__device__ __forceinline__ void tc_mma_ts_k8_quarters(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                                      uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 ta;\n\t.reg .b64 rb;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        ATTN_TS_QUARTER(8, 128) ATTN_TS_QUARTER(32, 256) ATTN_TS_QUARTER(40, 384) ATTN_TS_QUARTER(64, 512)
+        ATTN_TS_QUARTER(72, 640) ATTN_TS_QUARTER(96, 768) ATTN_TS_QUARTER(104, 896) "}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+#undef ATTN_TS_QUARTER
+
+// 128 x d accumulation: D[tmem] (+)= A[tmem] B, A = 128 x 128 bf16 written by the warpgroups (each its
+// columns' pairs at the first of them: k-indices 0-63 and 64-127 in columns 0-31 and 64-95 of a_tmem, or
+// 0-31 in columns 0-15 and so on), B = a 128-row tile read MN-major (k-index = tile row).
+template <int D, int F>
 __device__ __forceinline__ void mma_accum(uint32_t d_tmem, uint32_t a_tmem, const __nv_bfloat16 *b, bool first) {
     constexpr uint32_t id = idesc_bf16_f32(kT, D, false, true);
     const uint64_t db = sdesc_sw128(smem_u32(b), kBoxBytes, 1024);
     static_assert(kT / 16 == 8, "one group of eight k-steps");
-    tc_mma_ts_k8_halves(d_tmem, a_tmem, db, id, first ? 0u : 1u);
+    if constexpr (kGroups<F> == 2) tc_mma_ts_k8_halves(d_tmem, a_tmem, db, id, first ? 0u : 1u);
+    else tc_mma_ts_k8_quarters(d_tmem, a_tmem, db, id, first ? 0u : 1u);
 }
 
 // The bias -slope |d| (log2 domain) over a row of 64 columns at distances d = d0 + Step c (Step 1:
@@ -172,12 +198,13 @@ template <int F> __device__ __forceinline__ float score_factor(const Params<F> &
     else return p.scale_log2;
 }
 
-// 64 TMEM columns of this thread's lane -> registers.
-__device__ __forceinline__ void load64(uint32_t taddr, uint32_t (&x)[2][32]) {
-    tmem_ld32(taddr, x[0]);
-    tmem_ld32(taddr + 32, x[1]);
-    tmem_wait_ld(x[0]);
-    tmem_wait_ld(x[1]);
+// 32 H TMEM columns of this thread's lane -> registers.
+template <int H>
+__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&x)[H][32]) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) tmem_ld32(taddr + 32 * h, x[h]);
+#pragma unroll
+    for (int h = 0; h < H; ++h) tmem_wait_ld(x[h]);
 }
 
 // Writes NCOLS (a multiple of 16) columns of this thread's row of an fp32 TMEM accumulator,
@@ -454,7 +481,7 @@ __device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
             const int slot = j % kStages;
             if (!(ok = mbar_wait(&sm.p_full, (uint32_t)(j & 1), wc, 65))) break;
             tc_fence_after_sync();
-            mma_accum<D>(tdV, tS, sm.dout[slot], j == 0);  // dV += P^T dO
+            mma_accum<D, F>(tdV, tS, sm.dout[slot], j == 0);  // dV += P^T dO
             if (j + 1 < n) {
                 const int u = j + 1;
                 if (!(ok = mbar_wait(&sm.u_full[u % kStages], (uint32_t)((u / kStages) & 1), wc, 66))) break;
@@ -463,7 +490,7 @@ __device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
             }
             if (!(ok = mbar_wait(&sm.ds_full, (uint32_t)(j & 1), wc, 67))) break;
             tc_fence_after_sync();
-            mma_accum<D>(tdK, tdP, sm.q[slot], j == 0);  // dK += dS^T Q
+            mma_accum<D, F>(tdK, tdP, sm.q[slot], j == 0);  // dK += dS^T Q
             tc_commit(&sm.u_empty[slot]);
             if (j == n - 1) tc_commit(&sm.acc_done);
             if (j + 1 < n) {
@@ -480,13 +507,13 @@ __device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
 template <int D, int F>
 __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh_kv, int k0,
                              int kv_end, int delta, int qi_start, int nqt, int u0, int n, WaitCtx wc) {
+    constexpr int kC = kCols<F>, kH = kC / 32;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
-    const uint32_t tS = lane_base + (uint32_t)(w * 64);
-    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * 64);
+    const uint32_t tS = lane_base + (uint32_t)(w * kC);
+    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * kC);
     const int key = k0 + r;
     const bool key_ok = key < kv_end;
-    // with the cap, x becomes tanh and c2 its factor cap * log2(e)
     // with the cap, the scores become tanh in place and the factor to the log2 domain is cap * log2(e)
     [[maybe_unused]] const TanhCap cap(cap_in_of<F>(p), 1.f);
     const float to_log2 = score_factor<F>(p);
@@ -494,12 +521,12 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
     bool ok = true;
     for (int j = 0; j < n; ++j) {
         const int slot = j % kStages;
-        const int col0 = (qi_start + (u0 + j) % nqt) * kT + w * 64;  // query of this half's column 0
+        const int col0 = (qi_start + (u0 + j) % nqt) * kT + w * kC;  // query of this part's column 0
         // valid columns lo <= c < hi: query < Nq, key < kv_end, and key <= query + delta if causal
-        int lo = 0, hi = min(64, p.Nq - col0);
+        int lo = 0, hi = min(kC, p.Nq - col0);
         if (p.causal) lo = max(0, key - delta - col0);
         if (!key_ok) hi = 0;
-        bool need_mask = lo > 0 || hi < 64;
+        bool need_mask = lo > 0 || hi < kC;
 
         // The columns' statistics are read before the score waits so that their latency hides
         // behind them.  The producer wrote them before arriving on the unit's full barrier; waiting
@@ -510,32 +537,33 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
             break;
         }
         if constexpr (kIsMod<F>) need_mask = sm.inside[slot] == 0;
-        float4 L4[16];
-        const float4 *l2 = reinterpret_cast<const float4 *>(sm.nlse2[slot] + w * 64);
+        constexpr int kAheadStats = kGroups<F> == 2 ? kC / 4 : 0;  // (four groups hide the latency, and lack the registers)
+        float4 L4[kAheadStats + 1];
+        const float4 *l2 = reinterpret_cast<const float4 *>(sm.nlse2[slot] + w * kC);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) L4[i] = l2[i];
+        for (int i = 0; i < kAheadStats; ++i) L4[i] = l2[i];
         if (!__all_sync(kFull, mbar_wait(&sm.s_full, (uint32_t)(j & 1), wc, 70))) {
             ok = false;
             break;
         }
         tc_fence_after_sync();
-        uint32_t x[2][32];
-        load64(tS, x);
-        if constexpr (kHasCap<F>) cap.apply(cap.tier(fmaxf(max64_of(x), -min64(x))), x);
+        uint32_t x[kH][32];
+        load_cols(tS, x);
+        if constexpr (kHasCap<F>) cap.apply(cap.tier(abs_max(x)), x);
         // column c is the query at position col0 + c + delta; under the causal mask the keys after it are
         // masked, so the linear form serves there too
         [[maybe_unused]] Distance<1> dist;
         if constexpr (kHasBias<F>) {
             const int first = col0 + delta;
-            dist.set(sm.slope2[slot], first - key, p.causal || first >= k0 + kT - 1, first + 63 <= k0);
+            dist.set(sm.slope2[slot], first - key, p.causal || first >= k0 + kT - 1, first + kC - 1 <= k0);
         }
         // P^T = 2^(s * scale * log2e - lse2): bf16 pairs over the scores, fp32 kept in x
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kH; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 L = L4[(h * 32 + i) / 4];
+                const float4 L = kAheadStats ? L4[(h * 32 + i) / 4] : l2[(h * 32 + i) / 4];
                 const uint64_t x01 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
                 const uint64_t x23 = f32x2_pack(__uint_as_float(x[h][i + 2]), __uint_as_float(x[h][i + 3]));
                 [[maybe_unused]] float g[4];  // 1 - tanh^2
@@ -566,7 +594,7 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
                 }
                 if constexpr (kIsMod<F>) {
                     if (need_mask) {  // the columns' intervals, four queries at a time
-                        const int4 a = sm.lo[slot][w * 16 + (h * 32 + i) / 4], z = sm.hi[slot][w * 16 + (h * 32 + i) / 4];
+                        const int4 a = sm.lo[slot][(w * kC + h * 32 + i) / 4], z = sm.hi[slot][(w * kC + h * 32 + i) / 4];
                         const int al[4] = {a.x, a.y, a.z, a.w}, zl[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
@@ -589,24 +617,24 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
         tc_fence_before_sync();
         mbar_arrive(&sm.p_full);
 
-        float4 D4[16];
-        const float4 *dd = reinterpret_cast<const float4 *>(sm.dterm[slot] + w * 64);
+        float4 D4[kAheadStats + 1];
+        const float4 *dd = reinterpret_cast<const float4 *>(sm.dterm[slot] + w * kC);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) D4[i] = dd[i];
+        for (int i = 0; i < kAheadStats; ++i) D4[i] = dd[i];
         if (!__all_sync(kFull, mbar_wait(&sm.dp_full, (uint32_t)(j & 1), wc, 71))) {
             ok = false;
             break;
         }
         tc_fence_after_sync();
-        uint32_t y[2][32];
-        load64(tdP, y);
+        uint32_t y[kH][32];
+        load_cols(tdP, y);
         // dS^T = P^T * (dP^T - D): bf16 pairs over dP^T
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kH; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 Dv = D4[(h * 32 + i) / 4];
+                const float4 Dv = kAheadStats ? D4[(h * 32 + i) / 4] : dd[(h * 32 + i) / 4];
                 float s0 = __uint_as_float(x[h][i]) * (__uint_as_float(y[h][i]) - Dv.x);
                 float s1 = __uint_as_float(x[h][i + 1]) * (__uint_as_float(y[h][i + 1]) - Dv.y);
                 float s2 = __uint_as_float(x[h][i + 2]) * (__uint_as_float(y[h][i + 2]) - Dv.z);
@@ -634,19 +662,27 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
         else tc_fence_after_sync();
     }
     if (!ok) return;
-    // warpgroup 0 writes dV, warpgroup 1 writes dK (times scale); rows past Nkv are not stored
+    // dV, and dK (times scale), a warpgroup each or two; rows past Nkv are not stored
     const bool store = key < p.Nkv;
+    const size_t row = (size_t)bh_kv * p.Nkv + (store ? key : 0);
+    const bool is_k = w >= kGroups<F> / 2;
+    const uint32_t acc = lane_base + 256u + (is_k ? (uint32_t)kBPad<D> : 0u);
+    const float mul = is_k ? p.scale : 1.f;
+    constexpr int c1 = kDqSplit<D>;  // of two: the second one's first column
     if constexpr (kIsMod<F>) {
         if (p.kv_splits > 1) {  // a part of the queries: fp32 sums, added up by the reduction kernel
-            const size_t rows = (size_t)p.B * p.Hkv * p.Nkv;
-            const size_t part = (size_t)(blockIdx.x % p.kv_splits) * 2 + (w == 0 ? 0 : 1);
-            float *out = p.kv_parts + (part * rows + (size_t)bh_kv * p.Nkv + (store ? key : 0)) * D;
-            store_rows_f32<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, out);
+            const size_t part = (size_t)(blockIdx.x % p.kv_splits) * 2 + (is_k ? 1 : 0);
+            float *out = p.kv_parts + (part * p.B * p.Hkv * p.Nkv + row) * D;
+            if constexpr (kGroups<F> == 2) store_rows_f32<D>(acc, n > 0, store, out);
+            else if (w & 1) store_rows_f32<D - c1>(acc + c1, n > 0, store, out + c1);
+            else store_rows_f32<c1>(acc, n > 0, store, out);
             return;
         }
     }
-    __nv_bfloat16 *dst = (w == 0 ? p.dv : p.dk) + ((size_t)bh_kv * p.Nkv + (store ? key : 0)) * D;
-    store_rows<D>(lane_base + 256u + (uint32_t)(w * kBPad<D>), n > 0, store, w == 0 ? 1.f : p.scale, dst);
+    __nv_bfloat16 *dst = (is_k ? p.dk : p.dv) + row * D;
+    if constexpr (kGroups<F> == 2) store_rows<D>(acc, n > 0, store, mul, dst);
+    else if (w & 1) store_rows<D - c1>(acc + c1, n > 0, store, mul, dst + c1);
+    else store_rows<c1>(acc, n > 0, store, mul, dst);
 }
 
 template <int D, int F>
@@ -682,15 +718,15 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
             mbar_init(&sm.u_empty[s], 1);
         }
         mbar_init(&sm.s_full, 1);
-        mbar_init(&sm.p_full, 256);
+        mbar_init(&sm.p_full, 128 * kGroups<F>);
         mbar_init(&sm.dp_full, 1);
-        mbar_init(&sm.ds_full, 256);
+        mbar_init(&sm.ds_full, 128 * kGroups<F>);
         mbar_init(&sm.acc_done, 1);
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp<F>) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -728,21 +764,21 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     }
 
     // (each role inside the branch that sets its registers: code after a join gets the smaller limit)
-    if (warp >= kProducerWarp) {
-        if constexpr (kIsMod<F>) setmaxnreg_dec<kRegsOther>();
-        if (warp == kProducerWarp) {
+    if (warp >= kProducerWarp<F>) {
+        if constexpr (kSplitRegs<F>) setmaxnreg_dec<kRegsOther>();
+        if (warp == kProducerWarp<F>) {
             if (n > 0) dkdv_producer<D, F>(sm, p, &tmQ, &tmdO, &tmK, &tmV, b, hkv, bh_kv, k0, qi_start, nqt, u0, n, wc);
-        } else if (warp == kMmaWarp) {
+        } else if (warp == kMmaWarp<F>) {
             if (lane == 0 && n > 0) dkdv_mma<D, F>(sm, tmem, n, wc);
         }
     } else {
-        if constexpr (kIsMod<F>) setmaxnreg_inc<kRegsCompute>();
+        if constexpr (kSplitRegs<F>) setmaxnreg_inc<kRegsCompute>();
         dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, u0, n, wc);
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp<F>) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -821,7 +857,7 @@ __device__ void dq_mma(DqSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
             }
             if (!(ok = mbar_wait(&sm.ds_full, (uint32_t)(j & 1), wc, 87))) break;
             tc_fence_after_sync();
-            mma_accum<D>(tdQ, tdP, sm.k[slot], j == 0);  // dQ += dS K
+            mma_accum<D, F>(tdQ, tdP, sm.k[slot], j == 0);  // dQ += dS K
             tc_commit(&sm.u_empty[slot]);
             if (j == n - 1) tc_commit(&sm.acc_done);
             if (j + 1 < n) {
@@ -838,10 +874,11 @@ __device__ void dq_mma(DqSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
 template <int D, int F>
 __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh, int q0, int kv_end,
                            int delta, int n, int j0, int2 span, WaitCtx wc) {
+    constexpr int kC = kCols<F>, kH = kC / 32;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
-    const uint32_t tS = lane_base + (uint32_t)(w * 64);
-    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * 64);
+    const uint32_t tS = lane_base + (uint32_t)(w * kC);
+    const uint32_t tdP = lane_base + 128u + (uint32_t)(w * kC);
     const int row = q0 + r;
     const bool row_ok = row < p.Nq;
     const float lse2 = row_ok ? p.lse[(size_t)bh * p.Nq + row] * kLog2e : 0.f;
@@ -858,9 +895,9 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
     const uint64_t nl2 = f32x2_pack(-lse2, -lse2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-        const int key0 = (j0 + j) * kT + w * 64;
+        const int key0 = (j0 + j) * kT + w * kC;
         const int nvalid = lim - key0;  // columns c < nvalid are valid
-        bool need_mask = nvalid < 64;
+        bool need_mask = nvalid < kC;
         [[maybe_unused]] int lo = 0;  // modified forms: and columns from lo on
         if constexpr (kIsMod<F>) {
             lo = span.x - key0;
@@ -871,18 +908,18 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
             break;
         }
         tc_fence_after_sync();
-        uint32_t x[2][32];
-        load64(tS, x);
+        uint32_t x[kH][32];
+        load_cols(tS, x);
         tc_fence_before_sync();
         mbar_arrive(&sm.s_free);
-        if constexpr (kHasCap<F>) cap.apply(cap.tier(fmaxf(max64_of(x), -min64(x))), x);
+        if constexpr (kHasCap<F>) cap.apply(cap.tier(abs_max(x)), x);
         [[maybe_unused]] Distance<-1> dist;
         if constexpr (kHasBias<F>) {
             const int at = q0 + delta;  // position of the tile's first query
-            dist.set(slope2, row + delta - key0, p.causal || key0 + 63 <= at, key0 >= at + kT - 1);
+            dist.set(slope2, row + delta - key0, p.causal || key0 + kC - 1 <= at, key0 >= at + kT - 1);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kH; ++h)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 const uint64_t x2 = f32x2_pack(__uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
@@ -912,11 +949,11 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
             break;
         }
         tc_fence_after_sync();
-        uint32_t y[2][32];
-        load64(tdP, y);
+        uint32_t y[kH][32];
+        load_cols(tdP, y);
         // dS = P * (dP - D): bf16 pairs over dP
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kH; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -939,7 +976,7 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
             if (rows0 < kT && kv_end < p.Nkv) {
                 uint4 *tile = reinterpret_cast<uint4 *>(sm.k[j % kStages]);
                 for (int box = 0; box < kBBoxes<D>; ++box)
-                    for (int i = rows0 * 8 + (int)threadIdx.x; i < kT * 8; i += 256)
+                    for (int i = rows0 * 8 + (int)threadIdx.x; i < kT * 8; i += 128 * kGroups<F>)
                         tile[box * (kT * 8) + i] = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
@@ -954,6 +991,7 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
         else tc_fence_after_sync();
     }
     if (!ok) return;
+    if (w > 1) return;
     // warpgroup 0 writes columns 0 .. kDqSplit - 1 of dQ, warpgroup 1 the rest (times scale)
     __nv_bfloat16 *dst = p.dq + ((size_t)bh * p.Nq + (row_ok ? row : 0)) * D + (w ? kDqSplit<D> : 0);
     if (w == 0) store_rows<kDqSplit<D>>(lane_base + 256u, n > 0, row_ok, p.scale, dst);
@@ -983,7 +1021,7 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     int j0 = 0;  // modified forms: the first key tile that a row of the CTA sees
     int2 span = make_int2(0, 0);
     if constexpr (kIsMod<F>) {
-        if (warp < 8) {
+        if (warp < kProducerWarp<F>) {
             span = bwd_row_span(p, b, q0 + ((int)threadIdx.x & 127), kv_end);
             const int lo = __reduce_min_sync(kFull, span.x < span.y ? span.x : 0x7fffffff);
             const int hi = __reduce_max_sync(kFull, span.x < span.y ? span.y : 0);
@@ -1001,15 +1039,15 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
             mbar_init(&sm.u_empty[s], 1);
         }
         mbar_init(&sm.s_full, 1);
-        mbar_init(&sm.s_free, 256);
+        mbar_init(&sm.s_free, 128 * kGroups<F>);
         mbar_init(&sm.dp_full, 1);
-        mbar_init(&sm.ds_full, 256);
+        mbar_init(&sm.ds_full, 128 * kGroups<F>);
         mbar_init(&sm.acc_done, 1);
         mbar_init(&sm.drain, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp<F>) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -1025,21 +1063,21 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
         n = hi > 0 ? (hi + kT - 1) / kT - j0 : 0;
     }
 
-    if (warp >= kProducerWarp) {
-        if constexpr (kIsMod<F>) setmaxnreg_dec<kRegsOther>();
-        if (warp == kProducerWarp) {
+    if (warp >= kProducerWarp<F>) {
+        if constexpr (kSplitRegs<F>) setmaxnreg_dec<kRegsOther>();
+        if (warp == kProducerWarp<F>) {
             if (lane == 0 && n > 0) dq_producer<D, F>(sm, &tmQ, &tmdO, &tmK, &tmV, bh, bh_kv, q0, n, j0, wc);
-        } else if (warp == kMmaWarp) {
+        } else if (warp == kMmaWarp<F>) {
             if (lane == 0 && n > 0) dq_mma<D, F>(sm, tmem, n, wc);
         }
     } else {
-        if constexpr (kIsMod<F>) setmaxnreg_inc<kRegsCompute>();
+        if constexpr (kSplitRegs<F>) setmaxnreg_inc<kRegsCompute>();
         dq_compute<D, F>(sm, p, tmem, warp >> 2, bh, q0, kv_end, delta, n, j0, span, wc);
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp<F>) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -1090,7 +1128,7 @@ int heads_per_chunk(double bytes_per_head, int n_heads) {
 // The register split draws on the launch allocation; a larger one would wait forever.
 template <int F>
 cudaError_t check_register_split(const void *kernel) {
-    if (!kIsMod<F>) return cudaSuccess;
+    if (!kSplitRegs<F>) return cudaSuccess;
     cudaFuncAttributes fa;
     const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;

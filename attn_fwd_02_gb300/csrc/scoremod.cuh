@@ -15,6 +15,12 @@
 
 namespace attn {
 
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // tanh(u) for u >= 1 (1 once e^(2u) overflows).
 __device__ __forceinline__ float tanh_large(float u) {
     return 1.f - __fdividef(2.f, 1.f + ex2_approx(u * 2.885390082f));  // 2 log2(e)
@@ -101,6 +107,18 @@ __device__ __forceinline__ float min64(const uint32_t (&s)[2][32]) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) m[a] = fmin3(m[a], __uint_as_float(s[0][i + a]), __uint_as_float(s[1][i + a]));
     return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
+}
+// Largest absolute value of a thread's scores.
+template <int H>
+__device__ __forceinline__ float abs_max(const uint32_t (&s)[H][32]) {
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) m[a] = fmax3_abs(m[a], __uint_as_float(s[h][i + 2 * a]), __uint_as_float(s[h][i + 2 * a + 1]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 // Largest of them.
 __device__ __forceinline__ float max64_of(const uint32_t (&s)[2][32]) {
