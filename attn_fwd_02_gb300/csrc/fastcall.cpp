@@ -9,8 +9,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -67,14 +68,31 @@ struct Call {
     attn_stream_t stream() const {
         return reinterpret_cast<attn_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream());
     }
-    // The output given, or a new one.
+    // The output given, or a new one (made directly: a new tensor through the dispatcher costs 1.3 us, a call with
+    // all of its outputs given 2.8).  The call's device is the current one here, and the memory belongs to its
+    // current stream.
     at::Tensor output(const at::Tensor *given, at::IntArrayRef shape, at::ScalarType type) const {
         if (given) return *given;
-        return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)device));
+        return at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
+                                         c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
     }
-    // The workspace given (its size is the library's to check), or a new one of `need` bytes.
-    at::Tensor workspace(const at::Tensor *given, size_t need) const {
-        return output(given, {(int64_t)(need > 16 ? need : 16)}, at::kByte);
+};
+
+// The workspace given (its size is the library's to check), or new memory of `need` bytes for the call: freed on
+// the stream that it was made for, as a tensor's.
+struct Workspace {
+    c10::DataPtr own;
+    void *data;
+    size_t bytes;
+    Workspace(const at::Tensor *given, size_t need) {
+        if (given) {
+            data = given->data_ptr();
+            bytes = (size_t)given->numel();
+        } else {
+            bytes = need > 16 ? need : 16;
+            own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+            data = own.get();
+        }
     }
 };
 
@@ -120,13 +138,13 @@ PyObject *pair(const at::Tensor &a, const at::Tensor *b) {
     Py_XDECREF(y);
     return r;
 }
-// Runs a body that may throw (torch allocations); errors become Python's.
+// Runs a body whose allocations may throw (before anything is launched): such a call is left to the binding,
+// where torch raises its own error.
 template <class F> PyObject *guarded(F &&body) {
     try {
         return body();
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    } catch (const std::exception &) {
+        return none();
     }
 }
 #define WITHOUT_GIL(call)        \
@@ -270,13 +288,14 @@ PyObject *bwd_scoremod(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!c.here()) return none();
         const int B = i32(x.B), Hq = i32(x.Hq), Hkv = i32(x.Hkv), Nq = i32(x.Nq), Nkv = i32(x.Nkv), d = i32(x.d);
         at::Tensor dq = c.output(gq, x.q->sizes(), at::kBFloat16), dk = c.output(gk, x.k->sizes(), at::kBFloat16);
-        at::Tensor dv = c.output(gv, x.k->sizes(), at::kBFloat16), w = c.workspace(gw, f_bwd_ws(B, Hq, Hkv, Nq, Nkv, d));
+        at::Tensor dv = c.output(gv, x.k->sizes(), at::kBFloat16);
+        const Workspace w(gw, f_bwd_ws(B, Hq, Hkv, Nq, Nkv, d));
         const attn_stream_t s = c.stream();
         int st;
         WITHOUT_GIL(f_bwd(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), o->data_ptr(), ptr<float>(l), g->data_ptr(),
                           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nkv, d, causal, (float)scale,
                           (float)cap, ptr<float>(x.slopes), ptr<int32_t>(x.begin), ptr<int32_t>(x.end),
-                          ptr<int32_t>(x.lens), w.data_ptr(), (size_t)w.numel(), s));
+                          ptr<int32_t>(x.lens), w.data, w.bytes, s));
         if (st) return PyLong_FromLong(st);
         PyObject *p[3] = {THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dv)};
         PyObject *r = p[0] && p[1] && p[2] ? PyTuple_Pack(3, p[0], p[1], p[2]) : nullptr;
@@ -328,7 +347,7 @@ PyObject *decode_scoremod(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!c.here()) return none();
         at::Tensor o = c.output(go, x.q->sizes(), at::kBFloat16), l;
         if (gl || want) l = c.output(gl, {x.B, x.H}, at::kFloat);
-        at::Tensor w = c.workspace(gw, f_decode_ws(x.B, x.H, x.Hkv, x.d, x.max_pages, x.page_size));
+        const Workspace w(gw, f_decode_ws(x.B, x.H, x.Hkv, x.d, x.max_pages, x.page_size));
         float *lp = l.defined() ? ptr<float>(&l) : nullptr;
         const attn_stream_t s = c.stream();
         int st;
@@ -336,12 +355,12 @@ PyObject *decode_scoremod(PyObject *, PyObject *const *a, Py_ssize_t n) {
             WITHOUT_GIL(f_decode_fp8(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), (float)x.ks, (float)x.vs,
                                      ptr<int32_t>(x.table), ptr<int32_t>(x.ctx), x.page_size, o.data_ptr(), lp, x.B, x.H,
                                      x.Hkv, x.d, x.max_pages, x.num_pages, (float)scale, (float)cap, ptr<float>(slopes),
-                                     ptr<int32_t>(begin), w.data_ptr(), (size_t)w.numel(), s));
+                                     ptr<int32_t>(begin), w.data, w.bytes, s));
         else
             WITHOUT_GIL(f_decode(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), ptr<int32_t>(x.table),
                                  ptr<int32_t>(x.ctx), x.page_size, o.data_ptr(), lp, x.B, x.H, x.Hkv, x.d, x.max_pages,
                                  x.num_pages, (float)scale, (float)cap, ptr<float>(slopes), ptr<int32_t>(begin),
-                                 w.data_ptr(), (size_t)w.numel(), s));
+                                 w.data, w.bytes, s));
         if (st) return PyLong_FromLong(st);
         return pair(o, l.defined() ? &l : nullptr);
     });
@@ -366,7 +385,7 @@ PyObject *decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!shared || !c.here()) return none();
         at::Tensor o = c.output(go, x.q->sizes(), at::kBFloat16), l;
         if (gl || want) l = c.output(gl, {x.B, x.H}, at::kFloat);
-        at::Tensor w = c.workspace(gw, f_shared_ws(x.B, x.H, x.Hkv, x.d, x.max_pages, S, x.page_size));
+        const Workspace w(gw, f_shared_ws(x.B, x.H, x.Hkv, x.d, x.max_pages, S, x.page_size));
         float *lp = l.defined() ? ptr<float>(&l) : nullptr;
         const attn_stream_t s = c.stream();
         int st;
@@ -374,11 +393,11 @@ PyObject *decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
             WITHOUT_GIL(f_shared_fp8(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), (float)x.ks, (float)x.vs,
                                      ptr<int32_t>(x.table), ptr<int32_t>(x.ctx), ptr<int32_t>(shared), S, x.page_size,
                                      o.data_ptr(), lp, x.B, x.H, x.Hkv, x.d, x.max_pages, x.num_pages, (float)scale,
-                                     w.data_ptr(), (size_t)w.numel(), s));
+                                     w.data, w.bytes, s));
         else
             WITHOUT_GIL(f_shared(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), ptr<int32_t>(x.table),
                                  ptr<int32_t>(x.ctx), ptr<int32_t>(shared), S, x.page_size, o.data_ptr(), lp, x.B, x.H,
-                                 x.Hkv, x.d, x.max_pages, x.num_pages, (float)scale, w.data_ptr(), (size_t)w.numel(), s));
+                                 x.Hkv, x.d, x.max_pages, x.num_pages, (float)scale, w.data, w.bytes, s));
         if (st) return PyLong_FromLong(st);
         return pair(o, l.defined() ? &l : nullptr);
     });

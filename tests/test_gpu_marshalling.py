@@ -129,6 +129,24 @@ def test_same_errors(lib, monkeypatch, name):
             assert both(lib, monkeypatch, name, args, dict(kw, softcap=cap))[0] == "AttnError"
 
 
+def test_no_memory(lib, monkeypatch):
+    q, pages = rnd(64, 32, 128), rnd(1, 8, 16, 128)
+    table, ctx = torch.zeros(64, 4096, dtype=torch.int32, device="cuda"), i32([16] * 64)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    room = torch.cuda.memory_reserved() + (32 << 20)  # the workspace takes 69 MB
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        for fast in (lib._fast, None):
+            with monkeypatch.context() as m:
+                m.setattr(lib, "_fast", fast)
+                with pytest.raises(torch.OutOfMemoryError):
+                    lib.paged_attn_decode_scoremod(q, pages, pages, table, ctx)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.isfinite(lib.paged_attn_decode_scoremod(q, pages, pages, table, ctx)[0]).all()
+
+
 def test_a_stream_of_its_own_takes_the_same_path_to_the_result(lib):
     args, kw = calls()["paged_attn_decode_scoremod"]
     want = lib.paged_attn_decode_scoremod(*args, **kw)
