@@ -95,12 +95,22 @@ struct BwdModParams : BwdParams {
     const float *slopes;
     float cap_in, cap_out;
     int2 *spans;
-    int kv_splits;    // CTAs per key tile of the dK/dV kernel, each with a share of the query tiles
-    float *kv_parts;  // their sums [split][dV, dK][B, Hkv, Nkv, d] (kv_splits > 1)
+    int kv_target;    // dK/dV kernel: most steps that a CTA of a key tile takes (0: all of them)
+    float *kv_parts;  // the sums of key tiles with several CTAs: [CTA][dV, dK][B, Hkv, Nkv, d]
 };
 template <bool MOD> struct ParamsOf { using type = BwdParams; };
 template <> struct ParamsOf<true> { using type = BwdModParams; };
 template <int F> using Params = typename ParamsOf<kIsMod<F>>::type;
+
+// CTAs of key tile t in the dK/dV kernel: shares of at most `target` of its steps (query tiles x query heads of
+// the group, as the causal mask leaves them; the intervals, which may leave fewer, are on the device).
+constexpr int kMaxSplits = 16;
+__host__ __device__ inline int tile_splits(int t, int target, int group, int Nq, int Nkv, bool causal) {
+    if (target <= 0) return 1;
+    const int n_qt = (Nq + kT - 1) / kT, first = causal ? (t * kT - (Nkv - Nq)) / kT : 0;
+    const int steps = group * (n_qt - (first > 0 ? first : 0)), n = (steps + target - 1) / target;
+    return n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n);
+}
 
 // Keys lo <= j < hi that query `row` of sequence b sees (none past the last query).
 __device__ __forceinline__ int2 bwd_row_span(const BwdModParams &p, int b, int row, int kv_end) {
@@ -356,11 +366,6 @@ struct alignas(1024) DkvTiles {
 };
 template <int D, int F> struct DkvSmem : DkvTiles<D>, QuerySpans<kIsMod<F>> {};
 
-template <int F> __device__ __forceinline__ unsigned splits_of(const Params<F> &p) {
-    if constexpr (kIsMod<F>) return (unsigned)p.kv_splits;
-    else return 1u;
-}
-
 // Query tiles a key tile [k0, k0+128) must visit: queries i >= k0 - delta can see its keys
 // under the causal mask (query i sees key j iff j <= i + delta).
 __device__ __forceinline__ void dkdv_range(const BwdParams &p, int k0, int kv_end, int delta, int &qi_start,
@@ -506,7 +511,7 @@ __device__ void dkdv_mma(DkvSmem<D, F> &sm, uint32_t tmem, int n, WaitCtx wc) {
 
 template <int D, int F>
 __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, int w, int bh_kv, int k0,
-                             int kv_end, int delta, int qi_start, int nqt, int u0, int n, WaitCtx wc) {
+                             int kv_end, int delta, int qi_start, int nqt, int u0, int n, int split, int splits, WaitCtx wc) {
     constexpr int kC = kCols<F>, kH = kC / 32;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
@@ -670,8 +675,8 @@ __device__ void dkdv_compute(DkvSmem<D, F> &sm, const Params<F> &p, uint32_t tme
     const float mul = is_k ? p.scale : 1.f;
     constexpr int c1 = kDqSplit<D>;  // of two: the second one's first column
     if constexpr (kIsMod<F>) {
-        if (p.kv_splits > 1) {  // a part of the queries: fp32 sums, added up by the reduction kernel
-            const size_t part = (size_t)(blockIdx.x % p.kv_splits) * 2 + (is_k ? 1 : 0);
+        if (splits > 1) {  // a part of the queries: fp32 sums, added up by the reduction kernel
+            const size_t part = (size_t)split * 2 + (is_k ? 1 : 0);
             float *out = p.kv_parts + (part * p.B * p.Hkv * p.Nkv + row) * D;
             if constexpr (kGroups<F> == 2) store_rows_f32<D>(acc, n > 0, store, out);
             else if (w & 1) store_rows_f32<D - c1>(acc + c1, n > 0, store, out + c1);
@@ -695,8 +700,23 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
         *reinterpret_cast<DkvSmem<D, F> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    int bh_kv, level;
-    unit_of(p, p.B * p.Hkv, kIsMod<F> ? blockIdx.x / splits_of<F>(p) : blockIdx.x, bh_kv, level);
+    int bh_kv, level, split = 0, splits = 1;
+    bool shared_out = false;
+    if constexpr (kIsMod<F>) shared_out = p.kv_target > 0;
+    if (!shared_out) unit_of(p, p.B * p.Hkv, blockIdx.x, bh_kv, level);
+    if constexpr (kIsMod<F>) {
+        if (shared_out) {
+            const int heads = p.B * p.Hkv;
+            int at = (int)blockIdx.x;
+            for (level = 0;; ++level) {  // key tiles in order across the heads, the longest shares first
+                splits = tile_splits(level, p.kv_target, p.group, p.Nq, p.Nkv, p.causal != 0);
+                if (at < splits * heads) break;
+                at -= splits * heads;
+            }
+            bh_kv = at % heads;
+            split = at / heads;
+        }
+    }
     const int b = bh_kv / p.Hkv, hkv = bh_kv % p.Hkv;
     const int k0 = level * kT;  // level 0 = key tile 0, seen by the most queries when causal
     const int kv_end = kv_end_for(p, b);
@@ -758,9 +778,9 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
             qi_start = sm.first;
             nqt = sm.last - sm.first + 1;
         }
-        const int all = nqt * p.group, split = (int)(blockIdx.x % p.kv_splits);
-        u0 = (int)((long long)all * split / p.kv_splits);
-        n = (int)((long long)all * (split + 1) / p.kv_splits) - u0;
+        const int all = nqt * p.group;
+        u0 = (int)((long long)all * split / splits);
+        n = (int)((long long)all * (split + 1) / splits) - u0;
     }
 
     // (each role inside the branch that sets its registers: code after a join gets the smaller limit)
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
         }
     } else {
         if constexpr (kSplitRegs<F>) setmaxnreg_inc<kRegsCompute>();
-        dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, u0, n, wc);
+        dkdv_compute<D, F>(sm, p, tmem, warp >> 2, bh_kv, k0, kv_end, delta, qi_start, nqt, u0, n, split, splits, wc);
     }
 
     tc_fence_before_sync();
@@ -1085,37 +1105,82 @@ __global__ void __launch_bounds__(kThreadsOf<F>, 1)
     if constexpr (kIsMod<F>) griddep_wait();
 }
 
-// dV and dK [rows, D] from the splits' sums: four columns per thread, in the splits' order.
+// dV and dK [B, Hkv, Nkv, D] of the key tiles with several CTAs from those CTAs' sums: four columns per thread, in
+// the CTAs' order.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_reduce_kernel(const float4 *parts, uint2 *dv, uint2 *dk, long long rows,
-                                                         int splits, float scale) {
-    griddep_wait();  // (launched as the dQ grid, whose end includes the dK/dV grid's, drains)
-    const long long n4 = rows * (D / 4), i = (long long)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) bwd_reduce_kernel(const BwdModParams p, unsigned rows) {
+    const unsigned n4 = rows * (D / 4), i = blockIdx.x * 256 + threadIdx.x;  // (few key tiles: both below 2^31)
     if (i >= 2 * n4) return;
     const bool is_k = i >= n4;
+    const unsigned at = is_k ? i - n4 : i;
+    const int tile = (int)(at / (D / 4) % (unsigned)p.Nkv) / kT;
+    const int splits = tile_splits(tile, p.kv_target, p.group, p.Nq, p.Nkv, p.causal != 0);
+    griddep_wait();  // (launched as the dQ grid, whose end includes the dK/dV grid's, drains)
+    if (splits == 1) return;
+    const float4 *parts = reinterpret_cast<const float4 *>(p.kv_parts);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) {
-        const float4 v = parts[(long long)s * 2 * n4 + i];
+        const float4 v = parts[(size_t)s * 2 * n4 + i];
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
     }
-    const float f = is_k ? scale : 1.f;
-    (is_k ? dk : dv)[is_k ? i - n4 : i] =
+    const float f = is_k ? p.scale : 1.f;
+    reinterpret_cast<uint2 *>(is_k ? p.dk : p.dv)[at] =
         make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
 }
 
-// Splits of the dK/dV kernel of the modified forms: one CTA per key tile leaves the GPU empty for short
-// sequences with few key/value heads, so the steps of a key tile (query tiles x query heads) are shared out.
-// A split costs about 3 steps of start and end and half a step of partial sums, 3.5 n ctas / 152 in all, and
-// n of them leave steps / n in a row: least at n = sqrt(152 steps / (3.5 ctas)).  Measured on 2 x 16 heads (4
-// key/value heads) x 1000, d 64 (64 key tiles of 32 steps), the whole backward: 1 split 122 us, 5 60, 4 56.
-int dkdv_splits(int B, int Hkv, int group, int Nq, int Nkv) {
-    const long long ctas = (long long)B * Hkv * ((Nkv + kT - 1) / kT);
-    const long long steps = (long long)group * ((Nq + kT - 1) / kT);
-    if (ctas >= 152 || steps < 4) return 1;
-    const int n = (int)std::sqrt(152.0 * (double)steps / (3.5 * (double)ctas));
-    const int most = steps / 2 < 16 ? (int)(steps / 2) : 16;
-    return n < 1 ? 1 : (n > most ? most : n);
+// Steps per CTA of the dK/dV kernel of the modified forms, 0 for a key tile's all.  Short sequences with few
+// key/value heads leave the GPU empty at one CTA per key tile, and the causal mask makes those uneven; so the steps
+// are shared out, a key tile's in equal shares of at most `target`: of the targets that cut the longest key tile
+// (`steps`) into 1 to 16, and the shortest whose CTAs are resident at once, the one whose CTAs end first -- one wave
+// after its longest share, more after their common work and, on average, half a share.  A CTA's start and end cost
+// about 6 steps, and the addition of the sums 3.  Measured, the
+// whole backward, causal with a cap, us (shares / the same number of CTAs for each key tile; heads x queries with
+// the key/value heads): d 64 2 x 16 (4) x 1000 53 / 57, 16 (4) x 2048 79 / 91, 16 (8) x 2048 81 / 91, 4 x 16 (4) x
+// 1024 97 / 100, 8 (2) x 512 18.8 / 17.0; d 128 66 / 74, 96 / 115, 99 / 117, 123 / 133, 23.6 / 21.7.
+struct DkdvPlan {
+    int target, head_ctas, most;  // most: CTAs of one key tile
+};
+DkdvPlan dkdv_plan(int B, int Hkv, int group, int Nq, int Nkv, bool causal) {
+    constexpr float kSms = 152.f, kStart = 6.f, kSums = 3.f;
+    const int tiles = (Nkv + kT - 1) / kT;
+    const long long heads = (long long)B * Hkv, steps = (long long)group * ((Nq + kT - 1) / kT);
+    DkdvPlan pl{0, tiles, 1};
+    if (heads * tiles >= 304 || steps < 4 || steps > 100000000) return pl;
+    long long total = 0;
+    for (int t = 0; t < tiles; ++t) {
+        const int first = causal ? (t * kT - (Nkv - Nq)) / kT : 0;
+        const long long n = (Nq + kT - 1) / kT - (first > 0 ? first : 0);
+        total += n > 0 ? n * group : 0;
+    }
+    auto ctas_of = [&](int target) {  // of one head
+        int n = 0;
+        for (int t = 0; t < tiles; ++t) n += tile_splits(t, target, group, Nq, Nkv, causal);
+        return n;
+    };
+    float best = (float)steps + kStart;
+    if ((float)(heads * tiles) > kSms)
+        best = fmaxf(best, ((float)(heads * total) + kStart * (float)(heads * tiles)) / kSms + 0.5f * (float)steps);
+    auto consider = [&](int target) {
+        const int ctas = ctas_of(target);
+        const float all = (float)(heads * ctas);
+        float cost = (float)target + kStart + kSums;
+        if (all > kSms) cost = fmaxf(cost, ((float)(heads * total) + kStart * all) / kSms + 0.5f * (float)target + kSums);
+        if (cost < best) {
+            best = cost;
+            pl = DkdvPlan{target, ctas, (int)((steps + target - 1) / target)};
+            if (pl.most > kMaxSplits) pl.most = kMaxSplits;
+        }
+    };
+    for (int k = 2; k <= kMaxSplits && 2 * k <= steps; ++k) consider((int)((steps + k - 1) / k));
+    int lo = 2, hi = (int)steps;  // the shortest shares of one wave
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if ((float)(heads * ctas_of(mid)) <= kSms) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo < steps) consider(lo);
+    return pl;
 }
 
 int heads_per_chunk(double bytes_per_head, int n_heads) {
@@ -1161,6 +1226,7 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
     p.causal = a.causal;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
+    [[maybe_unused]] DkdvPlan plan{};
     if constexpr (kIsMod<F>) {
         p.key_begin = a.key_begin;
         p.key_end = a.key_end;
@@ -1168,7 +1234,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
         p.cap_out = a.softcap * kLog2e;
         p.spans = a.spans;
-        p.kv_splits = dkdv_splits(a.B, a.Hkv, p.group, a.Nq, a.Nkv);
+        plan = dkdv_plan(a.B, a.Hkv, p.group, a.Nq, a.Nkv, a.causal != 0);
+        p.kv_target = plan.target;
         p.kv_parts = a.kv_parts;
     }
 
@@ -1200,8 +1267,8 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         const unsigned grid = (unsigned)((size_t)pk.units_per_head * BHkv);
         if constexpr (kIsMod<F>) {
-            e = launch_dependent(bwd_dkdv_kernel<D, F>, dim3(grid * p.kv_splits), kThreadsOf<F>, smem, stream, tq, tdo, tk,
-                                 tv, pk);
+            e = launch_dependent(bwd_dkdv_kernel<D, F>, dim3((unsigned)plan.head_ctas * BHkv), kThreadsOf<F>, smem, stream, tq,
+                                 tdo, tk, tv, pk);
         } else {
             bwd_dkdv_kernel<D, F><<<grid, kThreadsOf<F>, smem, stream>>>(tq, tdo, tk, tv, pk);
             e = cudaGetLastError();
@@ -1228,12 +1295,10 @@ cudaError_t launch_bwd_d(const BwdArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     if constexpr (kIsMod<F>) {
-        if (p.kv_splits > 1) {
+        if (p.kv_target > 0) {
             const long long kv_rows = (long long)a.B * a.Hkv * a.Nkv;
-            const cudaError_t e = launch_dependent(
-                bwd_reduce_kernel<D>, dim3((unsigned)((kv_rows * (D / 2) + 255) / 256)), 256, 0, stream,
-                reinterpret_cast<const float4 *>(p.kv_parts), reinterpret_cast<uint2 *>(p.dv),
-                reinterpret_cast<uint2 *>(p.dk), kv_rows, (int)p.kv_splits, a.scale);
+            const cudaError_t e = launch_dependent(bwd_reduce_kernel<D>, dim3((unsigned)((kv_rows * (D / 2) + 255) / 256)),
+                                                   256, 0, stream, static_cast<const BwdModParams &>(p), (unsigned)kv_rows);
             if (e != cudaSuccess) return e;
         }
     }

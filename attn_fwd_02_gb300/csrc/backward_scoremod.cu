@@ -31,7 +31,8 @@ size_t bwd_scoremod_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int
     if (dterm == 0 || Hkv <= 0 || Hq % Hkv != 0 || Nkv <= 0 || d <= 0) return 0;
     offsets[0] = dterm;
     offsets[1] = (dterm + (size_t)B * (((size_t)Nq + kT - 1) / kT) * sizeof(int2) + 255) & ~(size_t)255;
-    const int splits = dkdv_splits(B, Hkv, Hq / Hkv, Nq, Nkv);
+    const int causal = dkdv_plan(B, Hkv, Hq / Hkv, Nq, Nkv, true).most, dense = dkdv_plan(B, Hkv, Hq / Hkv, Nq, Nkv, false).most;
+    const int splits = causal > dense ? causal : dense;
     return offsets[1] + (splits > 1 ? (size_t)splits * 2 * B * Hkv * Nkv * d * sizeof(float) : 0);
 }
 

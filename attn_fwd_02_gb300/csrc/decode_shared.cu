@@ -6,8 +6,8 @@
 // the GPU.  Each sequence's own pages go through the rows kernel, which may start as the first kernel's
 // CTAs leave, and one merge joins the partial results.  Elsewhere the rows kernel reads the shared pages
 // too.  Measured (32 query and 8 key/value heads, d 128): 32 sequences behind one prompt of 8192 tokens
-// 29.2 us, of which the shared pages' kernel takes about 18 and the rows kernel 16, overlapping; 128 sequences
-// in two groups behind documents of up to 16384 tokens over an e4m3 cache 70.7 us (47 and 31).  Both kernels are
+// 28.9 us, of which the shared pages' kernel takes about 18 and the rows kernel 16, overlapping; 128 sequences
+// in two groups behind documents of up to 16384 tokens over an e4m3 cache 70.5 us (47 and 31).  Both kernels are
 // bound by latency, not bandwidth (15 to 52 % of it): a few key tiles per CTA in the first, a page's chain in the
 // second.
 #include "decode_rows.cuh"
