@@ -229,6 +229,18 @@ def test_backward(lib, size, kind, mod):
         assert (err <= tol).all(), (name, float(err.max()), float((err / tol).max()))
 
 
+SHARED_SIZES = [  # key tiles whose steps are shared out: 16 CTAs, several, and more CTAs in all than the GPU holds at once
+    (1, 8, 1, 700, 300, 32), (1, 8, 2, 300, 900, 80), (5, 16, 4, 700, 700, 32),
+]
+
+
+@pytest.mark.parametrize("mod", [(0.0, True), (30.0, True)], ids=["bias", "cap30_bias"])
+@pytest.mark.parametrize("kind", ["causal", "docs", "window", "empty_rows"])
+@pytest.mark.parametrize("size", SHARED_SIZES, ids=["x".join(map(str, s)) for s in SHARED_SIZES])
+def test_backward_of_shared_out_key_tiles(lib, size, kind, mod):
+    test_backward(lib, size, kind, mod)
+
+
 def test_backward_of_a_plain_call_equals_the_plain_backward(lib):
     # 192 key tiles fill the GPU: no split of the queries, and the sums run in the plain kernels' order
     q, k, v, g = (rand(20 + i, 4, h, 650, 128).cuda() for i, h in enumerate((16, 8, 8, 16)))
