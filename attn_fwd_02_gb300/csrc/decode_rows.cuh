@@ -220,13 +220,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
     for (int k = 0; k < first; ++k) issue(k);
 
     // Q as B fragments: column n = g of n-tile nt is query head h0 + 8 nt + g (zero past the group)
-    float c = a.c, cin = a.cap_in;
     uint32_t qb[NT][KS][2];
+    // per score column (heads 2t, 2t + 1 of an n-tile): the factor of its products, to the cap's argument or, without
+    // a cap, to the log2 domain
+    const float c = MOD && a.cap_in > 0.f ? a.cap_in : a.c;
+    float cc[NT][2];
     {
         const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * a.H + h0) * D;
-        float amax = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            float amax = 0.f;
             const uint32_t *qr = reinterpret_cast<const uint32_t *>(q + (size_t)(8 * nt + g) * D);
             const bool have = 8 * nt + g < rows;
 #pragma unroll
@@ -244,24 +247,24 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
                     qb[nt][ks][1] = have ? qr[ks * 8 + 4 + t] : 0u;
                 }
             }
-        }
-        if constexpr (FP8) {
-            // rounded to f16 after 2^-sh, which keeps |Q| below 2^15 (sh 0 but for huge queries; at most 113)
+            cc[nt][0] = cc[nt][1] = c;
+            if constexpr (FP8) {
+                // each head is rounded to f16 after a 2^-sh of its own, which keeps it below 2^15 (sh 0 but for huge
+                // queries; at most 113); its four lanes hold its dims
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-            const int sh = e >= 15 ? min(e - 14, 113) : 0;
-            const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
+                const int sh = e >= 15 ? min(e - 14, 113) : 0;
+                const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         qb[nt][ks][i] = pack_f16x2(__uint_as_float(qb[nt][ks][i] << 16) * f,
                                                    __uint_as_float(qb[nt][ks][i] & 0xffff0000u) * f);
-            c *= back;
-            cin *= back;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) cc[nt][j] *= __shfl_sync(0xffffffffu, back, 4 * (2 * t + j));
+            }
         }
     }
     // modified scores: the slopes of this lane's heads (columns 2t, 2t + 1)
@@ -360,21 +363,19 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[nt][i] += sc2[nt][i];
                 if constexpr (MOD) {
-                    if (cin > 0.f) {
-                        const TanhCap cap(cin, a.cap_out);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[nt][i] *= cc[nt][i & 1];
+                    if (a.cap_in > 0.f) {
                         const float big = fmaxf(fmaxf(fabsf(sc[nt][0]), fabsf(sc[nt][1])),
                                                 fmaxf(fabsf(sc[nt][2]), fabsf(sc[nt][3])));
-                        const uint64_t s01 = f32x2_pack(sc[nt][0], sc[nt][1]), s23 = f32x2_pack(sc[nt][2], sc[nt][3]);
-                        if (__any_sync(0xffffffffu, big * cin > 1.f)) {
-                            f32x2_unpack(cap.eval<2>(s01), sc[nt][0], sc[nt][1]);
-                            f32x2_unpack(cap.eval<2>(s23), sc[nt][2], sc[nt][3]);
+                        const uint64_t u01 = f32x2_pack(sc[nt][0], sc[nt][1]), u23 = f32x2_pack(sc[nt][2], sc[nt][3]);
+                        if (__any_sync(0xffffffffu, big > 1.f)) {
+                            f32x2_unpack(TanhCap::eval_u<2>(u01, a.cap_out), sc[nt][0], sc[nt][1]);
+                            f32x2_unpack(TanhCap::eval_u<2>(u23, a.cap_out), sc[nt][2], sc[nt][3]);
                         } else {
-                            f32x2_unpack(cap.eval<1>(s01), sc[nt][0], sc[nt][1]);
-                            f32x2_unpack(cap.eval<1>(s23), sc[nt][2], sc[nt][3]);
+                            f32x2_unpack(TanhCap::eval_u<1>(u01, a.cap_out), sc[nt][0], sc[nt][1]);
+                            f32x2_unpack(TanhCap::eval_u<1>(u23, a.cap_out), sc[nt][2], sc[nt][3]);
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[nt][i] *= c;
                     }
                     const float far0 = (float)(pr.hi - 1 - tok0 - g);  // distance of token g (token g + 8: 8 less)
 #pragma unroll
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
                         sc[nt][i] = fmaf(-slope2[nt][i & 1], i < 2 ? far0 : far0 - 8.f, sc[nt][i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[nt][i] *= c;
+                    for (int i = 0; i < 4; ++i) sc[nt][i] *= cc[nt][i & 1];
                 }
                 if (ragged) {
 #pragma unroll

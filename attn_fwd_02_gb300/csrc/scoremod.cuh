@@ -51,23 +51,28 @@ struct TanhCap {
             const uint64_t z = f32x2_mul(raw, raw);
             return f32x2_mul(f32x2_fma(z, f32x2_fma(z, n2, n1), n0), raw);
         } else {
-            constexpr float kP[6] = {0.999999414f, -0.333290424f, 0.13281434f,
-                                     -0.0516056762f, 0.0167431162f, -0.00306706033f};
-            const uint64_t u = f32x2_mul(raw, f32x2_pack(in, in)), z = f32x2_mul(u, u);
-            uint64_t t = f32x2_fma(z, f32x2_pack(kP[5] * out, kP[5] * out), f32x2_pack(kP[4] * out, kP[4] * out));
-#pragma unroll
-            for (int k = 3; k >= 0; --k) t = f32x2_fma(z, t, f32x2_pack(kP[k] * out, kP[k] * out));
-            t = f32x2_mul(t, u);
-            if constexpr (T == 2) {
-                float u0, u1, t0, t1;
-                f32x2_unpack(u, u0, u1);
-                f32x2_unpack(t, t0, t1);
-                t0 = fabsf(u0) > 1.f ? copysignf(tanh_large(fabsf(u0)) * out, u0) : t0;
-                t1 = fabsf(u1) > 1.f ? copysignf(tanh_large(fabsf(u1)) * out, u1) : t1;
-                t = f32x2_pack(t0, t1);
-            }
-            return t;
+            return eval_u<T>(f32x2_mul(raw, f32x2_pack(in, in)), out);
         }
+    }
+    // out * tanh(u) of a pair, by the mid (1) or the far (2) form.
+    template <int T>
+    static __device__ __forceinline__ uint64_t eval_u(uint64_t u, float out) {
+        constexpr float kP[6] = {0.999999414f, -0.333290424f, 0.13281434f,
+                                 -0.0516056762f, 0.0167431162f, -0.00306706033f};
+        const uint64_t z = f32x2_mul(u, u);
+        uint64_t t = f32x2_fma(z, f32x2_pack(kP[5] * out, kP[5] * out), f32x2_pack(kP[4] * out, kP[4] * out));
+#pragma unroll
+        for (int k = 3; k >= 0; --k) t = f32x2_fma(z, t, f32x2_pack(kP[k] * out, kP[k] * out));
+        t = f32x2_mul(t, u);
+        if constexpr (T == 2) {
+            float u0, u1, t0, t1;
+            f32x2_unpack(u, u0, u1);
+            f32x2_unpack(t, t0, t1);
+            t0 = fabsf(u0) > 1.f ? copysignf(tanh_large(fabsf(u0)) * out, u0) : t0;
+            t1 = fabsf(u1) > 1.f ? copysignf(tanh_large(fabsf(u1)) * out, u1) : t1;
+            t = f32x2_pack(t0, t1);
+        }
+        return t;
     }
     // One score.
     __device__ __forceinline__ float one(int tier, float raw) const {
