@@ -178,22 +178,21 @@ __device__ __forceinline__ void mma_accum(uint32_t d_tmem, uint32_t a_tmem, cons
     else tc_mma_ts_k8_quarters(d_tmem, a_tmem, db, id, first ? 0u : 1u);
 }
 
-// The bias -slope |d| (log2 domain) over a row of 64 columns at distances d = d0 + Step c (Step 1:
-// columns are queries, -1: columns are keys); nonneg, nonpos: d has one sign over the whole tile, and the
-// bias is linear in the column.
+// The bias -slope |d| (log2 domain) over a row of columns at distances d = d0 + Step c (Step 1: columns are
+// queries, -1: columns are keys); nonneg, nonpos: d has one sign over the whole tile, and |d| needs no operation.  The
+// distances are whole numbers, so that the products are exact to a rounding however steep the slope.
 template <int Step>
 struct Distance {
-    float sl, base, d0;
+    float mul, d0;
     bool linear;
     __device__ __forceinline__ void set(float slope, int d, bool nonneg, bool nonpos) {
-        const float sign = nonneg ? -slope : slope;
         linear = nonneg || nonpos;
+        mul = nonneg || !nonpos ? -slope : slope;
         d0 = (float)d;
-        base = linear ? sign * d0 : -slope;
-        sl = sign * (float)Step;
     }
     __device__ __forceinline__ float add(int c, float e) const {
-        return linear ? fmaf(sl, (float)c, e + base) : fmaf(base, fabsf(d0 + (float)(Step * c)), e);
+        const float d = d0 + (float)(Step * c);
+        return fmaf(mul, linear ? d : fabsf(d), e);
     }
 };
 
@@ -423,7 +422,7 @@ __device__ void dkdv_producer(DkvSmem<D, F> &sm, const Params<F> &p, const CUten
         if constexpr (kIsMod<F>) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) s4n[t] = bwd_row_span(p, b, (qi_start + (u0 + u) % nqt) * kT + lane * 4 + t, kv_end);
-            slope_n = p.slopes ? p.slopes[hkv * p.group + (u0 + u) / nqt] * kLog2e : 0.f;
+            slope_n = p.slopes ? bias_slope(p.slopes[hkv * p.group + (u0 + u) / nqt]) : 0.f;
         }
     };
     if constexpr (kIsMod<F>) load_spans(0);
@@ -911,7 +910,7 @@ __device__ void dq_compute(DqSmem<D, F> &sm, const Params<F> &p, uint32_t tmem, 
     const float to_log2 = score_factor<F>(p);
     const uint64_t c2 = f32x2_pack(to_log2, to_log2);
     [[maybe_unused]] float slope2 = 0.f;
-    if constexpr (kHasBias<F>) slope2 = p.slopes[bh % p.Hq] * kLog2e;
+    if constexpr (kHasBias<F>) slope2 = bias_slope(p.slopes[bh % p.Hq]);
     const uint64_t nl2 = f32x2_pack(-lse2, -lse2);
     bool ok = true;
     for (int j = 0; j < n; ++j) {

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = 8 * nt + 2 * t + j;
-                slope2[nt][j] = a.slopes && r < rows ? a.slopes[h0 + r] * kRowLog2e : 0.f;
+                slope2[nt][j] = a.slopes && r < rows ? bias_slope(a.slopes[h0 + r]) : 0.f;
             }
     }
 

@@ -724,24 +724,28 @@ __device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r) {
     return __uint_as_float((uint32_t)(127 + sh) << 23);
 }
 
-// The distance bias of a row, -slope |pos - key| in the log2 domain, where a score x is mul * raw.  apply adds
-// it to the raw scores, divided by mul, up to a term that is the same for the whole tile, which it returns: the
-// exponential's FMA takes that with the maximum, so the bias costs one FMA a score (16 heads x 8192, d 128,
-// causal: 266 us, 280 with the whole of it added here, 212 without a bias).
+// The distance bias of a row, -slope |pos - key| in the log2 domain, where a score x is c * raw.  apply adds it to a
+// tile's raw scores; their log2-domain values are then mul * (what it leaves) + (what it returns).  Where the bias is
+// linear in the key it is divided by c and its part that is the same for the whole tile is returned: the exponential's
+// FMA takes that with the maximum, so the bias costs one FMA a score (16 heads x 8192, d 128, causal: 266 us, 280
+// with the whole of it added here, 212 without a bias).  Else, and under slopes past kLinearSlope, the scores are
+// brought to the log2 domain (mul 1): with a factor left, the exponential's FMA, whose product is exact, would leave
+// the rounding error of a large maximum in the exponent.
 struct DistanceBias {
-    float slope = 0.f;  // slope * log2(e) / mul
-    float mul = 1.f;
-    int pos = 0;        // the row's position among the keys
+    float slope2 = 0.f;  // slope * log2(e)
+    float lin = 0.f;     // the same / c
+    int pos = 0;         // the row's position among the keys
 
     // key0: the tile's first key; row0: the position of the tile's first row.
     template <int H>
-    __device__ __forceinline__ float apply(uint32_t (&s)[H][2][32], int key0, bool causal, int row0) const {
+    __device__ __forceinline__ float apply(uint32_t (&s)[H][2][32], int key0, bool causal, int row0, float c,
+                                           float &mul) const {
         const float d0 = (float)(pos - key0);
         // all keys of the tile at or before the rows (under the causal mask the later ones are masked),
         // or all after them: the distance is linear in the key
         const bool below = causal || key0 + H * 64 - 1 <= row0, above = key0 >= row0 + kBM;
-        if (below || above) {
-            const float sl = below ? slope : -slope;
+        if (fabsf(slope2) <= kLinearSlope && (below || above)) {
+            const float sl = below ? lin : -lin;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -750,7 +754,8 @@ struct DistanceBias {
                     for (int i = 0; i < 32; ++i)
                         s[h][cc][i] =
                             __float_as_uint(fmaf(sl, (float)(h * 64 + cc * 32 + i), __uint_as_float(s[h][cc][i])));
-            return -sl * d0 * mul;
+            mul = c;
+            return -sl * d0 * c;
         }
 #pragma unroll
         for (int h = 0; h < H; ++h)
@@ -759,7 +764,8 @@ struct DistanceBias {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     s[h][cc][i] = __float_as_uint(
-                        fmaf(-slope, fabsf(d0 - (float)(h * 64 + cc * 32 + i)), __uint_as_float(s[h][cc][i])));
+                        fmaf(-slope2, fabsf(d0 - (float)(h * 64 + cc * 32 + i)), __uint_as_float(s[h][cc][i]) * c));
+        mul = 1.f;
         return 0.f;
     }
 };
@@ -795,11 +801,11 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
     std::conditional_t<kHasBias<M>, DistanceBias, Without> bias;
     if constexpr (kHasCap<M>) c = 1.f;
     if constexpr (kHasBias<M>) {
-        bias.mul = c;
-        bias.slope = p.slopes[bh % p.H] * kLog2e / c;
+        bias.slope2 = bias_slope(p.slopes[bh % p.H]);
+        bias.lin = bias.slope2 / c;
         bias.pos = row + delta;
     }
-    const uint64_t c2 = f32x2_pack(c, c);
+    std::conditional_t<kHasBias<M>, uint64_t, const uint64_t> c2 = f32x2_pack(c, c);
 
     float m_ref = -INFINITY;  // reference max (log2 domain) shared by l and O
     float l = 0.f;
@@ -881,7 +887,8 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
             }
         }
         [[maybe_unused]] float shift = 0.f;  // the tile's common part of the bias
-        if constexpr (kHasBias<M>) shift = bias.template apply<kHalves>(s, key0, p.causal != 0, qs + delta);
+        if constexpr (kHasBias<M>)
+            shift = bias.template apply<kHalves>(s, key0, p.causal != 0, qs + delta, kHasCap<M> ? 1.f : p.scale_log2, c);
         if (need_mask) {
             if constexpr (kHasSpan<M>) nvalid = span.hi - key0;
 #pragma unroll
@@ -918,6 +925,7 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
         float negm = -m_use;
         if constexpr (kHasBias<M>) negm += shift;
         const uint64_t negm2 = f32x2_pack(negm, negm);
+        if constexpr (kHasBias<M>) c2 = f32x2_pack(c, c);
 
         // P = 2^(s*c - m_use) as bf16 pairs (even key in the low half, as the TMEM A operand
         // expects): keys 64h .. 64h + 63 -> columns 32h .. 32h + 31, over the scores already

@@ -102,6 +102,15 @@ struct TanhCap {
     }
 };
 
+// A slope in the log2 domain; finite whatever the slope, so that a distance of 0 adds 0.
+__device__ __forceinline__ float bias_slope(float slope) {
+    return fminf(fmaxf(slope * 1.4426950408889634f, -3.4028235e38f), 3.4028235e38f);
+}
+// Up to this slope (log2 domain) the forward takes the bias of a tile as linear in the column, which is off by 2^-24
+// of its largest value in the tile, 128 slopes (3e-5 of a score here), where -slope |distance| is off by 2^-24 of
+// itself: a steep slope's error would swamp the keys near the query, whose weights are the ones left.
+constexpr float kLinearSlope = 4.f;
+
 // Smallest of the 64 scores a thread holds (four chains of three-input minima).
 __device__ __forceinline__ float min64(const uint32_t (&s)[2][32]) {
     float m[4];

@@ -130,7 +130,8 @@ int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *ls
  *     J    = { j : key_begin[b, i] <= j < key_end[b, i], 0 <= j < kv_lens[b], j <= p_i if causal }
  * and O, LSE as in attn_fwd_gqa over these scores and keys (no visible key: O = 0, LSE = -inf).
  *   softcap       0, or positive; it and scale / softcap at most 2^100
- *   alibi_slopes  [Hq] fp32 (device), finite; NULL: no distance bias.  With slopes, scale >= 2^-100
+ *   alibi_slopes  [Hq] fp32 (device), finite; NULL: no distance bias.  With slopes, scale >= 2^-100.  Scores and
+ *                 LSE are fp32: a score below its range counts as a key that is not seen
  *   key_begin, key_end [B, Nq] int32 (device): any values, clamped; NULL: 0 and Nkv
  * The intervals say documents packed into a row (begin and end of the query's document), a prefix that
  * every query sees (key_end = max(p_i + 1, prefix), causal 0), a window (key_begin = p_i - window + 1)
@@ -420,7 +421,9 @@ int attn_bwd(const void *q, const void *k, const void *v, const void *o, const f
  * cap) the gradient of the modified score, dS = P * (dP - D), times 1 - t_ij^2 is that of scale <q_i, k_j>:
  *     dV = P^T dO,   dK = scale (dS (1 - t^2))^T Q,   dQ = scale (dS (1 - t^2)) K
  * (without the cap the factor is 1; the slopes and the intervals get no gradient).
- *   lse, o: attn_fwd_scoremod's for the same inputs and modification; dout finite
+ *   lse, o: attn_fwd_scoremod's for the same inputs and modification; dout finite.  The weights are exp(s - LSE)
+ *     with LSE in fp32: a row whose |LSE| passes 2^16 (steep slopes, no key near the query) has gradients off by
+ *     |LSE| 2^-24 of themselves and more
  *   workspace: at least attn_bwd_scoremod_workspace_size(B, Hq, Hkv, Nq, Nkv, d) bytes, 16-byte aligned
  * Rows of k and v past kv_lens[b] may hold anything; dk and dv get zeros there.  Other arguments as
  * attn_bwd and attn_fwd_scoremod.
