@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
             if (g == 0) {
-                sm.u.red.m[warp][r] = m_ref[nt][j];
+                // (a sum of NaN counts as seen, so that a query with NaN gives NaN)
+                sm.u.red.m[warp][r] = ls == ls ? m_ref[nt][j] : 0.f;
                 sm.u.red.l[warp][r] = ls;
             }
 #pragma unroll
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
                     O.y = fmaf(ov[c0].y, wgt, O.y);
                 }
             }
-            const bool any = L > 0.f;
+            const bool any = L != 0.f;
             const float inv = any ? (FP8 ? a.v_scale : 1.f) / L : 0.f;
             *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(O.x * inv, O.y * inv);
             if (pair == 0 && a.lse) a.lse[(size_t)b * a.H + h0 + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(128) decode_rows_merge_kernel(const RowsParams
             }
         }
     }
-    const bool any = L > 0.f;
+    const bool any = L != 0.f;
     const float inv = any ? 1.f / L : 0.f;
     if (4 * lane < D)
         *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + (size_t)row * D + 4 * lane) =

@@ -998,10 +998,11 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
                                         __uint_as_float(ov[i + 2]) * p.o_scale, __uint_as_float(ov[i + 3]) * p.o_scale);
             }
         }
-        if (mine) *reinterpret_cast<float2 *>(w + D) = make_float2(l > 0.f ? m_ref : -INFINITY, l);
+        if (mine) *reinterpret_cast<float2 *>(w + D) = make_float2(l > 0.f ? m_ref : (l == 0.f ? -INFINITY : 0.f), l);  // NaN: kept
         return;
     }
-    const bool have = (n_tiles > 0) && (l > 0.f);
+    // (modified scores: a row whose sum is NaN keeps it, in O and LSE)
+    const bool have = (n_tiles > 0) && (kIsMod<M> ? l != 0.f : l > 0.f);
     const float inv_l = have ? (kIsE4m3<M> ? p.o_scale : 1.f) / l : 0.f;
     uint8_t *stage = reinterpret_cast<uint8_t *>(sm.q[t]) + r * 128;
     auto put = [&](int col0, const uint32_t *pk, int nchunks) {  // 16-byte chunks from column col0
