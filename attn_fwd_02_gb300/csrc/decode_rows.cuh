@@ -48,7 +48,7 @@ struct RowsParams {
     const float *slopes;       // [H], may be null
     const int32_t *key_begin;  // [B], may be null
     int chunk_pages;           // pages per split (0: even shares of the pages)
-    int cluster;               // the splits of a row are the CTAs of one cluster, which merges them itself
+    int cluster;               // splits of a row that are the CTAs of one cluster, which merges them itself (0: none)
 };
 
 namespace {
@@ -694,9 +694,9 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int threads, size_t smem, cudaSt
 }
 
 // The rows kernel (dependent: it may overlap the grid before it) and the merge, or one kernel whose
-// clusters merge.
+// clusters merge, where the device can place them.
 template <int D, bool FP8, int NT, bool MOD>
-cudaError_t launch_rows_n(const RowsParams &p, const CUtensorMap &tk, const CUtensorMap &tv, bool dependent,
+cudaError_t launch_rows_n(RowsParams p, const CUtensorMap &tk, const CUtensorMap &tv, bool dependent,
                           cudaStream_t stream) {
     const size_t smem = sizeof(RowsSmem<D, FP8, NT>) + 1024;
     auto kernel = decode_rows_kernel<D, FP8, NT, MOD>;
@@ -704,9 +704,14 @@ cudaError_t launch_rows_n(const RowsParams &p, const CUtensorMap &tk, const CUte
     if (e != cudaSuccess) return e;
     const dim3 grid(p.n_splits, p.Hkv * p.rgroups, p.B);
     if (p.cluster) {
-        if (p.n_splits > 8) e = ensure_large_clusters(reinterpret_cast<const void *>(kernel));
-        if (e != cudaSuccess) return e;
-        return launch_cluster(kernel, grid, kRowWarps * 32, smem, stream, tk, tv, p);
+        if (p.cluster > 8) e = ensure_large_clusters(reinterpret_cast<const void *>(kernel));
+        if (e == cudaSuccess && cluster_fits(reinterpret_cast<const void *>(kernel), p.cluster, kRowWarps * 32, smem)) {
+            RowsParams c = p;
+            c.n_splits = p.cluster;
+            c.chunk_pages = 0;
+            return launch_cluster(kernel, dim3(p.cluster, grid.y, grid.z), kRowWarps * 32, smem, stream, tk, tv, c);
+        }
+        p.cluster = 0;  // no room for the cluster (a part of a GPU): the splits go through the workspace
     }
     if (dependent) {
         e = launch_dependent(kernel, grid, kRowWarps * 32, smem, stream, tk, tv, p);

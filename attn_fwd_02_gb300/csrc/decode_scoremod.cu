@@ -48,11 +48,7 @@ cudaError_t launch_decode_scoremod(const DecodeMoreArgs &a, cudaStream_t stream)
     p.num_pages = a.num_pages;
     p.chunk_pages = chunk_pages_for(a.B, a.H, a.Hkv, a.max_pages);
     p.n_splits = p.ws_splits = (a.max_pages + p.chunk_pages - 1) / p.chunk_pages;
-    if (const int n = cluster_splits(a.B, a.H, a.Hkv, a.d, a.max_pages, a.kv_fp8 != 0)) {
-        p.n_splits = n;
-        p.chunk_pages = 0;
-        p.cluster = 1;
-    }
+    p.cluster = cluster_splits(a.B, a.H, a.Hkv, a.d, a.max_pages, a.kv_fp8 != 0);
     const float kscale = a.scale * (a.kv_fp8 ? a.k_scale : 1.f);
     p.c = kscale * kRowLog2e;
     p.v_scale = a.v_scale;

@@ -159,10 +159,7 @@ cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
     p.shared_pages = a.shared_pages;
     p.S = a.group_size;
     p.own_only = pl.prefix_splits > 0;
-    if (const int n = p.own_only ? 0 : cluster_splits(a.B, a.H, a.Hkv, a.d, a.max_pages, a.kv_fp8 != 0)) {
-        p.n_splits = n;
-        p.cluster = 1;
-    }
+    if (!p.own_only) p.cluster = cluster_splits(a.B, a.H, a.Hkv, a.d, a.max_pages, a.kv_fp8 != 0);
     switch (a.d) {
         case 32: return launch_decode_shared_d<32>(a, pl, p, stream);
         case 64: return launch_decode_shared_d<64>(a, pl, p, stream);

@@ -82,6 +82,8 @@ cudaError_t current_sm_count(int *sms);
 cudaError_t ensure_max_dynamic_smem(const void *kernel, int bytes);
 // Allows clusters of more than 8 CTAs (once per kernel and device).
 cudaError_t ensure_large_clusters(const void *kernel);
+// Whether the current device can hold a cluster of n CTAs of this kernel (asked once per kernel, device and n).
+bool cluster_fits(const void *kernel, int n, int threads, size_t smem);
 
 // TMA descriptor of a bf16 [BH, N, D] tensor viewed as 3-D (innermost first) with boxes of
 // 64 x box_rows x 1 and the 128-byte swizzle; rows past N read as zeros.
