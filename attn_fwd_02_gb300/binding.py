@@ -10,6 +10,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -528,16 +529,28 @@ def _torch():
     if _t is None:
         import torch
         lib = load_library()
-        try:
-            from . import _fastcall
-        except ImportError:
-            _fastcall = None
-        if _fastcall is not None and _fastcall.torch_version == torch.__version__.split("+")[0]:
+        fast = _load_fastcall(torch.__version__, torch.compiled_with_cxx11_abi())
+        if fast is not None:
             address = {n: ctypes.cast(getattr(lib, n), P).value for n in SIGNATURES}
-            if _fastcall.bind(address):
-                _fast = _fastcall
+            if fast.bind(address):
+                _fast = fast
         _t = torch
     return _t
+
+
+def _load_fastcall(torch_version, cxx11_abi):
+    """The compiled marshalling built for this torch and this Python, or None."""
+    from .build import fastcall_path
+    path = fastcall_path(str(torch_version))
+    if not os.path.exists(path):
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location(__package__ + "._fastcall", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+    except ImportError:
+        return None
+    return m if m.torch_version == str(torch_version) and bool(m.cxx11_abi) == bool(cxx11_abi) else None
 
 
 _t = None

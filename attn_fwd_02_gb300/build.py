@@ -5,9 +5,10 @@
 Each translation unit under csrc/ compiles in parallel to an object file under
 _build/, then nvcc links them into attn_fwd_02_gb300/libattn_gb300.so with the
 CUDA runtime linked statically (the library loads without a GPU present).
-g++ also compiles csrc/fastcall.cpp, the binding's compiled argument marshalling, into
-_fastcall.so against the installed torch; where that is not possible (no Python or torch
-headers), the binding marshals in Python alone, with the same results.
+g++ also compiles csrc/fastcall.cpp, the binding's compiled argument marshalling, against the
+installed torch, into a file named by that torch's and this Python's versions; where that is
+not possible (no Python or torch headers), the binding marshals in Python alone, with the
+same results.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import argparse
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -24,7 +26,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libattn_gb300.so")
-FAST_SRC, FAST_OUT = os.path.join(CSRC, "fastcall.cpp"), os.path.join(HERE, "_fastcall.so")
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -65,18 +67,38 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def fastcall_path(torch_version: str) -> str:
+    """The compiled marshalling for one torch (its full version) and this Python: one built for others is not found."""
+    return os.path.join(HERE, f"_fastcall-{torch_version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _installed_torch() -> tuple[str, str]:
+    """Folder and full version of the installed torch, which is not imported ('' without one)."""
+    spec = importlib.util.find_spec("torch")
+    folder = spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else ""
+    try:
+        with open(os.path.join(folder, "version.py")) as f:
+            found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)['\"]", f.read(), re.M)
+    except OSError:
+        found = None
+    return folder, found.group(1) if found else ""
+
+
 def _compile_fastcall() -> str | None:
     header = os.path.join(ROOT, "include", "attn_gb300.h")
-    if os.path.exists(FAST_OUT) and os.path.getmtime(FAST_OUT) >= max(map(os.path.getmtime, (FAST_SRC, header))):
-        return FAST_OUT
-    spec = importlib.util.find_spec("torch")
-    torch = spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else ""
+    torch, version = _installed_torch()
+    if not version:
+        sys.stderr.write("fastcall.cpp was not compiled (the binding marshals in Python): no torch\n")
+        return None
+    out = fastcall_path(version)
+    if os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, (FAST_SRC, header))):
+        return out
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     inc = [os.path.dirname(header), os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
-    tmp = FAST_OUT + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{i}" for i in inc), FAST_SRC,
-           "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f'-DATTN_TORCH_VERSION="{version}"',
+           *(f"-I{i}" for i in inc), FAST_SRC, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         why = r.stderr if r.returncode else ""
@@ -85,8 +107,8 @@ def _compile_fastcall() -> str | None:
     if why:
         sys.stderr.write(f"fastcall.cpp was not compiled (the binding marshals in Python):\n{why[-2000:]}\n")
         return None
-    os.replace(tmp, FAST_OUT)
-    return FAST_OUT
+    os.replace(tmp, out)
+    return out
 
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
@@ -95,8 +117,9 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         for f in os.listdir(BUILD):
             if f.endswith(".o"):
                 os.remove(os.path.join(BUILD, f))
-        if os.path.exists(FAST_OUT):
-            os.remove(FAST_OUT)
+        for f in os.listdir(HERE):
+            if f.startswith("_fastcall") and f.endswith(".so"):
+                os.remove(os.path.join(HERE, f))
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         fast = ex.submit(_compile_fastcall)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))

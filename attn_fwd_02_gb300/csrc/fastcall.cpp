@@ -15,7 +15,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include "attn_gb300.h"
 
@@ -440,8 +439,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, 
 
 PyMODINIT_FUNC PyInit__fastcall() {
     PyObject *m = PyModule_Create(&module);
-    // the torch that this was compiled against; the binding uses the module with that one only
-    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    // the torch (its full version) and the C++ ABI that this was compiled against; the binding uses the module with
+    // those only
+    if (m && (PyModule_AddStringConstant(m, "torch_version", ATTN_TORCH_VERSION) < 0 ||
+              PyModule_AddIntConstant(m, "cxx11_abi", _GLIBCXX_USE_CXX11_ABI) < 0)) {
         Py_DECREF(m);
         return nullptr;
     }
