@@ -821,7 +821,7 @@ ATTN_API const char *attn_status_string(int status) {
     switch (status) {
         case ATTN_OK: return "ok";
         case ATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or oversized dimension, bad scale or cap)";
-        case ATTN_ERR_UNSUPPORTED: return "unsupported (head dim 32, 64, 80, 96 or 128; 64 or 128 for the backward; page size 16; device sm_103)";
+        case ATTN_ERR_UNSUPPORTED: return "unsupported (head dim 32, 64, 80, 96 or 128; page size 16; rotation of a multiple of 16 dims, at most the head dim; device sm_103)";
         case ATTN_ERR_MISALIGNED: return "misaligned pointer (tensors need 16-byte alignment)";
         case ATTN_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than the call's *_workspace_size() (paged_attn_decode_workspace_size(), attn_bwd_workspace_size() and so on)";
         case ATTN_ERR_CUDA: return "CUDA runtime error or launch failure";
