@@ -95,15 +95,16 @@ struct BwdModParams : BwdParams {
     const float *slopes;
     float cap_in, cap_out;
     int2 *spans;
-    int kv_target;    // dK/dV kernel: most steps that a CTA of a key tile takes (0: all of them)
+    int kv_target;    // dK/dV kernel: steps of a key tile that a CTA is to take (0: all of them); see tile_splits
     float *kv_parts;  // the sums of key tiles with several CTAs: [CTA][dV, dK][B, Hkv, Nkv, d]
 };
 template <bool MOD> struct ParamsOf { using type = BwdParams; };
 template <> struct ParamsOf<true> { using type = BwdModParams; };
 template <int F> using Params = typename ParamsOf<kIsMod<F>>::type;
 
-// CTAs of key tile t in the dK/dV kernel: shares of at most `target` of its steps (query tiles x query heads of
-// the group, as the causal mask leaves them; the intervals, which may leave fewer, are on the device).
+// CTAs of key tile t in the dK/dV kernel: equal shares of its steps (query tiles x query heads of the group, as the
+// causal mask leaves them; the intervals, which may leave fewer, are on the device), of at most `target` steps where
+// kMaxSplits shares allow it, else kMaxSplits longer ones.
 constexpr int kMaxSplits = 16;
 __host__ __device__ inline int tile_splits(int t, int target, int group, int Nq, int Nkv, bool causal) {
     if (target <= 0) return 1;
@@ -1133,8 +1134,9 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(const BwdModParams p, u
 // are shared out, a key tile's in equal shares of at most `target`: of the targets that cut the longest key tile
 // (`steps`) into 1 to 16, and the shortest whose CTAs are resident at once, the one whose CTAs end first -- one wave
 // after its longest share, more after their common work and, on average, half a share.  A CTA's start and end cost
-// about 6 steps, and the addition of the sums 3.  Measured, the
-// whole backward, causal with a cap, us (shares / the same number of CTAs for each key tile; heads x queries with
+// about 6 steps, and the addition of the sums 3.  (A target that kMaxSplits shares of the longest key tile do not reach
+// is costed too low, as if its shares were that short; over 20000 sizes that never led to a longer longest share.)
+// Measured, the whole backward, causal with a cap, us (shares / the same number of CTAs for each key tile; heads x queries with
 // the key/value heads): d 64 2 x 16 (4) x 1000 53 / 57, 16 (4) x 2048 79 / 91, 16 (8) x 2048 81 / 91, 4 x 16 (4) x
 // 1024 97 / 100, 8 (2) x 512 18.8 / 17.0; d 128 66 / 74, 96 / 115, 99 / 117, 123 / 133, 23.6 / 21.7.
 struct DkdvPlan {
