@@ -711,6 +711,7 @@ cudaError_t launch_rows_n(RowsParams p, const CUtensorMap &tk, const CUtensorMap
             c.chunk_pages = 0;
             return launch_cluster(kernel, dim3(p.cluster, grid.y, grid.z), kRowWarps * 32, smem, stream, tk, tv, c);
         }
+        (void)cudaGetLastError();
         p.cluster = 0;  // no room for the cluster (a part of a GPU): the splits go through the workspace
     }
     if (dependent) {

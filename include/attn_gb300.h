@@ -131,7 +131,7 @@ int attn_fwd_gqa(const void *q, const void *k, const void *v, void *o, float *ls
  * and O, LSE as in attn_fwd_gqa over these scores and keys (no visible key: O = 0, LSE = -inf).
  *   softcap       0, or positive; it and scale / softcap at most 2^100
  *   alibi_slopes  [Hq] fp32 (device), finite; NULL: no distance bias.  With slopes, scale >= 2^-100.  Scores and
- *                 LSE are fp32: a score below its range counts as a key that is not seen
+ *                 LSE are fp32: a score below its range counts as a key that is not seen, one above it gives NaN
  *   key_begin, key_end [B, Nq] int32 (device): any values, clamped; NULL: 0 and Nkv
  * The intervals say documents packed into a row (begin and end of the query's document), a prefix that
  * every query sees (key_end = max(p_i + 1, prefix), causal 0), a window (key_begin = p_i - window + 1)

@@ -6,9 +6,10 @@
 #include "decode_scoremod.cu"
 
 static bool room;
+static cudaError_t pending = cudaSuccess;  // what the runtime's last error would be
 namespace attn {
 bool cluster_fits(const void *, int, int, size_t) { return room; }
-cudaError_t ensure_large_clusters(const void *) { return room ? cudaSuccess : cudaErrorInvalidValue; }
+cudaError_t ensure_large_clusters(const void *) { return pending = room ? cudaSuccess : cudaErrorInvalidValue; }
 cudaError_t ensure_max_dynamic_smem(const void *, int) { return cudaSuccess; }
 cudaError_t current_sm_count(int *n) { return *n = 152, cudaSuccess; }
 bool encode_qkv_map(CUtensorMap *, const void *, int, int, int, int) { return true; }
@@ -39,7 +40,11 @@ extern "C" cudaError_t __wrap_cudaLaunchKernel(const void *, dim3 g, dim3, void 
 extern "C" cudaError_t __wrap___cudaLaunchKernel(cudaKernel_t, dim3 g, dim3, void **args, size_t, cudaStream_t) {
     return plain(g, args);
 }
-extern "C" cudaError_t __wrap_cudaGetLastError() { return cudaSuccess; }
+extern "C" cudaError_t __wrap_cudaGetLastError() {
+    const cudaError_t e = pending;
+    pending = cudaSuccess;
+    return e;
+}
 
 // room B H Hkv max_pages
 int main(int, char **v) {
