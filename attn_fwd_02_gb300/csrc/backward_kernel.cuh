@@ -53,7 +53,8 @@ template <int F> constexpr bool kHasBias = (F > 0 && (F & 2) != 0);
 // Compute warpgroups, and the columns of a score tile that each takes.  The capped forms do the most per score and
 // take four of 32 columns, whose warps hide one another's latency; the others two of 64.  Measured (causal, 16
 // heads x 8192, the whole backward, four / two): d 128 cap 1049 / 1080 us, cap and bias 1151 / 1217, no cap 964 /
-// 930, bias 1057 / 1018; d 64 cap 889 / 949, both 984 / 1123, no cap 775 / 722, bias 902 / 854.
+// 930, bias 1057 / 1018; d 64 cap 889 / 949, both 984 / 1123, no cap 775 / 722, bias 902 / 854.  (With the distances
+// multiplied as they are, the forms kept take 1021 for the bias and 1143 for both; at d 64 843 and 966.)
 template <int F> constexpr int kGroups = kHasCap<F> ? 4 : 2;
 template <int F> constexpr int kCols = kT / kGroups<F>;
 // Two groups of a modified form hold more per thread than the plain form's: a third warpgroup is launched whose

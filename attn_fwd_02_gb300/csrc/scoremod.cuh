@@ -7,8 +7,10 @@
 //   far                the exponential form 1 - 2 / (1 + e^(2|u|)) where |u| > 1 (its cancellation is
 //                      harmless from there on), the six terms elsewhere.
 // The polynomials are fits of tanh(u) / u in u^2 by iterated weighted least squares.  A warp takes the
-// tier that its largest |u| needs, as one.  Measured on a causal forward of 16 heads x 8192, d = 128: no cap
-// 212 us, scores in the near tier 270, in the far one 561.
+// tier that its largest |u| needs, as one: one score past the cap sends all of a warp's through the exponential form.
+// Measured on a causal forward / backward of 16 heads x 8192, us, with no cap and with the largest score at 0.2, 0.7,
+// 1.5 and 4 times the cap: d = 128 249 / 929, 316 / 1043, 396 / 1080, 807 / 1109, 665 / 1306; d = 64 171 / 718, 258 / 879,
+// 335 / 967, 344 / 973, 516 / 1216.
 #pragma once
 
 #include "sm103_ptx.cuh"
