@@ -247,9 +247,9 @@ def _quantise(x, scale):
 def _pack(codes, scales, value):
     """Pages [P, Hkv, 9 d] of codes [P, Hkv, 16, d] and scales [P, Hkv, 16, d / 16]; value: the values' form."""
     P, h, _, d = codes.shape
-    if value:  # bytes of token pairs in blocks of 16 dims; scales in quads of tokens
-        c = codes.view(P, h, 8, 2, d // 16, 16).permute(0, 1, 4, 2, 5, 3)
-        s = scales.view(P, h, 4, 4, d // 16).transpose(3, 4)
+    if value:  # blocks of 16 dims; quads of tokens 2t, 2t + 1, 2t + 8, 2t + 9, a pair of them in a byte
+        c = codes.view(P, h, 2, 4, 2, d // 16, 16).permute(0, 1, 5, 3, 2, 6, 4)
+        s = scales.view(P, h, 2, 4, 2, d // 16).permute(0, 1, 3, 5, 2, 4)
     else:
         c, s = codes.view(P, h, 16, d // 2, 2), scales
     return torch.cat([(c[..., 0] | (c[..., 1] << 4)).reshape(P, h, 8 * d), s.reshape(P, h, d)], -1)
@@ -260,8 +260,8 @@ def _unpack(pages, d, value):
     P, h, _ = pages.shape
     b, s = pages[..., :8 * d], pages[..., 8 * d:]
     if value:
-        c = torch.stack([b & 15, b >> 4], -1).view(P, h, d // 16, 8, 16, 2).permute(0, 1, 3, 5, 2, 4)
-        return c.reshape(P, h, 16, d), s.view(P, h, 4, d // 16, 4).transpose(3, 4).reshape(P, h, 16, d // 16)
+        c = torch.stack([b & 15, b >> 4], -1).view(P, h, d // 16, 4, 2, 16, 2).permute(0, 1, 4, 3, 6, 2, 5)
+        return c.reshape(P, h, 16, d), s.reshape(P, h, 4, d // 16, 2, 2).permute(0, 1, 4, 2, 5, 3).reshape(P, h, 16, d // 16)
     return torch.stack([b & 15, b >> 4], -1).view(P, h, 16, d), s.reshape(P, h, 16, d // 16)
 
 
@@ -579,9 +579,10 @@ def exact(case, seed):
     def read4(pool, value):
         """The pool's values, without the tensor's scale, by the place of each nibble and scale: [P, Hkv, 16, d]."""
         t, x = torch.arange(16, device=DEV)[:, None], torch.arange(d, device=DEV)[None, :]
-        at = x // 16 * 128 + t // 2 * 16 + x % 16 if value else t * (d // 2) + x // 2
+        quad, half = t % 8 // 2, t // 8
+        at = x // 16 * 128 + quad * 32 + half * 16 + x % 16 if value else t * (d // 2) + x // 2
         high = (t if value else x) % 2 * 4
-        sc = 8 * d + (t // 4 * (d // 4) + x // 16 * 4 + t % 4 if value else t * (d // 16) + x // 16)
+        sc = 8 * d + (quad * (d // 4) + x // 16 * 4 + half * 2 + t % 2 if value else t * (d // 16) + x // 16)
         b = pool.flatten(0, 1)
         code = (b[:, at.expand(16, d).flatten()].view(-1, 16, d) >> high.to(torch.uint8)) & 15
         mag = torch.tensor(E2M1, dtype=f, device=DEV)[(code & 7).int()]
