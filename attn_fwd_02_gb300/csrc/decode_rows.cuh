@@ -63,17 +63,21 @@ constexpr int kRowCluster = 16;  // most splits of a row that one cluster merges
 template <int D, bool FP8> constexpr int kRowBoxes = FP8 ? 1 : (D + 63) / 64;  // 128-byte-row boxes per block
 template <int D, bool FP8> constexpr int kRowBlock = kRowBoxes<D, FP8> * kRowPS * 128;
 
+// What a CTA's warps leave for the merge.
+template <int D, int NT>
+struct RowsRed {
+    float o[kRowWarps][8 * NT][D];
+    float m[kRowWarps][8 * NT];
+    float l[kRowWarps][8 * NT];
+    float2 ml[8 * NT];  // of the CTA (whose O is then in o[0])
+};
+
 template <int D, bool FP8, int NT>
 struct RowsSmem {
     // the merge starts after every warp has consumed its last page: it shares the ring's bytes
     union {
         alignas(1024) uint8_t kv[kRowWarps][kRowSlots<FP8>][2][kRowBlock<D, FP8>];
-        struct {
-            float o[kRowWarps][8 * NT][D];
-            float m[kRowWarps][8 * NT];
-            float l[kRowWarps][8 * NT];
-            float2 ml[8 * NT];  // of the CTA (whose O is then in o[0])
-        } red;
+        RowsRed<D, NT> red;
     } u;
     uint64_t full[kRowWarps][kRowSlots<FP8>];
     int abort_flag;
@@ -133,6 +137,123 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
         r.p1 = base + (int)(n * (split + 1) / a.n_splits);
     }
     return r;
+}
+
+// The end of a CTA's splits: its warps' states are merged in shared memory, over the ring once every warp is done with its
+// pages, and the CTA's goes to the workspace or, through distributed shared memory, into the cluster's result.  CODES: rows
+// g, g + 8 of a tile of O^T are the even and odd dims of its 16, not its halves, and the values have a scale.
+template <int D, int NT, bool CODES, bool MOD>
+__device__ __forceinline__ void rows_finish(RowsRed<D, NT> &red, volatile int *abort_flag, const RowsParams &a,
+                                            const float (&o)[NT][D / 16][4], const float (&m_ref)[NT][2],
+                                            const float (&l)[NT][2], int rows, int h0, int b, int split, float *ws,
+                                            size_t ws_row) {
+    constexpr int KS = D / 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * nt + 2 * t + j;
+            float ls = l[nt][j];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
+            if (g == 0) {
+                // (a sum of NaN counts as seen, so that a query with NaN gives NaN)
+                red.m[warp][r] = ls == ls ? m_ref[nt][j] : 0.f;
+                red.l[warp][r] = ls;
+            }
+#pragma unroll
+            for (int nd = 0; nd < KS; ++nd) {
+                const int d0 = CODES ? 16 * nd + 2 * g : 16 * nd + g;
+                red.o[warp][r][d0] = o[nt][nd][j];
+                red.o[warp][r][d0 + (CODES ? 1 : 8)] = o[nt][nd][j + 2];
+            }
+        }
+    __syncthreads();
+    if (a.cluster) {
+        // the CTA's state, over the first warp's
+        for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
+            const int r = e / D, dd = e % D;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, red.m[w][r]);
+            float L = 0.f, O = 0.f;
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kRowWarps; ++w) {
+                    const float wgt = ex2_approx(red.m[w][r] - M);
+                    L += red.l[w][r] * wgt;
+                    O += red.o[w][r][dd] * wgt;
+                }
+            }
+            red.o[0][r][dd] = O;
+            if (dd == 0) red.ml[r] = make_float2(M, L);
+        }
+        cluster_sync_all();
+        // the cluster's: the rows' pairs of columns are shared out over its threads
+        const uint32_t ml0 = smem_u32(red.ml), o0 = smem_u32(red.o[0]);
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.o) + ((size_t)b * a.H + h0) * D;
+        for (int e = split * kRowWarps * 32 + threadIdx.x; e < rows * (D / 2); e += a.n_splits * kRowWarps * 32) {
+            const int r = e / (D / 2), pair = e % (D / 2);
+            float2 ml[kRowCluster], ov[kRowCluster];
+#pragma unroll
+            for (int c0 = 0; c0 < kRowCluster; ++c0) {
+                ml[c0] = make_float2(-INFINITY, 0.f), ov[c0] = make_float2(0.f, 0.f);
+                if (c0 < a.n_splits) {
+                    ml[c0] = cluster_load2(cluster_map(ml0 + r * 8, c0));
+                    ov[c0] = cluster_load2(cluster_map(o0 + (r * D + 2 * pair) * 4, c0));
+                }
+            }
+            float M = -INFINITY;
+#pragma unroll
+            for (int c0 = 0; c0 < kRowCluster; ++c0) M = fmaxf(M, ml[c0].x);
+            float L = 0.f;
+            float2 O = make_float2(0.f, 0.f);
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int c0 = 0; c0 < kRowCluster; ++c0) {
+                    const float wgt = ex2_approx(ml[c0].x - M);  // 0 for an empty one, whose O is 0
+                    L = fmaf(ml[c0].y, wgt, L);
+                    O.x = fmaf(ov[c0].x, wgt, O.x);
+                    O.y = fmaf(ov[c0].y, wgt, O.y);
+                }
+            }
+            const bool any = L != 0.f;
+            const float inv = any ? (CODES ? a.v_scale : 1.f) / L : 0.f;
+            *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(O.x * inv, O.y * inv);
+            if (pair == 0 && a.lse) a.lse[(size_t)b * a.H + h0 + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its state
+        return;
+    }
+    if (!*abort_flag) {
+        for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
+            const int r = e / D, dd = e % D;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, red.m[w][r]);
+            float L = 0.f, O = 0.f;
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kRowWarps; ++w) {
+                    const float wgt = ex2_approx(red.m[w][r] - M);
+                    L += red.l[w][r] * wgt;
+                    O += red.o[w][r][dd] * wgt;
+                }
+            }
+            ws[r * ws_row + dd] = CODES ? O * a.v_scale : O;
+            if (dd == 0) {
+                ws[r * ws_row + D] = M;
+                ws[r * ws_row + D + 1] = L;
+            }
+        }
+    }
+    // own pages: this grid may have started while the shared pages' grid was still running; its
+    // completion, which the merge relies on, is to include that grid's
+    if (!MOD) griddep_wait();
+    griddep_launch_dependents();
 }
 
 template <int D, bool FP8, int NT, bool MOD>
@@ -475,111 +596,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
         __syncwarp();
     }
 
-    // this warp's state -> shared memory, over the ring once every warp is done with its pages
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = 8 * nt + 2 * t + j;
-            float ls = l[nt][j];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-            if (g == 0) {
-                // (a sum of NaN counts as seen, so that a query with NaN gives NaN)
-                sm.u.red.m[warp][r] = ls == ls ? m_ref[nt][j] : 0.f;
-                sm.u.red.l[warp][r] = ls;
-            }
-#pragma unroll
-            for (int nd = 0; nd < KS; ++nd) {
-                const int d0 = FP8 ? 16 * nd + 2 * g : 16 * nd + g;
-                sm.u.red.o[warp][r][d0] = o[nt][nd][j];
-                sm.u.red.o[warp][r][d0 + (FP8 ? 1 : 8)] = o[nt][nd][j + 2];
-            }
-        }
-    __syncthreads();
-    if (a.cluster) {
-        // the CTA's state, over the first warp's
-        for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
-            const int r = e / D, dd = e % D;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, sm.u.red.m[w][r]);
-            float L = 0.f, O = 0.f;
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < kRowWarps; ++w) {
-                    const float wgt = ex2_approx(sm.u.red.m[w][r] - M);
-                    L += sm.u.red.l[w][r] * wgt;
-                    O += sm.u.red.o[w][r][dd] * wgt;
-                }
-            }
-            sm.u.red.o[0][r][dd] = O;
-            if (dd == 0) sm.u.red.ml[r] = make_float2(M, L);
-        }
-        cluster_sync_all();
-        // the cluster's: the rows' pairs of columns are shared out over its threads
-        const uint32_t ml0 = smem_u32(sm.u.red.ml), o0 = smem_u32(sm.u.red.o[0]);
-        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.o) + ((size_t)b * a.H + h0) * D;
-        for (int e = split * kRowWarps * 32 + threadIdx.x; e < rows * (D / 2); e += a.n_splits * kRowWarps * 32) {
-            const int r = e / (D / 2), pair = e % (D / 2);
-            float2 ml[kRowCluster], ov[kRowCluster];
-#pragma unroll
-            for (int c0 = 0; c0 < kRowCluster; ++c0) {
-                ml[c0] = make_float2(-INFINITY, 0.f), ov[c0] = make_float2(0.f, 0.f);
-                if (c0 < a.n_splits) {
-                    ml[c0] = cluster_load2(cluster_map(ml0 + r * 8, c0));
-                    ov[c0] = cluster_load2(cluster_map(o0 + (r * D + 2 * pair) * 4, c0));
-                }
-            }
-            float M = -INFINITY;
-#pragma unroll
-            for (int c0 = 0; c0 < kRowCluster; ++c0) M = fmaxf(M, ml[c0].x);
-            float L = 0.f;
-            float2 O = make_float2(0.f, 0.f);
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int c0 = 0; c0 < kRowCluster; ++c0) {
-                    const float wgt = ex2_approx(ml[c0].x - M);  // 0 for an empty one, whose O is 0
-                    L = fmaf(ml[c0].y, wgt, L);
-                    O.x = fmaf(ov[c0].x, wgt, O.x);
-                    O.y = fmaf(ov[c0].y, wgt, O.y);
-                }
-            }
-            const bool any = L != 0.f;
-            const float inv = any ? (FP8 ? a.v_scale : 1.f) / L : 0.f;
-            *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(O.x * inv, O.y * inv);
-            if (pair == 0 && a.lse) a.lse[(size_t)b * a.H + h0 + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
-        }
-        cluster_sync_all();  // no CTA leaves while another reads its state
-        return;
-    }
-    if (!sm.abort_flag) {
-        for (int e = threadIdx.x; e < rows * D; e += kRowWarps * 32) {
-            const int r = e / D, dd = e % D;
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, sm.u.red.m[w][r]);
-            float L = 0.f, O = 0.f;
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < kRowWarps; ++w) {
-                    const float wgt = ex2_approx(sm.u.red.m[w][r] - M);
-                    L += sm.u.red.l[w][r] * wgt;
-                    O += sm.u.red.o[w][r][dd] * wgt;
-                }
-            }
-            ws[r * ws_row + dd] = FP8 ? O * a.v_scale : O;
-            if (dd == 0) {
-                ws[r * ws_row + D] = M;
-                ws[r * ws_row + D + 1] = L;
-            }
-        }
-    }
-    // own pages: this grid may have started while the shared pages' grid was still running; its
-    // completion, which the merge relies on, is to include that grid's
-    if (!MOD) griddep_wait();
-    griddep_launch_dependents();
+    rows_finish<D, NT, FP8, MOD>(sm.u.red, &sm.abort_flag, a, o, m_ref, l, rows, h0, b, split, ws, ws_row);
 }
 
 // Merge of the partials of one (sequence, query head) per warp: lanes hold 4 columns each, the weights
