@@ -57,6 +57,21 @@ SIGNATURES = {
     "paged_attn_decode_shared": (I, [P, P, P, P, P, P, I, I, P, P, I, I, I, I, I, I, F, P, Z, P]),
     "paged_attn_decode_shared_fp8": (I, [P, P, P, F, F, P, P, P, I, I, P, P, I, I, I, I, I, I, F, P, Z, P]),
     "attn_check_device_status": (I, [P]),
+    "paged_attn_decode_fp4_workspace_size": (Z, [I, I, I, I, I, I]),
+    "paged_attn_decode_fp4": (I, [P, P, P, F, F, P, P, I, P, P, I, I, I, I, I, I, F, F, P, P, P, Z, P]),
+    "paged_kv_append_fp4": (I, [P, P, P, P, P, P, P, P, P, F, F, P, I, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, P]),
+    "paged_kv_unpack_fp4": (I, [P, P, F, F, P, I, P, P, I, I, I, I, P]),
+    "paged_kv_append_rope_axes": (I, [P, P, P, P, P, P, P, P, P, P, I, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I, P]),
+    "paged_kv_append_rope_axes_fp8": (I, [P, P, P, P, P, P, P, P, P, F, F, P, I, I, I, P, I, P, P, P, P, I, I, I, I, I, I, I, I,
+                                          P]),
+    "attn_rope_axes": (I, [P, P, P, P, P, I, I, I, P, I, I, P, P, P, P, P, I, I, I, I, I, P]),
+    "attn_rope_axes_bwd": (I, [P, P, P, P, P, I, I, I, P, I, I, P, P, P, P, P, I, I, I, I, I, P]),
+    "paged_kv_fork": (I, [P, P, P, P, P, P, P, I, I, I, I, I, P]),
+    "paged_kv_reserve_workspace_size": (Z, [I, I]),
+    "paged_kv_reserve": (I, [P, P, P, P, P, P, P, P, P, I, I, I, I, P, Z, P]),
+    "paged_kv_compact_workspace_size": (Z, [I]),
+    "paged_kv_compact": (I, [P, P, P, P, P, P, P, I, I, I, P, Z, P]),
+    "paged_kv_copy_pages": (I, [P, I, Z, P, P, P, I, I, P]),
     "attn_last_device_status": (I, []),
     "attn_selftest_bounded_wait": (I, [P]),
     "attn_status_string": (ctypes.c_char_p, [I]),
@@ -619,20 +634,49 @@ def _rows_in(t, name, shape, device=None):
     return t.data_ptr(), _Strides(b, h, n)
 
 
+def _axes_in(positions, pair_axis, B, N, cos_sin, device, shared=False):
+    """Positions [axes, B, N] (``shared``: or [axes, 1, N]) and the axis of each pair: the C call's three arguments (four
+    with ``shared``).  The axes' bytes live as long as the tuple."""
+    p = _in(positions, "positions", _t.int32, 3, device)
+    A, Bp, Np = positions.shape
+    if Np != N or (Bp != B and not (shared and Bp == 1)):
+        raise ValueError(f"positions must be [axes, {B}{' or 1' if shared else ''}, {N}], got {tuple(positions.shape)}")
+    try:
+        axis = bytes(pair_axis)
+    except (TypeError, ValueError):
+        raise TypeError("pair_axis must be a sequence of axis numbers") from None
+    if 2 * len(axis) != cos_sin.shape[1]:
+        raise ValueError(f"pair_axis must have one entry for each of the {cos_sin.shape[1] // 2} pairs, got {len(axis)}")
+    return (p, A, Bp, axis) if shared else (p, A, axis)
+
+
 def _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_sin, page_table, start_pos,
-                 interleaved, new_lens, q_out, stream):
+                 interleaved, new_lens, q_out, stream, axes=None, fp4=False):
     torch = _torch()
     kp, ks = _rows_in(k_new, "k_new", None)
     device = k_new.device
     B, Hkv, N, d = k_new.shape
     vp, vs = _rows_in(v_new, "v_new", k_new.shape, device)
-    kpool, vpool = _in(k_pages, "k_pages", page_dtype, 4, device), _in(v_pages, "v_pages", page_dtype, 4, device)
-    cs = _in(cos_sin, "cos_sin", torch.float32, 2, device)
+    dims = 3 if fp4 else 4
+    kpool, vpool = _in(k_pages, "k_pages", page_dtype, dims, device), _in(v_pages, "v_pages", page_dtype, dims, device)
+    cs = None if fp4 and cos_sin is None else _in(cos_sin, "cos_sin", torch.float32, 2, device)
     table = _in(page_table, "page_table", torch.int32, 2, device)
     start = _in(start_pos, "start_pos", torch.int32, 1, device)
-    num_pages, Hk, page_size, dk = k_pages.shape
-    if (Hk, dk) != (Hkv, d) or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d] matching k_new")
+    if fp4:
+        num_pages, page_size = k_pages.shape[0], 16
+        if tuple(k_pages.shape) != (num_pages, Hkv, 9 * d) or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must be [num_pages, Hkv, 9 d] matching k_new")
+        if cs is None and (q is not None or axes is not None):
+            raise ValueError("q and positions need cos_sin")
+    else:
+        num_pages, Hk, page_size, dk = k_pages.shape
+        if (Hk, dk) != (Hkv, d) or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d] matching k_new")
+    where = ()
+    if axes is not None:
+        where = _axes_in(*axes, B, N, cos_sin, device)
+    elif fp4:
+        where = (None, 0, None)
     Bt, max_pages = page_table.shape
     if Bt != B or start_pos.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages] and start_pos [B]")
@@ -655,13 +699,14 @@ def _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_
     if ctx is not None:
         with ctx:
             return _append_rope(fn, q, k_new, v_new, k_pages, v_pages, page_dtype, scales, cos_sin, page_table,
-                                start_pos, interleaved, new_lens, q_out, None)
+                                start_pos, interleaved, new_lens, q_out, None, axes, fp4)
     if q is not None and q_out is None:
         q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
         qo = q_out.data_ptr()
     st = getattr(load_library(), fn)(
-        qp, qs, kp, ks, vp, vs, qo, kpool, vpool, *scales, cs, cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)),
-        table, start, new, page_size, B, H, Hkv, N, d, max_pages, num_pages, _current_stream(device))
+        qp, qs, kp, ks, vp, vs, qo, kpool, vpool, *scales, cs, *((0, 0) if cs is None else cos_sin.shape[::-1]),
+        int(bool(interleaved)), *where, table, start, new, page_size, B, H, Hkv, N, d, max_pages, num_pages,
+        _current_stream(device))
     if st:
         _check(fn, st)
     return q_out
@@ -726,6 +771,294 @@ def _output(t, name, dtype, shape, device):
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t, p
+
+
+def paged_kv_append_rope_axes(q, k_new, v_new, k_pages, v_pages, cos_sin, positions, pair_axis, page_table, start_pos,
+                              interleaved: bool = False, new_lens=None, q_out=None, stream=None):
+    """paged_kv_append_rope by positions with several axes: pair i of token t of sequence b turns by column i of row
+    positions[pair_axis[i], b, t] of cos_sin; start_pos says where in the cache the tokens go.  positions [axes,B,Nnew]
+    int32 (at most 4 axes); pair_axis: an axis for each of the rope_dim / 2 pairs (bytes are taken as they are, other
+    sequences converted at each call).  Tokens with a position outside the table are padding."""
+    if _fast is not None and stream is None:
+        r = _fast.append_rope(None, q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos, interleaved,
+                              new_lens, q_out, positions, pair_axis)
+        if r is not None:
+            return _appended("paged_kv_append_rope_axes", r)
+    return _append_rope("paged_kv_append_rope_axes", q, k_new, v_new, k_pages, v_pages, _torch().bfloat16, (), cos_sin,
+                        page_table, start_pos, interleaved, new_lens, q_out, stream, (positions, pair_axis))
+
+
+def paged_kv_append_rope_axes_fp8(q, k_new, v_new, k_pages, v_pages, k_scale: float, v_scale: float, cos_sin, positions,
+                                  pair_axis, page_table, start_pos, interleaved: bool = False, new_lens=None, q_out=None,
+                                  stream=None):
+    """paged_kv_append_rope_axes into an e4m3 cache (k_pages, v_pages uint8 [P,Hkv,16,d])."""
+    if _fast is not None and stream is None:
+        r = _fast.append_rope((k_scale, v_scale), q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos,
+                              interleaved, new_lens, q_out, positions, pair_axis)
+        if r is not None:
+            return _appended("paged_kv_append_rope_axes_fp8", r)
+    return _append_rope("paged_kv_append_rope_axes_fp8", q, k_new, v_new, k_pages, v_pages, _torch().uint8,
+                        (float(k_scale), float(v_scale)), cos_sin, page_table, start_pos, interleaved, new_lens,
+                        q_out, stream, (positions, pair_axis))
+
+
+def paged_kv_append_fp4(q, k_new, v_new, k_pages, v_pages, k_scale: float, v_scale: float, page_table, start_pos,
+                        cos_sin=None, positions=None, pair_axis=None, interleaved: bool = False, new_lens=None, q_out=None,
+                        stream=None):
+    """New tokens into the 4-bit cache (k_pages, v_pages uint8 [P,Hkv,9 d]: e2m1 codes with an e4m3 scale per 16 dims and
+    one scale per tensor, as the C header lays them out).  With cos_sin queries and keys are rotated on the way, as in
+    paged_kv_append_rope, or, with positions and pair_axis, as in paged_kv_append_rope_axes; without it q must be None.
+    No two sequences of a call may write to the same page.  Returns q_out (None without q)."""
+    if _fast is not None and stream is None:
+        r = _fast.append_fp4((k_scale, v_scale), q, k_new, v_new, k_pages, v_pages, cos_sin, page_table, start_pos,
+                             interleaved, new_lens, q_out, positions, pair_axis)
+        if r is not None:
+            return _appended("paged_kv_append_fp4", r)
+    if positions is None and pair_axis is not None:
+        raise ValueError("pair_axis is given without positions")
+    return _append_rope("paged_kv_append_fp4", q, k_new, v_new, k_pages, v_pages, _torch().uint8,
+                        (float(k_scale), float(v_scale)), cos_sin, page_table, start_pos, interleaved, new_lens,
+                        q_out, stream, None if positions is None else (positions, pair_axis), True)
+
+
+def paged_kv_unpack_fp4(k_pages, v_pages, k_scale: float, v_scale: float, page_ids, k_out=None, v_out=None, stream=None):
+    """Pages page_ids [n] int32 of the 4-bit cache as bf16 pages k_out, v_out [n,Hkv,16,d], over which (with a table of
+    their places) paged_attn_prefill attends.  An id outside the pool leaves its page as it was.  Returns (k_out, v_out)."""
+    if _fast is not None and stream is None:
+        r = _fast.unpack_fp4((k_scale, v_scale), k_pages, v_pages, page_ids, k_out, v_out)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("paged_kv_unpack_fp4", r)
+    torch = _torch()
+    kp = _in(k_pages, "k_pages", torch.uint8, 3)
+    device = k_pages.device
+    vp, ids = _in(v_pages, "v_pages", torch.uint8, 3, device), _in(page_ids, "page_ids", torch.int32, 1, device)
+    num_pages, Hkv, size = k_pages.shape
+    if size % 9 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, 9 d]")
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_unpack_fp4(k_pages, v_pages, k_scale, v_scale, page_ids, k_out, v_out)
+    n, d = page_ids.shape[0], size // 9
+    k_out, ko = _output(k_out, "k_out", torch.bfloat16, (n, Hkv, 16, d), device)
+    v_out, vo = _output(v_out, "v_out", torch.bfloat16, (n, Hkv, 16, d), device)
+    st = load_library().paged_kv_unpack_fp4(kp, vp, float(k_scale), float(v_scale), ids, n, ko, vo, 16, Hkv, d, num_pages,
+                                            _current_stream(device))
+    if st:
+        _check("paged_kv_unpack_fp4", st)
+    return k_out, v_out
+
+
+def _rope_axes(fn, q, k, cos_sin, positions, pair_axis, interleaved, q_out, k_out, stream):
+    if _fast is not None and stream is None:
+        r = _fast.rope_axes(fn.endswith("_bwd"), q, k, cos_sin, positions, pair_axis, interleaved, q_out, k_out)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(fn, r)
+    torch = _torch()
+    qp, qs = _rows_in(q, "q", None)
+    device = q.device
+    B, H, N, d = q.shape
+    Hkv, kp, ks, kop, kos = 0, None, None, None, None
+    if k is not None:
+        Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kp, ks = _rows_in(k, "k", torch.Size((B, Hkv, N, d)), device)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    cs = _in(cos_sin, "cos_sin", torch.float32, 2, device)
+    where = _axes_in(positions, pair_axis, B, N, cos_sin, device, True)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return _rope_axes(fn, q, k, cos_sin, positions, pair_axis, interleaved, q_out, k_out, None)
+    if q_out is None:
+        q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=device)
+    qop, qos = _rows_in(q_out, "q_out", q.shape, device)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, Hkv, N, d), dtype=torch.bfloat16, device=device)
+        kop, kos = _rows_in(k_out, "k_out", k.shape, device)
+    st = getattr(load_library(), fn)(qp, qs, kp, ks, cs, cos_sin.shape[1], cos_sin.shape[0], int(bool(interleaved)), *where,
+                                     qop, qos, kop, kos, B, H, Hkv, N, d, _current_stream(device))
+    if st:
+        _check(fn, st)
+    return q_out, k_out
+
+
+def attn_rope_axes(q, k, cos_sin, positions, pair_axis, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary embedding by positions with several axes: pair i of token t of sequence b turns by column i of row
+    positions[pair_axis[i], b, t] of cos_sin [max_pos, rope_dim] fp32 (cos of the pairs, then sin).  q [B,H,N,d], k
+    [B,Hkv,N,d] (or None) and their outputs: bf16 CUDA views whose rows are contiguous (strides in multiples of 8 elements;
+    an output may be its input); positions [axes,B,N] or [axes,1,N] int32.  Tokens with a position outside the table give
+    zeros.  Returns (q_out, k_out)."""
+    return _rope_axes("attn_rope_axes", q, k, cos_sin, positions, pair_axis, interleaved, q_out, k_out, stream)
+
+
+def attn_rope_axes_bwd(dq, dk, cos_sin, positions, pair_axis, interleaved: bool = False, q_out=None, k_out=None,
+                       stream=None):
+    """Gradient of attn_rope_axes: from those of its outputs, dq and dk (or None), to those of q and k, which may go into
+    views of a fused projection's gradient.  Returns (q_out, k_out)."""
+    return _rope_axes("attn_rope_axes_bwd", dq, dk, cos_sin, positions, pair_axis, interleaved, q_out, k_out, stream)
+
+
+def paged_kv_fork(page_table, ctx_lens, parents, ref_counts, page_table_out=None, ctx_lens_out=None, ref_counts_out=None,
+                  stream=None):
+    """Row b of the result continues row parents[b] of page_table [B,max_pages] (the pages of its ctx_lens[b] tokens;
+    parents[b] == b keeps the row, one outside [0, B) gives an empty row); parents [B_out], ctx_lens [B], ref_counts
+    [num_pages] int32.  Rows that none continues are freed.  ref_counts_out may be ref_counts.  Returns (page_table_out,
+    ctx_lens_out, ref_counts_out)."""
+    if _fast is not None and stream is None:
+        r = _fast.kv_fork(page_table, ctx_lens, parents, ref_counts, page_table_out, ctx_lens_out, ref_counts_out)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("paged_kv_fork", r)
+    i32 = _torch().int32
+    table = _in(page_table, "page_table", i32, 2)
+    device = page_table.device
+    B, W = page_table.shape
+    ctx_p = _optional(ctx_lens, "ctx_lens", i32, (B,), device)
+    par, ref = _in(parents, "parents", i32, 1, device), _in(ref_counts, "ref_counts", i32, 1, device)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_fork(page_table, ctx_lens, parents, ref_counts, page_table_out, ctx_lens_out, ref_counts_out)
+    Bo, P_ = parents.shape[0], ref_counts.shape[0]
+    page_table_out, to = _output(page_table_out, "page_table_out", i32, (Bo, W), device)
+    ctx_lens_out, co = _output(ctx_lens_out, "ctx_lens_out", i32, (Bo,), device)
+    ref_counts_out, ro = _output(ref_counts_out, "ref_counts_out", i32, (P_,), device)
+    st = load_library().paged_kv_fork(table, ctx_p, par, ref, to, co, ro, 16, B, Bo, W, P_, _current_stream(device))
+    if st:
+        _check("paged_kv_fork", st)
+    return page_table_out, ctx_lens_out, ref_counts_out
+
+
+def paged_kv_reserve_workspace_size(B: int, num_pages: int) -> int:
+    return int(load_library().paged_kv_reserve_workspace_size(B, num_pages))
+
+
+def paged_kv_reserve(page_table, ctx_lens, new_lens, ref_counts, page_table_out=None, ref_counts_out=None, reserved=None,
+                     src_pages=None, dst_pages=None, workspace=None, stream=None):
+    """Pages for new_lens[b] more tokens of each row of page_table [B,max_pages]: entries that name no page, or a shared
+    one, get a free page (the lowest ids in order of rows; free: a count of 0 or less).  All int32; page_table_out and
+    ref_counts_out may be the inputs.  Returns (page_table_out, ref_counts_out, reserved, src_pages, dst_pages): reserved
+    [B] is new_lens[b], or 0 for a row without room; paged_kv_copy_pages is to copy src_pages[b] to dst_pages[b] ([B], -1
+    where nothing is to copy)."""
+    if _fast is not None and stream is None:
+        r = _fast.kv_reserve(page_table, ctx_lens, new_lens, ref_counts, page_table_out, ref_counts_out, reserved, src_pages,
+                             dst_pages, workspace)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("paged_kv_reserve", r)
+    i32 = _torch().int32
+    table = _in(page_table, "page_table", i32, 2)
+    device = page_table.device
+    B, W = page_table.shape
+    ctx_p = _optional(ctx_lens, "ctx_lens", i32, (B,), device)
+    new, ref = _optional(new_lens, "new_lens", i32, (B,), device), _in(ref_counts, "ref_counts", i32, 1, device)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_reserve(page_table, ctx_lens, new_lens, ref_counts, page_table_out, ref_counts_out, reserved,
+                                    src_pages, dst_pages, workspace)
+    P_ = ref_counts.shape[0]
+    page_table_out, to = _output(page_table_out, "page_table_out", i32, (B, W), device)
+    ref_counts_out, ro = _output(ref_counts_out, "ref_counts_out", i32, (P_,), device)
+    reserved, rp = _output(reserved, "reserved", i32, (B,), device)
+    src_pages, sp = _output(src_pages, "src_pages", i32, (B,), device)
+    dst_pages, dp = _output(dst_pages, "dst_pages", i32, (B,), device)
+    lib = load_library()
+    workspace, wp, wn = _workspace(workspace, lib.paged_kv_reserve_workspace_size(B, P_), device)
+    st = lib.paged_kv_reserve(table, ctx_p, new, ref, to, ro, rp, sp, dp, 16, B, W, P_, wp, wn, _current_stream(device))
+    if st:
+        _check("paged_kv_reserve", st)
+    return page_table_out, ref_counts_out, reserved, src_pages, dst_pages
+
+
+def paged_kv_compact_workspace_size(num_pages: int) -> int:
+    return int(load_library().paged_kv_compact_workspace_size(num_pages))
+
+
+def paged_kv_compact(page_table, ref_counts, page_table_out=None, ref_counts_out=None, src_pages=None, dst_pages=None,
+                     count=None, workspace=None, stream=None):
+    """Moves the live pages (count positive) to the front of the pool: page_table_out [B,max_pages] (may be page_table) and
+    ref_counts_out [num_pages] name them at their new places, and paged_kv_copy_pages is to copy src_pages[i] to
+    dst_pages[i] ([num_pages], -1 past the first count[0]).  All int32.  Returns (page_table_out, ref_counts_out, src_pages,
+    dst_pages, count)."""
+    if _fast is not None and stream is None:
+        r = _fast.kv_compact(page_table, ref_counts, page_table_out, ref_counts_out, src_pages, dst_pages, count, workspace)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check("paged_kv_compact", r)
+    i32 = _torch().int32
+    table = _in(page_table, "page_table", i32, 2)
+    device = page_table.device
+    ref = _in(ref_counts, "ref_counts", i32, 1, device)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_compact(page_table, ref_counts, page_table_out, ref_counts_out, src_pages, dst_pages, count,
+                                    workspace)
+    (B, W), P_ = page_table.shape, ref_counts.shape[0]
+    page_table_out, to = _output(page_table_out, "page_table_out", i32, (B, W), device)
+    ref_counts_out, ro = _output(ref_counts_out, "ref_counts_out", i32, (P_,), device)
+    src_pages, sp = _output(src_pages, "src_pages", i32, (P_,), device)
+    dst_pages, dp = _output(dst_pages, "dst_pages", i32, (P_,), device)
+    count, cp = _output(count, "count", i32, (1,), device)
+    lib = load_library()
+    workspace, wp, wn = _workspace(workspace, lib.paged_kv_compact_workspace_size(P_), device)
+    st = lib.paged_kv_compact(table, ref, to, ro, sp, dp, cp, B, W, P_, wp, wn, _current_stream(device))
+    if st:
+        _check("paged_kv_compact", st)
+    return page_table_out, ref_counts_out, src_pages, dst_pages, count
+
+
+def paged_kv_copy_pages(pools, src_pages, dst_pages, count=None, stream=None) -> None:
+    """Page dst_pages[i] of each of the pools becomes a copy of page src_pages[i]; src_pages, dst_pages [n] int32 (pairs with
+    an id outside the pool, as -1, are skipped), of which only the first count[0] count if count [1] int32 is given.  pools:
+    a sequence of contiguous CUDA tensors [num_pages, ...] of any type, keys and values of every layer, with pages of the
+    same size, a multiple of 16 bytes.  No page may be a destination twice, or a destination and a source."""
+    if _fast is not None and stream is None:
+        r = _fast.kv_copy_pages(pools, src_pages, dst_pages, count)
+        if r == 0:
+            return
+        if r is not None:
+            _check("paged_kv_copy_pages", r)
+    torch = _torch()
+    sp = _in(src_pages, "src_pages", torch.int32, 1)
+    device = src_pages.device
+    n = src_pages.shape[0]
+    dp, cp = _optional(dst_pages, "dst_pages", torch.int32, (n,), device), _optional(count, "count", torch.int32, (1,), device)
+    if dp is None:
+        raise TypeError("dst_pages must be a torch.Tensor")
+    pools = list(pools)
+    if not pools:
+        raise ValueError("pools is empty")
+    first = None
+    for t in pools:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("pools must be torch.Tensors")
+        _in(t, "a pool", t.dtype, t.dim(), device)
+        if t.dim() < 1 or t.numel() == 0:
+            raise ValueError("a pool must be [num_pages, ...] and not empty")
+        shape = t.shape[0], t.numel() * t.element_size() // t.shape[0]
+        if first is None:
+            first = shape
+        elif shape != first:
+            raise ValueError("all pools must have the same number of pages and bytes per page")
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_copy_pages(pools, src_pages, dst_pages, count)
+    at = (ctypes.c_void_p * len(pools))(*(t.data_ptr() for t in pools))
+    st = load_library().paged_kv_copy_pages(at, len(pools), first[1], sp, dp, cp, n, first[0], _current_stream(device))
+    if st:
+        _check("paged_kv_copy_pages", st)
 
 
 def _dense_inputs(q, k, v):
@@ -841,17 +1174,18 @@ def paged_attn_decode_shared_workspace_size(B: int, H: int, Hkv: int, d: int, ma
                                                                       page_size))
 
 
-def _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens):
+def _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens, fp4=False):
     """Addresses and sizes of a decode batch over a paged cache, on one device."""
     torch = _torch()
     qp = _in(q, "q", torch.bfloat16, 3)
     device = q.device
-    kp, vp = _in(k_pages, "k_pages", page_dtype, 4, device), _in(v_pages, "v_pages", page_dtype, 4, device)
+    dims = 3 if fp4 else 4
+    kp, vp = _in(k_pages, "k_pages", page_dtype, dims, device), _in(v_pages, "v_pages", page_dtype, dims, device)
     table, ctx = _in(page_table, "page_table", torch.int32, 2, device), _in(ctx_lens, "ctx_lens", torch.int32, 1, device)
     B, H, d = q.shape
-    num_pages, Hkv, page_size, dk = k_pages.shape
-    if dk != d or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d] matching q")
+    num_pages, Hkv, page_size, dk = (*k_pages.shape[:2], 16, k_pages.shape[2]) if fp4 else k_pages.shape
+    if dk != (9 * d if fp4 else d) or v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages/v_pages must be [num_pages, Hkv, {'9 d' if fp4 else 'page_size, d'}] matching q")
     Bt, max_pages = page_table.shape
     if Bt != B or ctx_lens.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages] and ctx_lens [B]")
@@ -868,14 +1202,16 @@ def _decode_outputs(out, lse, return_lse, B, H, d, device):
 
 def _decode_scoremod(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes,
                      key_begin, out, lse, workspace, return_lse, stream):
+    fp4 = fn == "paged_attn_decode_fp4"
     if _fast is not None and stream is None:
-        r = _fast.decode_scoremod(scales or None, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap,
-                                  alibi_slopes, key_begin, out, lse, workspace, return_lse)
+        r = (_fast.decode_fp4 if fp4 else _fast.decode_scoremod)(
+            scales or None, q, k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes, key_begin, out, lse,
+            workspace, return_lse)
         if r.__class__ is tuple:
             return r
         if r is not None:
             _check(fn, r)
-    device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens)
+    device, (qp, kp, vp, table, ctx_p), sizes, ps = _paged_inputs(q, k_pages, v_pages, page_dtype, page_table, ctx_lens, fp4)
     B, H, Hkv, d, max_pages, num_pages = sizes
     slopes = _optional(alibi_slopes, "alibi_slopes", _t.float32, (H,), device)
     begin = _optional(key_begin, "key_begin", _t.int32, (B,), device)
@@ -886,8 +1222,8 @@ def _decode_scoremod(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ct
                                     alibi_slopes, key_begin, out, lse, workspace, return_lse, None)
     out, op, lse, lp = _decode_outputs(out, lse, return_lse, B, H, d, device)
     lib = load_library()
-    workspace, wp, wn = _workspace(
-        workspace, lib.paged_attn_decode_scoremod_workspace_size(B, H, Hkv, d, max_pages, ps), device)
+    size = lib.paged_attn_decode_fp4_workspace_size if fp4 else lib.paged_attn_decode_scoremod_workspace_size
+    workspace, wp, wn = _workspace(workspace, size(B, H, Hkv, d, max_pages, ps), device)
     st = getattr(lib, fn)(qp, kp, vp, *scales, table, ctx_p, ps, op, lp, *sizes, d ** -0.5 if scale is None else scale,
                           softcap, slopes, begin, wp, wn, _current_stream(device))
     if st:
@@ -914,6 +1250,21 @@ def paged_attn_decode_scoremod_fp8(q, k_pages, v_pages, k_scale: float, v_scale:
     return _decode_scoremod("paged_attn_decode_scoremod_fp8", _torch().uint8, (float(k_scale), float(v_scale)), q,
                             k_pages, v_pages, page_table, ctx_lens, scale, softcap, alibi_slopes, key_begin, out, lse,
                             workspace, return_lse, stream)
+
+
+def paged_attn_decode_fp4_workspace_size(B: int, H: int, Hkv: int, d: int, max_pages_per_seq: int,
+                                         page_size: int = 16) -> int:
+    return int(load_library().paged_attn_decode_fp4_workspace_size(B, H, Hkv, d, max_pages_per_seq, page_size))
+
+
+def paged_attn_decode_fp4(q, k_pages, v_pages, k_scale: float, v_scale: float, page_table, ctx_lens,
+                          scale: float | None = None, softcap: float = 0.0, alibi_slopes=None, key_begin=None, out=None,
+                          lse=None, workspace=None, return_lse: bool = True, stream=None):
+    """Paged decode over the 4-bit cache (k_pages, v_pages uint8 [P,Hkv,9 d], as paged_kv_append_fp4 writes them), with the
+    optional cap, distance bias and first visible token of paged_attn_decode_scoremod.  Returns (o, lse)."""
+    return _decode_scoremod("paged_attn_decode_fp4", _torch().uint8, (float(k_scale), float(v_scale)), q, k_pages, v_pages,
+                            page_table, ctx_lens, scale, softcap, alibi_slopes, key_begin, out, lse, workspace, return_lse,
+                            stream)
 
 
 def _decode_shared(fn, page_dtype, scales, q, k_pages, v_pages, page_table, ctx_lens, shared_pages, group_size, scale,

@@ -33,7 +33,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden,-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 SOURCES = ["abi.cu", "prefill.cu", "prefill_scoremod.cu", "decode.cu", "kvcache.cu", "backward.cu", "backward_scoremod.cu", "append_rope.cu",
-           "decode_scoremod.cu", "decode_shared.cu"]
+           "decode_scoremod.cu", "decode_shared.cu", "append_fp4.cu", "decode_fp4.cu", "rope_axes.cu", "pages.cu"]
 
 
 def nvcc() -> str:

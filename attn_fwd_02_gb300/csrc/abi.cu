@@ -437,6 +437,8 @@ ATTN_API size_t paged_attn_decode_gqa_workspace_size(int B, int H, int Hkv, int 
 
 namespace {
 bool finite_positive(float x) { return x > 0.f && x < 3.0e38f; }
+// A tensor's scale of the 4-bit cache: it and its reciprocal are normal fp32 numbers.
+bool fp4_scale(float x) { return x >= 1e-37f && x <= 1e37f; }
 // Head dims of the decode kernels: the same five as the prefill.
 bool decode_head_dim(int d) { return prefill_head_dim(d); }
 
@@ -576,16 +578,41 @@ int input_strides(const int64_t *given, int B, int H, int N, int d, int64_t (&ou
     return ATTN_OK;
 }
 
+// Positions with several axes: [axes, B, N] (or [axes, 1, N] for all sequences), and the axis of each of the rope_dim / 2
+// pairs, on the host.
+int rope_axes_arg(const int32_t *positions, int n_axes, int positions_batch, const uint8_t *pair_axis, int rope_dim, int B,
+                  int N, attn::RopeAxes &out) {
+    if (!positions || !pair_axis || n_axes <= 0 || B <= 0 || N <= 0) return ATTN_ERR_INVALID_ARG;
+    if (positions_batch != 1 && positions_batch != B) return ATTN_ERR_INVALID_ARG;
+    if (n_axes > attn::kMaxAxes) return ATTN_ERR_UNSUPPORTED;
+    if (rope_dim <= 0 || rope_dim > attn::kMaxRope || rope_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned4(positions)) return ATTN_ERR_MISALIGNED;
+    out.positions = positions;
+    out.batch_stride = positions_batch == 1 ? 0 : N;
+    out.axis_stride = (long long)positions_batch * N;
+    out.axes = n_axes;
+    out.pair_axis[0] = out.pair_axis[1] = 0;
+    for (int i = 0; i < rope_dim / 2; ++i) {
+        if (pair_axis[i] >= n_axes) return ATTN_ERR_INVALID_ARG;
+        out.pair_axis[i >> 5] |= (uint64_t)pair_axis[i] << (2 * (i & 31));
+    }
+    return ATTN_OK;
+}
+
+// fp4: into the 4-bit cache, where the rotation may be left out (cos_sin null, and then no queries).
 int append_rope(attn::RopeAppendArgs a, const int64_t *q_strides, const int64_t *k_strides, const int64_t *v_strides,
-                int page_size, attn_stream_t stream) {
-    if (!a.k_new || !a.v_new || !a.k_pages || !a.v_pages || !a.cos_sin || !a.page_table || !a.start_pos)
-        return ATTN_ERR_INVALID_ARG;
+                int page_size, attn_stream_t stream, bool fp4 = false) {
+    if (!a.k_new || !a.v_new || !a.k_pages || !a.v_pages || !a.page_table || !a.start_pos) return ATTN_ERR_INVALID_ARG;
+    const bool plain = fp4 && !a.cos_sin;
+    if (!a.cos_sin && (!plain || a.q || a.axes.positions)) return ATTN_ERR_INVALID_ARG;
+    if (plain) a.rope_dim = 16, a.max_pos = 1, a.interleaved = 0;
     if ((a.q == nullptr) != (a.q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
     if (a.B <= 0 || a.Hkv <= 0 || a.Nnew <= 0 || a.d <= 0 || page_size <= 0 || a.max_pages <= 0 || a.num_pages <= 0 ||
         a.max_pos <= 0 || (a.q && a.H <= 0))
         return ATTN_ERR_INVALID_ARG;
     if (a.interleaved != 0 && a.interleaved != 1) return ATTN_ERR_INVALID_ARG;
     if (a.kv_fp8 && (!finite_positive(a.k_scale) || !finite_positive(a.v_scale))) return ATTN_ERR_INVALID_ARG;
+    if (fp4 && (!fp4_scale(a.k_scale) || !fp4_scale(a.v_scale))) return ATTN_ERR_INVALID_ARG;
     if (!prefill_head_dim(a.d) || page_size != 16) return ATTN_ERR_UNSUPPORTED;
     if (a.rope_dim <= 0 || a.rope_dim > a.d || a.rope_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
     if ((uint64_t)a.max_pages * 16 > (1ull << 30)) return ATTN_ERR_INVALID_ARG;
@@ -603,7 +630,8 @@ int append_rope(attn::RopeAppendArgs a, const int64_t *q_strides, const int64_t 
     int *status = nullptr;
     st = device_setup(&status);
     if (st != ATTN_OK) return st;
-    const cudaError_t e = attn::launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = fp4 ? attn::launch_kv_append_fp4(a, reinterpret_cast<cudaStream_t>(stream))
+                              : attn::launch_kv_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 }  // namespace
@@ -633,6 +661,254 @@ ATTN_API int paged_kv_append_rope_fp8(const void *q, const int64_t *q_strides, c
     return append_rope(a, q_strides, k_strides, v_strides, page_size, stream);
 }
 
+ATTN_API int paged_kv_append_rope_axes(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                                       const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages,
+                                       void *v_pages, const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                                       const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                                       const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                                       int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                                       int num_pages, attn_stream_t stream) {
+    attn::RopeAppendArgs a{q, k_new, v_new, {}, {}, {}, q_out, k_pages, v_pages, cos_sin, rope_dim, max_pos,
+                           interleaved, page_table, start_pos, new_lens, B, H, Hkv, Nnew, d, max_pages_per_seq,
+                           num_pages};
+    const int st = rope_axes_arg(positions, n_axes, B, pair_axis, rope_dim, B, Nnew, a.axes);
+    return st == ATTN_OK ? append_rope(a, q_strides, k_strides, v_strides, page_size, stream) : st;
+}
+
+ATTN_API int paged_kv_append_rope_axes_fp8(const void *q, const int64_t *q_strides, const void *k_new,
+                                           const int64_t *k_strides, const void *v_new, const int64_t *v_strides,
+                                           void *q_out, void *k_pages, void *v_pages, float k_scale, float v_scale,
+                                           const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                                           const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                                           const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                                           int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                                           int num_pages, attn_stream_t stream) {
+    attn::RopeAppendArgs a{q, k_new, v_new, {}, {}, {}, q_out, k_pages, v_pages, cos_sin, rope_dim, max_pos,
+                           interleaved, page_table, start_pos, new_lens, B, H, Hkv, Nnew, d, max_pages_per_seq,
+                           num_pages, 1, k_scale, v_scale};
+    const int st = rope_axes_arg(positions, n_axes, B, pair_axis, rope_dim, B, Nnew, a.axes);
+    return st == ATTN_OK ? append_rope(a, q_strides, k_strides, v_strides, page_size, stream) : st;
+}
+
+ATTN_API int paged_kv_append_fp4(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                                 const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                                 float k_scale, float v_scale, const float *cos_sin, int rope_dim, int max_pos,
+                                 int interleaved, const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                                 const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens, int page_size,
+                                 int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq, int num_pages,
+                                 attn_stream_t stream) {
+    attn::RopeAppendArgs a{q, k_new, v_new, {}, {}, {}, q_out, k_pages, v_pages, cos_sin, rope_dim, max_pos,
+                           interleaved, page_table, start_pos, new_lens, B, H, Hkv, Nnew, d, max_pages_per_seq,
+                           num_pages, 0, k_scale, v_scale};
+    if ((uint64_t)(B > 0 ? B : 0) * ((uint64_t)(Nnew > 0 ? Nnew : 0) / 2 + 1) > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
+    int st = ATTN_OK;
+    if (positions) st = rope_axes_arg(positions, n_axes, B, pair_axis, rope_dim, B, Nnew, a.axes);
+    return st == ATTN_OK ? append_rope(a, q_strides, k_strides, v_strides, page_size, stream, true) : st;
+}
+
+ATTN_API int paged_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale, float v_scale,
+                                 const int32_t *page_ids, int n, void *k_out, void *v_out, int page_size, int Hkv, int d,
+                                 int num_pages, attn_stream_t stream) {
+    if (!k_pages || !v_pages || !page_ids || !k_out || !v_out) return ATTN_ERR_INVALID_ARG;
+    if (n <= 0 || Hkv <= 0 || d <= 0 || page_size <= 0 || num_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!fp4_scale(k_scale) || !fp4_scale(v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (!prefill_head_dim(d) || page_size != 16) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(page_ids))
+        return ATTN_ERR_MISALIGNED;
+    int *status = nullptr;
+    const int st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_kv_unpack_fp4(k_pages, v_pages, k_scale, v_scale, page_ids, n, k_out, v_out, Hkv, d,
+                                                     num_pages, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+namespace {
+int rope_axes(attn::RopeArgs a, const int64_t *q_strides, const int64_t *k_strides, const int64_t *q_out_strides,
+              const int64_t *k_out_strides, const int32_t *positions, int n_axes, int positions_batch,
+              const uint8_t *pair_axis, attn_stream_t stream) {
+    if (!a.q || !a.q_out || !a.cos_sin || (a.k == nullptr) != (a.k_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (a.B <= 0 || a.H <= 0 || a.N <= 0 || a.d <= 0 || a.max_pos <= 0 || (a.k && a.Hkv <= 0)) return ATTN_ERR_INVALID_ARG;
+    if (a.interleaved != 0 && a.interleaved != 1) return ATTN_ERR_INVALID_ARG;
+    if (!prefill_head_dim(a.d)) return ATTN_ERR_UNSUPPORTED;
+    if (a.rope_dim <= 0 || a.rope_dim > a.d || a.rope_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    int st = rope_axes_arg(positions, n_axes, positions_batch, pair_axis, a.rope_dim, a.B, a.N, a.axes);
+    if (st != ATTN_OK) return st;
+    if ((uint64_t)a.B * (uint64_t)a.N > (1ull << 31) - 1) return ATTN_ERR_INVALID_ARG;
+    if ((uint64_t)a.H + (uint64_t)(a.k ? a.Hkv : 0) > (1u << 24)) return ATTN_ERR_INVALID_ARG;
+    st = input_strides(q_strides, a.B, a.H, a.N, a.d, a.q_strides);
+    if (st == ATTN_OK) st = input_strides(q_out_strides, a.B, a.H, a.N, a.d, a.q_out_strides);
+    if (st == ATTN_OK && a.k) st = input_strides(k_strides, a.B, a.Hkv, a.N, a.d, a.k_strides);
+    if (st == ATTN_OK && a.k) st = input_strides(k_out_strides, a.B, a.Hkv, a.N, a.d, a.k_out_strides);
+    if (st != ATTN_OK) return st;
+    for (int i = 0; i < 3; ++i)  // in place: each row onto itself
+        if ((a.q == a.q_out && a.q_strides[i] != a.q_out_strides[i]) ||
+            (a.k && a.k == a.k_out && a.k_strides[i] != a.k_out_strides[i]))
+            return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(a.q) || !aligned16(a.q_out) || !aligned16(a.k) || !aligned16(a.k_out) || !aligned16(a.cos_sin))
+        return ATTN_ERR_MISALIGNED;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_rope_axes(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+}  // namespace
+
+ATTN_API int attn_rope_axes(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                            const float *cos_sin, int rope_dim, int max_pos, int interleaved, const int32_t *positions,
+                            int n_axes, int positions_batch, const uint8_t *pair_axis, void *q_out,
+                            const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, int B, int H, int Hkv,
+                            int N, int d, attn_stream_t stream) {
+    const attn::RopeArgs a{q, k, q_out, k_out, {}, {}, {}, {}, cos_sin, rope_dim, max_pos, interleaved, 0, B, H, Hkv, N, d, {}};
+    return rope_axes(a, q_strides, k_strides, q_out_strides, k_out_strides, positions, n_axes, positions_batch, pair_axis, stream);
+}
+
+ATTN_API int attn_rope_axes_bwd(const void *dq, const int64_t *dq_strides, const void *dk, const int64_t *dk_strides,
+                                const float *cos_sin, int rope_dim, int max_pos, int interleaved, const int32_t *positions,
+                                int n_axes, int positions_batch, const uint8_t *pair_axis, void *q_out,
+                                const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, int B, int H,
+                                int Hkv, int N, int d, attn_stream_t stream) {
+    const attn::RopeArgs a{dq, dk, q_out, k_out, {}, {}, {}, {}, cos_sin, rope_dim, max_pos, interleaved, 1, B, H, Hkv, N, d, {}};
+    return rope_axes(a, dq_strides, dk_strides, q_out_strides, k_out_strides, positions, n_axes, positions_batch, pair_axis, stream);
+}
+
+// ---------------------------------------------------------------- page tables and reference counts
+namespace {
+int pages_sizes(int B, int max_pages, int num_pages, int page_size) {
+    if (B <= 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+    if (page_size != 16) return ATTN_ERR_UNSUPPORTED;
+    if ((uint64_t)max_pages * 16 > (1ull << 30)) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+}  // namespace
+
+ATTN_API int paged_kv_fork(const int32_t *page_table, const int32_t *ctx_lens, const int32_t *parents,
+                           const int32_t *ref_counts, int32_t *page_table_out, int32_t *ctx_lens_out,
+                           int32_t *ref_counts_out, int page_size, int B, int B_out, int max_pages_per_seq, int num_pages,
+                           attn_stream_t stream) {
+    if (!page_table || !ctx_lens || !parents || !ref_counts || !page_table_out || !ctx_lens_out || !ref_counts_out)
+        return ATTN_ERR_INVALID_ARG;
+    int st = pages_sizes(B, max_pages_per_seq, num_pages, page_size);
+    if (st != ATTN_OK) return st;
+    if (B_out <= 0 || page_table_out == page_table || ctx_lens_out == ctx_lens || ctx_lens_out == parents)
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned4(page_table) || !aligned4(ctx_lens) || !aligned4(parents) || !aligned4(ref_counts) ||
+        !aligned4(page_table_out) || !aligned4(ctx_lens_out) || !aligned4(ref_counts_out))
+        return ATTN_ERR_MISALIGNED;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    attn::PagesArgs a{};
+    a.page_table = page_table;
+    a.ctx_lens = ctx_lens;
+    a.parents = parents;
+    a.ref_counts = ref_counts;
+    a.page_table_out = page_table_out;
+    a.ctx_lens_out = ctx_lens_out;
+    a.ref_counts_out = ref_counts_out;
+    a.B = B;
+    a.B_out = B_out;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    const cudaError_t e = attn::launch_pages_fork(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+ATTN_API size_t paged_kv_reserve_workspace_size(int B, int num_pages) {
+    return attn::pages_reserve_workspace_bytes(B, num_pages);
+}
+
+ATTN_API int paged_kv_reserve(const int32_t *page_table, const int32_t *ctx_lens, const int32_t *new_lens,
+                              const int32_t *ref_counts, int32_t *page_table_out, int32_t *ref_counts_out,
+                              int32_t *reserved, int32_t *src_pages, int32_t *dst_pages, int page_size, int B,
+                              int max_pages_per_seq, int num_pages, void *workspace, size_t workspace_bytes,
+                              attn_stream_t stream) {
+    if (!page_table || !ctx_lens || !new_lens || !ref_counts || !page_table_out || !ref_counts_out || !reserved ||
+        !src_pages || !dst_pages)
+        return ATTN_ERR_INVALID_ARG;
+    int st = pages_sizes(B, max_pages_per_seq, num_pages, page_size);
+    if (st != ATTN_OK) return st;
+    if (!aligned16(ref_counts) || !aligned16(ref_counts_out)) return ATTN_ERR_MISALIGNED;
+    if (!aligned4(page_table) || !aligned4(ctx_lens) || !aligned4(new_lens) || !aligned4(page_table_out) ||
+        !aligned4(reserved) || !aligned4(src_pages) || !aligned4(dst_pages))
+        return ATTN_ERR_MISALIGNED;
+    const size_t need = attn::pages_reserve_workspace_bytes(B, num_pages);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    attn::PagesArgs a{};
+    a.page_table = page_table;
+    a.ctx_lens = ctx_lens;
+    a.new_lens = new_lens;
+    a.ref_counts = ref_counts;
+    a.page_table_out = page_table_out;
+    a.ref_counts_out = ref_counts_out;
+    a.reserved = reserved;
+    a.src = src_pages;
+    a.dst = dst_pages;
+    a.B = a.B_out = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.workspace = workspace;
+    const cudaError_t e = attn::launch_pages_reserve(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+ATTN_API size_t paged_kv_compact_workspace_size(int num_pages) { return attn::pages_compact_workspace_bytes(num_pages); }
+
+ATTN_API int paged_kv_compact(const int32_t *page_table, const int32_t *ref_counts, int32_t *page_table_out,
+                              int32_t *ref_counts_out, int32_t *src_pages, int32_t *dst_pages, int32_t *count, int B,
+                              int max_pages_per_seq, int num_pages, void *workspace, size_t workspace_bytes,
+                              attn_stream_t stream) {
+    if (!page_table || !ref_counts || !page_table_out || !ref_counts_out || !src_pages || !dst_pages || !count)
+        return ATTN_ERR_INVALID_ARG;
+    int st = pages_sizes(B, max_pages_per_seq, num_pages, 16);
+    if (st != ATTN_OK) return st;
+    if (ref_counts_out == ref_counts) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(ref_counts) || !aligned16(ref_counts_out)) return ATTN_ERR_MISALIGNED;
+    if (!aligned4(page_table) || !aligned4(page_table_out) || !aligned4(src_pages) || !aligned4(dst_pages) || !aligned4(count))
+        return ATTN_ERR_MISALIGNED;
+    const size_t need = attn::pages_compact_workspace_bytes(num_pages);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    int *status = nullptr;
+    st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    attn::PagesArgs a{};
+    a.page_table = page_table;
+    a.ref_counts = ref_counts;
+    a.page_table_out = page_table_out;
+    a.ref_counts_out = ref_counts_out;
+    a.src = src_pages;
+    a.dst = dst_pages;
+    a.count = count;
+    a.B = a.B_out = B;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.workspace = workspace;
+    const cudaError_t e = attn::launch_pages_compact(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+ATTN_API int paged_kv_copy_pages(void *const *pools, int n_pools, size_t page_bytes, const int32_t *src_pages,
+                                 const int32_t *dst_pages, const int32_t *count, int n, int num_pages,
+                                 attn_stream_t stream) {
+    if (!pools || !src_pages || !dst_pages || n_pools <= 0 || n <= 0 || num_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (page_bytes == 0 || page_bytes > (1ull << 31) || page_bytes % 16 != 0) return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i]) return ATTN_ERR_INVALID_ARG;
+        if (!aligned16(pools[i])) return ATTN_ERR_MISALIGNED;
+    }
+    if (!aligned4(src_pages) || !aligned4(dst_pages) || !aligned4(count)) return ATTN_ERR_MISALIGNED;
+    int *status = nullptr;
+    const int st = device_setup(&status);
+    if (st != ATTN_OK) return st;
+    const cudaError_t e = attn::launch_pages_copy(pools, n_pools, page_bytes, src_pages, dst_pages, count, n, num_pages,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 ATTN_API int paged_attn_decode_gqa(const void *q, const void *k_pages, const void *v_pages,
                                    const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o,
                                    float *lse, int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages,
@@ -660,8 +936,8 @@ ATTN_API size_t paged_attn_decode_shared_workspace_size(int B, int H, int Hkv, i
 }
 
 namespace {
-// Decode with modified scores (k_scale, v_scale 1 for a bf16 cache).
-int decode_scoremod(attn::DecodeMoreArgs a, size_t workspace_bytes, attn_stream_t stream) {
+// Decode with modified scores (k_scale, v_scale 1 for a bf16 cache); fp4: over the 4-bit cache.
+int decode_scoremod(attn::DecodeMoreArgs a, size_t workspace_bytes, attn_stream_t stream, bool fp4 = false) {
     int st = decode_arg_checks(a.q, a.k_pages, a.v_pages, a.page_table, a.ctx_lens, a.page_size, a.o, a.lse, a.B, a.H,
                                a.Hkv, a.d, a.max_pages, a.num_pages, a.scale);
     if (st != ATTN_OK) return st;
@@ -669,11 +945,12 @@ int decode_scoremod(attn::DecodeMoreArgs a, size_t workspace_bytes, attn_stream_
     if (!finite_positive(a.k_scale) || !finite_positive(a.v_scale)) return ATTN_ERR_INVALID_ARG;
     st = scoremod_checks(a.scale * a.k_scale, a.softcap, a.slopes, a.key_begin, nullptr);
     if (st != ATTN_OK) return st;
-    const size_t need = attn::decode_scoremod_workspace_bytes(a.B, a.H, a.Hkv, a.d, a.max_pages, a.page_size);
+    const size_t need = (fp4 ? attn::decode_fp4_workspace_bytes : attn::decode_scoremod_workspace_bytes)(
+        a.B, a.H, a.Hkv, a.d, a.max_pages, a.page_size);
     if (!a.workspace || !aligned16(a.workspace) || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
     st = device_setup(&a.status);
     if (st != ATTN_OK) return st;
-    const cudaError_t e = attn::launch_decode_scoremod(a, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = (fp4 ? attn::launch_decode_fp4 : attn::launch_decode_scoremod)(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -721,6 +998,24 @@ ATTN_API int paged_attn_decode_scoremod_fp8(const void *q, const void *k_pages, 
     a.slopes = alibi_slopes;
     a.key_begin = key_begin;
     return decode_scoremod(a, workspace_bytes, stream);
+}
+
+ATTN_API size_t paged_attn_decode_fp4_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq, int page_size) {
+    return attn::decode_fp4_workspace_bytes(B, H, Hkv, d, max_pages_per_seq, page_size);
+}
+
+ATTN_API int paged_attn_decode_fp4(const void *q, const void *k_pages, const void *v_pages, float k_scale, float v_scale,
+                                   const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o, float *lse,
+                                   int B, int H, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale,
+                                   float softcap, const float *alibi_slopes, const int32_t *key_begin, void *workspace,
+                                   size_t workspace_bytes, attn_stream_t stream) {
+    attn::DecodeMoreArgs a{{q, k_pages, v_pages, page_table, ctx_lens, o, lse, workspace, nullptr, B, H, d, page_size,
+                       max_pages_per_seq, num_pages, scale, Hkv, 0, k_scale, v_scale}};
+    a.softcap = softcap;
+    a.slopes = alibi_slopes;
+    a.key_begin = key_begin;
+    if (!fp4_scale(k_scale) || !fp4_scale(v_scale)) return ATTN_ERR_INVALID_ARG;
+    return decode_scoremod(a, workspace_bytes, stream, true);
 }
 
 ATTN_API int paged_attn_decode_shared(const void *q, const void *k_pages, const void *v_pages,
@@ -821,7 +1116,7 @@ ATTN_API const char *attn_status_string(int status) {
     switch (status) {
         case ATTN_OK: return "ok";
         case ATTN_ERR_INVALID_ARG: return "invalid argument (null pointer, non-positive or oversized dimension, bad scale or cap)";
-        case ATTN_ERR_UNSUPPORTED: return "unsupported (head dim 32, 64, 80, 96 or 128; page size 16; rotation of a multiple of 16 dims, at most the head dim; device sm_103)";
+        case ATTN_ERR_UNSUPPORTED: return "unsupported (head dim 32, 64, 80, 96 or 128; page size 16; rotation of a multiple of 16 dims, at most the head dim, by at most 4 axes; device sm_103)";
         case ATTN_ERR_MISALIGNED: return "misaligned pointer (tensors need 16-byte alignment)";
         case ATTN_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than the call's *_workspace_size() (paged_attn_decode_workspace_size(), attn_bwd_workspace_size() and so on)";
         case ATTN_ERR_CUDA: return "CUDA runtime error or launch failure";

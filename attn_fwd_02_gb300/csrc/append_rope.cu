@@ -19,8 +19,9 @@
 // block, 23 with 256 before); 128 tokens into an e4m3 cache 2.3 us (3.0).
 #include <cuda_fp8.h>
 
-#include "launch.h"
-#include "sm103_ptx.cuh"
+#include <type_traits>
+
+#include "rope.cuh"
 
 namespace attn {
 namespace {
@@ -39,19 +40,10 @@ struct RopeParams {
     float k_inv, v_inv;         // 1 / scale of an e4m3 cache
     int rope, max_pos, H, Hkv, N, d, max_pages, num_pages;
 };
+struct RopeAxesParams : RopeParams {
+    RopeAxes axes;
+};
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
 // e4m3 nearest-even of f * inv, saturating at +-448, as the unrotated append converts.
 __device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
     uint32_t out[2] = {0u, 0u};
@@ -63,8 +55,10 @@ __device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
     return make_uint2(out[0], out[1]);
 }
 
-template <bool INTER, bool FP8>
-__global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const RopeParams p) {
+// AXES: the rows of the angles come from positions with several axes, not from the token's place in the cache.
+template <bool INTER, bool FP8, bool AXES>
+__global__ void __launch_bounds__(kThreads)
+    kv_append_rope_kernel(const std::conditional_t<AXES, RopeAxesParams, RopeParams> p) {
     const int b = (int)(blockIdx.x / (unsigned)p.N), t = (int)(blockIdx.x % (unsigned)p.N);
     if (p.new_lens && t >= p.new_lens[b]) return;  // padding
     // Thread = (item of a row, first row): an item is two vectors -- the two halves of eight pairs, or two
@@ -99,12 +93,25 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const RopePara
         vy = v[r0 * p.vs[1] + 2 * i + 1];
     }
     const long long pos = (long long)max(p.start_pos[b], 0) + t;
-    if (pos >= p.max_pos) return;  // past the rotation table: padding too
+    [[maybe_unused]] AxisRows rows;
+    if constexpr (AXES) {
+        rows = axis_rows(p.axes, b, t, p.max_pos);
+        if (!rows.ok) return;  // an axis past the rotation table: padding too (uniform over the block)
+    } else {
+        if (pos >= p.max_pos) return;  // past the rotation table: padding too
+    }
     const long long lp = pos / kPS;
     const int page = lp < p.max_pages ? p.page_table[(size_t)b * p.max_pages + lp] : -1;
     float c[8], s[8];
+    const float *angles = p.cos_sin + (AXES ? 0 : (size_t)pos * p.rope);
+    if constexpr (AXES) {
+        __shared__ __align__(16) float gathered[kMaxRope];
+        gather_angles(gathered, p.cos_sin, p.axes, rows, p.rope, threadIdx.x, per_pass * ipr);
+        __syncthreads();  // of the threads that are left
+        angles = gathered;
+    }
     if (turns) {
-        const float *cs = p.cos_sin + (size_t)pos * p.rope + 8 * i;
+        const float *cs = angles + 8 * i;
         const float4 *c4 = reinterpret_cast<const float4 *>(cs), *s4 = reinterpret_cast<const float4 *>(cs + p.rope / 2);
         const float4 ca = c4[0], cb = c4[1], sa = s4[0], sb = s4[1];
         c[0] = ca.x, c[1] = ca.y, c[2] = ca.z, c[3] = ca.w, c[4] = cb.x, c[5] = cb.y, c[6] = cb.z, c[7] = cb.w;
@@ -202,12 +209,23 @@ cudaError_t launch_kv_append_rope(const RopeAppendArgs &a, cudaStream_t stream) 
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     const unsigned grid = (unsigned)((long long)a.B * a.Nnew);
-    if (a.kv_fp8) {
-        if (a.interleaved) kv_append_rope_kernel<true, true><<<grid, kThreads, 0, stream>>>(p);
-        else kv_append_rope_kernel<false, true><<<grid, kThreads, 0, stream>>>(p);
+    if (a.axes.positions) {
+        RopeAxesParams x;
+        static_cast<RopeParams &>(x) = p;
+        x.axes = a.axes;
+        if (a.kv_fp8) {
+            if (a.interleaved) kv_append_rope_kernel<true, true, true><<<grid, kThreads, 0, stream>>>(x);
+            else kv_append_rope_kernel<false, true, true><<<grid, kThreads, 0, stream>>>(x);
+        } else {
+            if (a.interleaved) kv_append_rope_kernel<true, false, true><<<grid, kThreads, 0, stream>>>(x);
+            else kv_append_rope_kernel<false, false, true><<<grid, kThreads, 0, stream>>>(x);
+        }
+    } else if (a.kv_fp8) {
+        if (a.interleaved) kv_append_rope_kernel<true, true, false><<<grid, kThreads, 0, stream>>>(p);
+        else kv_append_rope_kernel<false, true, false><<<grid, kThreads, 0, stream>>>(p);
     } else {
-        if (a.interleaved) kv_append_rope_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
-        else kv_append_rope_kernel<false, false><<<grid, kThreads, 0, stream>>>(p);
+        if (a.interleaved) kv_append_rope_kernel<true, false, false><<<grid, kThreads, 0, stream>>>(p);
+        else kv_append_rope_kernel<false, false, false><<<grid, kThreads, 0, stream>>>(p);
     }
     return cudaGetLastError();
 }

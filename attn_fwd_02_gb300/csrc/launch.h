@@ -139,6 +139,15 @@ cudaError_t launch_kv_append_fp8(const void *k_new, const void *v_new, void *k_p
                                  const int32_t *start_pos, int B, int Hkv, int Nnew, int d, int max_pages,
                                  int num_pages, cudaStream_t stream);
 
+// Positions with several axes: pair i of a token turns by row positions[axis(i)][b][t] of the table.
+constexpr int kMaxAxes = 4, kMaxRope = 128;
+struct RopeAxes {
+    const int32_t *positions = nullptr;  // null: none
+    long long axis_stride = 0, batch_stride = 0;
+    int axes = 0;
+    uint64_t pair_axis[2] = {0, 0};  // two bits a pair
+};
+
 // As the append, with the queries and keys rotated to their positions on the way.
 struct RopeAppendArgs {
     const void *q, *k_new, *v_new;                   // q may be null (keys and values only)
@@ -150,8 +159,41 @@ struct RopeAppendArgs {
     int B, H, Hkv, Nnew, d, max_pages, num_pages;
     int kv_fp8 = 0;
     float k_scale = 1.f, v_scale = 1.f;
+    RopeAxes axes;
 };
 cudaError_t launch_kv_append_rope(const RopeAppendArgs &a, cudaStream_t stream);
+// Into the 4-bit cache (cos_sin may be null: no rotation, and no queries), and its pages as bf16.
+cudaError_t launch_kv_append_fp4(const RopeAppendArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale, float v_scale,
+                                 const int32_t *page_ids, int n, void *k_out, void *v_out, int Hkv, int d, int num_pages,
+                                 cudaStream_t stream);
+
+// The rotation alone, of queries and keys (k may be null) in strided views; back: by the transposed rotation.
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];  // batch, head, token, in elements
+    const float *cos_sin;
+    int rope_dim, max_pos, interleaved, back;
+    int B, H, Hkv, N, d;
+    RopeAxes axes;
+};
+cudaError_t launch_rope_axes(const RopeArgs &a, cudaStream_t stream);
+
+// Page tables and reference counts (see the header): forking, reserving, compacting, and copies of pages.
+struct PagesArgs {
+    const int32_t *page_table, *ctx_lens, *parents, *new_lens, *ref_counts;
+    int32_t *page_table_out, *ctx_lens_out, *ref_counts_out, *reserved, *src, *dst, *count;
+    int B, B_out, max_pages, num_pages;
+    void *workspace;
+};
+cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream);
+size_t pages_reserve_workspace_bytes(int B, int num_pages);
+cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream);
+size_t pages_compact_workspace_bytes(int num_pages);
+cudaError_t launch_pages_copy(void *const *pools, int n_pools, size_t page_bytes, const int32_t *src, const int32_t *dst,
+                              const int32_t *count, int n, int num_pages, cudaStream_t stream);
 
 // Launches the split kernel and the combine kernel.
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
@@ -163,6 +205,8 @@ size_t decode_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int p
 // Decode with modified scores, and decode of a batch whose groups share their first pages.
 cudaError_t launch_decode_scoremod(const DecodeMoreArgs &a, cudaStream_t stream);
 size_t decode_scoremod_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
+cudaError_t launch_decode_fp4(const DecodeMoreArgs &a, cudaStream_t stream);
+size_t decode_fp4_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int page_size);
 cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream);
 size_t decode_shared_workspace_bytes(int B, int H, int Hkv, int d, int max_pages, int S, int page_size);
 

@@ -1,0 +1,452 @@
+// pages.cu -- page tables and reference counts of a paged cache: sequences that continue others, pages for new tokens,
+// pages moved to the front of the pool; and the copies of pages that these ask for.
+//
+// A page's reference count is the number of table entries that name it (plus what the caller adds); a page is free iff its
+// count is not positive.  Which free page goes where is fixed by the order of the rows and of the page numbers (prefix sums,
+// no counters that race), so equal inputs give equal tables.  The counts' sums use integer atomics, whose order does not
+// show in the result.
+//
+// The scans over the counts and over the rows are one cluster's work: each CTA takes an even part of the pool, the parts'
+// totals are exchanged at a cluster barrier.
+#include "launch.h"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kPS = 16;
+constexpr int kScanThreads = 1024;
+constexpr int kScanCtas = 8;       // of the scanning cluster
+constexpr int kScanTile = kScanThreads * 4;
+
+__device__ __forceinline__ bool in_pool(int page, int num_pages) { return (unsigned)page < (unsigned)num_pages; }
+
+// ---------------------------------------------------------------- fork
+struct ForkParams {
+    const int32_t *table, *ctx, *parents, *ref;
+    int32_t *table_out, *ctx_out, *ref_out;
+    int B, B_out, W, P;
+};
+__device__ __forceinline__ int fork_entry(const ForkParams &p, int b, int c) {
+    const int par = p.parents[b];
+    if (par < 0 || par >= p.B) return -1;
+    if (par != b) {
+        const int n = min(max(p.ctx[par], 0), p.W * kPS);
+        if (c >= (n + kPS - 1) / kPS) return -1;
+    }
+    return p.table[(size_t)par * p.W + c];
+}
+__global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
+    const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    for (long long i = i0; i < (long long)p.B_out * p.W; i += step) p.table_out[i] = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
+    for (long long i = i0; i < p.P; i += step) p.ref_out[i] = p.ref[i];
+    for (long long i = i0; i < p.B_out; i += step) {
+        const int par = p.parents[i];
+        p.ctx_out[i] = par < 0 || par >= p.B ? 0 : p.ctx[par];
+    }
+}
+// Counts: what a place of the table names now, less what it named.
+__global__ void __launch_bounds__(256) pages_fork_count_kernel(const ForkParams p) {
+    griddep_wait();
+    const long long rows = max(p.B, p.B_out);
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < rows * p.W; i += (long long)gridDim.x * 256) {
+        const int was = i < (long long)p.B * p.W ? p.table[i] : -1;
+        const int is = i < (long long)p.B_out * p.W ? p.table_out[i] : -1;
+        if (was == is) continue;
+        if (in_pool(was, p.P)) atomicSub(p.ref_out + was, 1);
+        if (in_pool(is, p.P)) atomicAdd(p.ref_out + is, 1);
+    }
+}
+
+// ---------------------------------------------------------------- scans
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Sum over the block's threads before this one, and over all of them (in `total`).
+__device__ __forceinline__ int block_scan(int v, int (&warp_sums)[33], int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    __syncthreads();  // the sums of a scan before this one have been read
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    return (warp ? warp_sums[warp - 1] : 0) + x - v;
+}
+// The four counts from page i on (past the end: `beyond`).
+__device__ __forceinline__ int4 counts4(const int32_t *ref, int i, int end, int beyond) {
+    if (i + 4 <= end) return *reinterpret_cast<const int4 *>(ref + i);
+    int4 v = make_int4(beyond, beyond, beyond, beyond);
+    if (i < end) v.x = ref[i];
+    if (i + 1 < end) v.y = ref[i + 1];
+    if (i + 2 < end) v.z = ref[i + 2];
+    return v;
+}
+// The CTA's part [begin, end) of n pages, of which only the last may not be whole vectors.
+__device__ __forceinline__ void scan_part(int n, int cta, int ctas, int &begin, int &end) {
+    const long long per = ((long long)(n + ctas - 1) / ctas + 3) & ~3LL;
+    begin = (int)min(per * cta, (long long)n);
+    end = (int)min(per * (cta + 1), (long long)n);
+}
+
+// ---------------------------------------------------------------- reserve
+struct ReserveParams {
+    const int32_t *table, *ctx, *new_lens, *ref;
+    int32_t *table_out, *ref_out, *reserved, *src, *dst;
+    int32_t *frozen;  // the counts at the call's start (the caller's, or a copy when they change in place)
+    int32_t *need;    // [B]
+    int32_t *ids;     // [P]: free pages in order
+    int32_t *parts;   // [kScanCtas]: free pages of each part
+    int B, W, P, ctas, copy_table, copy_ref, copy_frozen;
+};
+__global__ void __launch_bounds__(256) pages_reserve_copy_kernel(const ReserveParams p) {
+    const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    if (p.copy_table)
+        for (long long i = i0; i < (long long)p.B * p.W; i += step) p.table_out[i] = p.table[i];
+    for (long long i = i0; i < p.P; i += step) {
+        if (p.copy_ref) p.ref_out[i] = p.ref[i];
+        if (p.copy_frozen) p.frozen[i] = p.ref[i];
+    }
+}
+// Entries [from, to) of row b that cover its new tokens (to 0: none wanted, or more than the table holds).
+__device__ __forceinline__ void reserve_range(const ReserveParams &p, int b, int &n, int &from, int &to) {
+    const int add = p.new_lens[b];
+    n = min(max(p.ctx[b], 0), p.W * kPS);
+    const long long end = ((long long)n + add + kPS - 1) / kPS;
+    from = n / kPS;
+    to = add > 0 && end <= p.W ? (int)end : 0;
+}
+__global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const ReserveParams p) {
+    __shared__ int sums[33];
+    const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first_warp = cta * 32 + warp, all_warps = p.ctas * 32;
+    griddep_wait();
+    // an entry to be given a page: it has none, or shares it
+    auto lacks = [&](int e) { return !in_pool(e, p.P) || p.frozen[e] > 1; };
+    for (int b = first_warp; b < p.B; b += all_warps) {
+        int n, from, to, need = 0;
+        reserve_range(p, b, n, from, to);
+        for (int c0 = from; c0 < to; c0 += 32) {
+            const bool lack = c0 + lane < to && lacks(p.table[(size_t)b * p.W + c0 + lane]);
+            need += __popc(__ballot_sync(0xffffffffu, lack));
+        }
+        if (lane == 0) p.need[b] = need;
+    }
+    int begin, end, mine = 0;
+    scan_part(p.P, cta, p.ctas, begin, end);
+    for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
+        const int4 v = counts4(p.frozen, i, end, 1);
+        mine += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
+    }
+    int total;
+    block_scan(mine, sums, total);
+    if (threadIdx.x == 0) p.parts[cta] = total;
+    cluster_sync();
+    int before = 0, free_pages = 0;
+    for (int i = 0; i < p.ctas; ++i) {
+        const int v = __ldcg(p.parts + i);
+        before += i < cta ? v : 0;
+        free_pages += v;
+    }
+    // the rows' offsets into the free pages: every CTA sums them all, and keeps those of its own rows in `need`'s place
+    // after the barrier; the pages that are wanted at all end at `wanted`
+    long long wanted = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        int sum;
+        block_scan(b < p.B ? __ldcg(p.need + b) : 0, sums, sum);
+        wanted += sum;
+    }
+    const int last = (int)min(wanted, (long long)free_pages);
+    for (int i0 = begin; i0 < end && before < last; i0 += kScanTile) {
+        const int i = i0 + 4 * (int)threadIdx.x;
+        const int4 v = counts4(p.frozen, i, end, 1);
+        const bool f[4] = {v.x <= 0, v.y <= 0, v.z <= 0, v.w <= 0};
+        int at = before + block_scan(f[0] + f[1] + f[2] + f[3], sums, total);
+        before += total;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (f[j]) p.ids[at++] = i + j;
+    }
+    cluster_sync();
+    // rows, a tile of kScanThreads at a time: their offsets in shared memory, then a warp for each
+    __shared__ int offsets[kScanThreads];
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+        const int bt = b0 + (int)threadIdx.x;
+        int sum;
+        const int need_t = bt < p.B ? __ldcg(p.need + bt) : 0;
+        const int at_t = block_scan(need_t, sums, sum);
+        const long long off = base + at_t;
+        offsets[threadIdx.x] = need_t == 0 ? 0 : (off + need_t <= free_pages ? (int)off : -1);
+        base += sum;
+        __syncthreads();
+        for (int b = b0 + ((first_warp - b0 % all_warps) % all_warps + all_warps) % all_warps; b < min(b0 + kScanThreads, p.B);
+             b += all_warps) {
+            int n, from, to;
+            reserve_range(p, b, n, from, to);
+            const int off_b = offsets[b - b0];
+            const bool served = to > 0 && off_b >= 0;
+            int src = -1, dst = -1, taken = 0;
+            for (int c0 = from; served && c0 < to; c0 += 32) {
+                const int c = c0 + lane;
+                const int old = c < to ? p.table[(size_t)b * p.W + c] : -1;
+                const bool lack = c < to && lacks(old);
+                const unsigned mask = __ballot_sync(0xffffffffu, lack);
+                if (lack) {
+                    const int page = __ldcg(p.ids + off_b + taken + __popc(mask & ((1u << lane) - 1)));
+                    p.table_out[(size_t)b * p.W + c] = page;
+                    p.ref_out[page] = 1;
+                    if (in_pool(old, p.P)) {
+                        atomicSub(p.ref_out + old, 1);
+                        if (c == from && n % kPS != 0) src = old, dst = page;  // (lane 0: its tokens move along)
+                    }
+                }
+                taken += __popc(mask);
+            }
+            if (lane == 0) {
+                p.reserved[b] = served ? p.new_lens[b] : 0;
+                p.src[b] = src;
+                p.dst[b] = dst;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- compact
+struct CompactParams {
+    const int32_t *table, *ref;
+    int32_t *table_out, *ref_out, *src, *dst, *count;
+    int32_t *to;     // [P]: where a page goes (-1: it is not live)
+    int32_t *parts;  // [2 kScanCtas]
+    int B, W, P, ctas;
+};
+__global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const CompactParams p) {
+    __shared__ int sums[33];
+    const int cta = blockIdx.x;
+    int begin, end, mine = 0, total;
+    scan_part(p.P, cta, p.ctas, begin, end);
+    for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
+        const int4 v = counts4(p.ref, i, end, 0);
+        mine += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+    }
+    block_scan(mine, sums, total);
+    if (threadIdx.x == 0) p.parts[cta] = total;
+    cluster_sync();
+    int before = 0, live = 0;  // live pages of the parts before, and of all
+    for (int i = 0; i < p.ctas; ++i) {
+        const int v = __ldcg(p.parts + i);
+        before += i < cta ? v : 0;
+        live += v;
+    }
+    // live pages below `live`, which stay: of this part, then of all
+    mine = 0;
+    for (int i = begin + 4 * (int)threadIdx.x; i < min(end, live); i += kScanTile) {
+        const int4 v = counts4(p.ref, i, end, 0);
+        mine += (v.x > 0) + (v.y > 0 && i + 1 < live) + (v.z > 0 && i + 2 < live) + (v.w > 0 && i + 3 < live);
+    }
+    block_scan(mine, sums, total);
+    if (threadIdx.x == 0) p.parts[kScanCtas + cta] = total;
+    cluster_sync();
+    int stay = 0;
+    for (int i = 0; i < p.ctas; ++i) stay += __ldcg(p.parts + kScanCtas + i);
+    const int moves = live - stay;
+    if (cta == 0 && threadIdx.x == 0) *p.count = moves;
+    for (int i0 = begin; i0 < end; i0 += kScanTile) {
+        const int i = i0 + 4 * (int)threadIdx.x;
+        const int4 v = counts4(p.ref, i, end, 0);
+        const int c[4] = {v.x, v.y, v.z, v.w};
+        int at = before + block_scan((c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0), sums, total);  // live before i + j
+        before += total;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int page = i + j;
+            if (page >= end) break;
+            if (page < live) {
+                p.to[page] = c[j] > 0 ? page : -1;
+                if (c[j] > 0) p.ref_out[page] = c[j];
+                else p.dst[page - at] = page;  // the holes, in order
+            } else {
+                p.ref_out[page] = 0;
+                if (c[j] > 0) p.src[at - stay] = page;  // the pages that fill them, in order
+                else p.to[page] = -1;
+            }
+            at += c[j] > 0;
+            if (page >= moves) p.src[page] = p.dst[page] = -1;  // (places past the moves; below them, written above)
+        }
+    }
+    cluster_sync();
+    for (int i = cta * kScanThreads + (int)threadIdx.x; i < moves; i += p.ctas * kScanThreads) {
+        const int s = __ldcg(p.src + i), d = __ldcg(p.dst + i);
+        p.to[s] = d;
+        p.ref_out[d] = p.ref[s];
+    }
+}
+__global__ void __launch_bounds__(256) pages_compact_table_kernel(const CompactParams p) {
+    griddep_wait();
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)p.B * p.W; i += (long long)gridDim.x * 256) {
+        const int e = p.table[i];
+        p.table_out[i] = in_pool(e, p.P) ? p.to[e] : -1;
+    }
+}
+
+// ---------------------------------------------------------------- copies
+constexpr int kCopyPools = 256;  // pools of one launch
+constexpr int kCopyChunk = 16384;  // bytes a block moves at a time
+
+struct CopyParams {
+    const int32_t *src, *dst, *count;  // count may be null
+    size_t page_bytes;
+    int n, num_pages, n_pools, chunks;
+    uint8_t *pools[kCopyPools];
+};
+__global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ CopyParams p) {
+    const int n = p.count ? min(max(*p.count, 0), p.n) : p.n;
+    const long long per_pair = (long long)p.n_pools * p.chunks, units = n * per_pair;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int i = (int)(u / per_pair), r = (int)(u % per_pair);
+        const int src = p.src[i], dst = p.dst[i];
+        if (!in_pool(src, p.num_pages) || !in_pool(dst, p.num_pages)) continue;
+        const size_t from = (size_t)(r % p.chunks) * kCopyChunk;
+        const int vectors = (int)(min((size_t)kCopyChunk, p.page_bytes - from) / 16);
+        uint8_t *pool = p.pools[r / p.chunks];
+        const uint4 *s = reinterpret_cast<const uint4 *>(pool + src * p.page_bytes + from);
+        uint4 *d = reinterpret_cast<uint4 *>(pool + dst * p.page_bytes + from);
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((int)threadIdx.x + 256 * k < vectors) v[k] = s[threadIdx.x + 256 * k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((int)threadIdx.x + 256 * k < vectors) d[threadIdx.x + 256 * k] = v[k];
+    }
+}
+
+// Blocks of 256 threads for `work` items, at most `waves` on every SM.
+int blocks_for(long long work, int waves) {
+    int sms = 0;
+    if (current_sm_count(&sms) != cudaSuccess || sms <= 0) sms = 1;
+    const long long want = (work + 255) / 256, most = (long long)sms * waves;
+    return (int)(want < 1 ? 1 : (want < most ? want : most));
+}
+// CTAs of the scanning cluster: one for a pool that it passes over in a few steps.
+int scan_ctas(int num_pages) { return num_pages <= 2 * kScanTile ? 1 : kScanCtas; }
+
+template <class K, class A>
+cudaError_t launch_scan(K kernel, A &p, bool dependent, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+size_t ints(size_t n) { return (n * sizeof(int32_t) + 15) & ~size_t(15); }
+
+}  // namespace
+
+cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream) {
+    const ForkParams p{a.page_table, a.ctx_lens, a.parents, a.ref_counts, a.page_table_out, a.ctx_lens_out,
+                       a.ref_counts_out, a.B, a.B_out, a.max_pages, a.num_pages};
+    const long long out = (long long)a.B_out * a.max_pages, all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages;
+    pages_fork_kernel<<<blocks_for(out > a.num_pages ? out : a.num_pages, 8), 256, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(pages_fork_count_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
+}
+
+size_t pages_reserve_workspace_bytes(int B, int num_pages) {
+    return B <= 0 || num_pages <= 0 ? 0 : ints(B) + 2 * ints(num_pages) + ints(kScanCtas);
+}
+cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
+    ReserveParams p{};
+    p.table = a.page_table;
+    p.ctx = a.ctx_lens;
+    p.new_lens = a.new_lens;
+    p.ref = a.ref_counts;
+    p.table_out = a.page_table_out;
+    p.ref_out = a.ref_counts_out;
+    p.reserved = a.reserved;
+    p.src = a.src;
+    p.dst = a.dst;
+    char *ws = static_cast<char *>(a.workspace);
+    p.need = reinterpret_cast<int32_t *>(ws);
+    p.ids = reinterpret_cast<int32_t *>(ws += ints(a.B));
+    p.copy_table = a.page_table_out != a.page_table;
+    p.copy_ref = a.ref_counts_out != a.ref_counts;
+    p.copy_frozen = !p.copy_ref;
+    p.frozen = p.copy_frozen ? reinterpret_cast<int32_t *>(ws + ints(a.num_pages)) : const_cast<int32_t *>(a.ref_counts);
+    p.parts = reinterpret_cast<int32_t *>(ws + 2 * ints(a.num_pages));
+    p.B = a.B;
+    p.W = a.max_pages;
+    p.P = a.num_pages;
+    p.ctas = scan_ctas(a.num_pages);
+    const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0;
+    pages_reserve_copy_kernel<<<blocks_for(cells > a.num_pages ? cells : a.num_pages, 8), 256, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_scan(pages_reserve_kernel, p, true, stream);
+}
+
+size_t pages_compact_workspace_bytes(int num_pages) {
+    return num_pages <= 0 ? 0 : ints(num_pages) + ints(2 * kScanCtas);
+}
+cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream) {
+    CompactParams p{a.page_table, a.ref_counts, a.page_table_out, a.ref_counts_out, a.src, a.dst, a.count,
+                    static_cast<int32_t *>(a.workspace),
+                    reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + ints(a.num_pages)),
+                    a.B, a.max_pages, a.num_pages, scan_ctas(a.num_pages)};
+    const cudaError_t e = launch_scan(pages_compact_kernel, p, false, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(pages_compact_table_kernel, dim3(blocks_for((long long)a.B * a.max_pages, 8)), 256, 0, stream, p);
+}
+
+cudaError_t launch_pages_copy(void *const *pools, int n_pools, size_t page_bytes, const int32_t *src, const int32_t *dst,
+                              const int32_t *count, int n, int num_pages, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    for (int first = 0; first < n_pools; first += kCopyPools) {
+        CopyParams p;
+        p.src = src;
+        p.dst = dst;
+        p.count = count;
+        p.page_bytes = page_bytes;
+        p.n = n;
+        p.num_pages = num_pages;
+        p.n_pools = n_pools - first < kCopyPools ? n_pools - first : kCopyPools;
+        p.chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
+        for (int i = 0; i < kCopyPools; ++i) p.pools[i] = i < p.n_pools ? static_cast<uint8_t *>(pools[first + i]) : nullptr;
+        const long long units = (long long)n * p.n_pools * p.chunks, most = (long long)sms * 8;
+        pages_copy_kernel<<<(unsigned)(units < most ? units : most), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace attn

@@ -392,6 +392,145 @@ int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_pages, voi
                         int max_pages_per_seq, int num_pages, attn_stream_t stream);
 
 /*
+ * 4-bit KV cache.  A value is e2m1(code) * e4m3(block scale) * the tensor's scale: a 4-bit code (1 sign, 2 exponent bits
+ * of bias 1, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one e4m3 scale per block of 16 dims of a token.  k_pages,
+ * v_pages are [num_pages, Hkv, 9 d] bytes; the 9 d bytes of a page of a head are, with token t of 0 .. 15 and dim x,
+ *   keys    the code of (t, x) in byte t d / 2 + x / 2, low nibble for even x; the scale of (t, block j) in byte
+ *           8 d + t d / 16 + j
+ *   values  with q = (t mod 8) / 2 and h = t / 8, the code of (t, x) in byte 128 (x / 16) + 32 q + 16 h + x mod 16, low nibble
+ *           for even t; the scale of (t, block j) in byte 8 d + q d / 4 + 4 j + 2 h + t mod 2
+ * (all divisions whole).  k_scale, v_scale lie in [1e-37, 1e37].  d and page_size as everywhere.
+ *
+ * paged_kv_append_fp4: new tokens into such a cache, optionally rotated on the way.  cos_sin NULL: keys and values as they
+ *   are (q must be NULL).  Else as paged_kv_append_rope (positions NULL: token t turns by row start_pos[b] + t) or as
+ *   paged_kv_append_rope_axes (positions [n_axes, B, Nnew]).  With u = fp32(x * fp32(1 / scale)) of a block (x in fp32,
+ *   after the rotation): the block scale is e4m3(fp32(max |u| * fp32(1/6))), nearest-even and at most 448, a code is
+ *   e2m1(fp32(u / block scale)), nearest-even and at most 6, and 0 in a block whose scale is 0.  Inputs must be finite.
+ *   Tokens at positions 2m and 2m + 1 share bytes: no two sequences of a call may write to the same page.
+ * paged_kv_unpack_fp4: pages page_ids[i] (n of them, device) as bf16, k_out and v_out [n, Hkv, 16, d]: fp32(code * block
+ *   scale) * scale, rounded to bf16.  An id outside [0, num_pages) leaves out[i] as it was.  With a table of the places i
+ *   paged_attn_prefill attends over the result: the chunked prefill over a 4-bit cache.
+ * paged_attn_decode_fp4: paged_attn_decode_scoremod over such a cache (softcap 0, alibi_slopes and key_begin NULL: the plain
+ *   decode).  The codes are widened exactly to f16, both products run in f16 with fp32 accumulation (each query rounded to
+ *   f16 after a power of two of its own, the weights to f16).  Slots that a query does not see may hold anything.
+ *   workspace: at least paged_attn_decode_fp4_workspace_size(...) bytes.
+ */
+size_t paged_attn_decode_fp4_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq, int page_size);
+
+int paged_attn_decode_fp4(const void *q, const void *k_pages, const void *v_pages, float k_scale, float v_scale,
+                          const int32_t *page_table, const int32_t *ctx_lens, int page_size, void *o, float *lse, int B,
+                          int H, int Hkv, int d, int max_pages_per_seq, int num_pages, float scale, float softcap,
+                          const float *alibi_slopes, const int32_t *key_begin, void *workspace, size_t workspace_bytes,
+                          attn_stream_t stream);
+
+int paged_kv_append_fp4(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                        const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                        float k_scale, float v_scale, const float *cos_sin, int rope_dim, int max_pos, int interleaved,
+                        const int32_t *positions, int n_axes, const uint8_t *pair_axis, const int32_t *page_table,
+                        const int32_t *start_pos, const int32_t *new_lens, int page_size, int B, int H, int Hkv, int Nnew,
+                        int d, int max_pages_per_seq, int num_pages, attn_stream_t stream);
+
+int paged_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale, float v_scale, const int32_t *page_ids,
+                        int n, void *k_out, void *v_out, int page_size, int Hkv, int d, int num_pages,
+                        attn_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of an image's or a video's tokens; equal ones for text).
+ *   positions  [n_axes, B, N] int32 (device), n_axes 1 to 4
+ *   pair_axis  HOST array of rope_dim / 2 entries < n_axes: pair i of a token turns by column i of row
+ *              positions[pair_axis[i]][b][t] of cos_sin, so sections of the pairs, axes taken in turn, and frequencies that
+ *              start again for each axis are all a matter of this array and the table's columns
+ * and the pairs, cos_sin, rope_dim and interleaved as in paged_kv_append_rope.
+ *
+ * paged_kv_append_rope_axes(_fp8): paged_kv_append_rope with such positions; start_pos says only where in the cache the
+ *   tokens go.  Of a token with a position outside [0, max_pos) nothing is written.
+ * attn_rope_axes: the rotation alone.  q [B, H, N, d], k [B, Hkv, N, d] (k and k_out may both be NULL; Hkv is then ignored)
+ *   and their outputs are bf16 views with contiguous rows, *_strides as in paged_kv_append_rope; an output may be its input
+ *   (the same strides), and must else not overlap an input.  positions_batch: B, or 1 for positions [n_axes, 1, N] that all
+ *   sequences share.  A token with a position outside [0, max_pos) gives zeros.
+ * attn_rope_axes_bwd: its gradient: dq, dk are those of the outputs, q_out and k_out get those of q and k (the transposed
+ *   rotation; zeros for tokens outside the table).
+ */
+int paged_kv_append_rope_axes(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                              const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                              const float *cos_sin, int rope_dim, int max_pos, int interleaved, const int32_t *positions,
+                              int n_axes, const uint8_t *pair_axis, const int32_t *page_table, const int32_t *start_pos,
+                              const int32_t *new_lens, int page_size, int B, int H, int Hkv, int Nnew, int d,
+                              int max_pages_per_seq, int num_pages, attn_stream_t stream);
+
+int paged_kv_append_rope_axes_fp8(const void *q, const int64_t *q_strides, const void *k_new, const int64_t *k_strides,
+                                  const void *v_new, const int64_t *v_strides, void *q_out, void *k_pages, void *v_pages,
+                                  float k_scale, float v_scale, const float *cos_sin, int rope_dim, int max_pos,
+                                  int interleaved, const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                                  const int32_t *page_table, const int32_t *start_pos, const int32_t *new_lens,
+                                  int page_size, int B, int H, int Hkv, int Nnew, int d, int max_pages_per_seq,
+                                  int num_pages, attn_stream_t stream);
+
+int attn_rope_axes(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, const float *cos_sin,
+                   int rope_dim, int max_pos, int interleaved, const int32_t *positions, int n_axes, int positions_batch,
+                   const uint8_t *pair_axis, void *q_out, const int64_t *q_out_strides, void *k_out,
+                   const int64_t *k_out_strides, int B, int H, int Hkv, int N, int d, attn_stream_t stream);
+
+int attn_rope_axes_bwd(const void *dq, const int64_t *dq_strides, const void *dk, const int64_t *dk_strides,
+                       const float *cos_sin, int rope_dim, int max_pos, int interleaved, const int32_t *positions,
+                       int n_axes, int positions_batch, const uint8_t *pair_axis, void *q_out, const int64_t *q_out_strides,
+                       void *k_out, const int64_t *k_out_strides, int B, int H, int Hkv, int N, int d,
+                       attn_stream_t stream);
+
+/*
+ * Page tables and reference counts of a cache, on the device throughout: no call reads them on the host, so all may be
+ * captured into a graph.
+ *   page_table [B, max_pages_per_seq], ctx_lens [B] int32 as everywhere; entries outside [0, num_pages) (-1) name no page
+ *   ref_counts [num_pages] int32: how many entries of the table name each page (a caller may add its own).  A page is free
+ *              iff its count is not positive.
+ * Which page goes where follows from the order of rows and page numbers alone.  Outputs must not overlap inputs but where it
+ * says that an output may be its input.
+ *
+ * paged_kv_fork: row b of the result continues row parents[b] of the table (b < B_out, parents [B_out] int32): the entries of
+ *   its ceil(ctx_lens / 16) pages, the others -1; parents[b] == b keeps the whole row as it is, parents[b] outside [0, B)
+ *   gives an empty one.  A row of the table that no row continues is thereby freed.  ref_counts_out (may be ref_counts): the
+ *   counts plus the new table's entries less the old one's.
+ * paged_kv_reserve: makes the entries that cover positions ctx_lens[b] .. ctx_lens[b] + new_lens[b] - 1 the row's own: an
+ *   entry that names no page gets a free one, and so does one whose page has a count over 1 at the call's start (it is
+ *   shared).  Free pages are given out in ascending order, to rows and entries in ascending order.  A row that needs more
+ *   pages than rows before it leave, or more entries than the table has, is left as it is; the former rows' needs count for
+ *   the rows after them, the latter's do not.
+ *     reserved [B]: new_lens[b] if the row can take its tokens, else 0 (and 0 where new_lens[b] <= 0), which is what the
+ *       append takes as new_lens
+ *     src_pages, dst_pages [B]: where ctx_lens[b] ends inside a page that was shared, that page and the row's new one, into
+ *       which paged_kv_copy_pages is to copy it; else -1
+ *     page_table_out, ref_counts_out (may be the inputs); counts 16-byte aligned
+ *     workspace: at least paged_kv_reserve_workspace_size(B, num_pages) bytes, 16-byte aligned
+ * paged_kv_compact: with L live pages (count positive), moves those at ids >= L, in order, to the free ids < L, in order.
+ *   src_pages, dst_pages [num_pages]: the moves, then -1; count [1]: how many.  page_table_out (may be page_table) names
+ *   the pages' new places, and -1 where an entry names no live page; ref_counts_out (not ref_counts) their counts, both
+ *   counts 16-byte aligned.  workspace: at least paged_kv_compact_workspace_size(num_pages) bytes, 16-byte aligned.
+ * paged_kv_copy_pages: page dst_pages[i] of each pool becomes a copy of page src_pages[i], for i < n and, if count (device
+ *   [1], may be NULL) is given, i < count[0].  pools: HOST array of n_pools device pointers, each to num_pages pages of
+ *   page_bytes contiguous bytes (a multiple of 16; keys and values of every layer).  Pairs with an id outside the pool are
+ *   skipped.  No page may be the destination of two pairs, or the destination of one and the source of another.
+ */
+int paged_kv_fork(const int32_t *page_table, const int32_t *ctx_lens, const int32_t *parents, const int32_t *ref_counts,
+                  int32_t *page_table_out, int32_t *ctx_lens_out, int32_t *ref_counts_out, int page_size, int B, int B_out,
+                  int max_pages_per_seq, int num_pages, attn_stream_t stream);
+
+size_t paged_kv_reserve_workspace_size(int B, int num_pages);
+
+int paged_kv_reserve(const int32_t *page_table, const int32_t *ctx_lens, const int32_t *new_lens,
+                     const int32_t *ref_counts, int32_t *page_table_out, int32_t *ref_counts_out, int32_t *reserved,
+                     int32_t *src_pages, int32_t *dst_pages, int page_size, int B, int max_pages_per_seq, int num_pages,
+                     void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+size_t paged_kv_compact_workspace_size(int num_pages);
+
+int paged_kv_compact(const int32_t *page_table, const int32_t *ref_counts, int32_t *page_table_out,
+                     int32_t *ref_counts_out, int32_t *src_pages, int32_t *dst_pages, int32_t *count, int B,
+                     int max_pages_per_seq, int num_pages, void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+int paged_kv_copy_pages(void *const *pools, int n_pools, size_t page_bytes, const int32_t *src_pages,
+                        const int32_t *dst_pages, const int32_t *count, int n, int num_pages, attn_stream_t stream);
+
+/*
  * Backward of attn_fwd_gqa: gradients of the loss with respect to q, k and v
  * given its gradient dout with respect to the forward output.  The method
  * (gpu-inference blog, section 02 "FlashAttention-2 in Triton"): the
