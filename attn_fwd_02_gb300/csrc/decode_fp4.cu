@@ -18,7 +18,9 @@
 // parts, two a CTA at most, are joined by a second kernel.  So neither the page table's width nor uneven lengths cost anything.
 // A small batch takes one cluster per row instead, which joins its CTAs' parts itself.
 // Measured (32/8 heads, d 128): 64 sequences of up to 16000 tokens 116 us (5.6 TB/s), 32 of up to 8192 37.7 us (4.0 TB/s; 51
-// with splits of the table's width), one of 103000 31.6 us (56); 2 of up to 900, 12 heads of 64, 6.2 us.
+// with splits of the table's width), one of 103000 31.6 us (56); 2 of up to 900, 12 heads of 64, with a distance bias 7.5 us.
+#include <type_traits>
+
 #include "decode_rows.cuh"
 #include "fp4.cuh"
 
@@ -259,13 +261,13 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
     if (a.cluster) {
         if (threadIdx.x == 0) {
             const PageRange r = seen_pages(a, blockIdx.z);
-            const long long n = r.p1 - r.p0;
+            const unsigned n = r.p1 - r.p0;  // (at most 2^26 pages, and 16 splits)
             Segment s;
             s.b = blockIdx.z;
             s.y = blockIdx.y;
             s.n = (int)n;
-            s.p0 = r.p0 + (int)(n * (int)blockIdx.x / a.n_splits);
-            s.p1 = r.p0 + (int)(n * ((int)blockIdx.x + 1) / a.n_splits);
+            s.p0 = r.p0 + (int)(n * blockIdx.x / (unsigned)a.n_splits);
+            s.p1 = r.p0 + (int)(n * (blockIdx.x + 1) / (unsigned)a.n_splits);
             s.lo = r.lo;
             s.hi = r.hi;
             s.end = min(r.hi, s.p1 * kRowPS);
@@ -287,23 +289,28 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
     int cur = 0;
     WaitCtx wc{&sm.abort_flag, a.status};
 
-    // Copies of step k of a segment into the ring: pages p0 + kStep (warp + 4 k) + {0, ..}.  Their ids are read for kIds steps at
-    // a time (lane l: page l % kStep of step k0 + l / kStep); which of them do not lie in the pool (and hold no token) is kept
-    // for two such blocks, the one that is read and the one that is issued.  Lane 2 j copies page j's keys, lane 2 j + 1 its values.
+    // A warp takes a quarter of the segment's pages, [w0, w1), kStep of them a step.  Their ids are read 32 at a time, one a lane;
+    // which of them do not lie in the pool (and hold no token) is kept for two such blocks, the one that is read and the one that
+    // is issued.  Of a step's pages lane 2 j copies page j's keys into the ring, lane 2 j + 1 its values.
     constexpr int kIds = 32 / kStep;
     int my_pid = -1;
     uint32_t gaps[2] = {0, 0}, sent = 0, done = 0;  // sent, done: steps of this warp's ring that were issued, and consumed
-    auto steps_of = [&](int p0, int p1) {
-        const int n = (p1 - p0 + kStep - 1) / kStep;
-        return n > warp ? (n - warp + kRowWarps - 1) / kRowWarps : 0;
+    int w0 = 0, w1 = 0;
+    auto quarter = [&] {
+        const int p0 = sm.seg[cur].p0, n = sm.seg[cur].p1 - p0;
+        const int unit = n < 4 * kRowWarps * kStep ? 1 : kStep;  // (whole steps where there are several)
+        const int units = (n + unit - 1) / unit;  // (at most 2^26)
+        w0 = p0 + unit * (units * warp / kRowWarps);
+        w1 = min(p0 + unit * (units * (warp + 1) / kRowWarps), p0 + n);
+        my_pid = w0 + lane < w1 ? a.page_table[(size_t)sm.seg[cur].b * a.max_pages + w0 + lane] : -1;  // the first ids
+        return (w1 - w0 + kStep - 1) / kStep;
     };
     const uint8_t *const my_pages = (lane & 1) ? v_pages : k_pages;
     auto issue = [&](int kvh, int k) {
         if (k % kIds == 0) {
-            const Segment &s = sm.seg[cur];
-            const int p = s.p0 + kStep * (warp + kRowWarps * (k + lane / kStep)) + lane % kStep;
-            my_pid = p < s.p1 ? a.page_table[(size_t)s.b * a.max_pages + p] : -1;
-            const uint32_t gap = __ballot_sync(0xffffffffu, p < s.p1 && (unsigned)my_pid >= (unsigned)a.num_pages);
+            const int p = w0 + kStep * k + lane;
+            if (k > 0) my_pid = p < w1 ? a.page_table[(size_t)sm.seg[cur].b * a.max_pages + p] : -1;
+            const uint32_t gap = __ballot_sync(0xffffffffu, p < w1 && (unsigned)my_pid >= (unsigned)a.num_pages);
             if ((k / kIds) & 1) gaps[1] = gap;
             else gaps[0] = gap;
         }
@@ -336,14 +343,14 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
             }
     };
 
-    int kvh = sm.seg[0].y / a.rgroups, nk = steps_of(sm.seg[0].p0, sm.seg[0].p1);
+    int kvh = sm.seg[0].y / a.rgroups, nk = quarter();
     load_q(kvh);
     for (int k = 0; k < min(nk, kSl); ++k) issue(kvh, k);
     bool failed = false;  // a wait ran out: this warp copies and reads nothing more, and only takes part in the barriers
     while (true) {
         // (the next part of the share is found meanwhile)
         if (threadIdx.x == 0 && !a.cluster) sm.seg[cur ^ 1] = next_segment(a, sm.seg[cur], left);
-        const int lo = sm.seg[cur].lo, end = sm.seg[cur].end;
+        const int lo = sm.seg[cur].lo, end = min(sm.seg[cur].end, w1 * kRowPS);
         // each head rounded to f16 after a 2^-sh of its own, which keeps it below 2^15 (exact but for values under f16's range;
         // sh 0 but for huge queries, at most 113); cc: per score column (heads 2t, 2t + 1 of an n-tile) the factor of its
         // products, to the cap's argument or, without a cap, to the log2 domain
@@ -403,14 +410,19 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
             m_neg[nt] = l[nt] = 0;
         }
 
-        int tok0 = (sm.seg[cur].p0 + kStep * warp) * kRowPS;
-        for (int k = 0; k < nk; ++k, tok0 += kStep * kRowWarps * kRowPS) {
+        int tok0 = w0 * kRowPS;
+        for (int k = 0; k < nk; ++k, tok0 += kStep * kRowPS) {
             const uint32_t slot = done % kSl;
             if (!mbar_wait(&sm.full[warp][slot], (done / kSl) & 1, wc, 150 + warp)) {
                 failed = true;
                 break;
             }
-            {
+            // slots that are not seen, and those of a page that is not there, may hold anything: their scales of the values become
+            // 0, and so do their scores, which choose the form of the cap with the others, until they become -inf.  Steps with such
+            // slots (PART) are a form of their own, which leaves out a second page past the end
+            const bool ragged = tok0 + kStep * kRowPS > end || tok0 < lo || (gaps[0] | gaps[1]);
+            auto step = [&](auto part) {
+                constexpr bool PART = decltype(part)::value;
                 uint8_t (*kv)[2][9 * D] = sm.kv[warp][slot];
                 // rows (tokens) g, g + 8 of each page, columns (heads) 2t, 2t + 1
                 float sc[kStep][NT][4];
@@ -418,6 +430,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                 for (int j = 0; j < kStep; ++j) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) sc[j][nt][0] = sc[j][nt][1] = sc[j][nt][2] = sc[j][nt][3] = 0.f;
+                    if (PART && j > 0 && tok0 + kRowPS * j >= end) continue;
                     const uint8_t *Kb = kv[j][0];
                     // one k-step: the f16 pairs of tokens g and g + 8 and their scales
                     auto k_step = [&](int ks, uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1, uint32_t s0, uint32_t s1) {
@@ -468,48 +481,75 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                         }
                     }
                 }
-                if constexpr (MOD) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < kStep; ++j) {
-                            float (&s)[4] = sc[j][nt];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s[i] *= cc[nt][i & 1];
-                            if (a.cap_in > 0.f) {
-                                const float big = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
-                                const uint64_t u01 = f32x2_pack(s[0], s[1]), u23 = f32x2_pack(s[2], s[3]);
-                                if (__any_sync(0xffffffffu, big > 1.f)) {
-                                    f32x2_unpack(TanhCap::eval_u<2>(u01, a.cap_out), s[0], s[1]);
-                                    f32x2_unpack(TanhCap::eval_u<2>(u23, a.cap_out), s[2], s[3]);
-                                } else {
-                                    f32x2_unpack(TanhCap::eval_u<1>(u01, a.cap_out), s[0], s[1]);
-                                    f32x2_unpack(TanhCap::eval_u<1>(u23, a.cap_out), s[2], s[3]);
-                                }
-                            }
-                            const float far0 = (float)(last - tok0 - kRowPS * j - g);  // distance of token g (g + 8: 8 less)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s[i] = fmaf(-slope2[nt][i & 1], i < 2 ? far0 : far0 - 8.f, s[i]);
-                        }
-                }
-                if (tok0 + kStep * kRowPS > end || tok0 < lo || (gaps[0] | gaps[1])) {
-                    // slots that are not seen, and those of a page that is not there, may hold anything
+                auto seen = [&](int j, int i) {
                     const uint32_t gone = (((k / kIds) & 1) ? gaps[1] : gaps[0]) >> (kStep * (k % kIds));
-                    auto seen = [&](int j, int i) {
-                        const int x = tok0 + kRowPS * j + i;
-                        return !((gone >> j) & 1u) && x >= lo && x < end;
-                    };
+                    const int x = tok0 + kRowPS * j + i;
+                    return !((gone >> j) & 1u) && x >= lo && x < end;
+                };
+                auto unseen_to = [&](int j, float v) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!seen(j, g + (i < 2 ? 0 : 8)))
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) sc[j][nt][i] = v;
+                };
+                if constexpr (PART) {
 #pragma unroll
                     for (int j = 0; j < kStep; ++j) {
                         for (int i = lane; i < kRowPS * KS; i += 32)
                             if (!seen(j, i & 15)) kv[j][1][fp4_v_scale(D, i & 15, i >> 4)] = 0;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (!seen(j, g + (i < 2 ? 0 : 8))) sc[j][nt][i] = -INFINITY;
+                        unseen_to(j, MOD ? 0.f : -INFINITY);
                     }
                     fence_proxy_async_smem();  // before the next copy into these bytes
+                    __syncwarp();
+                }
+                if constexpr (MOD) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint64_t c2 = f32x2_pack(cc[nt][0], cc[nt][1]);
+                        uint64_t u[kStep][2];
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) u[j][i] = f32x2_mul(f32x2_pack(sc[j][nt][2 * i], sc[j][nt][2 * i + 1]), c2);
+                        if (a.cap_in > 0.f) {
+                            float big = 0.f;
+#pragma unroll
+                            for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    float x, y;
+                                    f32x2_unpack(u[j][i], x, y);
+                                    big = fmax3_abs(big, x, y);
+                                }
+                            const int tier = !__any_sync(0xffffffffu, big > 0.25f) ? 0 : (__any_sync(0xffffffffu, big > 1.f) ? 2 : 1);
+#pragma unroll
+                            for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    u[j][i] = tier == 0 ? TanhCap::eval_u<0>(u[j][i], a.cap_out)
+                                                        : (tier == 1 ? TanhCap::eval_u<1>(u[j][i], a.cap_out)
+                                                                     : TanhCap::eval_u<2>(u[j][i], a.cap_out));
+                        }
+                        if (a.slopes) {
+                            const uint64_t s2 = f32x2_pack(-slope2[nt][0], -slope2[nt][1]);
+#pragma unroll
+                            for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {  // the distance of token g or g + 8
+                                    const float far = (float)(last - tok0 - kRowPS * j - g - 8 * i);
+                                    u[j][i] = f32x2_fma(s2, f32x2_pack(far, far), u[j][i]);
+                                }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kStep; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) f32x2_unpack(u[j][i], sc[j][nt][2 * i], sc[j][nt][2 * i + 1]);
+                    }
+                }
+                if constexpr (MOD && PART) {
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) unseen_to(j, -INFINITY);
                     __syncwarp();
                 }
                 auto most_of = [&](int nt, int i) {  // this lane's largest score of a head
@@ -552,6 +592,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                 }
 #pragma unroll
                 for (int j = 0; j < kStep; ++j) {
+                    if (PART && j > 0 && tok0 + kRowPS * j >= end) continue;
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -601,7 +642,9 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                         }
                     }
                 }
-            }
+            };
+            if (ragged) step(std::true_type{});
+            else step(std::false_type{});
             __syncwarp();  // the slot's reads are done
             ++done;
             if (k + kSl < nk) issue(kvh, k + kSl);
@@ -628,8 +671,9 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
         const bool more = sm.seg[cur].b >= 0;
         if (more) {
             kvh = sm.seg[cur].y / a.rgroups;
+            nk = quarter();
             load_q(kvh);
-            nk = failed ? 0 : steps_of(sm.seg[cur].p0, sm.seg[cur].p1);
+            if (failed) nk = 0;
             for (int k = 0; k < min(nk, kSl); ++k) issue(kvh, k);
         }
         // a part of a row that begins in an earlier CTA goes to the CTA's first place, one that only begins here to its second

@@ -56,9 +56,15 @@ struct TanhCap {
             return eval_u<T>(f32x2_mul(raw, f32x2_pack(in, in)), out);
         }
     }
-    // out * tanh(u) of a pair, by the mid (1) or the far (2) form.
+    // out * tanh(u) of a pair, by the near (0; the three terms, of u itself), the mid (1) or the far (2) form.
     template <int T>
     static __device__ __forceinline__ uint64_t eval_u(uint64_t u, float out) {
+        if constexpr (T == 0) {
+            const uint64_t z = f32x2_mul(u, u);
+            uint64_t t = f32x2_fma(z, f32x2_pack(0.128416134f * out, 0.128416134f * out), f32x2_pack(-0.333219082f * out, -0.333219082f * out));
+            t = f32x2_fma(z, t, f32x2_pack(0.999999604f * out, 0.999999604f * out));
+            return f32x2_mul(t, u);
+        }
         constexpr float kP[6] = {0.999999414f, -0.333290424f, 0.13281434f,
                                  -0.0516056762f, 0.0167431162f, -0.00306706033f};
         const uint64_t z = f32x2_mul(u, u);
