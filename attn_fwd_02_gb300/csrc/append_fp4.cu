@@ -5,6 +5,12 @@
 // a token that comes alone keeps the other nibble of each byte as it is, and no other block of the call writes there.  A
 // thread takes 16 dims of a row, one block of the cache's scales; for a key it reads the 16 dims that they turn with as
 // well (from L1 the second time), so that the block's maximum needs no exchange between threads.
+//
+// The append is bound by its instructions as much as by memory: about 2260 a warp for a token of 32 + 8 heads of 128, the
+// queries' rotation, the keys' and values' quotients (one fused correction each instead of a division: 21 -> 19 us) in about
+// equal parts.  Measured: up to 1024 new tokens of 8 sequences, ragged, 19 us, and their pages as bf16 11 us; the two calls
+// 29.7 us, of which the second starts while the first drains.  64 threads a block 30.7, 256 31.6; the rows' vectors read one
+// row ahead 34.8 (more registers).  One token of 4 sequences: 6.0 us for the two calls, which is the host's time.
 #include "fp4.cuh"
 #include "rope.cuh"
 
@@ -28,6 +34,8 @@ struct Fp4AppendParams {
 template <bool INTER>
 __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4AppendParams p) {
     __shared__ float angles[2][kMaxRope];
+    griddep_launch_dependents();
+    griddep_wait();
     const int b = (int)(blockIdx.x / (unsigned)p.pairs);
     const int start = max(p.start_pos[b], 0);
     const long long pos0 = (long long)(start & ~1) + 2LL * (blockIdx.x % (unsigned)p.pairs);
@@ -59,11 +67,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
     if (page >= p.num_pages) page = -1;
     __syncthreads();
 
-    // Thread = (16-dim block j of a row, first row): it takes that block of every per_pass-th row.
+    // Thread = (16-dim block j of a row, first row): it takes that block of every per_pass-th row.  The rows are those of the
+    // tokens' keys, then the values' (a row for both tokens), then the tokens' queries.
     const int vpr = p.d / 8, bpr = p.d / 16, half = p.rope / 2;
     const int per_pass = kThreads / bpr;
     const int j = threadIdx.x % bpr, r0 = threadIdx.x / bpr;
     if (r0 >= per_pass) return;
+    const int e0 = have[0] ? 0 : 1, tokens = have[0] && have[1] ? 2 : 1;
+    const int k_rows = page < 0 ? 0 : tokens * p.Hkv, kv_rows = page < 0 ? 0 : k_rows + p.Hkv;
+    const int rows = kv_rows + (p.q ? tokens * p.H : 0);
+    const int slot = (int)(pos0 % kFp4PS);  // even
+    const size_t block = (size_t)9 * p.d;
     // A row's 8 dims from vector w on, turned: x c - y s in the first half of the pairs, y c + x s in the second.
     auto turned = [&](const uint4 *row, int w, const float *cs, float (&x)[8]) {
         unpack8(row[w], x);
@@ -81,38 +95,87 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
             float y[8];
             unpack8(row[first ? w + half / 8 : w - half / 8], y);
             const float *c = cs + (first ? 8 * w : 8 * w - half), *s = c + half;
+            const float sign = first ? -1.f : 1.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * c[i] - y[i] * s[i] : x[i] * c[i] + y[i] * s[i];
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + y[i] * (sign * s[i]);
         }
     };
-    // 16 values times 1 / scale
-    auto load_block = [&](const uint4 *row, const float *cs, float inv, bool turn, float (&u)[16]) {
-        float x[2][8];
+    for (int row = r0; row < rows; row += per_pass) {
+        if (row < k_rows) {
+            const int second = row >= p.Hkv, e = e0 + second, h = row - second * p.Hkv;
+            const uint4 *k = p.k + b * p.ks[0] + h * p.ks[1] + tok[e] * p.ks[2];
+            uint8_t *kd = p.k_pages + ((size_t)page * p.Hkv + h) * block;
+            float u[16], x[8];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            if (turn) turned(row, 2 * j + w, cs, x[w]);
-            else unpack8(row[2 * j + w], x[w]);
+            for (int w = 0; w < 2; ++w) {
+                turned(k, 2 * j + w, angles[e], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[8 * w + i] = __fmul_rn(x[w][i], inv);
-        }
-    };
-    if (p.q) {
-        // (in place too: a thread reads both halves of its pairs before it writes them)
-        const int rot = p.rope / 16;
-        const bool turns = !INTER && j < rot;
-        const int w0 = turns ? j : 2 * j, w1 = turns ? j + rot : 2 * j + 1;
+                for (int i = 0; i < 8; ++i) u[8 * w + i] = __fmul_rn(x[i], p.k_inv);
+            }
+            const uint32_t s = fp4_scale_code(u);
+            fp4_quotients(u, e4m3_to_float(s));
+            float lo[8], hi[8];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (!have[e]) continue;
-            const uint4 *q = p.q + b * p.qs[0] + tok[e] * p.qs[2];
-            uint4 *out = p.q_out + ((size_t)b * p.H * p.N + tok[e]) * vpr;
-            for (int h = r0; h < p.H; h += per_pass) {
-                float x[8], y[8];
-                const uint4 *row = q + h * p.qs[1];
-                uint4 *to = out + (size_t)h * p.N * vpr;
-                if (turns) {
-                    unpack8(row[w0], x);
-                    unpack8(row[w1], y);
+            for (int i = 0; i < 8; ++i) lo[i] = u[i], hi[i] = u[8 + i];
+            kd[fp4_k_scale(p.d, slot + e, j)] = (uint8_t)s;
+            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo), f32x8_to_e2m1x8(hi));
+        } else if (row < kv_rows) {
+            const int h = row - k_rows;
+            const uint4 *v = p.v + b * p.vs[0] + h * p.vs[1] + 2 * j;
+            uint8_t *vd = p.v_pages + ((size_t)page * p.Hkv + h) * block;
+            uint4 *at = reinterpret_cast<uint4 *>(vd + fp4_v_codes(slot, j));
+            uint4 old = make_uint4(0u, 0u, 0u, 0u);  // the codes of a token that is not there stay
+            if (tokens == 1) old = *at;
+            float u[2][16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+                if (have[e]) x0 = v[tok[e] * p.vs[2]], x1 = v[tok[e] * p.vs[2] + 1];
+                float x[2][8];
+                unpack8(x0, x[0]);
+                unpack8(x1, x[1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[e][i] = __fmul_rn(x[i >> 3][i & 7], p.v_inv);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t s = fp4_scale_code(u[e]);
+                fp4_quotients(u[e], e4m3_to_float(s));
+                if (have[e]) vd[fp4_v_scale(p.d, slot + e, j)] = (uint8_t)s;
+            }
+            // byte x of the block: dim x of both tokens
+            uint32_t bytes[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[8];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) y[2 * n] = u[0][4 * i + n], y[2 * n + 1] = u[1][4 * i + n];
+                bytes[i] = f32x8_to_e2m1x8(y);
+            }
+            if (tokens == 1) {
+                const uint32_t keep = e0 == 0 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
+                bytes[0] = (bytes[0] & ~keep) | (old.x & keep);
+                bytes[1] = (bytes[1] & ~keep) | (old.y & keep);
+                bytes[2] = (bytes[2] & ~keep) | (old.z & keep);
+                bytes[3] = (bytes[3] & ~keep) | (old.w & keep);
+            }
+            *at = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
+        } else {
+            // (in place too: a thread reads both halves of its pairs before it writes them)
+            const int second = row - kv_rows >= p.H, e = e0 + second, h = row - kv_rows - second * p.H;
+            const uint4 *q = p.q + b * p.qs[0] + h * p.qs[1] + tok[e] * p.qs[2];
+            uint4 *to = p.q_out + (((size_t)b * p.H + h) * p.N + tok[e]) * vpr;
+            const int rot = p.rope / 16;
+            const bool halves = !INTER && j < rot;  // x in the first half, its y in the second
+            const int w0 = halves ? j : 2 * j, w1 = halves ? j + rot : 2 * j + 1;
+            float x[8], y[8];
+            if (INTER) {
+                turned(q, w0, angles[e], x);
+                turned(q, w1, angles[e], y);
+            } else {
+                unpack8(q[w0], x);
+                unpack8(q[w1], y);
+                if (halves) {
                     const float *c = angles[e] + 8 * j, *s = c + half;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -120,54 +183,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
                         y[i] = y[i] * c[i] + x[i] * s[i];
                         x[i] = u;
                     }
-                } else if (INTER) {
-                    turned(row, w0, angles[e], x);
-                    turned(row, w1, angles[e], y);
-                } else {
-                    unpack8(row[w0], x);
-                    unpack8(row[w1], y);
                 }
-                to[w0] = pack8(x);
-                to[w1] = pack8(y);
             }
+            to[w0] = pack8(x);
+            to[w1] = pack8(y);
         }
-    }
-    if (page < 0) return;
-    const int slot = (int)(pos0 % kFp4PS);  // even
-    const size_t block = (size_t)9 * p.d;
-    for (int h = r0; h < p.Hkv; h += per_pass) {
-        uint8_t *kd = p.k_pages + ((size_t)page * p.Hkv + h) * block, *vd = p.v_pages + ((size_t)page * p.Hkv + h) * block;
-        float u[16];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (!have[e]) continue;
-            uint32_t codes[2];
-            load_block(p.k + b * p.ks[0] + h * p.ks[1] + tok[e] * p.ks[2], angles[e], p.k_inv, p.cos_sin != nullptr, u);
-            kd[fp4_k_scale(p.d, slot + e, j)] = (uint8_t)fp4_block(u, codes);
-            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(codes[0], codes[1]);
-        }
-        // values: nibble e of byte x holds dim x of token e
-        uint4 *at = reinterpret_cast<uint4 *>(vd + fp4_v_codes(slot, j));
-        uint32_t bytes[4] = {0u, 0u, 0u, 0u};
-        if (!have[0] || !have[1]) {
-            const uint4 old = *at;
-            const uint32_t keep = have[0] ? 0xf0f0f0f0u : 0x0f0f0f0fu;
-            bytes[0] = old.x & keep, bytes[1] = old.y & keep, bytes[2] = old.z & keep, bytes[3] = old.w & keep;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (!have[e]) continue;
-            uint32_t codes[2];
-            load_block(p.v + b * p.vs[0] + h * p.vs[1] + tok[e] * p.vs[2], nullptr, p.v_inv, false, u);
-            vd[fp4_v_scale(p.d, slot + e, j)] = (uint8_t)fp4_block(u, codes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // nibbles 4i .. 4i + 3 into the bytes of a word
-                const uint32_t n = codes[i >> 1] >> (16 * (i & 1));
-                const uint32_t w = (n & 0xfu) | (n & 0xf0u) << 4 | (n & 0xf00u) << 8 | (n & 0xf000u) << 12;
-                bytes[i] |= w << (4 * e);
-            }
-        }
-        *at = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
     }
 }
 
@@ -186,53 +206,49 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t h2, float s, float scal
     return pack_bf16x2(__fmul_rn(__low2float(h) * s, scale), __fmul_rn(__high2float(h) * s, scale));
 }
 
-// A thread takes 16 dims of two tokens (a byte of the values' codes holds both); z: keys, values.
+// One CTA a page's keys or values (blockIdx.y).  A thread takes 8 dims of two tokens that share the values' bytes, so that its
+// vectors of the output are neighbours of the next lanes'.
+template <int D>
 __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p) {
-    const int bpr = p.d / 16, per_head = bpr * 8;
+    constexpr int kVpr = D / 8, kPerHead = kVpr * 8;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int page = p.page_ids[blockIdx.x];
+    if (page < 0 || page >= p.num_pages) return;
     const bool value = blockIdx.y != 0;
-    const long long total = (long long)p.n * p.Hkv * per_head;
-    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long long)gridDim.x * 256) {
-        const int j = (int)(e % bpr), pair = (int)(e / bpr % 8);
-        const long long row = e / per_head;  // page * Hkv + head
-        const int page = p.page_ids[row / p.Hkv];
-        if (page < 0 || page >= p.num_pages) continue;
-        const uint8_t *src = (value ? p.v_pages : p.k_pages) + ((size_t)page * p.Hkv + row % p.Hkv) * (size_t)(9 * p.d);
-        uint4 *dst = (value ? p.v_out : p.k_out) + ((size_t)row * kFp4PS + 2 * pair) * (size_t)(p.d / 8) + 2 * j;
-        const float scale = value ? p.v_scale : p.k_scale;
-        uint32_t out[2][8];
+    const float scale = value ? p.v_scale : p.k_scale;
+    const uint8_t *pages = (value ? p.v_pages : p.k_pages) + (size_t)page * p.Hkv * (9 * D);
+    uint4 *out = (value ? p.v_out : p.k_out) + (size_t)blockIdx.x * p.Hkv * kFp4PS * kVpr;
+    for (int e = threadIdx.x; e < p.Hkv * kPerHead; e += 256) {
+        const int w = e % kVpr, token = 2 * (e / kVpr % 8), h = e / kPerHead;  // vector w of tokens `token`, `token` + 1
+        const uint8_t *src = pages + (size_t)h * (9 * D);
+        uint4 *dst = out + ((size_t)h * kFp4PS + token) * kVpr + w;
+        uint32_t r[2][4], x[2][4];
+        float s[2];
         if (value) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + fp4_v_codes(2 * pair, j));
-            const float s0 = e4m3_to_float(src[fp4_v_scale(p.d, 2 * pair, j)]);
-            const float s1 = e4m3_to_float(src[fp4_v_scale(p.d, 2 * pair + 1, j)]);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+            const uint2 c = *reinterpret_cast<const uint2 *>(src + fp4_v_codes(token, w / 2) + (w & 1) * 8);
+            const uint32_t two = *reinterpret_cast<const uint16_t *>(src + fp4_v_scale(D, token, w / 2));
+            s[0] = e4m3_to_float(two);
+            s[1] = e4m3_to_float(two >> 8);
+            e2m1x8_to_f16x2x4(c.x, x[0]);  // dims 0 .. 3, a pair of tokens each
+            e2m1x8_to_f16x2x4(c.y, x[1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t r[4];  // dims 4i .. 4i + 3, a pair of tokens each
-                e2m1x8_to_f16x2x4(ws[i], r);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t lo = __byte_perm(r[2 * h], r[2 * h + 1], 0x5410), hi = __byte_perm(r[2 * h], r[2 * h + 1], 0x7632);
-                    out[0][2 * i + h] = scaled_pair(lo, s0, scale);
-                    out[1][2 * i + h] = scaled_pair(hi, s1, scale);
-                }
+                const uint32_t a = x[i >> 1][2 * (i & 1)], b = x[i >> 1][2 * (i & 1) + 1];
+                r[0][i] = __byte_perm(a, b, 0x5410);
+                r[1][i] = __byte_perm(a, b, 0x7632);
             }
         } else {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src + fp4_k_codes(p.d, 2 * pair + t, j));
-                const float s = e4m3_to_float(src[fp4_k_scale(p.d, 2 * pair + t, j)]);
-                uint32_t r[2][4];
-                e2m1x8_to_f16x2x4(w.x, r[0]);
-                e2m1x8_to_f16x2x4(w.y, r[1]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) out[t][i] = scaled_pair(r[i >> 2][i & 3], s, scale);
+                e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t *>(src + fp4_k_codes(D, token + t, 0) + 4 * w), r[t]);
+                s[t] = e4m3_to_float(src[fp4_k_scale(D, token + t, w / 2)]);
             }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            dst[t * (p.d / 8)] = make_uint4(out[t][0], out[t][1], out[t][2], out[t][3]);
-            dst[t * (p.d / 8) + 1] = make_uint4(out[t][4], out[t][5], out[t][6], out[t][7]);
-        }
+        for (int t = 0; t < 2; ++t)
+            dst[t * kVpr] = make_uint4(scaled_pair(r[t][0], s[t], scale), scaled_pair(r[t][1], s[t], scale),
+                                       scaled_pair(r[t][2], s[t], scale), scaled_pair(r[t][3], s[t], scale));
     }
 }
 
@@ -267,23 +283,25 @@ cudaError_t launch_kv_append_fp4(const RopeAppendArgs &a, cudaStream_t stream) {
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.axes = a.axes;
-    const unsigned grid = (unsigned)((long long)a.B * p.pairs);
-    if (a.interleaved) kv_append_fp4_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-    else kv_append_fp4_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)((long long)a.B * p.pairs));
+    return a.interleaved ? launch_dependent(kv_append_fp4_kernel<true>, grid, kThreads, 0, stream, p)
+                         : launch_dependent(kv_append_fp4_kernel<false>, grid, kThreads, 0, stream, p);
 }
 
 cudaError_t launch_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale, float v_scale,
                                  const int32_t *page_ids, int n, void *k_out, void *v_out, int Hkv, int d, int num_pages,
                                  cudaStream_t stream) {
-    int sms = 0;
-    const cudaError_t e = current_sm_count(&sms);
-    if (e != cudaSuccess) return e;
     const UnpackParams p{static_cast<const uint8_t *>(k_pages), static_cast<const uint8_t *>(v_pages), page_ids,
                          static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out), k_scale, v_scale, n, Hkv, d, num_pages};
-    const long long want = ((long long)n * Hkv * (d / 2) + 255) / 256, most = (long long)sms * 8;
-    kv_unpack_fp4_kernel<<<dim3((unsigned)(want < most ? want : most), 2), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)n, 2);
+    switch (d) {
+        case 32: return launch_dependent(kv_unpack_fp4_kernel<32>, grid, 256, 0, stream, p);
+        case 64: return launch_dependent(kv_unpack_fp4_kernel<64>, grid, 256, 0, stream, p);
+        case 80: return launch_dependent(kv_unpack_fp4_kernel<80>, grid, 256, 0, stream, p);
+        case 96: return launch_dependent(kv_unpack_fp4_kernel<96>, grid, 256, 0, stream, p);
+        case 128: return launch_dependent(kv_unpack_fp4_kernel<128>, grid, 256, 0, stream, p);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace attn

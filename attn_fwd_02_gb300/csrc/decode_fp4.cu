@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
     }
 
     griddep_launch_dependents();  // the joining kernel's CTAs come as this one's leave
+    if (a.cluster) griddep_wait();  // as this one's may come as those of the kernel before leave
     long long left = 0;  // of the share, in units, after the segment that was found last (of the thread that finds them)
     if (a.cluster) {
         if (threadIdx.x == 0) {
@@ -701,6 +702,7 @@ __global__ void __launch_bounds__(kFp4Threads) decode_fp4_join_kernel(const Fp4P
     const int in_group = h % a.group, y = h / a.group * a.rgroups + in_group / (8 * NT);
     const PageRange r = seen_pages(a, b);
     const bool any_page = r.p0 < r.p1;
+    griddep_launch_dependents();
     griddep_wait();  // (by every CTA, so that this grid does not end before the one that it depends on)
     int2 ctas = make_int2(0, 0);
     if (any_page) {
@@ -806,11 +808,26 @@ cudaError_t launch_fp4_n(const DecodeMoreArgs &a, Fp4Params p, cudaStream_t stre
         if (e == cudaSuccess && cluster_fits(reinterpret_cast<const void *>(kernel), p.cluster, kFp4Threads, smem)) {
             Fp4Params c = p;
             c.n_splits = p.cluster;
-            return launch_cluster(kernel, dim3(p.cluster, p.Hkv * p.rgroups, p.B), kFp4Threads, smem, stream, k, v, c);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(p.cluster, p.Hkv * p.rgroups, p.B);
+            cfg.blockDim = dim3(kFp4Threads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = p.cluster;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, kernel, k, v, c);
         }
         (void)cudaGetLastError();
         p.cluster = 0;  // no room for the cluster (a part of a GPU): shares through the workspace
     }
+    // (not as a dependent: one that comes while the last kernel's CTAs leave does not fill the SMs in turn, 37 -> 49 us)
     kernel<<<kSms * kFp4Ctas<NT>, kFp4Threads, smem, stream>>>(k, v, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

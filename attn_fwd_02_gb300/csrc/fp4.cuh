@@ -70,23 +70,25 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
     return f;
 }
 
-// The block's scale and codes of 16 values (already times 1 / the tensor's scale): s = e4m3(max |u| / 6), nearest and at
-// most 448, with 1/6 as an fp32 factor; codes = e2m1(u / s), or 0 where s is 0.  The division is the correctly rounded
-// one, so that a code is a function of the definition alone.
-__device__ __forceinline__ uint32_t fp4_block(const float (&u)[16], uint32_t (&codes)[2]) {
+// The scale of a block of 16 values u (already times 1 / the tensor's scale): s = e4m3(max |u| / 6), nearest and at most 448, with
+// 1/6 as an fp32 factor; its code.
+__device__ __forceinline__ uint32_t fp4_scale_code(const float (&u)[16]) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(u[i]));
-    const uint32_t s = __nv_cvt_float_to_fp8(__fmul_rn(m, 0.16666667163372039794921875f), __NV_SATFINITE, __NV_E4M3);
-    const float f = e4m3_to_float(s);
+    for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(fabsf(u[i]), fabsf(u[i + 1])));
+    return __nv_cvt_float_to_fp8(__fmul_rn(m, 0.16666667163372039794921875f), __NV_SATFINITE, __NV_E4M3);
+}
+// u / s in place, correctly rounded, or 0 where s is 0: a code is then a function of the definition alone.  With r the nearest to
+// 1 / s, q = u r and the remainder u - q s (exact by fused multiply-add), q + remainder * r is the nearest to u / s (Markstein's
+// theorem, IBM J. Res. Dev. 34 (1990)); quotients past 2^100 are cut there, far above the largest code.
+__device__ __forceinline__ void fp4_quotients(float (&u)[16], float s) {
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = f > 0.f ? __fdiv_rn(u[8 * h + i], f) : 0.f;
-        codes[h] = f32x8_to_e2m1x8(y);
+    for (int i = 0; i < 16; ++i) {
+        const float q = fminf(fmaxf(u[i] * r, -1.2676506e30f), 1.2676506e30f);
+        const float y = fmaf(fmaf(-q, s, u[i]), r, q);
+        u[i] = s > 0.f ? copysignf(y, u[i]) : 0.f;  // (-0 stays -0)
     }
-    return s;
 }
 
 }  // namespace attn

@@ -7,7 +7,10 @@
 // show in the result.
 //
 // The scans over the counts and over the rows are one cluster's work: each CTA takes an even part of the pool, the parts'
-// totals are exchanged at a cluster barrier.
+// totals are exchanged at a cluster barrier.  There is next to nothing to read and write, so the launches count: tables and
+// pools of ordinary size are the work of one kernel a call, all of it by that cluster, and the kernels start while the ones
+// before them drain (a fork, a reservation and the copies for 16 rows: 20.5 us in five kernels, 14.1 in three, which is the
+// host's time for the three calls; a compaction of 400 pages with its copies 16.4 and 11.9).
 #include "launch.h"
 #include "sm103_ptx.cuh"
 
@@ -36,8 +39,7 @@ __device__ __forceinline__ int fork_entry(const ForkParams &p, int b, int c) {
     }
     return p.table[(size_t)par * p.W + c];
 }
-__global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
-    const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+__device__ __forceinline__ void fork_rows(const ForkParams &p, long long i0, long long step) {
     for (long long i = i0; i < (long long)p.B_out * p.W; i += step) p.table_out[i] = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
     for (long long i = i0; i < p.P; i += step) p.ref_out[i] = p.ref[i];
     for (long long i = i0; i < p.B_out; i += step) {
@@ -46,22 +48,41 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
     }
 }
 // Counts: what a place of the table names now, less what it named.
-__global__ void __launch_bounds__(256) pages_fork_count_kernel(const ForkParams p) {
-    griddep_wait();
+__device__ __forceinline__ void fork_counts(const ForkParams &p, long long i0, long long step) {
     const long long rows = max(p.B, p.B_out);
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < rows * p.W; i += (long long)gridDim.x * 256) {
+    for (long long i = i0; i < rows * p.W; i += step) {
         const int was = i < (long long)p.B * p.W ? p.table[i] : -1;
-        const int is = i < (long long)p.B_out * p.W ? p.table_out[i] : -1;
+        const int is = i < (long long)p.B_out * p.W ? __ldcg(p.table_out + i) : -1;
         if (was == is) continue;
         if (in_pool(was, p.P)) atomicSub(p.ref_out + was, 1);
         if (in_pool(is, p.P)) atomicAdd(p.ref_out + is, 1);
     }
 }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// One cluster: the rows, then the counts.
+__global__ void __launch_bounds__(kScanThreads) pages_fork_cluster_kernel(const ForkParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long i0 = (long long)blockIdx.x * kScanThreads + threadIdx.x, step = (long long)gridDim.x * kScanThreads;
+    fork_rows(p, i0, step);
+    cluster_sync();
+    fork_counts(p, i0, step);
+}
+// Large tables: two grids.
+__global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    fork_rows(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+}
+__global__ void __launch_bounds__(256) pages_fork_count_kernel(const ForkParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    fork_counts(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+}
 
 // ---------------------------------------------------------------- scans
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Sum over the block's threads before this one, and over all of them (in `total`).
 __device__ __forceinline__ int block_scan(int v, int (&warp_sums)[33], int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -107,20 +128,25 @@ __device__ __forceinline__ void scan_part(int n, int cta, int ctas, int &begin, 
 struct ReserveParams {
     const int32_t *table, *ctx, *new_lens, *ref;
     int32_t *table_out, *ref_out, *reserved, *src, *dst;
-    int32_t *frozen;  // the counts at the call's start (the caller's, or a copy when they change in place)
+    int32_t *frozen;  // a copy of the counts at the call's start, when they change in place
     int32_t *need;    // [B]
     int32_t *ids;     // [P]: free pages in order
     int32_t *parts;   // [kScanCtas]: free pages of each part
-    int B, W, P, ctas, copy_table, copy_ref, copy_frozen;
+    int B, W, P, ctas, copy_table, copy_ref, copy_frozen, copied;  // copied: by a grid before
 };
-__global__ void __launch_bounds__(256) pages_reserve_copy_kernel(const ReserveParams p) {
-    const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+__device__ __forceinline__ void reserve_copies(const ReserveParams &p, long long i0, long long step) {
     if (p.copy_table)
         for (long long i = i0; i < (long long)p.B * p.W; i += step) p.table_out[i] = p.table[i];
     for (long long i = i0; i < p.P; i += step) {
-        if (p.copy_ref) p.ref_out[i] = p.ref[i];
-        if (p.copy_frozen) p.frozen[i] = p.ref[i];
+        const int v = p.ref[i];
+        if (p.copy_ref) p.ref_out[i] = v;
+        if (p.copy_frozen) p.frozen[i] = v;
     }
+}
+__global__ void __launch_bounds__(256) pages_reserve_copy_kernel(const ReserveParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    reserve_copies(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
 }
 // Entries [from, to) of row b that cover its new tokens (to 0: none wanted, or more than the table holds).
 __device__ __forceinline__ void reserve_range(const ReserveParams &p, int b, int &n, int &from, int &to) {
@@ -134,9 +160,13 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     __shared__ int sums[33];
     const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first_warp = cta * 32 + warp, all_warps = p.ctas * 32;
+    griddep_launch_dependents();
     griddep_wait();
-    // an entry to be given a page: it has none, or shares it
-    auto lacks = [&](int e) { return !in_pool(e, p.P) || p.frozen[e] > 1; };
+    if (!p.copied) reserve_copies(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
+    // an entry to be given a page: it has none, or shares it (by the counts at the call's start: the input's, which do not
+    // change before the second barrier, and then its copy)
+    const int32_t *counts = p.ref;
+    auto lacks = [&](int e) { return !in_pool(e, p.P) || __ldcg(counts + e) > 1; };
     for (int b = first_warp; b < p.B; b += all_warps) {
         int n, from, to, need = 0;
         reserve_range(p, b, n, from, to);
@@ -149,7 +179,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     int begin, end, mine = 0;
     scan_part(p.P, cta, p.ctas, begin, end);
     for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
-        const int4 v = counts4(p.frozen, i, end, 1);
+        const int4 v = counts4(p.ref, i, end, 1);
         mine += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
     }
     int total;
@@ -174,7 +204,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     const int last = (int)min(wanted, (long long)free_pages);
     for (int i0 = begin; i0 < end && before < last; i0 += kScanTile) {
         const int i = i0 + 4 * (int)threadIdx.x;
-        const int4 v = counts4(p.frozen, i, end, 1);
+        const int4 v = counts4(p.ref, i, end, 1);
         const bool f[4] = {v.x <= 0, v.y <= 0, v.z <= 0, v.w <= 0};
         int at = before + block_scan(f[0] + f[1] + f[2] + f[3], sums, total);
         before += total;
@@ -183,6 +213,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
             if (f[j]) p.ids[at++] = i + j;
     }
     cluster_sync();
+    if (p.copy_frozen) counts = p.frozen;
     // rows, a tile of kScanThreads at a time: their offsets in shared memory, then a warp for each
     __shared__ int offsets[kScanThreads];
     long long base = 0;
@@ -234,11 +265,19 @@ struct CompactParams {
     int32_t *table_out, *ref_out, *src, *dst, *count;
     int32_t *to;     // [P]: where a page goes (-1: it is not live)
     int32_t *parts;  // [2 kScanCtas]
-    int B, W, P, ctas;
+    int B, W, P, ctas, rename;  // rename: the table too
 };
+__device__ __forceinline__ void rename_entries(const CompactParams &p, long long i0, long long step) {
+    for (long long i = i0; i < (long long)p.B * p.W; i += step) {
+        const int e = p.table[i];
+        p.table_out[i] = in_pool(e, p.P) ? __ldcg(p.to + e) : -1;
+    }
+}
 __global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const CompactParams p) {
     __shared__ int sums[33];
     const int cta = blockIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();
     int begin, end, mine = 0, total;
     scan_part(p.P, cta, p.ctas, begin, end);
     for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
@@ -296,16 +335,18 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const Compa
         p.to[s] = d;
         p.ref_out[d] = p.ref[s];
     }
+    if (!p.rename) return;
+    cluster_sync();
+    rename_entries(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
 }
 __global__ void __launch_bounds__(256) pages_compact_table_kernel(const CompactParams p) {
+    griddep_launch_dependents();
     griddep_wait();
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)p.B * p.W; i += (long long)gridDim.x * 256) {
-        const int e = p.table[i];
-        p.table_out[i] = in_pool(e, p.P) ? p.to[e] : -1;
-    }
+    rename_entries(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
 }
 
 // ---------------------------------------------------------------- copies
+// Bound by memory: 3930 pages of 32 KB in four pools take 155 us of the call's 180 (6.6 TB/s read and written).
 constexpr int kCopyPools = 256;  // pools of one launch
 constexpr int kCopyChunk = 16384;  // bytes a block moves at a time
 
@@ -316,6 +357,8 @@ struct CopyParams {
     uint8_t *pools[kCopyPools];
 };
 __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ CopyParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int n = p.count ? min(max(*p.count, 0), p.n) : p.n;
     const long long per_pair = (long long)p.n_pools * p.chunks, units = n * per_pair;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -344,24 +387,29 @@ int blocks_for(long long work, int waves) {
     const long long want = (work + 255) / 256, most = (long long)sms * waves;
     return (int)(want < 1 ? 1 : (want < most ? want : most));
 }
-// CTAs of the scanning cluster: one for a pool that it passes over in a few steps.
-int scan_ctas(int num_pages) { return num_pages <= 2 * kScanTile ? 1 : kScanCtas; }
+// CTAs of the scanning cluster: one where it passes over the pool, and what else it reads and writes, in a few steps.
+int scan_ctas(long long items) { return items <= 2 * kScanTile ? 1 : kScanCtas; }
+// Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
+// us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
+// anew, 49.6 / 30.7.
+constexpr long long kClusterItems = 1 << 15;
 
+// A kernel that is one cluster of `ctas` CTAs.
 template <class K, class A>
-cudaError_t launch_scan(K kernel, A &p, bool dependent, cudaStream_t stream) {
+cudaError_t launch_scan(K kernel, const A &p, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kScanThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.ctas;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -372,9 +420,9 @@ size_t ints(size_t n) { return (n * sizeof(int32_t) + 15) & ~size_t(15); }
 cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream) {
     const ForkParams p{a.page_table, a.ctx_lens, a.parents, a.ref_counts, a.page_table_out, a.ctx_lens_out,
                        a.ref_counts_out, a.B, a.B_out, a.max_pages, a.num_pages};
-    const long long out = (long long)a.B_out * a.max_pages, all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages;
-    pages_fork_kernel<<<blocks_for(out > a.num_pages ? out : a.num_pages, 8), 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const long long all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages, items = all > a.num_pages ? all : a.num_pages;
+    if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(items), stream);
+    const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(pages_fork_count_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
 }
@@ -399,30 +447,33 @@ cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
     p.copy_table = a.page_table_out != a.page_table;
     p.copy_ref = a.ref_counts_out != a.ref_counts;
     p.copy_frozen = !p.copy_ref;
-    p.frozen = p.copy_frozen ? reinterpret_cast<int32_t *>(ws + ints(a.num_pages)) : const_cast<int32_t *>(a.ref_counts);
+    p.frozen = reinterpret_cast<int32_t *>(ws + ints(a.num_pages));
     p.parts = reinterpret_cast<int32_t *>(ws + 2 * ints(a.num_pages));
     p.B = a.B;
     p.W = a.max_pages;
     p.P = a.num_pages;
-    p.ctas = scan_ctas(a.num_pages);
-    const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0;
-    pages_reserve_copy_kernel<<<blocks_for(cells > a.num_pages ? cells : a.num_pages, 8), 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_scan(pages_reserve_kernel, p, true, stream);
+    const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0, items = cells > a.num_pages ? cells : a.num_pages;
+    p.ctas = scan_ctas(items);
+    p.copied = items > kClusterItems;
+    if (p.copied) {
+        const cudaError_t e = launch_dependent(pages_reserve_copy_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_scan(pages_reserve_kernel, p, p.ctas, stream);
 }
 
 size_t pages_compact_workspace_bytes(int num_pages) {
     return num_pages <= 0 ? 0 : ints(num_pages) + ints(2 * kScanCtas);
 }
 cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream) {
-    CompactParams p{a.page_table, a.ref_counts, a.page_table_out, a.ref_counts_out, a.src, a.dst, a.count,
-                    static_cast<int32_t *>(a.workspace),
-                    reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + ints(a.num_pages)),
-                    a.B, a.max_pages, a.num_pages, scan_ctas(a.num_pages)};
-    const cudaError_t e = launch_scan(pages_compact_kernel, p, false, stream);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(pages_compact_table_kernel, dim3(blocks_for((long long)a.B * a.max_pages, 8)), 256, 0, stream, p);
+    const long long cells = (long long)a.B * a.max_pages, items = cells > a.num_pages ? cells : a.num_pages;
+    const CompactParams p{a.page_table, a.ref_counts, a.page_table_out, a.ref_counts_out, a.src, a.dst, a.count,
+                          static_cast<int32_t *>(a.workspace),
+                          reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + ints(a.num_pages)),
+                          a.B, a.max_pages, a.num_pages, scan_ctas(items), cells <= kClusterItems};
+    const cudaError_t e = launch_scan(pages_compact_kernel, p, p.ctas, stream);
+    if (e != cudaSuccess || p.rename) return e;
+    return launch_dependent(pages_compact_table_kernel, dim3(blocks_for(cells, 8)), 256, 0, stream, p);
 }
 
 cudaError_t launch_pages_copy(void *const *pools, int n_pools, size_t page_bytes, const int32_t *src, const int32_t *dst,
@@ -442,8 +493,7 @@ cudaError_t launch_pages_copy(void *const *pools, int n_pools, size_t page_bytes
         p.chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
         for (int i = 0; i < kCopyPools; ++i) p.pools[i] = i < p.n_pools ? static_cast<uint8_t *>(pools[first + i]) : nullptr;
         const long long units = (long long)n * p.n_pools * p.chunks, most = (long long)sms * 8;
-        pages_copy_kernel<<<(unsigned)(units < most ? units : most), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
+        e = launch_dependent(pages_copy_kernel, dim3((unsigned)(units < most ? units : most)), 256, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

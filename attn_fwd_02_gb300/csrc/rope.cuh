@@ -43,12 +43,12 @@ __device__ __forceinline__ int axis_row(const RopeAxes &x, const AxisRows &r, in
     const int a = (int)(x.pair_axis[pair >> 5] >> (2 * (pair & 31))) & 3;
     return a < 2 ? (a == 0 ? r.row[0] : r.row[1]) : (a == 2 ? r.row[2] : r.row[3]);
 }
-// Threads i, i + n, ... gather a token's rope values (cosines of the pairs, then sines).
+// Threads i, i + n, ... gather a token's rope values (cosines of the pairs, then sines, times `sign`).
 __device__ __forceinline__ void gather_angles(float *to, const float *cos_sin, const RopeAxes &x, const AxisRows &r,
-                                              int rope, int i, int n) {
+                                              int rope, int i, int n, float sign = 1.f) {
     for (; i < rope; i += n) {
         const int pair = i < rope / 2 ? i : i - rope / 2;
-        to[i] = cos_sin[(size_t)axis_row(x, r, pair) * rope + i];
+        to[i] = cos_sin[(size_t)axis_row(x, r, pair) * rope + i] * (i < rope / 2 ? 1.f : sign);
     }
 }
 

@@ -7,14 +7,18 @@
 //
 // Memory-bound: every element is read and written once.  A block takes kTokens tokens of one sequence, gathers their
 // angles into shared memory, and turns the rows of all heads, 16 elements (8 pairs) a thread at a time, held in registers,
-// so that a view may be turned in place.
+// so that a view may be turned in place.  What counts is how much of its life a block has loads in flight: its first rows are
+// read before the angles are there, and blocks are small.  Measured, 8 x 1024 tokens, 16 + 16 heads of 80, forward / 2 x 16384
+// tokens, 32 + 8 heads of 128, gradients into strided views: one token and 64 threads a block 18.7 / 106 us (6.3 TB/s); four
+// tokens and 256 threads 19.4 / 111, and without the early reads 20.2 / 110; two rows in flight a thread 20.9 / 115, four
+// 24.9 / 135.
 #include "rope.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokens = 4;
+constexpr int kThreads = 64;
+constexpr int kTokens = 1;
 
 struct RopeOnlyParams {
     const uint4 *q, *k;
@@ -30,57 +34,68 @@ template <bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeOnlyParams p) {
     __shared__ __align__(16) float angles[kTokens][kMaxRope];
     __shared__ int inside[kTokens];
+    griddep_launch_dependents();
+    griddep_wait();
     const int b = (int)(blockIdx.x / (unsigned)p.blocks), t0 = (int)(blockIdx.x % (unsigned)p.blocks) * kTokens;
     const int tokens = min(kTokens, p.N - t0);
-    for (int t = threadIdx.x >> 6; t < tokens; t += kThreads / 64) {
-        const AxisRows rows = axis_rows(p.axes, b, t0 + t, p.max_pos);
-        if (rows.ok) gather_angles(angles[t], p.cos_sin, p.axes, rows, p.rope, threadIdx.x & 63, 64);
-        if ((threadIdx.x & 63) == 0) inside[t] = rows.ok;
+    const int ipr = p.d / 16, rot = p.rope / 16, half = p.rope / 2, heads = p.H + p.Hkv;
+    // Thread = (item i of a row, first row): two vectors of 8, the two halves of 8 pairs, or neighbours where nothing turns or
+    // the pairs are neighbours themselves.  Its rows are every per_pass-th of the tokens' heads, each read one ahead of its use,
+    // the first one before the angles.
+    const int per_pass = kThreads / ipr, i = threadIdx.x % ipr, r0 = threadIdx.x / ipr;
+    const bool turns = i < rot;
+    const int w0 = turns && !INTER ? i : 2 * i, w1 = turns && !INTER ? i + rot : 2 * i + 1;
+    const int t_step = per_pass / heads, h_step = per_pass % heads;
+    const uint4 *q = p.q + b * p.qs[0] + t0 * p.qs[2], *k = p.k + b * p.ks[0] + t0 * p.ks[2];
+    int t = r0 < per_pass ? r0 / heads : tokens, h = r0 % heads;
+    uint4 xv, yv;
+    auto fetch = [&] {
+        if (t >= tokens) return;
+        const uint4 *src = h >= p.H ? k + (h - p.H) * p.ks[1] + t * p.ks[2] : q + h * p.qs[1] + t * p.qs[2];
+        xv = src[w0];
+        yv = src[w1];
+    };
+    fetch();
+    for (int a = threadIdx.x >> 6; a < tokens; a += kThreads / 64) {
+        const AxisRows rows = axis_rows(p.axes, b, t0 + a, p.max_pos);
+        if (rows.ok) gather_angles(angles[a], p.cos_sin, p.axes, rows, p.rope, threadIdx.x & 63, 64, p.sign);
+        if ((threadIdx.x & 63) == 0) inside[a] = rows.ok;
     }
     __syncthreads();
-    const int ipr = p.d / 16, rot = p.rope / 16, half = p.rope / 2;
-    const int per_token = (p.H + p.Hkv) * ipr;
-    for (int e = threadIdx.x; e < tokens * per_token; e += kThreads) {
-        const int i = e % ipr, row = e / ipr % (p.H + p.Hkv), t = e / per_token;
-        const bool is_k = row >= p.H, turns = i < rot;
-        const int h = is_k ? row - p.H : row;
-        const long long *si = is_k ? p.ks : p.qs, *so = is_k ? p.ko : p.qo;
-        const uint4 *src = (is_k ? p.k : p.q) + b * si[0] + h * si[1] + (t0 + t) * si[2];
-        uint4 *dst = (is_k ? p.k_out : p.q_out) + b * so[0] + h * so[1] + (t0 + t) * so[2];
-        const int w0 = turns && !INTER ? i : 2 * i, w1 = turns && !INTER ? i + rot : 2 * i + 1;
-        uint4 xv = src[w0], yv = src[w1];
-        if (!inside[t]) {
-            xv = yv = make_uint4(0u, 0u, 0u, 0u);
+    uint4 *qo = p.q_out + b * p.qo[0] + t0 * p.qo[2], *ko = p.k_out + b * p.ko[0] + t0 * p.ko[2];
+    while (t < tokens) {
+        const int now = t;
+        uint4 *dst = h >= p.H ? ko + (h - p.H) * p.ko[1] + t * p.ko[2] : qo + h * p.qo[1] + t * p.qo[2];
+        uint4 xn = xv, yn = yv;
+        t += t_step;
+        h += h_step;
+        if (h >= heads) h -= heads, ++t;
+        fetch();
+        if (!inside[now]) {
+            xn = yn = make_uint4(0u, 0u, 0u, 0u);
         } else if (turns) {
+            const float *c = angles[now] + 8 * i;
+            const uint64_t *c2 = reinterpret_cast<const uint64_t *>(c), *s2 = reinterpret_cast<const uint64_t *>(c + half);
             float x[8], y[8];
-            unpack8(xv, x);
-            unpack8(yv, y);
-            const float *c = angles[t] + 8 * i, *s = c + half;
-            if constexpr (INTER) {
+            unpack8(xn, x);
+            unpack8(yn, y);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float s0 = p.sign * s[n], s1 = p.sign * s[4 + n];
-                    const float u = x[2 * n] * c[n] - x[2 * n + 1] * s0;
-                    x[2 * n + 1] = x[2 * n + 1] * c[n] + x[2 * n] * s0;
-                    x[2 * n] = u;
-                    const float v = y[2 * n] * c[4 + n] - y[2 * n + 1] * s1;
-                    y[2 * n + 1] = y[2 * n + 1] * c[4 + n] + y[2 * n] * s1;
-                    y[2 * n] = v;
-                }
-            } else {
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float sn = p.sign * s[n];
-                    const float u = x[n] * c[n] - y[n] * sn;
-                    y[n] = y[n] * c[n] + x[n] * sn;
-                    x[n] = u;
-                }
+            for (int m = 0; m < 4; ++m) {  // pairs 2m, 2m + 1 of the item: (a, e) of each
+                float (&z)[8] = INTER && m >= 2 ? y : x;
+                const int at = INTER ? 4 * (m & 1) : 2 * m;
+                float &a0 = z[at], &a1 = z[INTER ? at + 2 : at + 1];
+                float &e0 = INTER ? z[at + 1] : y[at], &e1 = INTER ? z[at + 3] : y[at + 1];
+                const uint64_t a = f32x2_pack(a0, a1), e = f32x2_pack(e0, e1);
+                const uint64_t minus = s2[m] ^ 0x8000000080000000ull;
+                // (rounded as the appends round it)
+                f32x2_unpack(f32x2_fma(a, c2[m], f32x2_mul(e, minus)), a0, a1);
+                f32x2_unpack(f32x2_fma(e, c2[m], f32x2_mul(a, s2[m])), e0, e1);
             }
-            xv = pack8(x);
-            yv = pack8(y);
+            xn = pack8(x);
+            yn = pack8(y);
         }
-        dst[w0] = xv;
-        dst[w1] = yv;
+        dst[w0] = xn;
+        dst[w1] = yn;
     }
 }
 
@@ -108,10 +123,9 @@ cudaError_t launch_rope_axes(const RopeArgs &a, cudaStream_t stream) {
     p.blocks = (a.N + kTokens - 1) / kTokens;
     p.sign = a.back ? -1.f : 1.f;
     p.axes = a.axes;
-    const unsigned grid = (unsigned)((long long)a.B * p.blocks);
-    if (a.interleaved) rope_axes_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-    else rope_axes_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)((long long)a.B * p.blocks));
+    return a.interleaved ? launch_dependent(rope_axes_kernel<true>, grid, kThreads, 0, stream, p)
+                         : launch_dependent(rope_axes_kernel<false>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace attn
