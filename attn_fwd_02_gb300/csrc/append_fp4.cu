@@ -6,11 +6,11 @@
 // thread takes 16 dims of a row, one block of the cache's scales; for a key it reads the 16 dims that they turn with as
 // well (from L1 the second time), so that the block's maximum needs no exchange between threads.
 //
-// The append is bound by its instructions as much as by memory: about 2260 a warp for a token of 32 + 8 heads of 128, the
-// queries' rotation, the keys' and values' quotients (one fused correction each instead of a division: 21 -> 19 us) in about
-// equal parts.  Measured: up to 1024 new tokens of 8 sequences, ragged, 19 us, and their pages as bf16 11 us; the two calls
-// 29.7 us, of which the second starts while the first drains.  64 threads a block 30.7, 256 31.6; the rows' vectors read one
-// row ahead 34.8 (more registers).  One token of 4 sequences: 6.0 us for the two calls, which is the host's time.
+// Neither memory nor the pipes are full (a fifth and a third to a half of the time): the chain position, angles, rows is what a
+// block waits for, so as many blocks as the registers allow count most.  Measured, up to 1024 new tokens of 8 sequences, ragged, 32
+// + 8 heads of 128, and their pages as bf16 (two calls, of which the second starts while the first drains): 6 / 8 / 10 / 12 blocks
+// an SM 29.8 / 28.3 / 27.8 / 29.0 us; 64 threads a block 30.7, 256 31.6; the rows' vectors read one row ahead 34.8 (more registers);
+// a division for each quotient 38.  One token of 4 sequences: 6.0 us for the two calls, which is the host's time.
 #include "fp4.cuh"
 #include "rope.cuh"
 
@@ -32,8 +32,8 @@ struct Fp4AppendParams {
 };
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4AppendParams p) {
-    __shared__ float angles[2][kMaxRope];
+__global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4AppendParams p) {
+    __shared__ __align__(16) float angles[2][kMaxRope];
     griddep_launch_dependents();
     griddep_wait();
     const int b = (int)(blockIdx.x / (unsigned)p.pairs);
@@ -94,10 +94,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
             const bool first = 8 * w < half;
             float y[8];
             unpack8(row[first ? w + half / 8 : w - half / 8], y);
-            const float *c = cs + (first ? 8 * w : 8 * w - half), *s = c + half;
-            const float sign = first ? -1.f : 1.f;
+            const float *c = cs + (first ? 8 * w : 8 * w - half);
+            const uint64_t *c2 = reinterpret_cast<const uint64_t *>(c), *s2 = reinterpret_cast<const uint64_t *>(c + half);
+            const uint64_t minus = first ? 0x8000000080000000ull : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + y[i] * (sign * s[i]);
+            for (int i = 0; i < 4; ++i)
+                f32x2_unpack(f32x2_fma(f32x2_pack(x[2 * i], x[2 * i + 1]), c2[i], f32x2_mul(f32x2_pack(y[2 * i], y[2 * i + 1]), s2[i] ^ minus)),
+                             x[2 * i], x[2 * i + 1]);
         }
     };
     for (int row = r0; row < rows; row += per_pass) {
@@ -112,13 +115,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[8 * w + i] = __fmul_rn(x[i], p.k_inv);
             }
-            const uint32_t s = fp4_scale_code(u);
-            fp4_quotients(u, e4m3_to_float(s));
+            const uint32_t s = fp4_quotients(u), keep = s ? ~0u : 0u;
             float lo[8], hi[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) lo[i] = u[i], hi[i] = u[8 + i];
             kd[fp4_k_scale(p.d, slot + e, j)] = (uint8_t)s;
-            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo), f32x8_to_e2m1x8(hi));
+            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo) & keep, f32x8_to_e2m1x8(hi) & keep);
         } else if (row < kv_rows) {
             const int h = row - k_rows;
             const uint4 *v = p.v + b * p.vs[0] + h * p.vs[1] + 2 * j;
@@ -127,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
             uint4 old = make_uint4(0u, 0u, 0u, 0u);  // the codes of a token that is not there stay
             if (tokens == 1) old = *at;
             float u[2][16];
+            uint32_t nonzero = ~0u;  // the nibbles of the tokens whose block has a scale
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
@@ -139,8 +142,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t s = fp4_scale_code(u[e]);
-                fp4_quotients(u[e], e4m3_to_float(s));
+                const uint32_t s = fp4_quotients(u[e]);
+                if (!s) nonzero &= e == 0 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
                 if (have[e]) vd[fp4_v_scale(p.d, slot + e, j)] = (uint8_t)s;
             }
             // byte x of the block: dim x of both tokens
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
                 float y[8];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) y[2 * n] = u[0][4 * i + n], y[2 * n + 1] = u[1][4 * i + n];
-                bytes[i] = f32x8_to_e2m1x8(y);
+                bytes[i] = f32x8_to_e2m1x8(y) & nonzero;
             }
             if (tokens == 1) {
                 const uint32_t keep = e0 == 0 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
@@ -176,12 +179,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_fp4_kernel(const Fp4Append
                 unpack8(q[w0], x);
                 unpack8(q[w1], y);
                 if (halves) {
-                    const float *c = angles[e] + 8 * j, *s = c + half;
+                    const float *c = angles[e] + 8 * j;
+                    const uint64_t *c2 = reinterpret_cast<const uint64_t *>(c), *s2 = reinterpret_cast<const uint64_t *>(c + half);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u = x[i] * c[i] - y[i] * s[i];
-                        y[i] = y[i] * c[i] + x[i] * s[i];
-                        x[i] = u;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t a = f32x2_pack(x[2 * i], x[2 * i + 1]), o = f32x2_pack(y[2 * i], y[2 * i + 1]);
+                        f32x2_unpack(f32x2_fma(a, c2[i], f32x2_mul(o, s2[i] ^ 0x8000000080000000ull)), x[2 * i], x[2 * i + 1]);
+                        f32x2_unpack(f32x2_fma(o, c2[i], f32x2_mul(a, s2[i])), y[2 * i], y[2 * i + 1]);
                     }
                 }
             }

@@ -131,6 +131,7 @@ __device__ __forceinline__ bool first_segment(const RowsParams &a, Segment &s, l
     const int lane = threadIdx.x & 31, R = a.Hkv * a.rgroups;
     const int per = (a.B + 31) / 32, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
     long long mine = 0;
+#pragma unroll 8
     for (int b = b0; b < b1; ++b) mine += cost_of(seen_pages(a, b));
     long long upto = mine;
 #pragma unroll

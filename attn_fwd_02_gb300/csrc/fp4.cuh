@@ -70,25 +70,35 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t code) {
     return f;
 }
 
-// The scale of a block of 16 values u (already times 1 / the tensor's scale): s = e4m3(max |u| / 6), nearest and at most 448, with
-// 1/6 as an fp32 factor; its code.
-__device__ __forceinline__ uint32_t fp4_scale_code(const float (&u)[16]) {
+// A block of 16 values u (already times 1 / the tensor's scale), in place of which it leaves the quotients by the block's scale
+// s = e4m3(max |u| / 6), nearest and at most 448, with 1/6 as an fp32 factor; returns the scale's code.
+//
+// The quotients are correctly rounded, so that a code is a function of the definition alone: with r the nearest to 1 / s, q = u r
+// and the remainder u - q s (exact by fused multiply-add), q + remainder * r is the nearest to u / s (Markstein's theorem, IBM J.
+// Res. Dev. 34 (1990)), two at a time in packed arithmetic.  Values past 2^100 times the tensor's scale, all of whose quotients
+// are far above the largest code or lost below it, are cut to that first.  Of a block with scale 0 the quotients are any; its
+// codes are to be 0.
+__device__ __forceinline__ uint32_t fp4_quotients(float (&u)[16]) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(fabsf(u[i]), fabsf(u[i + 1])));
-    return __nv_cvt_float_to_fp8(__fmul_rn(m, 0.16666667163372039794921875f), __NV_SATFINITE, __NV_E4M3);
-}
-// u / s in place, correctly rounded, or 0 where s is 0: a code is then a function of the definition alone.  With r the nearest to
-// 1 / s, q = u r and the remainder u - q s (exact by fused multiply-add), q + remainder * r is the nearest to u / s (Markstein's
-// theorem, IBM J. Res. Dev. 34 (1990)); quotients past 2^100 are cut there, far above the largest code.
-__device__ __forceinline__ void fp4_quotients(float (&u)[16], float s) {
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    constexpr float kMost = 1.2676506e30f;  // 2^100
+    if (m > kMost) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float q = fminf(fmaxf(u[i] * r, -1.2676506e30f), 1.2676506e30f);
-        const float y = fmaf(fmaf(-q, s, u[i]), r, q);
-        u[i] = s > 0.f ? copysignf(y, u[i]) : 0.f;  // (-0 stays -0)
+        for (int i = 0; i < 16; ++i) u[i] = fminf(fmaxf(u[i], -kMost), kMost);
     }
+    const uint32_t code = __nv_cvt_float_to_fp8(__fmul_rn(m, 0.16666667163372039794921875f), __NV_SATFINITE, __NV_E4M3);
+    const float s = e4m3_to_float(code), r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const uint64_t r2 = f32x2_pack(r, r), s2 = f32x2_pack(-s, -s);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const uint64_t x = f32x2_pack(u[i], u[i + 1]), q = f32x2_mul(x, r2);
+        float y0, y1;
+        f32x2_unpack(f32x2_fma(f32x2_fma(q, s2, x), r2, q), y0, y1);
+        u[i] = copysignf(y0, u[i]);  // (-0 stays -0)
+        u[i + 1] = copysignf(y1, u[i + 1]);
+    }
+    return code;
 }
 
 }  // namespace attn

@@ -387,8 +387,12 @@ int blocks_for(long long work, int waves) {
     const long long want = (work + 255) / 256, most = (long long)sms * waves;
     return (int)(want < 1 ? 1 : (want < most ? want : most));
 }
-// CTAs of the scanning cluster: one where it passes over the pool, and what else it reads and writes, in a few steps.
-int scan_ctas(long long items) { return items <= 2 * kScanTile ? 1 : kScanCtas; }
+// CTAs of the scanning cluster: one where it passes over the pool, and what else it reads and writes, in a few steps, or where
+// the device (a part of a GPU) cannot place more.
+template <class K>
+int scan_ctas(K kernel, long long items) {
+    return items <= 2 * kScanTile || !cluster_fits(reinterpret_cast<const void *>(kernel), kScanCtas, kScanThreads, 0) ? 1 : kScanCtas;
+}
 // Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
 // us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
 // anew, 49.6 / 30.7.
@@ -421,7 +425,7 @@ cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream) {
     const ForkParams p{a.page_table, a.ctx_lens, a.parents, a.ref_counts, a.page_table_out, a.ctx_lens_out,
                        a.ref_counts_out, a.B, a.B_out, a.max_pages, a.num_pages};
     const long long all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages, items = all > a.num_pages ? all : a.num_pages;
-    if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(items), stream);
+    if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(pages_fork_cluster_kernel, items), stream);
     const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(pages_fork_count_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
@@ -453,7 +457,7 @@ cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
     p.W = a.max_pages;
     p.P = a.num_pages;
     const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0, items = cells > a.num_pages ? cells : a.num_pages;
-    p.ctas = scan_ctas(items);
+    p.ctas = scan_ctas(pages_reserve_kernel, items);
     p.copied = items > kClusterItems;
     if (p.copied) {
         const cudaError_t e = launch_dependent(pages_reserve_copy_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
@@ -470,7 +474,7 @@ cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream) {
     const CompactParams p{a.page_table, a.ref_counts, a.page_table_out, a.ref_counts_out, a.src, a.dst, a.count,
                           static_cast<int32_t *>(a.workspace),
                           reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + ints(a.num_pages)),
-                          a.B, a.max_pages, a.num_pages, scan_ctas(items), cells <= kClusterItems};
+                          a.B, a.max_pages, a.num_pages, scan_ctas(pages_compact_kernel, items), cells <= kClusterItems};
     const cudaError_t e = launch_scan(pages_compact_kernel, p, p.ctas, stream);
     if (e != cudaSuccess || p.rename) return e;
     return launch_dependent(pages_compact_table_kernel, dim3(blocks_for(cells, 8)), 256, 0, stream, p);

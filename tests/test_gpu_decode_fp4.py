@@ -99,6 +99,27 @@ def test_unmapped_pages_and_odd_intervals(lib, spare):
     R.check(out[0].cpu(), torch.where(torch.isinf(w[1]), out[1].cpu().double(), w[1] + off - off.clamp(-most, most)), *w)
 
 
+@pytest.mark.parametrize("spare", **FORMS)
+@pytest.mark.parametrize("d", [32, 64, 80, 96, 128])
+def test_a_window_alone(lib, d, spare):
+    ctx, window = [700, 16, 1, 2049, 33], [100, 16, 5, 1, 2]
+    begin = [c - w for c, w in zip(ctx, window)]
+    x = make(5, 6, 2, d, ctx, 11, begin, spare)
+    out = run(lib, x, key_begin=torch.tensor(begin, dtype=torch.int32))
+    R.check(out[0].cpu(), out[1].cpu(), *want(x, d ** -0.5, 0.0, None, begin))
+
+
+def test_large_batches_of_uneven_lengths(lib):
+    # more sequences than a share's search takes in one go, most of them empty or a few tokens long, one of them long
+    for B, H, Hkv, d in ((1500, 2, 1, 32), (700, 24, 2, 64)):
+        g = torch.Generator().manual_seed(B)
+        ctx = (torch.rand(B, generator=g) ** 6 * 60).int().tolist()
+        ctx[B // 3] = 5000
+        x = make(B, H, Hkv, d, ctx, 12)
+        out = run(lib, x)
+        R.check(out[0].cpu(), out[1].cpu(), *want(x, d ** -0.5))
+
+
 def test_huge_and_nan_queries(lib):
     x = list(make(3, 4, 2, 64, [40, 90, 33], 7))
     x[0] = (x[0].float() * 2.0 ** 20).to(torch.bfloat16)
