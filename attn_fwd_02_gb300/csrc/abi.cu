@@ -779,6 +779,8 @@ int pages_sizes(int B, int max_pages, int num_pages, int page_size) {
     if (B <= 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
     if (page_size != 16) return ATTN_ERR_UNSUPPORTED;
     if ((uint64_t)max_pages * 16 > (1ull << 30)) return ATTN_ERR_INVALID_ARG;
+    // the kernels' sums over a table's entries and over the pool are 32 bits wide
+    if ((uint64_t)B * (uint64_t)max_pages > (1ull << 30) || num_pages > (1 << 30)) return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }
 }  // namespace
@@ -791,7 +793,7 @@ ATTN_API int paged_kv_fork(const int32_t *page_table, const int32_t *ctx_lens, c
         return ATTN_ERR_INVALID_ARG;
     int st = pages_sizes(B, max_pages_per_seq, num_pages, page_size);
     if (st != ATTN_OK) return st;
-    if (B_out <= 0 || page_table_out == page_table || ctx_lens_out == ctx_lens || ctx_lens_out == parents)
+    if (B_out <= 0 || (uint64_t)B_out * (uint64_t)max_pages_per_seq > (1ull << 30) || page_table_out == page_table || ctx_lens_out == ctx_lens || ctx_lens_out == parents)
         return ATTN_ERR_INVALID_ARG;
     if (!aligned4(page_table) || !aligned4(ctx_lens) || !aligned4(parents) || !aligned4(ref_counts) ||
         !aligned4(page_table_out) || !aligned4(ctx_lens_out) || !aligned4(ref_counts_out))
@@ -1014,7 +1016,8 @@ ATTN_API int paged_attn_decode_fp4(const void *q, const void *k_pages, const voi
     a.softcap = softcap;
     a.slopes = alibi_slopes;
     a.key_begin = key_begin;
-    if (!fp4_scale(k_scale) || !fp4_scale(v_scale)) return ATTN_ERR_INVALID_ARG;
+    // (their product is what a score's products are multiplied by: of 0, unseen scores of -inf would come to NaN)
+    if (!fp4_scale(k_scale) || !fp4_scale(v_scale) || !fp4_scale(scale * k_scale)) return ATTN_ERR_INVALID_ARG;
     return decode_scoremod(a, workspace_bytes, stream, true);
 }
 

@@ -413,6 +413,7 @@ int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_pages, voi
  * paged_attn_decode_fp4: paged_attn_decode_scoremod over such a cache (softcap 0, alibi_slopes and key_begin NULL: the plain
  *   decode).  The codes are widened exactly to f16, both products run in f16 with fp32 accumulation (each query rounded to
  *   f16 after a power of two of its own, the weights to f16).  Slots that a query does not see may hold anything.
+ *   scale * k_scale lies in [1e-37, 1e37] too.
  *   workspace: at least paged_attn_decode_fp4_workspace_size(...) bytes.
  */
 size_t paged_attn_decode_fp4_workspace_size(int B, int H, int Hkv, int d, int max_pages_per_seq, int page_size);
@@ -483,6 +484,7 @@ int attn_rope_axes_bwd(const void *dq, const int64_t *dq_strides, const void *dk
  *   page_table [B, max_pages_per_seq], ctx_lens [B] int32 as everywhere; entries outside [0, num_pages) (-1) name no page
  *   ref_counts [num_pages] int32: how many entries of the table name each page (a caller may add its own).  A page is free
  *              iff its count is not positive.
+ * A table has at most 2^30 entries, a pool at most 2^30 pages.
  * Which page goes where follows from the order of rows and page numbers alone.  Outputs must not overlap inputs but where it
  * says that an output may be its input.
  *

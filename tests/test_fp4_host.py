@@ -135,3 +135,11 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         b.paged_kv_unpack_fp4(pages, pages, S, S, i)
     with pytest.raises(TypeError):
         b.paged_kv_unpack_fp4(pages.float(), pages, S, S, i)
+
+
+@pytest.mark.parametrize("scale, k_scale", [(1e-10, 1e-30), (1e-30, 1e-20), (1e20, 1e30), (1e30, 1e9)])
+def test_decode_refuses_scales_whose_product_leaves_fp32(lib, scale, k_scale):
+    # a product of 0 or infinity would meet unseen scores of -infinity as NaN
+    for slopes in (None, A):
+        assert lib.paged_attn_decode_fp4(A, A, A, k_scale, S, A, A, 16, A, None, 2, 4, 2, 64, 8, 9, scale, 0.0, slopes, None, A,
+                                         1 << 30, None) == 1

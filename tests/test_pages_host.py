@@ -76,3 +76,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_pools():
             call()
     with pytest.raises(TypeError):
         b.paged_kv_fork(t.float(), i, i, i)
+
+
+@pytest.mark.parametrize("B, W, P", [(1 << 20, 1 << 11, 9), (64, 1 << 26, 9), (2, 4, (1 << 30) + 1), (2, 4, 2**31 - 1)])
+def test_tables_and_pools_past_32_bit_sums_are_refused(lib, B, W, P):
+    z = 1 << 62  # (a workspace's size is not what fails)
+    assert lib.paged_kv_fork(A, A, A, A, 2 * A, 2 * A, 2 * A, 16, B, 1, W, P, None) == 1
+    assert lib.paged_kv_reserve(A, A, A, A, A, A, A, A, A, 16, B, W, P, A, z, None) == 1
+    assert lib.paged_kv_compact(A, A, A, 2 * A, A, A, A, B, W, P, A, z, None) == 1
+    if P == 9:
+        assert lib.paged_kv_fork(A, A, A, A, 2 * A, 2 * A, 2 * A, 16, 1, B, W, P, None) == 1
