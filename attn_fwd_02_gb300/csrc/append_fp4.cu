@@ -211,7 +211,8 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t h2, float s, float scal
 }
 
 // One CTA a page's keys or values (blockIdx.y).  A thread takes 8 dims of two tokens that share the values' bytes, so that its
-// vectors of the output are neighbours of the next lanes'.
+// vectors of the output are neighbours of the next lanes', and reads kAtOnce such pieces before it writes the first.
+constexpr int kAtOnce = 4;
 template <int D>
 __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p) {
     constexpr int kVpr = D / 8, kPerHead = kVpr * 8;
@@ -223,36 +224,50 @@ __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p
     const float scale = value ? p.v_scale : p.k_scale;
     const uint8_t *pages = (value ? p.v_pages : p.k_pages) + (size_t)page * p.Hkv * (9 * D);
     uint4 *out = (value ? p.v_out : p.k_out) + (size_t)blockIdx.x * p.Hkv * kFp4PS * kVpr;
-    for (int e = threadIdx.x; e < p.Hkv * kPerHead; e += 256) {
-        const int w = e % kVpr, token = 2 * (e / kVpr % 8), h = e / kPerHead;  // vector w of tokens `token`, `token` + 1
-        const uint8_t *src = pages + (size_t)h * (9 * D);
-        uint4 *dst = out + ((size_t)h * kFp4PS + token) * kVpr + w;
-        uint32_t r[2][4], x[2][4];
-        float s[2];
-        if (value) {
-            const uint2 c = *reinterpret_cast<const uint2 *>(src + fp4_v_codes(token, w / 2) + (w & 1) * 8);
-            const uint32_t two = *reinterpret_cast<const uint16_t *>(src + fp4_v_scale(D, token, w / 2));
-            s[0] = e4m3_to_float(two);
-            s[1] = e4m3_to_float(two >> 8);
-            e2m1x8_to_f16x2x4(c.x, x[0]);  // dims 0 .. 3, a pair of tokens each
-            e2m1x8_to_f16x2x4(c.y, x[1]);
+    const int items = p.Hkv * kPerHead;
+    for (int e0 = threadIdx.x; e0 < items; e0 += 256 * kAtOnce) {
+        // vector w of tokens `token`, `token` + 1: the values' codes of both, or each token's of the keys; their two scales
+        uint32_t c[kAtOnce][2], s[kAtOnce][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = x[i >> 1][2 * (i & 1)], b = x[i >> 1][2 * (i & 1) + 1];
-                r[0][i] = __byte_perm(a, b, 0x5410);
-                r[1][i] = __byte_perm(a, b, 0x7632);
-            }
-        } else {
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int e = min(e0 + 256 * i, items - 1);
+            const int w = e % kVpr, token = 2 * (e / kVpr % 8), h = e / kPerHead;
+            const uint8_t *src = pages + (size_t)h * (9 * D);
+            if (value) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(src + fp4_v_codes(token, w / 2) + (w & 1) * 8);
+                const uint32_t two = *reinterpret_cast<const uint16_t *>(src + fp4_v_scale(D, token, w / 2));
+                c[i][0] = v.x, c[i][1] = v.y;
+                s[i][0] = two & 0xffu, s[i][1] = two >> 8;
+            } else {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                e2m1x8_to_f16x2x4(*reinterpret_cast<const uint32_t *>(src + fp4_k_codes(D, token + t, 0) + 4 * w), r[t]);
-                s[t] = e4m3_to_float(src[fp4_k_scale(D, token + t, w / 2)]);
+                for (int t = 0; t < 2; ++t) {
+                    c[i][t] = *reinterpret_cast<const uint32_t *>(src + fp4_k_codes(D, token + t, 0) + 4 * w);
+                    s[i][t] = src[fp4_k_scale(D, token + t, w / 2)];
+                }
             }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            dst[t * kVpr] = make_uint4(scaled_pair(r[t][0], s[t], scale), scaled_pair(r[t][1], s[t], scale),
-                                       scaled_pair(r[t][2], s[t], scale), scaled_pair(r[t][3], s[t], scale));
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int e = e0 + 256 * i;
+            if (e >= items) break;
+            const int w = e % kVpr, token = 2 * (e / kVpr % 8), h = e / kPerHead;
+            uint4 *dst = out + ((size_t)h * kFp4PS + token) * kVpr + w;
+            uint32_t r[2][4], x[2][4];
+            e2m1x8_to_f16x2x4(c[i][0], x[0]);
+            e2m1x8_to_f16x2x4(c[i][1], x[1]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {  // (values: dims 2n, 2n + 1, each with both tokens)
+                const uint32_t a = x[n >> 1][2 * (n & 1)], b = x[n >> 1][2 * (n & 1) + 1];
+                r[0][n] = value ? __byte_perm(a, b, 0x5410) : x[0][n];
+                r[1][n] = value ? __byte_perm(a, b, 0x7632) : x[1][n];
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float f = e4m3_to_float(s[i][t]);
+                dst[t * kVpr] = make_uint4(scaled_pair(r[t][0], f, scale), scaled_pair(r[t][1], f, scale),
+                                           scaled_pair(r[t][2], f, scale), scaled_pair(r[t][3], f, scale));
+            }
+        }
     }
 }
 

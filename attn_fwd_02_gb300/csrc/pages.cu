@@ -156,33 +156,54 @@ __device__ __forceinline__ void reserve_range(const ReserveParams &p, int b, int
     from = n / kPS;
     to = add > 0 && end <= p.W ? (int)end : 0;
 }
+// What waits on what: a row's lengths, its entries, their counts, the sums over the rows and over the pool, the free pages' ids.
+// A warp's first row and a thread's first counts are read before anything waits and stay in registers, and the sums over the first
+// kScanThreads rows in shared memory, so that nothing of an ordinary call is read twice.
 __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const ReserveParams p) {
     __shared__ int sums[33];
+    __shared__ int offsets[kScanThreads];  // of a tile of rows: where their free pages begin (-1: more than there are)
     const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first_warp = cta * 32 + warp, all_warps = p.ctas * 32;
     griddep_launch_dependents();
     griddep_wait();
-    if (!p.copied) reserve_copies(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
+    int begin, end, mine, total;
+    scan_part(p.P, cta, p.ctas, begin, end);
+    const int4 v0 = counts4(p.ref, begin + 4 * (int)threadIdx.x, end, 1);
     // an entry to be given a page: it has none, or shares it (by the counts at the call's start: the input's, which do not
     // change before the second barrier, and then its copy)
     const int32_t *counts = p.ref;
     auto lacks = [&](int e) { return !in_pool(e, p.P) || __ldcg(counts + e) > 1; };
+    // the first 32 entries of a row, one a lane: what they name, and which lack a page
+    struct Head {
+        int n, from, to, old;
+        bool lack;
+    };
+    auto head_of = [&](int b) {
+        Head r;
+        reserve_range(p, b, r.n, r.from, r.to);
+        r.old = r.from + lane < r.to ? p.table[(size_t)b * p.W + r.from + lane] : -1;
+        return r;
+    };
+    auto lack_of = [&](Head &r) { r.lack = r.from + lane < r.to && lacks(r.old); };
+    Head mine0{0, 0, 0, -1, false};
+    if (first_warp < p.B) mine0 = head_of(first_warp);
+    if (!p.copied) reserve_copies(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
+    if (first_warp < p.B) lack_of(mine0);
+    mine = (v0.x <= 0) + (v0.y <= 0) + (v0.z <= 0) + (v0.w <= 0);
+    for (int i = begin + kScanTile + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
+        const int4 v = counts4(p.ref, i, end, 1);
+        mine += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
+    }
     for (int b = first_warp; b < p.B; b += all_warps) {
-        int n, from, to, need = 0;
-        reserve_range(p, b, n, from, to);
-        for (int c0 = from; c0 < to; c0 += 32) {
-            const bool lack = c0 + lane < to && lacks(p.table[(size_t)b * p.W + c0 + lane]);
+        Head r = mine0;
+        if (b != first_warp) r = head_of(b), lack_of(r);
+        int need = __popc(__ballot_sync(0xffffffffu, r.lack));
+        for (int c0 = r.from + 32; c0 < r.to; c0 += 32) {
+            const bool lack = c0 + lane < r.to && lacks(p.table[(size_t)b * p.W + c0 + lane]);
             need += __popc(__ballot_sync(0xffffffffu, lack));
         }
         if (lane == 0) p.need[b] = need;
     }
-    int begin, end, mine = 0;
-    scan_part(p.P, cta, p.ctas, begin, end);
-    for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
-        const int4 v = counts4(p.ref, i, end, 1);
-        mine += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
-    }
-    int total;
     block_scan(mine, sums, total);
     if (threadIdx.x == 0) p.parts[cta] = total;
     cluster_sync();
@@ -192,10 +213,19 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
         before += i < cta ? v : 0;
         free_pages += v;
     }
-    // the rows' offsets into the free pages: every CTA sums them all, and keeps those of its own rows in `need`'s place
-    // after the barrier; the pages that are wanted at all end at `wanted`
-    long long wanted = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+    // a tile of rows' offsets into the free pages; returns what they need together
+    auto row_offsets = [&](int b0, long long base) {
+        const int b = b0 + (int)threadIdx.x;
+        const int need = b < p.B ? __ldcg(p.need + b) : 0;
+        int sum;
+        const long long off = base + block_scan(need, sums, sum);
+        offsets[threadIdx.x] = need == 0 ? 0 : (off + need <= free_pages ? (int)off : -1);
+        return sum;
+    };
+    // the free pages that are wanted at all, listed in order, each CTA those of its part
+    const long long base1 = row_offsets(0, 0);  // (every CTA: of all rows)
+    long long wanted = base1;
+    for (int b0 = kScanThreads; b0 < p.B; b0 += kScanThreads) {
         const int b = b0 + (int)threadIdx.x;
         int sum;
         block_scan(b < p.B ? __ldcg(p.need + b) : 0, sums, sum);
@@ -204,7 +234,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     const int last = (int)min(wanted, (long long)free_pages);
     for (int i0 = begin; i0 < end && before < last; i0 += kScanTile) {
         const int i = i0 + 4 * (int)threadIdx.x;
-        const int4 v = counts4(p.ref, i, end, 1);
+        const int4 v = i0 == begin ? v0 : counts4(p.ref, i, end, 1);
         const bool f[4] = {v.x <= 0, v.y <= 0, v.z <= 0, v.w <= 0};
         int at = before + block_scan(f[0] + f[1] + f[2] + f[3], sums, total);
         before += total;
@@ -214,37 +244,38 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     }
     cluster_sync();
     if (p.copy_frozen) counts = p.frozen;
-    // rows, a tile of kScanThreads at a time: their offsets in shared memory, then a warp for each
-    __shared__ int offsets[kScanThreads];
+    // rows, a tile of kScanThreads at a time, a warp each
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
-        const int bt = b0 + (int)threadIdx.x;
-        int sum;
-        const int need_t = bt < p.B ? __ldcg(p.need + bt) : 0;
-        const int at_t = block_scan(need_t, sums, sum);
-        const long long off = base + at_t;
-        offsets[threadIdx.x] = need_t == 0 ? 0 : (off + need_t <= free_pages ? (int)off : -1);
-        base += sum;
-        __syncthreads();
-        for (int b = b0 + ((first_warp - b0 % all_warps) % all_warps + all_warps) % all_warps; b < min(b0 + kScanThreads, p.B);
-             b += all_warps) {
-            int n, from, to;
-            reserve_range(p, b, n, from, to);
-            const int off_b = offsets[b - b0];
-            const bool served = to > 0 && off_b >= 0;
+        if (b0 > 0) {
+            __syncthreads();  // the last tile's offsets have been read
+            base += b0 == kScanThreads ? base1 : 0;
+            base += row_offsets(b0, base);
+            __syncthreads();
+        }
+        const int skip = (first_warp - b0 % all_warps + all_warps) % all_warps;  // (b mod all_warps is the warp, as above)
+        for (int b = b0 + skip; b < min(b0 + kScanThreads, p.B); b += all_warps) {
+            Head r = mine0;
+            if (b != first_warp) r = head_of(b), lack_of(r);
+            const int off = offsets[b - b0];
+            const bool served = r.to > 0 && off >= 0;
             int src = -1, dst = -1, taken = 0;
-            for (int c0 = from; served && c0 < to; c0 += 32) {
+            for (int c0 = r.from; served && c0 < r.to; c0 += 32) {
                 const int c = c0 + lane;
-                const int old = c < to ? p.table[(size_t)b * p.W + c] : -1;
-                const bool lack = c < to && lacks(old);
+                int old = r.old;
+                bool lack = r.lack;
+                if (c0 > r.from) {
+                    old = c < r.to ? p.table[(size_t)b * p.W + c] : -1;
+                    lack = c < r.to && lacks(old);
+                }
                 const unsigned mask = __ballot_sync(0xffffffffu, lack);
                 if (lack) {
-                    const int page = __ldcg(p.ids + off_b + taken + __popc(mask & ((1u << lane) - 1)));
+                    const int page = __ldcg(p.ids + off + taken + __popc(mask & ((1u << lane) - 1)));
                     p.table_out[(size_t)b * p.W + c] = page;
                     p.ref_out[page] = 1;
                     if (in_pool(old, p.P)) {
                         atomicSub(p.ref_out + old, 1);
-                        if (c == from && n % kPS != 0) src = old, dst = page;  // (lane 0: its tokens move along)
+                        if (c == r.from && r.n % kPS != 0) src = old, dst = page;  // (lane 0: its tokens move along)
                     }
                 }
                 taken += __popc(mask);
@@ -255,7 +286,6 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
                 p.dst[b] = dst;
             }
         }
-        __syncthreads();
     }
 }
 
