@@ -6,11 +6,14 @@
 // thread takes 16 dims of a row, one block of the cache's scales; for a key it reads the 16 dims that they turn with as
 // well (from L1 the second time), so that the block's maximum needs no exchange between threads.
 //
-// Neither memory nor the pipes are full (a fifth and a third to a half of the time): the chain position, angles, rows is what a
-// block waits for, so as many blocks as the registers allow count most.  Measured, up to 1024 new tokens of 8 sequences, ragged, 32
-// + 8 heads of 128, and their pages as bf16 (two calls, of which the second starts while the first drains): 6 / 8 / 10 / 12 blocks
-// an SM 29.8 / 28.3 / 27.8 / 29.0 us; 64 threads a block 30.7, 256 31.6; the rows' vectors read one row ahead 34.8 (more registers);
-// a division for each quotient 38.  One token of 4 sequences: 6.0 us for the two calls, which is the host's time.
+// Neither memory nor the pipes are full (a quarter and a third to a half of the time): the chain position, angles, rows is what a
+// block waits for, so what counts is the bytes that its threads ask for at once times the blocks that the registers allow.  Measured,
+// up to 1024 new tokens of 8 sequences, ragged, 32 + 8 heads of 128, and their pages as bf16 (two calls, of which the second starts
+// while the first drains), us:
+//   query rows at once / blocks an SM   1 / 10 28.3, 2 / 10 27.8, 2 / 8 26.5, 4 / 9 26.7, 4 / 8 25.9, 4 / 7 27.3, 4 / 6 28.2, 6 / 8 28.7
+//   4 / 8 in other shapes               64 threads a block 28.1, 256 29.0; the first query rows read before the angles 29.2
+// and a division for each quotient 38 where the corrected ones took 29.8.  One token of 4 sequences: 6.0 us for the two calls, which
+// is the host's time.
 #include "fp4.cuh"
 #include "rope.cuh"
 
@@ -18,6 +21,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kRows = 4;  // of the queries, in flight a thread
 
 struct Fp4AppendParams {
     const uint4 *q, *k, *v;         // 16-byte vectors of 8 bf16
@@ -32,7 +36,7 @@ struct Fp4AppendParams {
 };
 
 template <bool INTER>
-__global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4AppendParams p) {
     __shared__ __align__(16) float angles[2][kMaxRope];
     griddep_launch_dependents();
     griddep_wait();
@@ -79,18 +83,21 @@ __global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4Ap
     const int slot = (int)(pos0 % kFp4PS);  // even
     const size_t block = (size_t)9 * p.d;
     // A row's 8 dims from vector w on, turned: x c - y s in the first half of the pairs, y c + x s in the second.
+    auto turn_pairs = [&](float (&x)[8], int w, const float *cs) {  // neighbours
+        if (8 * w >= p.rope) return;
+        const float *c = cs + 4 * w, *s = c + half;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
+            x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
+            x[2 * i] = u;
+        }
+    };
     auto turned = [&](const uint4 *row, int w, const float *cs, float (&x)[8]) {
         unpack8(row[w], x);
-        if (8 * w >= p.rope) return;
         if constexpr (INTER) {
-            const float *c = cs + 4 * w, *s = c + half;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-                x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-                x[2 * i] = u;
-            }
-        } else {
+            turn_pairs(x, w, cs);
+        } else if (8 * w < p.rope) {
             const bool first = 8 * w < half;
             float y[8];
             unpack8(row[first ? w + half / 8 : w - half / 8], y);
@@ -103,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4Ap
                              x[2 * i], x[2 * i + 1]);
         }
     };
-    for (int row = r0; row < rows; row += per_pass) {
+    int row = r0;
+    for (; row < kv_rows; row += per_pass) {
         if (row < k_rows) {
             const int second = row >= p.Hkv, e = e0 + second, h = row - second * p.Hkv;
             const uint4 *k = p.k + b * p.ks[0] + h * p.ks[1] + tok[e] * p.ks[2];
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4Ap
             for (int i = 0; i < 8; ++i) lo[i] = u[i], hi[i] = u[8 + i];
             kd[fp4_k_scale(p.d, slot + e, j)] = (uint8_t)s;
             *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo) & keep, f32x8_to_e2m1x8(hi) & keep);
-        } else if (row < kv_rows) {
+        } else {
             const int h = row - k_rows;
             const uint4 *v = p.v + b * p.vs[0] + h * p.vs[1] + 2 * j;
             uint8_t *vd = p.v_pages + ((size_t)page * p.Hkv + h) * block;
@@ -163,30 +171,40 @@ __global__ void __launch_bounds__(kThreads, 10) kv_append_fp4_kernel(const Fp4Ap
                 bytes[3] = (bytes[3] & ~keep) | (old.w & keep);
             }
             *at = make_uint4(bytes[0], bytes[1], bytes[2], bytes[3]);
-        } else {
-            // (in place too: a thread reads both halves of its pairs before it writes them)
-            const int second = row - kv_rows >= p.H, e = e0 + second, h = row - kv_rows - second * p.H;
-            const uint4 *q = p.q + b * p.qs[0] + h * p.qs[1] + tok[e] * p.qs[2];
-            uint4 *to = p.q_out + (((size_t)b * p.H + h) * p.N + tok[e]) * vpr;
-            const int rot = p.rope / 16;
-            const bool halves = !INTER && j < rot;  // x in the first half, its y in the second
-            const int w0 = halves ? j : 2 * j, w1 = halves ? j + rot : 2 * j + 1;
-            float x[8], y[8];
-            if (INTER) {
-                turned(q, w0, angles[e], x);
-                turned(q, w1, angles[e], y);
-            } else {
-                unpack8(q[w0], x);
-                unpack8(q[w1], y);
-                if (halves) {
-                    const float *c = angles[e] + 8 * j;
-                    const uint64_t *c2 = reinterpret_cast<const uint64_t *>(c), *s2 = reinterpret_cast<const uint64_t *>(c + half);
+        }
+    }
+    // queries, kRows at once (in place too: a thread reads both halves of its pairs before it writes them)
+    const int rot = p.rope / 16;
+    const bool halves = !INTER && j < rot;  // x in the first half, its y in the second
+    const int w0 = halves ? j : 2 * j, w1 = halves ? j + rot : 2 * j + 1;
+    for (; row < rows; row += kRows * per_pass) {
+        uint4 xv[kRows], yv[kRows];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t a = f32x2_pack(x[2 * i], x[2 * i + 1]), o = f32x2_pack(y[2 * i], y[2 * i + 1]);
-                        f32x2_unpack(f32x2_fma(a, c2[i], f32x2_mul(o, s2[i] ^ 0x8000000080000000ull)), x[2 * i], x[2 * i + 1]);
-                        f32x2_unpack(f32x2_fma(o, c2[i], f32x2_mul(a, s2[i])), y[2 * i], y[2 * i + 1]);
-                    }
+        for (int i = 0; i < kRows; ++i) {
+            const int at = min(row + i * per_pass, rows - 1) - kv_rows, second = at >= p.H;
+            const uint4 *q = p.q + b * p.qs[0] + (at - second * p.H) * p.qs[1] + tok[e0 + second] * p.qs[2];
+            xv[i] = q[w0];
+            yv[i] = q[w1];
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int at = row + i * per_pass - kv_rows, second = at >= p.H, e = e0 + second, h = at - second * p.H;
+            if (at >= rows - kv_rows) break;
+            uint4 *to = p.q_out + (((size_t)b * p.H + h) * p.N + tok[e]) * vpr;
+            float x[8], y[8];
+            unpack8(xv[i], x);
+            unpack8(yv[i], y);
+            if (INTER) {
+                turn_pairs(x, w0, angles[e]);
+                turn_pairs(y, w1, angles[e]);
+            } else if (halves) {
+                const float *c = angles[e] + 8 * j;
+                const uint64_t *c2 = reinterpret_cast<const uint64_t *>(c), *s2 = reinterpret_cast<const uint64_t *>(c + half);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint64_t a = f32x2_pack(x[2 * n], x[2 * n + 1]), o = f32x2_pack(y[2 * n], y[2 * n + 1]);
+                    f32x2_unpack(f32x2_fma(a, c2[n], f32x2_mul(o, s2[n] ^ 0x8000000080000000ull)), x[2 * n], x[2 * n + 1]);
+                    f32x2_unpack(f32x2_fma(o, c2[n], f32x2_mul(a, s2[n])), y[2 * n], y[2 * n + 1]);
                 }
             }
             to[w0] = pack8(x);
