@@ -10,7 +10,7 @@
 // totals are exchanged at a cluster barrier.  There is next to nothing to read and write, so the launches count: tables and
 // pools of ordinary size are the work of one kernel a call, all of it by that cluster, and the kernels start while the ones
 // before them drain (a fork, a reservation and the copies for 16 rows: 20.5 us in five kernels, 14.1 in three, which is the
-// host's time for the three calls; a compaction of 400 pages with its copies 16.4 and 11.9).
+// host's time for the three calls; a compaction of 400 pages with its copies 16.4 and 10.7).
 #include "launch.h"
 #include "sm103_ptx.cuh"
 
@@ -294,6 +294,7 @@ struct CompactParams {
     const int32_t *table, *ref;
     int32_t *table_out, *ref_out, *src, *dst, *count;
     int32_t *to;     // [P]: where a page goes (-1: it is not live)
+    int32_t *back;   // [P]: the pages that move, the last one first
     int32_t *parts;  // [2 kScanCtas]
     int B, W, P, ctas, rename;  // rename: the table too
 };
@@ -308,9 +309,11 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const Compa
     const int cta = blockIdx.x;
     griddep_launch_dependents();
     griddep_wait();
-    int begin, end, mine = 0, total;
+    int begin, end, total;
     scan_part(p.P, cta, p.ctas, begin, end);
-    for (int i = begin + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
+    const int4 v0 = counts4(p.ref, begin + 4 * (int)threadIdx.x, end, 0);
+    int mine = (v0.x > 0) + (v0.y > 0) + (v0.z > 0) + (v0.w > 0);
+    for (int i = begin + kScanTile + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
         const int4 v = counts4(p.ref, i, end, 0);
         mine += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
     }
@@ -323,22 +326,12 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const Compa
         before += i < cta ? v : 0;
         live += v;
     }
-    // live pages below `live`, which stay: of this part, then of all
-    mine = 0;
-    for (int i = begin + 4 * (int)threadIdx.x; i < min(end, live); i += kScanTile) {
-        const int4 v = counts4(p.ref, i, end, 0);
-        mine += (v.x > 0) + (v.y > 0 && i + 1 < live) + (v.z > 0 && i + 2 < live) + (v.w > 0 && i + 3 < live);
-    }
-    block_scan(mine, sums, total);
-    if (threadIdx.x == 0) p.parts[kScanCtas + cta] = total;
-    cluster_sync();
-    int stay = 0;
-    for (int i = 0; i < p.ctas; ++i) stay += __ldcg(p.parts + kScanCtas + i);
-    const int moves = live - stay;
-    if (cta == 0 && threadIdx.x == 0) *p.count = moves;
+    // `stay` live pages lie below `live`; the others are `moves`, known after the next barrier, so those are listed from the last
+    // one, in `back`, and the holes from the first
+    int stays = 0;
     for (int i0 = begin; i0 < end; i0 += kScanTile) {
         const int i = i0 + 4 * (int)threadIdx.x;
-        const int4 v = counts4(p.ref, i, end, 0);
+        const int4 v = i0 == begin ? v0 : counts4(p.ref, i, end, 0);
         const int c[4] = {v.x, v.y, v.z, v.w};
         int at = before + block_scan((c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0), sums, total);  // live before i + j
         before += total;
@@ -348,22 +341,33 @@ __global__ void __launch_bounds__(kScanThreads) pages_compact_kernel(const Compa
             if (page >= end) break;
             if (page < live) {
                 p.to[page] = c[j] > 0 ? page : -1;
-                if (c[j] > 0) p.ref_out[page] = c[j];
+                if (c[j] > 0) p.ref_out[page] = c[j], ++stays;
                 else p.dst[page - at] = page;  // the holes, in order
             } else {
                 p.ref_out[page] = 0;
-                if (c[j] > 0) p.src[at - stay] = page;  // the pages that fill them, in order
+                if (c[j] > 0) p.back[live - 1 - at] = page;
                 else p.to[page] = -1;
             }
             at += c[j] > 0;
-            if (page >= moves) p.src[page] = p.dst[page] = -1;  // (places past the moves; below them, written above)
         }
     }
+    block_scan(stays, sums, total);
+    if (threadIdx.x == 0) p.parts[kScanCtas + cta] = total;
     cluster_sync();
-    for (int i = cta * kScanThreads + (int)threadIdx.x; i < moves; i += p.ctas * kScanThreads) {
-        const int s = __ldcg(p.src + i), d = __ldcg(p.dst + i);
-        p.to[s] = d;
-        p.ref_out[d] = p.ref[s];
+    int moves = live;
+    for (int i = 0; i < p.ctas; ++i) moves -= __ldcg(p.parts + kScanCtas + i);
+    if (cta == 0 && threadIdx.x == 0) *p.count = moves;
+    for (int i = cta * kScanThreads + (int)threadIdx.x; i < p.P; i += p.ctas * kScanThreads) {
+        int s = -1;
+        if (i < moves) {  // the pages that fill the holes, in order
+            s = __ldcg(p.back + moves - 1 - i);
+            const int d = __ldcg(p.dst + i);
+            p.to[s] = d;
+            p.ref_out[d] = p.ref[s];
+        } else {
+            p.dst[i] = -1;
+        }
+        p.src[i] = s;
     }
     if (!p.rename) return;
     cluster_sync();
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(256) pages_compact_table_kernel(const CompactP
 }
 
 // ---------------------------------------------------------------- copies
-// Bound by memory: 3930 pages of 32 KB in four pools take 155 us of the call's 180 (6.6 TB/s read and written).
+// Bound by memory: 3930 pages of 32 KB in four pools take 155 us of the 178 with the compaction (6.6 TB/s read and written).
 constexpr int kCopyPools = 256;  // pools of one launch
 constexpr int kCopyChunk = 16384;  // bytes a block moves at a time
 
@@ -425,7 +429,7 @@ int scan_ctas(K kernel, long long items) {
 }
 // Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
 // us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
-// anew, 49.6 / 30.7.
+// anew, 49.6 / 30.7 (28.8 with the reservation as it is now).
 constexpr long long kClusterItems = 1 << 15;
 
 // A kernel that is one cluster of `ctas` CTAs.
@@ -497,13 +501,14 @@ cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
 }
 
 size_t pages_compact_workspace_bytes(int num_pages) {
-    return num_pages <= 0 ? 0 : ints(num_pages) + ints(2 * kScanCtas);
+    return num_pages <= 0 ? 0 : 2 * ints(num_pages) + ints(2 * kScanCtas);
 }
 cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream) {
     const long long cells = (long long)a.B * a.max_pages, items = cells > a.num_pages ? cells : a.num_pages;
+    char *ws = static_cast<char *>(a.workspace);
     const CompactParams p{a.page_table, a.ref_counts, a.page_table_out, a.ref_counts_out, a.src, a.dst, a.count,
-                          static_cast<int32_t *>(a.workspace),
-                          reinterpret_cast<int32_t *>(static_cast<char *>(a.workspace) + ints(a.num_pages)),
+                          reinterpret_cast<int32_t *>(ws), reinterpret_cast<int32_t *>(ws + ints(a.num_pages)),
+                          reinterpret_cast<int32_t *>(ws + 2 * ints(a.num_pages)),
                           a.B, a.max_pages, a.num_pages, scan_ctas(pages_compact_kernel, items), cells <= kClusterItems};
     const cudaError_t e = launch_scan(pages_compact_kernel, p, p.ctas, stream);
     if (e != cudaSuccess || p.rename) return e;
