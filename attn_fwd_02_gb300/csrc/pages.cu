@@ -132,11 +132,10 @@ struct ReserveParams {
     int32_t *need;    // [B]
     int32_t *ids;     // [P]: free pages in order
     int32_t *parts;   // [kScanCtas]: free pages of each part
-    int B, W, P, ctas, copy_table, copy_ref, copy_frozen, copied;  // copied: by a grid before
+    int B, W, P, ctas, copy_table, copy_ref, copy_frozen;
+    int counts_copied, table_apart;  // by a grid before; by the grid's other clusters
 };
-__device__ __forceinline__ void reserve_copies(const ReserveParams &p, long long i0, long long step) {
-    if (p.copy_table)
-        for (long long i = i0; i < (long long)p.B * p.W; i += step) p.table_out[i] = p.table[i];
+__device__ __forceinline__ void reserve_copy_counts(const ReserveParams &p, long long i0, long long step) {
     for (long long i = i0; i < p.P; i += step) {
         const int v = p.ref[i];
         if (p.copy_ref) p.ref_out[i] = v;
@@ -146,7 +145,7 @@ __device__ __forceinline__ void reserve_copies(const ReserveParams &p, long long
 __global__ void __launch_bounds__(256) pages_reserve_copy_kernel(const ReserveParams p) {
     griddep_launch_dependents();
     griddep_wait();
-    reserve_copies(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+    reserve_copy_counts(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
 }
 // Entries [from, to) of row b that cover its new tokens (to 0: none wanted, or more than the table holds).
 __device__ __forceinline__ void reserve_range(const ReserveParams &p, int b, int &n, int &from, int &to) {
@@ -156,9 +155,28 @@ __device__ __forceinline__ void reserve_range(const ReserveParams &p, int b, int
     from = n / kPS;
     to = add > 0 && end <= p.W ? (int)end : 0;
 }
+// The entries that no new token touches, of all rows: a warp takes 256 of a row.
+constexpr int kCopyRun = 256;
+__device__ __forceinline__ void reserve_copy_rows(const ReserveParams &p, int warp, int warps) {
+    const int runs = (p.W + kCopyRun - 1) / kCopyRun, lane = threadIdx.x & 31;
+    for (long long u = warp; u < (long long)p.B * runs; u += warps) {
+        const int b = (int)(u / runs), c = (int)(u % runs) * kCopyRun + lane;
+        int n, from, to, v[kCopyRun / 32];
+        reserve_range(p, b, n, from, to);
+        const int32_t *row = p.table + (size_t)b * p.W;
+#pragma unroll
+        for (int i = 0; i < kCopyRun / 32; ++i)
+            if (c + 32 * i < p.W) v[i] = row[c + 32 * i];
+#pragma unroll
+        for (int i = 0; i < kCopyRun / 32; ++i)
+            if (c + 32 * i < p.W && (c + 32 * i < from || c + 32 * i >= to)) p.table_out[(size_t)b * p.W + c + 32 * i] = v[i];
+    }
+}
 // What waits on what: a row's lengths, its entries, their counts, the sums over the rows and over the pool, the free pages' ids.
 // A warp's first row and a thread's first counts are read before anything waits and stay in registers, and the sums over the first
-// kScanThreads rows in shared memory, so that nothing of an ordinary call is read twice.
+// kScanThreads rows in shared memory, so that nothing of an ordinary call is read twice.  The grid's first cluster does all but the
+// copy of a large table, which is left to the others (fork, reservation and copies for 128 rows of 1024 entries: 28.8 us with that
+// copy by a grid before, 27.0 so).
 __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const ReserveParams p) {
     __shared__ int sums[33];
     __shared__ int offsets[kScanThreads];  // of a tile of rows: where their free pages begin (-1: more than there are)
@@ -166,6 +184,10 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     const int first_warp = cta * 32 + warp, all_warps = p.ctas * 32;
     griddep_launch_dependents();
     griddep_wait();
+    if (cta >= p.ctas) {
+        reserve_copy_rows(p, (cta - p.ctas) * 32 + warp, ((int)gridDim.x - p.ctas) * 32);
+        return;
+    }
     int begin, end, mine, total;
     scan_part(p.P, cta, p.ctas, begin, end);
     const int4 v0 = counts4(p.ref, begin + 4 * (int)threadIdx.x, end, 1);
@@ -187,7 +209,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     auto lack_of = [&](Head &r) { r.lack = r.from + lane < r.to && lacks(r.old); };
     Head mine0{0, 0, 0, -1, false};
     if (first_warp < p.B) mine0 = head_of(first_warp);
-    if (!p.copied) reserve_copies(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
+    if (!p.counts_copied) reserve_copy_counts(p, (long long)cta * kScanThreads + threadIdx.x, (long long)p.ctas * kScanThreads);
+    if (p.copy_table && !p.table_apart) reserve_copy_rows(p, first_warp, all_warps);
     if (first_warp < p.B) lack_of(mine0);
     mine = (v0.x <= 0) + (v0.y <= 0) + (v0.z <= 0) + (v0.w <= 0);
     for (int i = begin + kScanTile + 4 * (int)threadIdx.x; i < end; i += kScanTile) {
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
             const int off = offsets[b - b0];
             const bool served = r.to > 0 && off >= 0;
             int src = -1, dst = -1, taken = 0;
-            for (int c0 = r.from; served && c0 < r.to; c0 += 32) {
+            for (int c0 = r.from; c0 < r.to; c0 += 32) {
                 const int c = c0 + lane;
                 int old = r.old;
                 bool lack = r.lack;
@@ -268,6 +291,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
                     old = c < r.to ? p.table[(size_t)b * p.W + c] : -1;
                     lack = c < r.to && lacks(old);
                 }
+                lack = lack && served;
+                if (p.copy_table && c < r.to && !lack) p.table_out[(size_t)b * p.W + c] = old;
                 const unsigned mask = __ballot_sync(0xffffffffu, lack);
                 if (lack) {
                     const int page = __ldcg(p.ids + off + taken + __popc(mask & ((1u << lane) - 1)));
@@ -429,14 +454,14 @@ int scan_ctas(K kernel, long long items) {
 }
 // Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
 // us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
-// anew, 49.6 / 30.7 (28.8 with the reservation as it is now).
+// anew, 49.6 / 30.7 (27.0 with the reservation as it is now).
 constexpr long long kClusterItems = 1 << 15;
 
-// A kernel that is one cluster of `ctas` CTAs.
+// A kernel of one cluster, or several, of `ctas` CTAs.
 template <class K, class A>
-cudaError_t launch_scan(K kernel, const A &p, int ctas, cudaStream_t stream) {
+cudaError_t launch_scan(K kernel, const A &p, int ctas, int clusters, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(ctas * clusters);
     cfg.blockDim = dim3(kScanThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -459,7 +484,7 @@ cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream) {
     const ForkParams p{a.page_table, a.ctx_lens, a.parents, a.ref_counts, a.page_table_out, a.ctx_lens_out,
                        a.ref_counts_out, a.B, a.B_out, a.max_pages, a.num_pages};
     const long long all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages, items = all > a.num_pages ? all : a.num_pages;
-    if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(pages_fork_cluster_kernel, items), stream);
+    if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(pages_fork_cluster_kernel, items), 1, stream);
     const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(pages_fork_count_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
@@ -490,14 +515,20 @@ cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
     p.B = a.B;
     p.W = a.max_pages;
     p.P = a.num_pages;
-    const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0, items = cells > a.num_pages ? cells : a.num_pages;
-    p.ctas = scan_ctas(pages_reserve_kernel, items);
-    p.copied = items > kClusterItems;
-    if (p.copied) {
-        const cudaError_t e = launch_dependent(pages_reserve_copy_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
+    const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0;
+    p.table_apart = cells > kClusterItems;
+    p.counts_copied = a.num_pages > kClusterItems;
+    p.ctas = scan_ctas(pages_reserve_kernel, cells > a.num_pages ? cells : a.num_pages);
+    if (p.counts_copied) {
+        const cudaError_t e = launch_dependent(pages_reserve_copy_kernel, dim3(blocks_for(a.num_pages, 8)), 256, 0, stream, p);
         if (e != cudaSuccess) return e;
     }
-    return launch_scan(pages_reserve_kernel, p, p.ctas, stream);
+    int clusters = 1;
+    if (p.table_apart) {  // a run a warp, on at most 16 more clusters
+        const long long runs = (long long)a.B * ((a.max_pages + kCopyRun - 1) / kCopyRun), want = (runs + 32 * p.ctas - 1) / (32 * p.ctas);
+        clusters += (int)(want < 16 ? want : 16);
+    }
+    return launch_scan(pages_reserve_kernel, p, p.ctas, clusters, stream);
 }
 
 size_t pages_compact_workspace_bytes(int num_pages) {
@@ -510,7 +541,7 @@ cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t stream) {
                           reinterpret_cast<int32_t *>(ws), reinterpret_cast<int32_t *>(ws + ints(a.num_pages)),
                           reinterpret_cast<int32_t *>(ws + 2 * ints(a.num_pages)),
                           a.B, a.max_pages, a.num_pages, scan_ctas(pages_compact_kernel, items), cells <= kClusterItems};
-    const cudaError_t e = launch_scan(pages_compact_kernel, p, p.ctas, stream);
+    const cudaError_t e = launch_scan(pages_compact_kernel, p, p.ctas, 1, stream);
     if (e != cudaSuccess || p.rename) return e;
     return launch_dependent(pages_compact_table_kernel, dim3(blocks_for(cells, 8)), 256, 0, stream, p);
 }

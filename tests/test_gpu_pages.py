@@ -262,3 +262,11 @@ def test_serving_loop_over_a_four_bit_cache(lib):
             for p in pools:
                 p[live:] = 0x7F  # the pool's end is free for anything
     assert lib.attn_check_device_status() == 0
+
+
+@pytest.mark.parametrize("B, W, P", [(128, 300, 20000), (40, 1000, 70001), (3, 20011, 9000), (1100, 40, 6000)])
+def test_large_tables(lib, B, W, P):
+    # tables past what one cluster copies, with pools of both kinds, and more rows than one tile of sums
+    test_fork(lib, B, W, P)
+    test_reserve(lib, B, W, P)
+    test_compact(lib, B, W, P)
