@@ -39,24 +39,17 @@ __device__ __forceinline__ int fork_entry(const ForkParams &p, int b, int c) {
     }
     return p.table[(size_t)par * p.W + c];
 }
-__device__ __forceinline__ void fork_rows(const ForkParams &p, long long i0, long long step) {
-    for (long long i = i0; i < (long long)p.B_out * p.W; i += step) p.table_out[i] = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
-    for (long long i = i0; i < p.P; i += step) p.ref_out[i] = p.ref[i];
+__device__ __forceinline__ void fork_lens(const ForkParams &p, long long i0, long long step) {
     for (long long i = i0; i < p.B_out; i += step) {
         const int par = p.parents[i];
         p.ctx_out[i] = par < 0 || par >= p.B ? 0 : p.ctx[par];
     }
 }
-// Counts: what a place of the table names now, less what it named.
-__device__ __forceinline__ void fork_counts(const ForkParams &p, long long i0, long long step) {
-    const long long rows = max(p.B, p.B_out);
-    for (long long i = i0; i < rows * p.W; i += step) {
-        const int was = i < (long long)p.B * p.W ? p.table[i] : -1;
-        const int is = i < (long long)p.B_out * p.W ? __ldcg(p.table_out + i) : -1;
-        if (was == is) continue;
-        if (in_pool(was, p.P)) atomicSub(p.ref_out + was, 1);
-        if (in_pool(is, p.P)) atomicAdd(p.ref_out + is, 1);
-    }
+// What a place of the table names now, and what it named.
+__device__ __forceinline__ void fork_count(const ForkParams &p, int was, int is) {
+    if (was == is) return;
+    if (in_pool(was, p.P)) atomicSub(p.ref_out + was, 1);
+    if (in_pool(is, p.P)) atomicAdd(p.ref_out + is, 1);
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
@@ -66,20 +59,37 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_cluster_kernel(const 
     griddep_launch_dependents();
     griddep_wait();
     const long long i0 = (long long)blockIdx.x * kScanThreads + threadIdx.x, step = (long long)gridDim.x * kScanThreads;
-    fork_rows(p, i0, step);
+    const long long olds = (long long)p.B * p.W, news = (long long)p.B_out * p.W;
+    for (long long i = i0; i < news; i += step) p.table_out[i] = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
+    for (long long i = i0; i < p.P; i += step) p.ref_out[i] = p.ref[i];
+    fork_lens(p, i0, step);
     cluster_sync();
-    fork_counts(p, i0, step);
+    for (long long i = i0; i < max(olds, news); i += step)
+        fork_count(p, i < olds ? p.table[i] : -1, i < news ? __ldcg(p.table_out + i) : -1);
 }
-// Large tables: two grids.
+// Large tables: rows and counts by one grid, for which another has copied the counts where they are not changed in place.  That
+// one lets it start when all before it has ended, so the rows are made while the counts are copied (fork, reservation and copies for
+// 128 rows of 1024 entries: rows and counts by grids one after the other 27.0 us, so 25.1).
+__global__ void __launch_bounds__(256) pages_fork_copy_kernel(const ForkParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < p.P; i += (long long)gridDim.x * 256) p.ref_out[i] = p.ref[i];
+}
 __global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
+    if (p.ref_out == p.ref) griddep_wait();
     griddep_launch_dependents();
-    griddep_wait();
-    fork_rows(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
-}
-__global__ void __launch_bounds__(256) pages_fork_count_kernel(const ForkParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    fork_counts(p, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+    const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    const long long olds = (long long)p.B * p.W, news = (long long)p.B_out * p.W;
+    fork_lens(p, i0, step);
+    int was = -1, is = -1;
+    auto entry = [&](long long i) {
+        was = i < olds ? p.table[i] : -1;
+        is = -1;
+        if (i < news) p.table_out[i] = is = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
+    };
+    entry(i0);
+    griddep_wait();  // the counts are there
+    for (long long i = i0; i < max(olds, news); i += step, entry(i)) fork_count(p, was, is);
 }
 
 // ---------------------------------------------------------------- scans
@@ -454,7 +464,7 @@ int scan_ctas(K kernel, long long items) {
 }
 // Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
 // us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
-// anew, 49.6 / 30.7 (27.0 with the reservation as it is now).
+// anew, 49.6 / 30.7 (25.1 as the large steps are now).
 constexpr long long kClusterItems = 1 << 15;
 
 // A kernel of one cluster, or several, of `ctas` CTAs.
@@ -485,9 +495,11 @@ cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t stream) {
                        a.ref_counts_out, a.B, a.B_out, a.max_pages, a.num_pages};
     const long long all = (long long)(a.B > a.B_out ? a.B : a.B_out) * a.max_pages, items = all > a.num_pages ? all : a.num_pages;
     if (items <= kClusterItems) return launch_scan(pages_fork_cluster_kernel, p, scan_ctas(pages_fork_cluster_kernel, items), 1, stream);
-    const cudaError_t e = launch_dependent(pages_fork_kernel, dim3(blocks_for(items, 8)), 256, 0, stream, p);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(pages_fork_count_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
+    if (p.ref_out != p.ref) {
+        const cudaError_t e = launch_dependent(pages_fork_copy_kernel, dim3(blocks_for(a.num_pages, 8)), 256, 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(pages_fork_kernel, dim3(blocks_for(all, 8)), 256, 0, stream, p);
 }
 
 size_t pages_reserve_workspace_bytes(int B, int num_pages) {
