@@ -693,15 +693,18 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
 }
 
 // Joins the parts of a query head's row, where several CTAs had one: W warps a head, which take its parts in turn, lanes four
-// columns each.  A sequence that sees nothing gets zeros.  Four warps a head up to kJoinHeads heads, whose rows may have many
-// parts, one for more (call with four / one: 32 sequences of 32 heads 37.9 / 39.0 us, 64 of 32 22.5 / 20.7, 128 of 12 29.7 / 28.9).
+// columns each.  A sequence that sees nothing gets zeros.  One warp a head past kJoinHeads heads, four up to there, whose rows may
+// have many parts (call with four / one: 32 sequences of 32 heads 37.9 / 39.0 us, 64 of 32 22.5 / 20.7, 128 of 12 29.7 / 28.9),
+// sixteen up to a head an SM (call with four / sixteen, 32 heads: one sequence of 103000 tokens 31.5 / 29.9 us, of up to 40000
+// 18.4 / 16.5, 4 of up to 30000 22.8 / 22.6; past that sixteen cost, 32 of up to 8192 38.3 / 43.0).
 constexpr int kJoinHeads = 1024;
+template <int W> constexpr int kJoinWarps = W > 4 ? W : 4;  // of a CTA
 template <int D, int NT, int W>
-__global__ void __launch_bounds__(kFp4Threads) decode_fp4_join_kernel(const Fp4Params a) {
-    __shared__ float4 acc_s[kRowWarps][32];
-    __shared__ float2 ml_s[kRowWarps];
+__global__ void __launch_bounds__(kJoinWarps<W> * 32) decode_fp4_join_kernel(const Fp4Params a) {
+    __shared__ float4 acc_s[kJoinWarps<W>][32];
+    __shared__ float2 ml_s[kJoinWarps<W>];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = (long long)blockIdx.x * (kRowWarps / W) + warp / W;  // (sequence, head)
+    const long long row = (long long)blockIdx.x * (kJoinWarps<W> / W) + warp / W;  // (sequence, head)
     const bool there = row < (long long)a.B * a.H;
     const int b = there ? (int)(row / a.H) : 0, h = (int)(row - (long long)b * a.H);
     const int in_group = h % a.group, y = h / a.group * a.rgroups + in_group / (8 * NT);
@@ -751,17 +754,18 @@ __global__ void __launch_bounds__(kFp4Threads) decode_fp4_join_kernel(const Fp4P
         }
     }
     if constexpr (W > 1) {
-        static_assert(W == kRowWarps, "one head a CTA: its threads all come here");
-        acc_s[warp][lane] = acc;
+        acc_s[warp][lane] = acc;  // (one head a CTA: its threads all come here)
         if (lane == 0) ml_s[warp] = make_float2(M, L);
         __syncthreads();
         if (warp != 0) return;
-        M = fmaxf(fmaxf(ml_s[0].x, ml_s[1].x), fmaxf(ml_s[2].x, ml_s[3].x));
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml_s[w].x);
         L = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (M != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kRowWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float wt = ex2_approx(ml_s[w].x - M);
                 const float4 v = acc_s[w][lane];
                 L = fmaf(ml_s[w].y, wt, L);
@@ -840,10 +844,12 @@ cudaError_t launch_fp4_n(const DecodeMoreArgs &a, Fp4Params p, cudaStream_t stre
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long heads = (long long)p.B * p.H;
-    if (heads <= kJoinHeads)
-        return launch_dependent(decode_fp4_join_kernel<D, NT, kRowWarps>, dim3((unsigned)heads), kFp4Threads, 0, stream, p);
-    const unsigned ctas = (unsigned)((heads + kRowWarps - 1) / kRowWarps);
-    return launch_dependent(decode_fp4_join_kernel<D, NT, 1>, dim3(ctas), kFp4Threads, 0, stream, p);
+    auto join = [&](auto w) {
+        constexpr int W = decltype(w)::value, kHeads = kJoinWarps<W> / W;
+        return launch_dependent(decode_fp4_join_kernel<D, NT, W>, dim3((unsigned)((heads + kHeads - 1) / kHeads)), kJoinWarps<W> * 32, 0, stream, p);
+    };
+    if (heads <= kSms) return join(std::integral_constant<int, 16>{});
+    return heads <= kJoinHeads ? join(std::integral_constant<int, 4>{}) : join(std::integral_constant<int, 1>{});
 }
 
 template <int D>
