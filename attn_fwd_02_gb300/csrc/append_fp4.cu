@@ -10,8 +10,9 @@
 // block waits for, so what counts is the bytes that its threads ask for at once times the blocks that the registers allow.  Measured,
 // up to 1024 new tokens of 8 sequences, ragged, 32 + 8 heads of 128, and their pages as bf16 (two calls, of which the second starts
 // while the first drains), us:
-//   query rows at once / blocks an SM   1 / 10 28.3, 2 / 10 27.8, 2 / 8 26.5, 4 / 9 26.7, 4 / 8 25.9, 4 / 7 27.3, 4 / 6 28.2, 6 / 8 28.7
-//   4 / 8 in other shapes               64 threads a block 28.1, 256 29.0; the first query rows read before the angles 29.2
+//   query rows at once / blocks an SM   2 / 10 27.5, 4 / 10 28.1, 4 / 9 26.1, 4 / 8 25.1, 4 / 7 25.7, 5 / 8 25.9
+//   before: the head dim at run time, the angles one by one   1 / 10 28.3, 2 / 10 27.8, 4 / 8 25.9; of that 64 threads a block 28.1, 256
+//   29.0, the first query rows read before the angles 29.2
 // and a division for each quotient 38 where the corrected ones took 29.8.  One token of 4 sequences: 6.0 us for the two calls, which
 // is the host's time.
 #include "fp4.cuh"
@@ -31,11 +32,11 @@ struct Fp4AppendParams {
     const float *cos_sin;           // null: no rotation
     const int32_t *page_table, *start_pos, *new_lens;  // new_lens may be null
     float k_inv, v_inv;             // 1 / scale
-    int rope, max_pos, H, Hkv, N, pairs, d, max_pages, num_pages;
+    int rope, max_pos, H, Hkv, N, pairs, max_pages, num_pages;
     RopeAxes axes;                  // positions null: the row of the table is the position in the cache
 };
 
-template <bool INTER>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4AppendParams p) {
     __shared__ __align__(16) float angles[2][kMaxRope];
     griddep_launch_dependents();
@@ -45,24 +46,34 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
     const long long pos0 = (long long)(start & ~1) + 2LL * (blockIdx.x % (unsigned)p.pairs);
     const int n_new = p.new_lens ? min(p.new_lens[b], p.N) : p.N;
     // the pair's tokens e: their place among the new ones, and whether they are there (uniform over the block)
+    const int half = p.rope / 2;
     int tok[2];
     bool have[2];
+    AxisRows at[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const long long t = pos0 + e - start;
         tok[e] = (int)t;
         have[e] = t >= 0 && t < n_new;
         if (have[e] && p.cos_sin) {
-            AxisRows rows;
             if (p.axes.positions) {
-                rows = axis_rows(p.axes, b, tok[e], p.max_pos);
+                at[e] = axis_rows(p.axes, b, tok[e], p.max_pos);
             } else {
-                rows.ok = pos0 + e < p.max_pos;
+                at[e].ok = pos0 + e < p.max_pos;
 #pragma unroll
-                for (int a = 0; a < kMaxAxes; ++a) rows.row[a] = (int)(pos0 + e);
+                for (int a = 0; a < kMaxAxes; ++a) at[e].row[a] = (int)(pos0 + e);
             }
-            have[e] = rows.ok;  // past the rotation table: padding too
-            if (rows.ok) gather_angles(angles[e], p.cos_sin, p.axes, rows, p.rope, threadIdx.x, kThreads);
+            have[e] = at[e].ok;  // past the rotation table: padding too
+        }
+    }
+    {  // their angles, a thread a pair of dims
+        static_assert(kThreads == kMaxRope, "two tokens' pairs");
+        const int e = threadIdx.x / (kMaxRope / 2), pair = threadIdx.x % (kMaxRope / 2);
+        if (pair < half && (e ? have[1] : have[0])) {
+            const int r0 = axis_row(p.axes, at[0], pair), r1 = axis_row(p.axes, at[1], pair);
+            const float *row = p.cos_sin + (size_t)(e ? r1 : r0) * p.rope + pair;
+            angles[e][pair] = row[0];
+            angles[e][half + pair] = row[half];
         }
     }
     if (!have[0] && !have[1]) return;
@@ -73,15 +84,14 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
 
     // Thread = (16-dim block j of a row, first row): it takes that block of every per_pass-th row.  The rows are those of the
     // tokens' keys, then the values' (a row for both tokens), then the tokens' queries.
-    const int vpr = p.d / 8, bpr = p.d / 16, half = p.rope / 2;
-    const int per_pass = kThreads / bpr;
+    constexpr int vpr = D / 8, bpr = D / 16, per_pass = kThreads / bpr;
     const int j = threadIdx.x % bpr, r0 = threadIdx.x / bpr;
     if (r0 >= per_pass) return;
     const int e0 = have[0] ? 0 : 1, tokens = have[0] && have[1] ? 2 : 1;
     const int k_rows = page < 0 ? 0 : tokens * p.Hkv, kv_rows = page < 0 ? 0 : k_rows + p.Hkv;
     const int rows = kv_rows + (p.q ? tokens * p.H : 0);
     const int slot = (int)(pos0 % kFp4PS);  // even
-    const size_t block = (size_t)9 * p.d;
+    constexpr size_t block = (size_t)9 * D;
     // A row's 8 dims from vector w on, turned: x c - y s in the first half of the pairs, y c + x s in the second.
     auto turn_pairs = [&](float (&x)[8], int w, const float *cs) {  // neighbours
         if (8 * w >= p.rope) return;
@@ -127,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
             float lo[8], hi[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) lo[i] = u[i], hi[i] = u[8 + i];
-            kd[fp4_k_scale(p.d, slot + e, j)] = (uint8_t)s;
-            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(p.d, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo) & keep, f32x8_to_e2m1x8(hi) & keep);
+            kd[fp4_k_scale(D, slot + e, j)] = (uint8_t)s;
+            *reinterpret_cast<uint2 *>(kd + fp4_k_codes(D, slot + e, j)) = make_uint2(f32x8_to_e2m1x8(lo) & keep, f32x8_to_e2m1x8(hi) & keep);
         } else {
             const int h = row - k_rows;
             const uint4 *v = p.v + b * p.vs[0] + h * p.vs[1] + 2 * j;
@@ -152,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
             for (int e = 0; e < 2; ++e) {
                 const uint32_t s = fp4_quotients(u[e]);
                 if (!s) nonzero &= e == 0 ? 0xf0f0f0f0u : 0x0f0f0f0fu;
-                if (have[e]) vd[fp4_v_scale(p.d, slot + e, j)] = (uint8_t)s;
+                if (have[e]) vd[fp4_v_scale(D, slot + e, j)] = (uint8_t)s;
             }
             // byte x of the block: dim x of both tokens
             uint32_t bytes[4];
@@ -289,6 +299,12 @@ __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p
     }
 }
 
+template <int D>
+cudaError_t launch_append_d(const Fp4AppendParams &p, dim3 grid, bool interleaved, cudaStream_t stream) {
+    return interleaved ? launch_dependent(kv_append_fp4_kernel<D, true>, grid, kThreads, 0, stream, p)
+                       : launch_dependent(kv_append_fp4_kernel<D, false>, grid, kThreads, 0, stream, p);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append_fp4(const RopeAppendArgs &a, cudaStream_t stream) {
@@ -316,13 +332,19 @@ cudaError_t launch_kv_append_fp4(const RopeAppendArgs &a, cudaStream_t stream) {
     p.Hkv = a.Hkv;
     p.N = a.Nnew;
     p.pairs = a.Nnew / 2 + 1;  // the positions may start at an odd one
-    p.d = a.d;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.axes = a.axes;
     const dim3 grid((unsigned)((long long)a.B * p.pairs));
-    return a.interleaved ? launch_dependent(kv_append_fp4_kernel<true>, grid, kThreads, 0, stream, p)
-                         : launch_dependent(kv_append_fp4_kernel<false>, grid, kThreads, 0, stream, p);
+    const bool inter = a.interleaved != 0;
+    switch (a.d) {
+        case 32: return launch_append_d<32>(p, grid, inter, stream);
+        case 64: return launch_append_d<64>(p, grid, inter, stream);
+        case 80: return launch_append_d<80>(p, grid, inter, stream);
+        case 96: return launch_append_d<96>(p, grid, inter, stream);
+        case 128: return launch_append_d<128>(p, grid, inter, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 cudaError_t launch_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale, float v_scale,
