@@ -69,12 +69,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
     {  // their angles, a thread a pair of dims
         static_assert(kThreads == kMaxRope, "two tokens' pairs");
         const int e = threadIdx.x / (kMaxRope / 2), pair = threadIdx.x % (kMaxRope / 2);
-        if (pair < half && (e ? have[1] : have[0])) {
-            const int r0 = axis_row(p.axes, at[0], pair), r1 = axis_row(p.axes, at[1], pair);
-            const float *row = p.cos_sin + (size_t)(e ? r1 : r0) * p.rope + pair;
-            angles[e][pair] = row[0];
-            angles[e][half + pair] = row[half];
-        }
+        if (e ? have[1] : have[0]) gather_pair(angles[e], p.cos_sin, p.axes, e ? at[1] : at[0], p.rope, pair);
     }
     if (!have[0] && !have[1]) return;
     const long long lp = pos0 / kFp4PS;

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads)
     const float *angles = p.cos_sin + (AXES ? 0 : (size_t)pos * p.rope);
     if constexpr (AXES) {
         __shared__ __align__(16) float gathered[kMaxRope];
-        gather_angles(gathered, p.cos_sin, p.axes, rows, p.rope, threadIdx.x, per_pass * ipr);
+        gather_pair(gathered, p.cos_sin, p.axes, rows, p.rope, threadIdx.x);  // (at least 120 threads, at most 64 pairs)
         __syncthreads();  // of the threads that are left
         angles = gathered;
     }

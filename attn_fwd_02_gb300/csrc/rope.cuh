@@ -43,13 +43,14 @@ __device__ __forceinline__ int axis_row(const RopeAxes &x, const AxisRows &r, in
     const int a = (int)(x.pair_axis[pair >> 5] >> (2 * (pair & 31))) & 3;
     return a < 2 ? (a == 0 ? r.row[0] : r.row[1]) : (a == 2 ? r.row[2] : r.row[3]);
 }
-// Threads i, i + n, ... gather a token's rope values (cosines of the pairs, then sines, times `sign`).
-__device__ __forceinline__ void gather_angles(float *to, const float *cos_sin, const RopeAxes &x, const AxisRows &r,
-                                              int rope, int i, int n, float sign = 1.f) {
-    for (; i < rope; i += n) {
-        const int pair = i < rope / 2 ? i : i - rope / 2;
-        to[i] = cos_sin[(size_t)axis_row(x, r, pair) * rope + i] * (i < rope / 2 ? 1.f : sign);
-    }
+// Pair `i` of a token (past the last one: none): its cosine and, times `sign`, its sine, to where the cosines of all pairs and
+// then their sines stand.
+__device__ __forceinline__ void gather_pair(float *to, const float *cos_sin, const RopeAxes &x, const AxisRows &r, int rope, int i,
+                                            float sign = 1.f) {
+    if (i >= rope / 2) return;
+    const float *row = cos_sin + (size_t)axis_row(x, r, i) * rope + i;
+    to[i] = row[0];
+    to[rope / 2 + i] = row[rope / 2] * sign;
 }
 
 }  // namespace attn

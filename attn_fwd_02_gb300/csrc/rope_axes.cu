@@ -54,11 +54,7 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeOnlyParam
     };
     fetch();
     const AxisRows rows = axis_rows(p.axes, b, t, p.max_pos);
-    if (rows.ok && (int)threadIdx.x < half) {  // (a thread a pair)
-        const float *row = p.cos_sin + (size_t)axis_row(p.axes, rows, threadIdx.x) * p.rope + threadIdx.x;
-        angles[threadIdx.x] = row[0];
-        angles[half + threadIdx.x] = row[half] * p.sign;
-    }
+    if (rows.ok) gather_pair(angles, p.cos_sin, p.axes, rows, p.rope, threadIdx.x, p.sign);
     __syncthreads();
     uint4 *qo = p.q_out + b * p.qo[0] + t * p.qo[2], *ko = p.k_out + b * p.ko[0] + t * p.ko[2] - p.H * p.ko[1];
     const float *c = angles + 8 * i;
