@@ -227,10 +227,14 @@ struct UnpackParams {
     int n, Hkv, d, num_pages;
 };
 
-// Eight codes' f16 words, low half first, times f (the block's scale times the tensor's) as bf16.
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t h2, float s, float scale) {
-    const __half2 h = *reinterpret_cast<const __half2 *>(&h2);
-    return pack_bf16x2(__fmul_rn(__low2float(h) * s, scale), __fmul_rn(__high2float(h) * s, scale));
+// A pair of codes, widened to f16, times their block's scale (exact: 6 bits, multiples of 2^-10 below 2^12) and the tensor's, as
+// bf16.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t h2, uint32_t block2, uint64_t scale2) {
+    const uint32_t v = f16x2_mul(h2, block2);
+    const __half2 h = *reinterpret_cast<const __half2 *>(&v);
+    float x, y;
+    f32x2_unpack(f32x2_mul(f32x2_pack(__low2float(h), __high2float(h)), scale2), x, y);
+    return pack_bf16x2(x, y);
 }
 
 // One CTA a page's keys or values (blockIdx.y).  A thread takes 8 dims of two tokens that share the values' bytes, so that its
@@ -244,7 +248,8 @@ __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p
     const int page = p.page_ids[blockIdx.x];
     if (page < 0 || page >= p.num_pages) return;
     const bool value = blockIdx.y != 0;
-    const float scale = value ? p.v_scale : p.k_scale;
+    const float f = value ? p.v_scale : p.k_scale;
+    const uint64_t scale = f32x2_pack(f, f);
     const uint8_t *pages = (value ? p.v_pages : p.k_pages) + (size_t)page * p.Hkv * (9 * D);
     uint4 *out = (value ? p.v_out : p.k_out) + (size_t)blockIdx.x * p.Hkv * kFp4PS * kVpr;
     const int items = p.Hkv * kPerHead;
@@ -286,9 +291,9 @@ __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const float f = e4m3_to_float(s[i][t]);
-                dst[t * kVpr] = make_uint4(scaled_pair(r[t][0], f, scale), scaled_pair(r[t][1], f, scale),
-                                           scaled_pair(r[t][2], f, scale), scaled_pair(r[t][3], f, scale));
+                const uint32_t b2 = e4m3_pair(s[i][t] * 0x101u);
+                dst[t * kVpr] = make_uint4(scaled_pair(r[t][0], b2, scale), scaled_pair(r[t][1], b2, scale),
+                                           scaled_pair(r[t][2], b2, scale), scaled_pair(r[t][3], b2, scale));
             }
         }
     }

@@ -54,13 +54,6 @@ struct Fp4Smem {
     int abort_flag;
 };
 
-// Both halves of a word: the f16 value of byte `i` of e4m3 codes.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t codes) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
-    return r;
-}
-
 // The dims of a lane's k-steps.  A row is cut into units of W dims, of which lane t takes W / 4 neighbours, 4 a k-step:
 // one unit of 128, or units of 64 and one of the rest.
 template <int D> constexpr int fp4_unit(int ks) { return D == 128 ? 128 : (D - ks / 4 * 64 >= 64 ? 64 : D % 64); }

@@ -33,6 +33,13 @@ __host__ __device__ constexpr int fp4_v_scale(int d, int token, int j) {
     return 8 * d + ((token & 7) >> 1) * (d / 4) + j * 4 + (token >> 3) * 2 + (token & 1);
 }
 
+// Both halves of a word: the f16 value of byte `i` of e4m3 codes.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
+    return r;
+}
+
 // Eight e2m1 codes -> four f16x2 words: r[i] holds the codes of byte i, the low nibble in the low half.
 __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
