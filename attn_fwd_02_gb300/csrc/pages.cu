@@ -30,19 +30,20 @@ struct ForkParams {
     int32_t *table_out, *ctx_out, *ref_out;
     int B, B_out, W, P;
 };
+// (Read through L2: the grid of a large table reads its inputs before it has waited itself.)
 __device__ __forceinline__ int fork_entry(const ForkParams &p, int b, int c) {
-    const int par = p.parents[b];
+    const int par = __ldcg(p.parents + b);
     if (par < 0 || par >= p.B) return -1;
     if (par != b) {
-        const int n = min(max(p.ctx[par], 0), p.W * kPS);
+        const int n = min(max(__ldcg(p.ctx + par), 0), p.W * kPS);
         if (c >= (n + kPS - 1) / kPS) return -1;
     }
-    return p.table[(size_t)par * p.W + c];
+    return __ldcg(p.table + (size_t)par * p.W + c);
 }
 __device__ __forceinline__ void fork_lens(const ForkParams &p, long long i0, long long step) {
     for (long long i = i0; i < p.B_out; i += step) {
-        const int par = p.parents[i];
-        p.ctx_out[i] = par < 0 || par >= p.B ? 0 : p.ctx[par];
+        const int par = __ldcg(p.parents + i);
+        p.ctx_out[i] = par < 0 || par >= p.B ? 0 : __ldcg(p.ctx + par);
     }
 }
 // What a place of the table names now, and what it named.
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_fork_cluster_kernel(const 
     fork_lens(p, i0, step);
     cluster_sync();
     for (long long i = i0; i < max(olds, news); i += step)
-        fork_count(p, i < olds ? p.table[i] : -1, i < news ? __ldcg(p.table_out + i) : -1);
+        fork_count(p, i < olds ? __ldcg(p.table + i) : -1, i < news ? __ldcg(p.table_out + i) : -1);
 }
 // Large tables: rows and counts by one grid, for which another has copied the counts where they are not changed in place.  That
 // one lets it start when all before it has ended, so the rows are made while the counts are copied (fork, reservation and copies for
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const ForkParams p) {
     fork_lens(p, i0, step);
     int was = -1, is = -1;
     auto entry = [&](long long i) {
-        was = i < olds ? p.table[i] : -1;
+        was = i < olds ? __ldcg(p.table + i) : -1;
         is = -1;
         if (i < news) p.table_out[i] = is = fork_entry(p, (int)(i / p.W), (int)(i % p.W));
     };
