@@ -177,3 +177,28 @@ def test_other_stream_graph_and_workspace(lib, spare):
     graph.replay()
     w = lib.paged_attn_decode_fp4(q, k, v, KS, VS, table, ctx, softcap=20.0)
     assert torch.equal(cap[0], w[0]) and torch.equal(cap[1], w[1])
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_sixteen_million_tokens(lib, cap):
+    """A context of 2^20 pages, the same 64 over and over: the result is theirs, with ln(2^14) more in LSE.
+
+    A lane adds at most 4 weights of each of its warp's pages (2^21 rows' pages over 2432 warps: 863) to its sum, a chain of
+    3452 roundings of 2^-24: 2.1e-4 relative, and so in LSE.  O, of the largest value: the weights' rounding to f16 (2^-11, here
+    2^-10) and 863 roundings of an accumulator, a few 2^-24 each (2^-12); of O: the sum's error and the rounding to bf16."""
+    x = make(1, 4, 2, 64, [1024], 21, spare=0)
+    o, lse = want(x, 0.125, cap)[:2]
+    table = x[3].repeat(1, 1 << 14)
+    ctx = torch.tensor([1 << 24], dtype=torch.int32)
+    got = run(lib, (x[0], x[1], x[2], table, ctx), scale=0.125, softcap=cap)
+    torch.cuda.synchronize()
+    assert lib.attn_check_device_status() == 0
+    more = torch.log(torch.tensor(2.0 ** 14, dtype=torch.float64))
+    assert (got[1].cpu().double() - (lse + more)).abs().max() <= 3e-4
+    top = (F.read(x[2], True) * VS)[x[3][0].long()].abs().max()
+    bound = (2.0 ** -8 + 2.0 ** -12) * o.abs() + (2.0 ** -10 + 2.0 ** -12) * top
+    assert ((got[0].cpu().double() - o).abs() <= bound).all()
+    # the last 1000 tokens alone, by a window
+    short = run(lib, (x[0], x[1], x[2], table, ctx), scale=0.125, softcap=cap, key_begin=torch.tensor([(1 << 24) - 1000], dtype=torch.int32))
+    begin = [24]
+    R.check(short[0].cpu(), short[1].cpu(), *want(x, 0.125, cap, None, begin))
