@@ -55,10 +55,15 @@ __device__ __forceinline__ uint2 quant8(const float (&f)[8], float inv) {
     return make_uint2(out[0], out[1]);
 }
 
-// AXES: the rows of the angles come from positions with several axes, not from the token's place in the cache.
+// AXES: the rows of the angles come from positions with several axes, not from the token's place in the cache; and it starts while
+// the kernel before it drains (128 tokens into an e4m3 cache, call after call: 10.3 to 12.4 us without, 9.0 to 9.6 with).
 template <bool INTER, bool FP8, bool AXES>
 __global__ void __launch_bounds__(kThreads)
     kv_append_rope_kernel(const std::conditional_t<AXES, RopeAxesParams, RopeParams> p) {
+    if constexpr (AXES) {
+        griddep_launch_dependents();
+        griddep_wait();
+    }
     const int b = (int)(blockIdx.x / (unsigned)p.N), t = (int)(blockIdx.x % (unsigned)p.N);
     if (p.new_lens && t >= p.new_lens[b]) return;  // padding
     // Thread = (item of a row, first row): an item is two vectors -- the two halves of eight pairs, or two
@@ -213,13 +218,9 @@ cudaError_t launch_kv_append_rope(const RopeAppendArgs &a, cudaStream_t stream) 
         RopeAxesParams x;
         static_cast<RopeParams &>(x) = p;
         x.axes = a.axes;
-        if (a.kv_fp8) {
-            if (a.interleaved) kv_append_rope_kernel<true, true, true><<<grid, kThreads, 0, stream>>>(x);
-            else kv_append_rope_kernel<false, true, true><<<grid, kThreads, 0, stream>>>(x);
-        } else {
-            if (a.interleaved) kv_append_rope_kernel<true, false, true><<<grid, kThreads, 0, stream>>>(x);
-            else kv_append_rope_kernel<false, false, true><<<grid, kThreads, 0, stream>>>(x);
-        }
+        auto go = [&](auto kernel) { return launch_dependent(kernel, dim3(grid), kThreads, 0, stream, x); };
+        if (a.kv_fp8) return a.interleaved ? go(kv_append_rope_kernel<true, true, true>) : go(kv_append_rope_kernel<false, true, true>);
+        return a.interleaved ? go(kv_append_rope_kernel<true, false, true>) : go(kv_append_rope_kernel<false, false, true>);
     } else if (a.kv_fp8) {
         if (a.interleaved) kv_append_rope_kernel<true, true, false><<<grid, kThreads, 0, stream>>>(p);
         else kv_append_rope_kernel<false, true, false><<<grid, kThreads, 0, stream>>>(p);
