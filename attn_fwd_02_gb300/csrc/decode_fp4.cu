@@ -346,9 +346,8 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
         // (the next part of the share is found meanwhile)
         if (threadIdx.x == 0 && !a.cluster) sm.seg[cur ^ 1] = next_segment(a, sm.seg[cur], left);
         const int lo = sm.seg[cur].lo, end = min(sm.seg[cur].end, w1 * kRowPS);
-        // each head rounded to f16 after a 2^-sh of its own, which keeps it below 2^15 (exact but for values under f16's range;
-        // sh 0 but for huge queries, at most 113); cc: per score column (heads 2t, 2t + 1 of an n-tile) the factor of its
-        // products, to the cap's argument or, without a cap, to the log2 domain
+        // each head rounded to f16 after a 2^-sh of its own (query_shift); cc: per score column (heads 2t, 2t + 1 of an n-tile) the
+        // factor of its products, to the cap's argument or, without a cap, to the log2 domain
         float cc[NT][2];
         {
             const float c = MOD && a.cap_in > 0.f ? a.cap_in : a.c;
@@ -363,8 +362,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                                                  fabsf(__uint_as_float(qb[nt][ks][i] & 0xffff0000u))));
 #pragma unroll
                 for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-                const int sh = e >= 15 ? min(e - 14, 113) : 0;
+                const int sh = query_shift(amax, c);
                 const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)

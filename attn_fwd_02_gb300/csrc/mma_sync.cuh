@@ -41,6 +41,16 @@ __device__ __forceinline__ uint32_t prmt(uint32_t lo, uint32_t hi, uint32_t sel)
     return r;
 }
 
+// A query head is rounded to f16 after a division by 2^query_shift: of its largest magnitude amax, 2^15 or more comes down below
+// 2^15, and less than 2^-7 up to [1, 2), as far as c, the factor of its products, times that power stays a normal fp32 number (past
+// that every score is 0 beside 1).  So all values are exact but those under f16's range, which are off by 2^-18 of amax at most.
+// From -126 to 113; 0 for magnitudes in between.
+__device__ __forceinline__ int query_shift(float amax, float c) {
+    const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127, ec = (int)((__float_as_uint(c) >> 23) & 0xffu) - 127;
+    if (e >= -7) return e >= 15 ? min(e - 14, 113) : 0;
+    return max(max(e, -126), min(0, -126 - ec));
+}
+
 // Byte offset of the 16-byte chunk holding column col (a multiple of 8) of row r in a page block
 // stored as 128-byte-swizzled boxes of 16 rows x 64 bf16 columns.
 __device__ __forceinline__ uint32_t swz_off(int r, int col) {
