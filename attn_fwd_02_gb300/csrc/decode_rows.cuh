@@ -370,12 +370,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
             }
             cc[nt][0] = cc[nt][1] = c;
             if constexpr (FP8) {
-                // each head is rounded to f16 after a 2^-sh of its own, which keeps it below 2^15 (sh 0 but for huge
-                // queries; at most 113); its four lanes hold its dims
+                // each head is rounded to f16 after a 2^-sh of its own (query_shift); its four lanes hold its dims
 #pragma unroll
                 for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-                const int sh = e >= 15 ? min(e - 14, 113) : 0;
+                const int sh = query_shift(amax, c);
                 const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
