@@ -735,20 +735,19 @@ __global__ void __launch_bounds__(kWarps * 32) decode_gqa_mma_kernel(const __gri
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(u.x << 16)), fabsf(__uint_as_float(u.x & 0xffff0000u))),
                                          fmaxf(fabsf(__uint_as_float(u.y << 16)), fabsf(__uint_as_float(u.y & 0xffff0000u)))));
             }
-        // each head by a factor of its own (row r0, held by four lanes; rows r0 + 8 are empty, so c is that of r0):
-        // 2^-sh * |q| < 2^15: sh = e - 14 when |q| >= 2^15 (e its binary exponent); at most 113
+        // each head by a 2^-sh of its own (query_shift; row r0, held by four lanes; rows r0 + 8 are empty, so c is that of r0)
         static_assert(GP <= 8, "one query head per lane");
 #pragma unroll
         for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-        const int sh = e >= 15 ? min(e - 14, 113) : 0;
+        const int sh = query_shift(amax, c * a.k_scale);
         const float f = __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 qa[ks][i] = pack_f16x2(__uint_as_float(qa[ks][i] << 16) * f, __uint_as_float(qa[ks][i] & 0xffff0000u) * f);
-        c *= a.k_scale * __uint_as_float((uint32_t)(127 + sh) << 23);
+        const float back = __uint_as_float((uint32_t)(127 + sh) << 23);
+        c = sh > 0 ? c * (a.k_scale * back) : c * a.k_scale * back;  // (in the order that stays in range)
     } else {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
