@@ -218,9 +218,9 @@ __device__ __forceinline__ void write_part(RowsRed<D, NT> &red, const float (&o)
         }
         if (whole) {
             const bool any = L != 0.f;
-            const float f = any ? a.v_scale / L : 0.f;
+            const OverSum over(a.v_scale, L, any);
             *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + (row + r) * D + x) =
-                make_uint2(pack_bf16x2(O.x * f, O.y * f), pack_bf16x2(O.z * f, O.w * f));
+                make_uint2(pack_bf16x2(over(O.x), over(O.y)), pack_bf16x2(over(O.z), over(O.w)));
             if (x == 0 && a.lse) a.lse[row + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
         } else {
             *reinterpret_cast<float4 *>(part + (size_t)r * (D + 4) + x) = O;
@@ -768,10 +768,10 @@ __global__ void __launch_bounds__(kJoinWarps<W> * 32) decode_fp4_join_kernel(con
         }
     }
     const bool any = L != 0.f;
-    const float f = any ? a.v_scale / L : 0.f;
+    const OverSum over(a.v_scale, L, any);
     if (4 * lane < D)
         *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + (size_t)row * D + 4 * lane) =
-            make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            make_uint2(pack_bf16x2(over(acc.x), over(acc.y)), pack_bf16x2(over(acc.z), over(acc.w)));
     if (lane == 0 && a.lse) a.lse[row] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
 }
 

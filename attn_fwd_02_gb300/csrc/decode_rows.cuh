@@ -139,6 +139,18 @@ __device__ __forceinline__ PageRange rows_range(const RowsParams &a, int b, int 
     return r;
 }
 
+// O / L of values with a scale.  Of a scale near the smallest and a large sum the quotient would leave fp32's normal numbers where
+// the result does not, so for scales below 1 it is taken 2^64 times as large (an exact power: nothing else changes).
+struct OverSum {
+    float f, back;
+    __device__ __forceinline__ OverSum(float scale, float L, bool any) {
+        const bool small = scale < 1.f;
+        f = any ? (small ? scale * 0x1p64f : scale) / L : 0.f;
+        back = small ? 0x1p-64f : 1.f;
+    }
+    __device__ __forceinline__ float operator()(float O) const { return O * f * back; }
+};
+
 // The end of a CTA's splits: its warps' states are merged in shared memory, over the ring once every warp is done with its
 // pages, and the CTA's goes to the workspace or, through distributed shared memory, into the cluster's result.  CODES: rows
 // g, g + 8 of a tile of O^T are the even and odd dims of its 16, not its halves, and the values have a scale.
@@ -221,8 +233,8 @@ __device__ __forceinline__ void rows_finish(RowsRed<D, NT> &red, volatile int *a
                 }
             }
             const bool any = L != 0.f;
-            const float inv = any ? (CODES ? a.v_scale : 1.f) / L : 0.f;
-            *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(O.x * inv, O.y * inv);
+            const OverSum over(CODES ? a.v_scale : 1.f, L, any);
+            *reinterpret_cast<uint32_t *>(out + (size_t)r * D + 2 * pair) = pack_bf16x2(over(O.x), over(O.y));
             if (pair == 0 && a.lse) a.lse[(size_t)b * a.H + h0 + r] = any ? kRowLn2 * (M + __log2f(L)) : -INFINITY;
         }
         cluster_sync_all();  // no CTA leaves while another reads its state
