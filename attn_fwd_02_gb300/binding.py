@@ -641,10 +641,12 @@ def _axes_in(positions, pair_axis, B, N, cos_sin, device, shared=False):
     A, Bp, Np = positions.shape
     if Np != N or (Bp != B and not (shared and Bp == 1)):
         raise ValueError(f"positions must be [axes, {B}{' or 1' if shared else ''}, {N}], got {tuple(positions.shape)}")
-    try:
-        axis = bytes(pair_axis)
-    except (TypeError, ValueError):
-        raise TypeError("pair_axis must be a sequence of axis numbers") from None
+    axis = pair_axis
+    if not isinstance(axis, bytes):
+        try:
+            axis = bytes(list(axis))  # (of its numbers: bytes of an int are zeros, of an array its memory)
+        except (TypeError, ValueError):
+            raise TypeError("pair_axis must be a sequence of axis numbers") from None
     if 2 * len(axis) != cos_sin.shape[1]:
         raise ValueError(f"pair_axis must have one entry for each of the {cos_sin.shape[1] // 2} pairs, got {len(axis)}")
     return (p, A, Bp, axis) if shared else (p, A, axis)
