@@ -894,7 +894,7 @@ def attn_rope_axes(q, k, cos_sin, positions, pair_axis, interleaved: bool = Fals
     """Rotary embedding by positions with several axes: pair i of token t of sequence b turns by column i of row
     positions[pair_axis[i], b, t] of cos_sin [max_pos, rope_dim] fp32 (cos of the pairs, then sin).  q [B,H,N,d], k
     [B,Hkv,N,d] (or None) and their outputs: bf16 CUDA views whose rows are contiguous (strides in multiples of 8 elements;
-    an output may be its input); positions [axes,B,N] or [axes,1,N] int32.  Tokens with a position outside the table give
+    an output may be its input, and its rows must not overlap); positions [axes,B,N] or [axes,1,N] int32.  Tokens with a position outside the table give
     zeros.  Returns (q_out, k_out)."""
     return _rope_axes("attn_rope_axes", q, k, cos_sin, positions, pair_axis, interleaved, q_out, k_out, stream)
 

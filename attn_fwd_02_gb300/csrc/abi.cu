@@ -724,6 +724,25 @@ ATTN_API int paged_kv_unpack_fp4(const void *k_pages, const void *v_pages, float
 }
 
 namespace {
+// Whether no two of an output's rows of d elements overlap: in ascending order, each stride steps past all that the ones before
+// it reach.  (Every stride is at most 2^40: what reaches past that is past every one.)
+bool rows_apart(const int64_t (&strides)[3], int B, int H, int N, int d) {
+    const int64_t size[3] = {B, H, N};
+    bool seen[3] = {size[0] == 1, size[1] == 1, size[2] == 1};
+    int64_t span = d;
+    for (int n = 0; n < 3; ++n) {
+        int at = -1;
+        for (int i = 0; i < 3; ++i)
+            if (!seen[i] && (at < 0 || strides[i] < strides[at])) at = i;
+        if (at < 0) break;
+        seen[at] = true;
+        if (strides[at] < span) return false;
+        constexpr int64_t kFar = 1ll << 41;
+        span = size[at] - 1 > kFar / strides[at] ? kFar : span + (size[at] - 1) * strides[at];
+    }
+    return true;
+}
+
 int rope_axes(attn::RopeArgs a, const int64_t *q_strides, const int64_t *k_strides, const int64_t *q_out_strides,
               const int64_t *k_out_strides, const int32_t *positions, int n_axes, int positions_batch,
               const uint8_t *pair_axis, attn_stream_t stream) {
@@ -747,6 +766,10 @@ int rope_axes(attn::RopeArgs a, const int64_t *q_strides, const int64_t *k_strid
             return ATTN_ERR_INVALID_ARG;
     if (!aligned16(a.q) || !aligned16(a.q_out) || !aligned16(a.k) || !aligned16(a.k_out) || !aligned16(a.cos_sin))
         return ATTN_ERR_MISALIGNED;
+    // (each row is written by a block of its own)
+    if (!rows_apart(a.q_out_strides, a.B, a.H, a.N, a.d) || (a.k && !rows_apart(a.k_out_strides, a.B, a.Hkv, a.N, a.d)) ||
+        a.q_out == a.k_out)
+        return ATTN_ERR_INVALID_ARG;
     int *status = nullptr;
     st = device_setup(&status);
     if (st != ATTN_OK) return st;

@@ -447,7 +447,8 @@ int paged_kv_unpack_fp4(const void *k_pages, const void *v_pages, float k_scale,
  *   tokens go.  Of a token with a position outside [0, max_pos) nothing is written.
  * attn_rope_axes: the rotation alone.  q [B, H, N, d], k [B, Hkv, N, d] (k and k_out may both be NULL; Hkv is then ignored)
  *   and their outputs are bf16 views with contiguous rows, *_strides as in paged_kv_append_rope; an output may be its input
- *   (the same strides), and must else not overlap an input.  positions_batch: B, or 1 for positions [n_axes, 1, N] that all
+ *   (the same strides), and must else not overlap an input or the other output.  An output whose own rows overlap (a stride of
+ *   0, or one that does not step past what the smaller ones reach) is refused.  positions_batch: B, or 1 for positions [n_axes, 1, N] that all
  *   sequences share.  A token with a position outside [0, max_pos) gives zeros.
  * attn_rope_axes_bwd: its gradient: dq, dk are those of the outputs, q_out and k_out get those of q and k (the transposed
  *   rotation; zeros for tokens outside the table).
