@@ -87,15 +87,15 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_fp4_kernel(const Fp4App
     const int rows = kv_rows + (p.q ? tokens * p.H : 0);
     const int slot = (int)(pos0 % kFp4PS);  // even
     constexpr size_t block = (size_t)9 * D;
-    // A row's 8 dims from vector w on, turned: x c - y s in the first half of the pairs, y c + x s in the second.
+    // A row's 8 dims from vector w on, turned: fma(x, c, -(y s)) in the first half of the pairs, fma(y, c, x s) in the second.
     auto turn_pairs = [&](float (&x)[8], int w, const float *cs) {  // neighbours
         if (8 * w >= p.rope) return;
         const float *c = cs + 4 * w, *s = c + half;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-            x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
-            x[2 * i] = u;
+        for (int i = 0; i < 4; ++i) {  // (rounded as the halves are, and as attn_rope_axes rounds)
+            const float a = x[2 * i], e = x[2 * i + 1];
+            x[2 * i] = __fmaf_rn(a, c[i], -__fmul_rn(e, s[i]));
+            x[2 * i + 1] = __fmaf_rn(e, c[i], __fmul_rn(a, s[i]));
         }
     };
     auto turned = [&](const uint4 *row, int w, const float *cs, float (&x)[8]) {
