@@ -457,16 +457,24 @@ int blocks_for(long long work, int waves) {
     const long long want = (work + 255) / 256, most = (long long)sms * waves;
     return (int)(want < 1 ? 1 : (want < most ? want : most));
 }
-// CTAs of the scanning cluster: one where it passes over the pool, and what else it reads and writes, in a few steps, or where
-// the device (a part of a GPU) cannot place more.
+// CTAs of the scanning cluster: one where it passes over the pool, and what else it reads and writes, in one step, or where
+// the device (a part of a GPU) cannot place more.  Calls one after the other, us, one CTA / eight; entries and pages alike:
+//             256           1024          2048          4096          8192
+//   fork      3.6 / 3.5     4.2 / 4.2     5.4 / 4.1     7.6 / 4.3    12.6 / 4.3
+//   reserve   7.1 / 7.6     7.1 / 7.6     7.1 / 7.3     9.0 / 8.4    12.4 / 8.5
+//   compact   6.5 / 7.2     6.5 / 7.3     8.1 / 7.6    10.8 / 7.8    16.7 / 8.2
+constexpr int kOneCta = 1024;
 template <class K>
 int scan_ctas(K kernel, long long items) {
-    return items <= 2 * kScanTile || !cluster_fits(reinterpret_cast<const void *>(kernel), kScanCtas, kScanThreads, 0) ? 1 : kScanCtas;
+    return items <= kOneCta || !cluster_fits(reinterpret_cast<const void *>(kernel), kScanCtas, kScanThreads, 0) ? 1 : kScanCtas;
 }
-// Table entries and pages that the cluster reads and writes itself; more take a grid of their own.  Fork, reservation and copies,
-// us, all by the cluster / the large steps by grids: 16 rows of 64 entries 14.1 / 15.5; 128 rows of 1024, 60000 of them counted
-// anew, 49.6 / 30.7 (25.1 as the large steps are now).
-constexpr long long kClusterItems = 1 << 15;
+// Table entries and pages that the cluster reads and writes itself; more take a grid of their own (the reservation's table: more
+// clusters).  As above, all by the cluster of eight / the large steps apart:
+//             2048          4096          8192          16384         32768         65536
+//   fork      4.1 / 4.4     4.3 / 4.4     4.3 / 4.2     5.9 / 4.3     8.2 / 4.4    13.8 / 4.2
+//   reserve   7.3 / 8.0     8.4 / 9.1     8.5 / 9.1     9.1 / 9.4     9.5 / 9.3    10.6 / 9.8
+//   compact   7.6 / 8.1     7.8 / 8.2     8.2 / 8.5     9.0 / 8.7    11.5 / 10.2   18.0 / 15.3
+constexpr long long kClusterItems = 1 << 13, kReserveItems = 1 << 15;
 
 // A kernel of one cluster, or several, of `ctas` CTAs.
 template <class K, class A>
@@ -529,8 +537,8 @@ cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t stream) {
     p.W = a.max_pages;
     p.P = a.num_pages;
     const long long cells = p.copy_table ? (long long)a.B * a.max_pages : 0;
-    p.table_apart = cells > kClusterItems;
-    p.counts_copied = a.num_pages > kClusterItems;
+    p.table_apart = cells > kReserveItems;
+    p.counts_copied = a.num_pages > kReserveItems;
     p.ctas = scan_ctas(pages_reserve_kernel, cells > a.num_pages ? cells : a.num_pages);
     if (p.counts_copied) {
         const cudaError_t e = launch_dependent(pages_reserve_copy_kernel, dim3(blocks_for(a.num_pages, 8)), 256, 0, stream, p);
