@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_gqa_mma_kernel(const __gri
         static_assert(GP <= 8, "one query head per lane");
 #pragma unroll
         for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const int sh = query_shift(amax, c * a.k_scale);
+        const int sh = query_shift(amax, query_low(c * a.k_scale));
         const float f = __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)

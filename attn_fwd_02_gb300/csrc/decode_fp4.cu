@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                                                  fabsf(__uint_as_float(qb[nt][ks][i] & 0xffff0000u))));
 #pragma unroll
                 for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                const int sh = query_shift(amax, c);
+                const int sh = query_shift(amax, a.q_low);
                 const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
@@ -882,6 +882,7 @@ cudaError_t launch_decode_fp4(const DecodeMoreArgs &a, cudaStream_t stream) {
     p.v_scale = a.v_scale;
     p.cap_in = a.softcap > 0.f ? kscale / a.softcap : 0.f;
     p.cap_out = a.softcap * kRowLog2e;
+    p.q_low = query_low(p.cap_in > 0.f ? p.cap_in : p.c);
     p.slopes = a.slopes;
     p.key_begin = a.key_begin;
     switch (a.d) {

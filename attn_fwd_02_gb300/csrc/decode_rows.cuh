@@ -39,6 +39,7 @@ struct RowsParams {
     int n_splits, ws_splits, ws_first;  // this kernel writes partials ws_first .. ws_first + n_splits - 1
     float c;                            // scale * log2(e) (times the key scale of an e4m3 cache)
     float v_scale;
+    int q_low;                          // of the queries' powers of two (query_shift)
     // groups of S sequences: the first shared_pages[b / S] pages are those of the group's first row of the
     // table; own_only: they are not read here
     const int32_t *shared_pages;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4)
                 // each head is rounded to f16 after a 2^-sh of its own (query_shift); its four lanes hold its dims
 #pragma unroll
                 for (int off = 1; off <= 2; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                const int sh = query_shift(amax, c);
+                const int sh = query_shift(amax, a.q_low);
                 const float f = __uint_as_float((uint32_t)(127 - sh) << 23), back = __uint_as_float((uint32_t)(127 + sh) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)

@@ -54,6 +54,7 @@ cudaError_t launch_decode_scoremod(const DecodeMoreArgs &a, cudaStream_t stream)
     p.v_scale = a.v_scale;
     p.cap_in = a.softcap > 0.f ? kscale / a.softcap : 0.f;
     p.cap_out = a.softcap * kRowLog2e;
+    p.q_low = query_low(p.cap_in > 0.f ? p.cap_in : p.c);
     p.slopes = a.slopes;
     p.key_begin = a.key_begin;
     switch (a.d) {

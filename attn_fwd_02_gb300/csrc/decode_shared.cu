@@ -155,6 +155,7 @@ cudaError_t launch_decode_shared(const DecodeMoreArgs &a, cudaStream_t stream) {
     p.ws_first = pl.prefix_splits;
     p.ws_splits = pl.prefix_splits + pl.own_splits;
     p.c = a.scale * kRowLog2e * (a.kv_fp8 ? a.k_scale : 1.f);
+    p.q_low = query_low(p.c);
     p.v_scale = a.v_scale;
     p.shared_pages = a.shared_pages;
     p.S = a.group_size;
