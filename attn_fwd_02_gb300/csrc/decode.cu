@@ -616,9 +616,9 @@ __global__ void __launch_bounds__(kWarps * 32) decode_split_kernel(const DecodeA
 //    16c + 2g and 16c + 2g + 1; one byte permute splits them into the B fragments of two n-tiles,
 //    one over the chunk's even dims and one over its odd dims, and the final write of O puts
 //    column n of n-tile (c, parity) at dim 16c + 2n + parity.
-// Q is rounded to f16 once per CTA after a power-of-two factor that keeps |Q| below 2^15 (exact
-// for every bf16 value in f16's normal range); the factor, the key scale and the softmax scale fold
-// into the score scale, the value scale into the partial O.
+// Q is rounded to f16 once per CTA after a power-of-two factor of each head's own (query_shift); the
+// factor, the key scale and the softmax scale fold into the score scale, the value scale into the
+// partial O.
 // Ring slots per warp of the grouped-query kernel: the page loads in flight per warp.  Measured
 // on 32 sequences x 8 cache heads (4 query heads each), contexts U[512, 8192], fraction of HBM:
 // bf16 pages 1 / 2 / 3 slots 0.853 / 0.880 / 0.844; e4m3 pages 2 / 3 / 4 slots 0.565 / 0.555 /

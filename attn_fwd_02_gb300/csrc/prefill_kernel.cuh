@@ -44,6 +44,7 @@
 #include <cmath>
 
 #include "launch.h"
+#include "mma_sync.cuh"
 #include "scoremod.cuh"
 #include "sm103_ptx.cuh"
 
@@ -692,11 +693,10 @@ __device__ __forceinline__ void exp_store(const uint32_t (&s)[2][32], uint32_t t
 }
 
 // Row r of a Q tile (kPad/64 boxes of kBM x 64 bf16, 128-byte swizzle) rounded to f16 in place after
-// the factor 2^-sh, sh = 0 unless |q| reaches 2^15 (then the smallest that brings the row below 2^15,
-// at most 113); returns 2^sh.  Chunk j of the row is read from position j ^ (r % 8) so that eight
-// consecutive rows fall in different banks.
+// the factor 2^-sh of query_shift (from `low` on); returns 2^sh.  Chunk j of the row is read from position
+// j ^ (r % 8) so that eight consecutive rows fall in different banks.
 template <int D>
-__device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r) {
+__device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r, int low) {
     constexpr int kBx = kPad<D> / 64;
     uint8_t *base = reinterpret_cast<uint8_t *>(qt) + r * 128;
     uint4 v[kBx * 8];
@@ -709,8 +709,7 @@ __device__ __forceinline__ float q_row_to_f16(__nv_bfloat16 *qt, int r) {
         for (int k = 0; k < 4; ++k)
             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
     }
-    const int e = (int)((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-    const int sh = e >= 15 ? min(e - 14, 113) : 0;
+    const int sh = query_shift(amax, low);
     const float f = __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
     for (int i = 0; i < kBx * 8; ++i) {
@@ -787,11 +786,11 @@ __device__ void run_softmax(PrefillSmem<D, M> &sm, const Params<M> &p, const CUt
     float c = p.scale_log2;
     if constexpr (kIsE4m3<M>) {
         // Over e4m3 pages the products run in f16: each thread rounds its Q row to f16 in place once
-        // Q has landed, after a power-of-two factor 2^-sh that keeps the row below 2^15 (exact for
-        // every value in f16's normal range), and folds 2^sh into its score scale.
+        // Q has landed, after a power-of-two factor 2^-sh (query_shift), and folds 2^sh into its score
+        // scale.
         if (n_all > 0) {
             if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, wc, 25))) return;
-            c *= q_row_to_f16<D>(sm.q[t], r);
+            c *= q_row_to_f16<D>(sm.q[t], r, query_low(c));
             fence_proxy_async_smem();  // before the MMA's reads of the tile
             mbar_arrive(&sm.q_conv[t]);
         }

@@ -359,8 +359,9 @@ int paged_kv_append_rope_fp8(const void *q, const int64_t *q_strides, const void
  *   table, the masks and the result are as in paged_attn_prefill, for the dequantised
  *   cache.  The codes are widened exactly to f16 in shared memory and both products run
  *   in f16 with fp32 accumulation: each query row is rounded to f16 after a power-of-two
- *   factor that keeps it below 2^15 (exact for bf16 values in f16's normal range).  The
- *   key scale multiplies the scores and the value scale the output.
+ *   factor of its own, which keeps it below 2^15 and its largest value from 2^-7 on (exact
+ *   but for values under f16's normal range, off by 2^-18 of the row's largest at most).
+ *   The key scale multiplies the scores and the value scale the output.
  * paged_attn_decode_fp8: paged_attn_decode_gqa over an e4m3 cache (k_pages,
  *   v_pages [num_pages, Hkv, page_size, d] uint8 codes; k_scale, v_scale > 0
  *   and finite).  q, o, lse, the table, the workspace and the result are as in
