@@ -282,8 +282,9 @@ int paged_attn_decode_shared_fp8(const void *q, const void *k_pages, const void 
  * A page id outside [0, num_pages) is an unmapped page, as in decode: the positions
  * it covers hold no token (their keys are masked out; the other positions keep their
  * places, so the causal alignment is unchanged), and a query that sees no mapped key
- * gets O = 0 and LSE = -inf.  Runs on the same tcgen05 pipeline as attn_fwd, with
- * each 128-key tile gathered page by page through TMA.
+ * gets O = 0 and LSE = -inf.  Slots of the last page past ctx_lens[b] may hold anything.
+ * Runs on the same tcgen05 pipeline as attn_fwd, with each 128-key tile gathered page by
+ * page through TMA.
  */
 int paged_attn_prefill(const void *q, const void *k_pages, const void *v_pages,
                        const int32_t *page_table, const int32_t *ctx_lens, int page_size,
