@@ -9,16 +9,22 @@
 // A byte of codes widens to one f16x2 register in one instruction and a product with the pair of block scales makes it the
 // value (exact).  The scales of slots that are not seen are zeroed, so whatever they hold adds nothing.
 //
-// At 4.5 bits a value the instructions per page are what the time goes by, not the bytes: of about 260 a page and warp (d 128)
-// the widening takes 82 and the products with the scales 64, so a warp takes two pages at a step, which share the waiting, the
-// vote on the maxima and the copies' issue, and the plain scores take one packed FMA into the exponent.
+// What the time goes by (32/8 heads, d 128, replayed graphs): 32 sequences of one length, 2048 / 4096 / 8192 / 16384 / 32768 tokens,
+// take 23.6 / 34.9 / 57.9 / 104.8 / 198.2 us, which is 6.4 to 6.6 TB/s for every further byte, near a copy's rate, and 11 to 12 us at
+// no bytes at all: the launch, then in a row the lengths of all sequences, the search for the share, page ids, the first pages, and
+// the joining kernel.  (One sequence of 16384 to 262144: the same rate, and 10 to 11 us.)  A warp issues about 260 instructions a page
+// (d 128), of which the widening takes 82 and the products with the scales 64, and it takes two pages at a step, which share the
+// waiting, the vote on the maxima and the copies' issue, and plain scores take one packed FMA into the exponent.
 //
 // The pages of all rows (a sequence's heads that one CTA takes) are shared out over the CTAs that fit the GPU, by the lengths
 // on the device: a CTA's share begins and ends anywhere in a row, rows that it has whole it writes itself, and the others'
-// parts, two a CTA at most, are joined by a second kernel.  So neither the page table's width nor uneven lengths cost anything.
-// A small batch takes one cluster per row instead, which joins its CTAs' parts itself.
-// Measured (32/8 heads, d 128): 64 sequences of up to 16000 tokens 116 us (5.6 TB/s), 32 of up to 8192 37.7 us (4.0 TB/s; 51
-// with splits of the table's width), one of 103000 29.9 us (56); 2 of up to 900, 12 heads of 64, with a distance bias 5.7 us.
+// parts, two a CTA at most, are joined by a second kernel.  So uneven lengths cost nothing, and of the page table's width nothing is
+// read that holds no token.  A small batch takes one cluster per row instead, which joins its CTAs' parts itself; the host
+// chooses by the table's width, so short sequences in a wide table pay for the shares' start and join: 2 of up to 900, 12 heads of
+// 64, with a distance bias, 5.6 us in a table of up to 1024 pages, 9.3 in a wider one (calls one after the other 6.1 and 11.3).
+// Measured (32/8 heads, d 128): 64 sequences of up to 16000 tokens 116 us (5.6 TB/s), 32 of up to 8192 38.3 us (4.0 TB/s; 51
+// with splits of the table's width), one of 103000 29.9 us (56).  More than 8 heads a group (a form that spills at d 128): 32 of
+// up to 8192 over 8 key/value heads, 4 / 8 / 16 heads a group 38.0 / 40.6 / 71.0 us, with a cap 39.5 / 43.6 / 80.3; d 64, 8 / 16 25.1 / 35.2.
 #include <type_traits>
 
 #include "decode_rows.cuh"
@@ -35,7 +41,8 @@ struct Fp4Params : RowsParams {
     int2 *row_ctas;  // [B, rows of a sequence]: the CTAs with a row's first and last page
 };
 
-// CTAs per SM, by registers (128 a thread for up to 8 heads, 168 for 16) and shared memory.  (Five of one page a step: 64 us.)
+// CTAs per SM, by registers (128 a thread for up to 8 heads, 168 for 16) and shared memory.  (Five of one page a step: 64 us.)  At
+// d 128 the form of 16 heads spills under its 168: 268 bytes stored and 300 loaded (plain), 276 and 336 (modified); that of 8 heads 12 and 20.
 template <int NT> constexpr int kFp4Ctas = NT == 1 ? 4 : 3;
 
 // A CTA's part of a row.
@@ -599,7 +606,10 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                             p[i + 1] = ex2_approx(p[i + 1]);
                             l[nt] = f32x2_add(l[nt], f32x2_pack(p[i], p[i + 1]));
                         }
-                        // tokens from the rows into the pairs of the B operand
+                        // tokens from the rows into the pairs of the B operand.  The weights are rounded to f16 once
+                        // (2^-11 of each at most; the sum takes them unrounded), as the product takes them: the rest in a
+                        // second product would cost as much as the first, and the result, rounded to bf16, is off by
+                        // 0.00168 of itself where fp32 weights give 0.00167.
                         pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));
                         pb[nt][1] = movmatrix_trans(pack_f16x2(p[2], p[3]));
                     }
@@ -779,10 +789,11 @@ size_t fp4_parts_bytes(int group, int d) {
     return (size_t)kSms * (group <= 8 ? kFp4Ctas<1> * 8 : kFp4Ctas<2> * 16) * 2 * (size_t)(d + 4) * sizeof(float);
 }
 
-// Splits of a row for the form whose splits are one cluster (0: shares).  It takes one launch and no workspace, but splits every
-// row alike and by the table's width: for rows that are resident all at once with up to kClusterPages pages a CTA.  Both ways,
+// Splits of a row for the form whose splits are one cluster (0: shares).  It takes one launch and no workspace, but as many CTAs for
+// a short row as for a long one, and how many is the host's choice, by the table's width: for rows that are resident all at once
+// with up to kClusterPages pages a CTA.  Both ways,
 // us (cluster / shares; 32/8 heads, d 128 unless said):
-//   2 sequences of up to 900, 12 heads of 64   6.4 / 10.3      32 of 1000 (32 pages a CTA)    14.4 / 16.4
+//   2 sequences of up to 900, 12 heads of 64   6.1 / 11.3      32 of 1000 (32 pages a CTA)    14.4 / 16.4
 //   1 of 16000 (63 pages a CTA)               13.4 / 14.3      64 of 200, 500, 1000 (63)      12.4 / 16.5, 16.4 / 18.5, 22.5 / 23.2
 //   1 of 32000 (125)                          18.5 / 16.4      32 of 2000 (63), 4000 (125)    20.0 / 20.5, 29.9 / 26.6
 //   not resident at once, one CTA a row: 128 of 110 and 600, 12 heads of 64, 17.5 / 16.4, 26.6 / 24.6; 256 of 100 32.6 / 28.7

@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kScanThreads) pages_reserve_kernel(const Reser
     scan_part(p.P, cta, p.ctas, begin, end);
     const int4 v0 = counts4(p.ref, begin + 4 * (int)threadIdx.x, end, 1);
     // an entry to be given a page: it has none, or shares it (by the counts at the call's start: the input's, which do not
-    // change before the second barrier, and then its copy)
+    // change before the second barrier, and then its copy).  So what a row needs hangs on no other row's fate, and the rows' sums
+    // are one scan; the price is one page more than needed where all that share one ask at once, free again at the next call.
     const int32_t *counts = p.ref;
     auto lacks = [&](int e) { return !in_pool(e, p.P) || __ldcg(counts + e) > 1; };
     // the first 32 entries of a row, one a lane: what they name, and which lack a page

@@ -497,7 +497,9 @@ int attn_rope_axes_bwd(const void *dq, const int64_t *dq_strides, const void *dk
  *   counts plus the new table's entries less the old one's.
  * paged_kv_reserve: makes the entries that cover positions ctx_lens[b] .. ctx_lens[b] + new_lens[b] - 1 the row's own: an
  *   entry that names no page gets a free one, and so does one whose page has a count over 1 at the call's start (it is
- *   shared).  Free pages are given out in ascending order, to rows and entries in ascending order.  A row that needs more
+ *   shared).  So of S rows that share a page and all write into it each gets one of its own, and the shared one is left with
+ *   S counts less (free, if no one else holds it): what a row needs does not hang on whether another row is served.  Free
+ *   pages are given out in ascending order, to rows and entries in ascending order.  A row that needs more
  *   pages than rows before it leave, or more entries than the table has, is left as it is; the former rows' needs count for
  *   the rows after them, the latter's do not.
  *     reserved [B]: new_lens[b] if the row can take its tokens, else 0 (and 0 where new_lens[b] <= 0), which is what the
