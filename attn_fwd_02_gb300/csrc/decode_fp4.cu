@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
     constexpr int kSl = kFp4Slots;
     constexpr uint32_t kBlock = 9 * D;
     constexpr int KS = D / 16;  // k-steps of S^T, and 16-dim tiles of O^T
-    constexpr float kThresh = 8.0f;
+    // A weight is 2^(score - reference), of which the reference moves when a score passes the last maximum by 2^kThresh.  It lies
+    // 2^kLift under that maximum, so that the weights fill f16's range (at most 2^15) and those from 2^-21 of the largest on keep 11
+    // bits: the values are often exactly 0 in 4 bits, and then a result is a sum over small weights alone.
+    constexpr float kThresh = 8.0f, kLift = 7.0f;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     using Smem = Fp4Smem<D, NT>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
         }
 
         float o[NT][KS][4];
-        // of heads 2t, 2t + 1: the reference maximum (log2 domain), the score (as the products give it; MOD: in the log2 domain)
+        // of heads 2t, 2t + 1: the reference (log2 domain), the score (as the products give it; MOD: in the log2 domain)
         // past which it moves, and as pairs what is added for it (0 before the first) and this lane's tokens' part of the sum
         float m_ref[NT][2], edge[NT][2];
         uint64_t m_neg[NT], l[NT];
@@ -573,8 +576,8 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                             al[i] = 1.f;
                             if (mx > edge[nt][i]) {
                                 const float m = MOD ? mx : mx * cc[nt][i];
-                                al[i] = ex2_approx(m_ref[nt][i] - m);  // 0 when the reference was -inf
-                                m_ref[nt][i] = m;
+                                al[i] = ex2_approx(m_ref[nt][i] - (m - kLift));  // 0 when the reference was -inf
+                                m_ref[nt][i] = m - kLift;
                                 edge[nt][i] = MOD ? m + kThresh : mx + kThresh / cc[nt][i];
                             }
                         }
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                             l[nt] = f32x2_add(l[nt], f32x2_pack(p[i], p[i + 1]));
                         }
                         // tokens from the rows into the pairs of the B operand.  The weights are rounded to f16 once
-                        // (2^-11 of each at most; the sum takes them unrounded), as the product takes them: the rest in a
+                        // (2^-11 of each at most, under 2^-21 of the largest 2^-32 of that; the sum takes them unrounded), as the product takes them: the rest in a
                         // second product would cost as much as the first, and the result, rounded to bf16, is off by
                         // 0.00168 of itself where fp32 weights give 0.00167.
                         pb[nt][0] = movmatrix_trans(pack_f16x2(p[0], p[1]));

@@ -414,7 +414,8 @@ int paged_kv_append_fp8(const void *k_new, const void *v_new, void *k_pages, voi
  *   paged_attn_prefill attends over the result: the chunked prefill over a 4-bit cache.
  * paged_attn_decode_fp4: paged_attn_decode_scoremod over such a cache (softcap 0, alibi_slopes and key_begin NULL: the plain
  *   decode).  The codes are widened exactly to f16, both products run in f16 with fp32 accumulation (each query rounded to
- *   f16 after a power of two of its own, the weights to f16).  Slots that a query does not see may hold anything.
+ *   f16 after a power of two of its own, the weights to f16: by 2^-11 of each, under 2^-21 of
+ *   the row's largest by 2^-32 of that).  Slots that a query does not see may hold anything.
  *   scale * k_scale lies in [1e-37, 1e37] too.
  *   workspace: at least paged_attn_decode_fp4_workspace_size(...) bytes.
  */

@@ -3,7 +3,7 @@ times the values' scale, and no step of that leaves fp32's normal numbers before
 
 One query sees keys of two scores: the first pages that each warp takes score 0, all others 2^a more, under the 2^8 at which
 the reference of the weights moves, so that the sum L is as large as it gets.  The sum and a are chosen so that a quotient
-scale / L in fp32's subnormal numbers would lie half way between two of them, 2.4 % off at least."""
+scale / L in fp32's subnormal numbers would be 2.4 % off at least (with the largest weight at 1 it lies half way between two)."""
 import math
 
 import pytest
