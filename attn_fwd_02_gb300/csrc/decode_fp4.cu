@@ -14,7 +14,7 @@
 // no bytes at all: the launch, then in a row the lengths of all sequences, the search for the share, page ids, the first pages, and
 // the joining kernel.  (One sequence of 16384 to 262144: the same rate, and 10 to 11 us.)  A warp issues about 260 instructions a page
 // (d 128), of which the widening takes 82 and the products with the scales 64, and it takes two pages at a step, which share the
-// waiting, the vote on the maxima and the copies' issue, and plain scores take one packed FMA into the exponent.
+// waiting, the vote on the maxima and the copies' issue.
 //
 // The pages of all rows (a sequence's heads that one CTA takes) are shared out over the CTAs that fit the GPU, by the lengths
 // on the device: a CTA's share begins and ends anywhere in a row, rows that it has whole it writes itself, and the others'
@@ -242,10 +242,13 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
     constexpr int kSl = kFp4Slots;
     constexpr uint32_t kBlock = 9 * D;
     constexpr int KS = D / 16;  // k-steps of S^T, and 16-dim tiles of O^T
-    // A weight is 2^(score - reference), of which the reference moves when a score passes the last maximum by 2^kThresh.  It lies
-    // 2^kLift under that maximum, so that the weights fill f16's range (at most 2^15) and those from 2^-21 of the largest on keep 11
-    // bits: the values are often exactly 0 in 4 bits, and then a result is a sum over small weights alone.
-    constexpr float kThresh = 8.0f, kLift = 7.0f;
+    // A weight is 2^(score - reference), of which the reference moves when a score passes the last maximum by kThresh.  It lies
+    // kLift under that maximum, so that the weights fill f16's range (at most 2^15) and those from 2^-21 of the largest on keep 11
+    // bits: the values are often exactly 0 in 4 bits, and then a result is a sum over small weights alone.  Scores in the log2
+    // domain are lifted up to kLifted, where the reference still has its bits; plain scores have the maximum taken off before
+    // they come to that domain, so that no rounding of a large product is left in the exponent (one packed addition a pair of scores:
+    // 32 sequences of up to 8192 tokens 38.0 -> 38.2 us).
+    constexpr float kThresh = 8.0f, kLift = 7.0f, kLifted = 1048576.f;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     using Smem = Fp4Smem<D, NT>;
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -401,7 +404,8 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
 
         float o[NT][KS][4];
         // of heads 2t, 2t + 1: the reference (log2 domain), the score (as the products give it; MOD: in the log2 domain)
-        // past which it moves, and as pairs what is added for it (0 before the first) and this lane's tokens' part of the sum
+        // past which it moves, and as pairs what is added to a score (plain: less the maximum; MOD: less the reference; 0 before
+        // the first) and this lane's tokens' part of the sum
         float m_ref[NT][2], edge[NT][2];
         uint64_t m_neg[NT], l[NT];
 #pragma unroll
@@ -567,7 +571,8 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float al[2];
+                        float al[2], last_max[2];
+                        f32x2_unpack(m_neg[nt] ^ 0x8000000080000000ull, last_max[0], last_max[1]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float mx = most_of(nt, i);
@@ -576,14 +581,20 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
                             al[i] = 1.f;
                             if (mx > edge[nt][i]) {
                                 const float m = MOD ? mx : mx * cc[nt][i];
-                                al[i] = ex2_approx(m_ref[nt][i] - (m - kLift));  // 0 when the reference was -inf
-                                m_ref[nt][i] = m - kLift;
-                                edge[nt][i] = MOD ? m + kThresh : mx + kThresh / cc[nt][i];
+                                const float ref = !MOD || fabsf(m) < kLifted ? m - kLift : m;
+                                const float past = MOD ? m_ref[nt][i] - ref : (last_max[i] - mx) * cc[nt][i];
+                                al[i] = m_ref[nt][i] == -INFINITY ? 0.f : ex2_approx(past);
+                                m_ref[nt][i] = ref;
+                                edge[nt][i] = __fadd_rd(mx, MOD ? kThresh : kThresh / cc[nt][i]);
+                                last_max[i] = mx;
                             }
                         }
                         l[nt] = f32x2_mul(l[nt], f32x2_pack(al[0], al[1]));
-                        m_neg[nt] = f32x2_pack(m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0],
-                                               m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1]);
+                        if constexpr (MOD)
+                            m_neg[nt] = f32x2_pack(m_ref[nt][0] == -INFINITY ? 0.f : -m_ref[nt][0],
+                                                   m_ref[nt][1] == -INFINITY ? 0.f : -m_ref[nt][1]);
+                        else
+                            m_neg[nt] = f32x2_pack(-last_max[0], -last_max[1]);
 #pragma unroll
                         for (int nd = 0; nd < KS; ++nd) {
                             o[nt][nd][0] *= al[0];
@@ -603,8 +614,8 @@ __global__ void __launch_bounds__(kFp4Threads, kFp4Ctas<NT>)
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {  // the two heads at once
                             const uint64_t x = f32x2_pack(sc[j][nt][i], sc[j][nt][i + 1]);
-                            f32x2_unpack(MOD ? f32x2_add(x, m_neg[nt]) : f32x2_fma(x, f32x2_pack(cc[nt][0], cc[nt][1]), m_neg[nt]),
-                                         p[i], p[i + 1]);
+                            const uint64_t y = f32x2_add(x, m_neg[nt]);
+                            f32x2_unpack(MOD ? y : f32x2_fma(y, f32x2_pack(cc[nt][0], cc[nt][1]), f32x2_pack(kLift, kLift)), p[i], p[i + 1]);
                             p[i] = ex2_approx(p[i]);
                             p[i + 1] = ex2_approx(p[i + 1]);
                             l[nt] = f32x2_add(l[nt], f32x2_pack(p[i], p[i + 1]));
